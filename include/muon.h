@@ -345,6 +345,142 @@ void muon_plan_destroy(muon_plan *p);
 const char *muon_status_string(muon_status s);
 const char *muon_last_error(void);
 
+/* ------------------------------------------------------------------------
+ * Operators around the step.  A training program turns token ids into the
+ * gradients that muon_accumulate adds up, and logits into a loss and its
+ * gradient; these entry points are the parts of that which are neither a
+ * matrix product nor the model's own: the embedding lookup and its gradient,
+ * the token log-probability, the clipped policy loss, the preference loss
+ * and the balance loss of a router.  They need no plan.
+ *
+ *  - Matrices are row-major with a row stride (`ld`, in elements, at least
+ *    the row length); elements are fp32 or bf16 (muon_dtype), whole numbers
+ *    int32 or int64 (muon_index_type).  Only element alignment is required.
+ *    A buffer of zero elements may be NULL.
+ *  - Arithmetic is fp32 an element and fp64 a row; bf16 results are rounded
+ *    once, to nearest even.  No float atomics: results are bitwise the same
+ *    from run to run.
+ *  - They enqueue kernels only (no copy, memset, event or allocation), so
+ *    they can be captured into a graph.
+ *  - A workspace is scratch for one call: its contents need not be set
+ *    before nor kept after it, and it must not be given to calls that can
+ *    overlap in time.
+ *  - Errors of all of them: INVALID_ARG (NULL pointer, negative size, ld
+ *    below the row length, unknown enum, non-finite factor), UNSUPPORTED (a
+ *    size beyond a stated limit), ALIAS (an output overlaps another buffer
+ *    of the call, except where in place is allowed), WORKSPACE (missing,
+ *    not 256-byte aligned, too small), HIP.
+ * ---------------------------------------------------------------------- */
+
+typedef enum { MUON_IDX_INT32 = 0, MUON_IDX_INT64 = 1 } muon_index_type;
+
+/* Embedding lookup: out[t] = scale * table[ids[t]] for t < tokens.  table is
+ * vocab x dim, out tokens x dim, both of type `dtype`.  An id outside
+ * [0, vocab) (padding) gives a row of zeros.  Limits: tokens, vocab < 2^31. */
+muon_status muon_embed_forward(const void *table, int64_t vocab, int64_t dim, int64_t table_ld, int32_t dtype,
+                               const void *ids, int32_t id_type, int64_t tokens, float scale, void *out,
+                               int64_t out_ld, void *stream);
+
+/* Its gradient by the table, accumulated in fp32 as muon_accumulate does:
+ *   acc[v] = (first != 0 ? 0 : acc[v]) + scale * sum of dout[t], ids[t] = v.
+ * acc is vocab x dim fp32; with first != 0 every element of it is written
+ * (rows without a token get 0), otherwise only rows that have a token are
+ * touched.  dout is tokens x dim of type `dtype`.  Ids outside [0, vocab)
+ * add nothing.  Limits: tokens, vocab < 2^31. */
+muon_status muon_embed_backward_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim, size_t *bytes);
+muon_status muon_embed_backward(const void *ids, int32_t id_type, int64_t tokens, const void *dout, int32_t dtype,
+                                int64_t dout_ld, float scale, float *acc, int64_t vocab, int64_t dim, int64_t acc_ld,
+                                int32_t first, void *ws, size_t ws_bytes, void *stream);
+
+/* Logits of type `dtype`, rows x vocab, and one target per row, as the
+ * three entry points below take them.  A row whose target is outside
+ * [0, vocab) has none: it is not read, its log-probability is 0 and so is
+ * its gradient.  -inf logits are probabilities of 0; a row with a target
+ * and nothing but -inf has lse = -inf and a NaN log-probability; NaN and
+ * +inf propagate within their row and the sums it enters.
+ * Limits: rows < 2^31, vocab < 2^31. */
+typedef struct {
+  const void *logits;
+  const void *targets;
+  int64_t rows, vocab, ld;
+  int32_t dtype;       /* muon_dtype                                     */
+  int32_t target_type; /* muon_index_type                                */
+} muon_logits;
+
+/* logp[r] = x[r][target] - lse[r], lse[r] = log sum_j exp x[r][j]; fp32.
+ * lse may be NULL; both are 0 in rows without a target. */
+muon_status muon_token_logprob(const muon_logits *x, float *logp, float *lse, void *stream);
+
+/* The clipped policy loss with a KL term over the rows' targets, and its
+ * gradient by the logits:
+ *   ratio = exp(logp - old_logp),  J = min(ratio A, clip(ratio, 1 - clip_low, 1 + clip_high) A)
+ *   kl = exp(d) - 1 - d,  d = ref_logp - logp
+ *   loss = sum_r weights[r] (-J + kl_coef kl)
+ * A row of weight 0 counts as one without a target.  old_logp NULL: the
+ * rows' own log-probabilities (ratio 1, its gradient kept).  ref_logp NULL:
+ * no KL term.  Where both branches of the minimum are equal the gradient is
+ * the unclipped one's.  advantages, weights, old_logp, ref_logp: fp32, one
+ * a row.
+ *   stats[0..4)  loss, its part -sum w J, sum w kl, and the sum of w over
+ *                the rows whose clipped branch was the smaller
+ *   logp         fp32, one a row (0 in rows that do not count)
+ *   dlogits      rows x vocab of x->dtype; may be the logits themselves
+ *                (same pointer and ld). */
+typedef struct {
+  double clip_low, clip_high; /* >= 0 */
+  double kl_coef;
+} muon_policy_options;
+muon_status muon_policy_loss_workspace_bytes(int64_t rows, size_t *bytes);
+muon_status muon_policy_loss(const muon_logits *x, const float *advantages, const float *weights,
+                             const float *old_logp, const float *ref_logp, const muon_policy_options *opt,
+                             float *stats, float *logp, void *dlogits, int64_t dlogits_ld, void *ws, size_t ws_bytes,
+                             void *stream);
+
+/* The preference loss of `pairs` pairs of sequences packed into the rows,
+ * and its gradient by the logits.  Sequence s has the rows
+ * [offsets[s], offsets[s + 1]) (offsets non-decreasing, 2 pairs + 1 of
+ * them; what falls outside [0, rows) is cut off); sequences i and pairs + i
+ * are the chosen and the rejected one of pair i.
+ *   gain_s = sum of the sequence's logp - ref_logp[s],  m = beta (gain_chosen - gain_rejected)
+ *   loss = mean over pairs of -(1 - label_smoothing) log sigmoid(m) - label_smoothing log sigmoid(-m)
+ *   rewards[s] = beta gain_s
+ * Rows of no sequence get a zero gradient.  ref_logp and rewards: fp32,
+ * 2 pairs of them; loss: one fp32.  dlogits may be the logits themselves
+ * (same pointer and ld).  pairs >= 1, 0 <= label_smoothing <= 1. */
+typedef struct {
+  double beta, label_smoothing;
+} muon_preference_options;
+muon_status muon_preference_loss_workspace_bytes(int64_t rows, int64_t pairs, size_t *bytes);
+muon_status muon_preference_loss(const muon_logits *x, const void *offsets, int32_t offset_type, int64_t pairs,
+                                 const float *ref_logp, const muon_preference_options *opt, float *loss,
+                                 float *rewards, void *dlogits, int64_t dlogits_ld, void *ws, size_t ws_bytes,
+                                 void *stream);
+
+/* The balance loss of a router with `experts` experts and k choices a token,
+ * the tokens each expert gets, and the gradient by the router's logits.  T
+ * counts the tokens with valid[t] != 0 (all of them if valid is NULL; at
+ * least 1 is divided by):
+ *   counts[e] = choices of e among the valid tokens,  f_e = counts[e] / (T k)
+ *   balance = experts * sum_e f_e mean_t p[t][e],  z = mean_t lse[t]^2
+ *   loss = coef balance + z_coef z
+ * p is the softmax of a token's logits, lse its log-sum-exp; the counts
+ * carry no gradient.  choices is tokens x k, dense; a choice outside
+ * [0, experts) is counted nowhere.  Tokens that are not valid get a zero
+ * gradient and are not read.
+ *   counts  int32, one an expert;  stats[0..3)  loss, balance, z
+ *   dlogits tokens x experts of type `dtype`; may be the logits themselves
+ *           (same pointer and ld).
+ * Limits: experts <= MUON_BALANCE_MAX_EXPERTS, tokens * k < 2^31. */
+#define MUON_BALANCE_MAX_EXPERTS 1024
+typedef struct {
+  double coef, z_coef;
+} muon_balance_options;
+muon_status muon_balance_loss_workspace_bytes(int64_t tokens, int64_t experts, size_t *bytes);
+muon_status muon_balance_loss(const void *logits, int64_t tokens, int64_t experts, int64_t ld, int32_t dtype,
+                              const void *choices, int32_t choice_type, int64_t k, const uint8_t *valid,
+                              const muon_balance_options *opt, int32_t *counts, float *stats, void *dlogits,
+                              int64_t dlogits_ld, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -2,7 +2,10 @@
 flat-partition writeback as HIP kernels behind a C ABI (include/muon.h).
 
 This package is the Python face of that library: ``_lib`` binds the C entry
-points by name; ``MuonGroup`` is a small convenience wrapper that owns a plan.
+points by name; ``MuonGroup`` is a small convenience wrapper that owns a plan;
+``train_ops`` holds the operators around the step on torch tensors (embedding
+lookup and gradient, token log-probability, policy, preference and balance
+losses).
 Device memory and streams come from the caller (e.g. torch tensors).
 """
 
@@ -13,9 +16,17 @@ from ._lib import (DTYPE, EXPORTS, NS_METHOD, PRECISION, SCHEDULE, MuonError, lo
                    muon_apply_update, muon_check_finite, muon_default_options, muon_last_error, muon_layout,
                    muon_plan_create, muon_plan_destroy, muon_plan_phase_ms, muon_plan_problems, muon_plan_runs,
                    muon_plan_set_timing, muon_plan_stats, muon_plan_workspace_bytes, muon_scatter,
-                   muon_status_string, muon_step, muon_step_ex, muon_step_noalloc)
+                   muon_status_string, muon_step, muon_step_ex, muon_step_noalloc,
+                   INDEX_TYPE, muon_balance_loss, muon_balance_loss_workspace_bytes, muon_balance_options,
+                   muon_embed_backward, muon_embed_backward_workspace_bytes, muon_embed_forward, muon_logits,
+                   muon_policy_loss, muon_policy_loss_workspace_bytes, muon_policy_options, muon_preference_loss,
+                   muon_preference_loss_workspace_bytes, muon_preference_options, muon_token_logprob)
+from . import train_ops
+from .train_ops import (balance_loss, balance_loss_workspace_bytes, embed_backward,  # noqa: F401
+                        embed_backward_workspace_bytes, embed_forward, policy_loss, policy_loss_workspace_bytes,
+                        preference_loss, preference_loss_workspace_bytes, token_logprob)
 
-__all__ = ["MuonGroup", "pack_layout", "MuonError", "load"] + list(EXPORTS)
+__all__ = ["MuonGroup", "pack_layout", "MuonError", "load"] + list(train_ops.__all__) + list(EXPORTS)
 
 
 def pack_layout(shapes, num_partitions: int, align: int = 16, interior_align: bool = False):

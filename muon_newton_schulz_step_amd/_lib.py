@@ -24,12 +24,16 @@ NS_METHOD = {"standard": 0, "gram": 1}
 PRECISION = {"fp32": 0, "bf16": 1}
 DTYPE = {"fp32": 0, "bf16": 1}
 SCHEDULE = {"launches": 0, "persistent": 1}
+INDEX_TYPE = {"int32": 0, "int64": 1}
 
 # every symbol include/muon.h declares
 EXPORTS = ("muon_default_options", "muon_plan_create", "muon_plan_workspace_bytes", "muon_accumulate",
            "muon_step", "muon_step_ex", "muon_step_noalloc", "muon_check_finite", "muon_apply_update", "muon_scatter",
            "muon_plan_stats", "muon_plan_runs", "muon_plan_problems", "muon_plan_set_timing",
-           "muon_plan_phase_ms", "muon_plan_destroy", "muon_status_string", "muon_last_error")
+           "muon_plan_phase_ms", "muon_plan_destroy", "muon_status_string", "muon_last_error",
+           "muon_embed_forward", "muon_embed_backward_workspace_bytes", "muon_embed_backward", "muon_token_logprob",
+           "muon_policy_loss_workspace_bytes", "muon_policy_loss", "muon_preference_loss_workspace_bytes",
+           "muon_preference_loss", "muon_balance_loss_workspace_bytes", "muon_balance_loss")
 
 
 class muon_matrix(C.Structure):
@@ -63,6 +67,23 @@ class muon_problem_info(C.Structure):
                 ("transposed", C.c_int32), ("wave", C.c_int32), ("flops", C.c_double)]
 
 
+class muon_logits(C.Structure):
+    _fields_ = [("logits", C.c_void_p), ("targets", C.c_void_p), ("rows", C.c_int64), ("vocab", C.c_int64),
+                ("ld", C.c_int64), ("dtype", C.c_int32), ("target_type", C.c_int32)]
+
+
+class muon_policy_options(C.Structure):
+    _fields_ = [("clip_low", C.c_double), ("clip_high", C.c_double), ("kl_coef", C.c_double)]
+
+
+class muon_preference_options(C.Structure):
+    _fields_ = [("beta", C.c_double), ("label_smoothing", C.c_double)]
+
+
+class muon_balance_options(C.Structure):
+    _fields_ = [("coef", C.c_double), ("z_coef", C.c_double)]
+
+
 _lib = None
 
 
@@ -76,7 +97,7 @@ def load(path: str | None = None) -> C.CDLL:
         raise ImportError(f"{LIB_NAME} is not built ({p} missing); run "
                           "`python -m muon_newton_schulz_step_amd.build` or __graft_entry__.build()")
     lib = C.CDLL(p)
-    vp, i32, sz = C.c_void_p, C.c_int32, C.c_size_t
+    vp, i32, i64, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
     sig = {
         "muon_default_options": (i32, [C.POINTER(muon_options)]),
         "muon_plan_create": (i32, [C.POINTER(vp), C.POINTER(muon_matrix), i32, C.POINTER(muon_options),
@@ -96,6 +117,19 @@ def load(path: str | None = None) -> C.CDLL:
         "muon_plan_set_timing": (i32, [vp, i32]),
         "muon_plan_phase_ms": (i32, [vp, C.POINTER(C.c_float), C.POINTER(i32)]),
         "muon_plan_destroy": (None, [vp]),
+        "muon_embed_forward": (i32, [vp, i64, i64, i64, i32, vp, i32, i64, C.c_float, vp, i64, vp]),
+        "muon_embed_backward_workspace_bytes": (i32, [i64, i64, i64, C.POINTER(sz)]),
+        "muon_embed_backward": (i32, [vp, i32, i64, vp, i32, i64, C.c_float, vp, i64, i64, i64, i32, vp, sz, vp]),
+        "muon_token_logprob": (i32, [C.POINTER(muon_logits), vp, vp, vp]),
+        "muon_policy_loss_workspace_bytes": (i32, [i64, C.POINTER(sz)]),
+        "muon_policy_loss": (i32, [C.POINTER(muon_logits), vp, vp, vp, vp, C.POINTER(muon_policy_options), vp, vp, vp,
+                                   i64, vp, sz, vp]),
+        "muon_preference_loss_workspace_bytes": (i32, [i64, i64, C.POINTER(sz)]),
+        "muon_preference_loss": (i32, [C.POINTER(muon_logits), vp, i32, i64, vp, C.POINTER(muon_preference_options),
+                                       vp, vp, vp, i64, vp, sz, vp]),
+        "muon_balance_loss_workspace_bytes": (i32, [i64, i64, C.POINTER(sz)]),
+        "muon_balance_loss": (i32, [vp, i64, i64, i64, i32, vp, i32, i64, vp, C.POINTER(muon_balance_options), vp,
+                                    vp, vp, i64, vp, sz, vp]),
         "muon_status_string": (C.c_char_p, [i32]),
         "muon_last_error": (C.c_char_p, []),
     }
@@ -318,3 +352,86 @@ def muon_status_string(status: int) -> str:
 def muon_last_error() -> str:
     v = load().muon_last_error()
     return v.decode() if v else ""
+
+
+# ------------------------------------------------- operators around the step
+# Matrices are (address, ld) pairs of ints or objects with data_ptr(); types
+# are named ("bf16", "int64") or given as the C enums' values.
+
+
+def _it(x) -> int:
+    return x if isinstance(x, int) else INDEX_TYPE[x]
+
+
+def _bytes_of(name: str, *sizes) -> int:
+    v = C.c_size_t()
+    _check(getattr(load(), name)(*[int(x) for x in sizes], C.byref(v)), name)
+    return int(v.value)
+
+
+def muon_embed_forward(table, vocab: int, dim: int, table_ld: int, dtype, ids, id_type, tokens: int, scale: float,
+                       out, out_ld: int, stream=None) -> None:
+    st = load().muon_embed_forward(_ptr(table), vocab, dim, table_ld, _dt(dtype), _ptr(ids), _it(id_type), tokens,
+                                   scale, _ptr(out), out_ld, _stream(stream))
+    if st:
+        _check(st, "muon_embed_forward")
+
+
+def muon_embed_backward_workspace_bytes(tokens: int, vocab: int, dim: int) -> int:
+    return _bytes_of("muon_embed_backward_workspace_bytes", tokens, vocab, dim)
+
+
+def muon_embed_backward(ids, id_type, tokens: int, dout, dtype, dout_ld: int, scale: float, acc, vocab: int, dim: int,
+                        acc_ld: int, first: bool, ws, ws_bytes: int, stream=None) -> None:
+    st = load().muon_embed_backward(_ptr(ids), _it(id_type), tokens, _ptr(dout), _dt(dtype), dout_ld, scale,
+                                    _ptr(acc), vocab, dim, acc_ld, 1 if first else 0, _ptr(ws),
+                                    _ws_bytes(ws, ws_bytes), _stream(stream))
+    if st:
+        _check(st, "muon_embed_backward")
+
+
+def muon_token_logprob(logits: muon_logits, logp, lse=None, stream=None) -> None:
+    st = load().muon_token_logprob(C.byref(logits), _ptr(logp), _ptr(lse), _stream(stream))
+    if st:
+        _check(st, "muon_token_logprob")
+
+
+def muon_policy_loss_workspace_bytes(rows: int) -> int:
+    return _bytes_of("muon_policy_loss_workspace_bytes", rows)
+
+
+def muon_policy_loss(logits: muon_logits, advantages, weights, old_logp, ref_logp, options: muon_policy_options,
+                     stats, logp, dlogits, dlogits_ld: int, ws, ws_bytes: int, stream=None) -> None:
+    st = load().muon_policy_loss(C.byref(logits), _ptr(advantages), _ptr(weights), _ptr(old_logp), _ptr(ref_logp),
+                                 C.byref(options), _ptr(stats), _ptr(logp), _ptr(dlogits), dlogits_ld, _ptr(ws),
+                                 _ws_bytes(ws, ws_bytes), _stream(stream))
+    if st:
+        _check(st, "muon_policy_loss")
+
+
+def muon_preference_loss_workspace_bytes(rows: int, pairs: int) -> int:
+    return _bytes_of("muon_preference_loss_workspace_bytes", rows, pairs)
+
+
+def muon_preference_loss(logits: muon_logits, offsets, offset_type, pairs: int, ref_logp,
+                         options: muon_preference_options, loss, rewards, dlogits, dlogits_ld: int, ws,
+                         ws_bytes: int, stream=None) -> None:
+    st = load().muon_preference_loss(C.byref(logits), _ptr(offsets), _it(offset_type), pairs, _ptr(ref_logp),
+                                     C.byref(options), _ptr(loss), _ptr(rewards), _ptr(dlogits), dlogits_ld, _ptr(ws),
+                                     _ws_bytes(ws, ws_bytes), _stream(stream))
+    if st:
+        _check(st, "muon_preference_loss")
+
+
+def muon_balance_loss_workspace_bytes(tokens: int, experts: int) -> int:
+    return _bytes_of("muon_balance_loss_workspace_bytes", tokens, experts)
+
+
+def muon_balance_loss(logits, tokens: int, experts: int, ld: int, dtype, choices, choice_type, k: int, valid,
+                      options: muon_balance_options, counts, stats, dlogits, dlogits_ld: int, ws, ws_bytes: int,
+                      stream=None) -> None:
+    st = load().muon_balance_loss(_ptr(logits), tokens, experts, ld, _dt(dtype), _ptr(choices), _it(choice_type), k,
+                                  _ptr(valid), C.byref(options), _ptr(counts), _ptr(stats), _ptr(dlogits),
+                                  dlogits_ld, _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream))
+    if st:
+        _check(st, "muon_balance_loss")

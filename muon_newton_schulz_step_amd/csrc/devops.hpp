@@ -1,0 +1,113 @@
+// Device helpers of the training-step operators: 16-byte element vectors,
+// bf16 conversion, index loads and fixed-order reductions.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "train_ops.hpp"
+
+namespace muon {
+namespace dev {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+// Start of a running maximum: the lowest finite value, so that a row of
+// -inf keeps a finite maximum and sums to exactly 0 instead of NaN.
+constexpr float kLowest = -3.402823466e+38f;
+
+__device__ __forceinline__ float bf16_f32(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+// fp32 pair -> packed bf16, round to nearest even (NaN stays NaN)
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const bf16x2 v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// Elements of one 16-byte vector, and their conversion.
+template <bool BF16>
+struct Elem;
+template <>
+struct Elem<true> {
+  typedef uint16_t type;
+  static constexpr int N = 8;
+  static __device__ __forceinline__ float get(type x) { return bf16_f32(x); }
+  static __device__ __forceinline__ type put(float x) { return (type)pack_bf16(x, 0.f); }
+  static __device__ __forceinline__ void unpack(uint4 w, float *v) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(x[k] << 16);
+      v[2 * k + 1] = __uint_as_float(x[k] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float *v) {
+    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  }
+};
+template <>
+struct Elem<false> {
+  typedef float type;
+  static constexpr int N = 4;
+  static __device__ __forceinline__ float get(type x) { return x; }
+  static __device__ __forceinline__ type put(float x) { return x; }
+  static __device__ __forceinline__ void unpack(uint4 w, float *v) {
+    v[0] = __uint_as_float(w.x);
+    v[1] = __uint_as_float(w.y);
+    v[2] = __uint_as_float(w.z);
+    v[3] = __uint_as_float(w.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float *v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+};
+
+// 16-byte accesses at element alignment (the hardware takes any alignment of
+// a 16-byte global access; an access off its own 16 bytes only costs more).
+template <class T>
+__device__ __forceinline__ uint4 load16(const T *p) {
+  uint4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+template <class T>
+__device__ __forceinline__ void store16(T *p, uint4 v) {
+  __builtin_memcpy(p, &v, 16);
+}
+
+__device__ __forceinline__ int64_t index_at(const IndexVec &v, int64_t i) {
+  return v.is64 ? static_cast<const int64_t *>(v.p)[i] : (int64_t)static_cast<const int32_t *>(v.p)[i];
+}
+
+// exp of a non-positive shifted logit: the difference is taken before the
+// change of base, so values at either end of the fp32 range cannot turn an
+// infinite product into NaN.
+__device__ __forceinline__ float exp_shift(float x, float m) { return __builtin_amdgcn_exp2f((x - m) * kLog2e); }
+
+__device__ __forceinline__ double shfl_xor_f64(double v, int m) {
+  union {
+    double d;
+    int i[2];
+  } u;
+  u.d = v;
+  u.i[0] = __shfl_xor(u.i[0], m);
+  u.i[1] = __shfl_xor(u.i[1], m);
+  return u.d;
+}
+
+// Sum over a workgroup of WAVES waves in a fixed order; every thread gets
+// it.  `red` holds WAVES doubles and is free again after the call.
+template <int WAVES>
+__device__ __forceinline__ double block_sum(double v, double *red) {
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) v += shfl_xor_f64(v, m);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double t = 0.0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) t += red[w];
+  __syncthreads();
+  return t;
+}
+
+}  // namespace dev
+}  // namespace muon

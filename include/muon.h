@@ -398,7 +398,7 @@ muon_status muon_embed_backward(const void *ids, int32_t id_type, int64_t tokens
  * its gradient.  -inf logits are probabilities of 0; a row with a target
  * and nothing but -inf has lse = -inf and a NaN log-probability; NaN and
  * +inf propagate within their row and the sums it enters.
- * Limits: rows < 2^31, vocab < 2^31. */
+ * Limits: rows < 2^31, vocab < 2^29. */
 typedef struct {
   const void *logits;
   const void *targets;

@@ -10,6 +10,7 @@ namespace muon {
 namespace dev {
 
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2eLow = (float)(1.44269504088896340736 - (double)kLog2e);  // what fp32 leaves of it
 // Start of a running maximum: the lowest finite value, so that a row of
 // -inf keeps a finite maximum and sums to exactly 0 instead of NaN.
 constexpr float kLowest = -3.402823466e+38f;
@@ -32,6 +33,9 @@ struct Elem<true> {
   static constexpr int N = 8;
   static __device__ __forceinline__ float get(type x) { return bf16_f32(x); }
   static __device__ __forceinline__ type put(float x) { return (type)pack_bf16(x, 0.f); }
+  static __device__ __forceinline__ uint4 none() {  // -inf in every element
+    return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+  }
   static __device__ __forceinline__ void unpack(uint4 w, float *v) {
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -50,6 +54,9 @@ struct Elem<false> {
   static constexpr int N = 4;
   static __device__ __forceinline__ float get(type x) { return x; }
   static __device__ __forceinline__ type put(float x) { return x; }
+  static __device__ __forceinline__ uint4 none() {
+    return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+  }
   static __device__ __forceinline__ void unpack(uint4 w, float *v) {
     v[0] = __uint_as_float(w.x);
     v[1] = __uint_as_float(w.y);
@@ -83,6 +90,25 @@ __device__ __forceinline__ int64_t index_at(const IndexVec &v, int64_t i) {
 // infinite product into NaN.
 __device__ __forceinline__ float exp_shift(float x, float m) { return __builtin_amdgcn_exp2f((x - m) * kLog2e); }
 
+// The same for terms of a row's sum.  log2(e) rounded to fp32 is low by 1.3e-8
+// of itself, an error of one sign in every term: a sequence adds up hundreds
+// of rows' log-probabilities, so the constant's rest is added back.
+__device__ __forceinline__ float exp_term(float x, float m) {
+  const float d = x - m;
+  return __builtin_amdgcn_exp2f(fmaf(d, kLog2eLow, d * kLog2e));
+}
+
+__device__ __forceinline__ double shfl_f64(double v, int lane) {
+  union {
+    double d;
+    int i[2];
+  } u;
+  u.d = v;
+  u.i[0] = __shfl(u.i[0], lane);
+  u.i[1] = __shfl(u.i[1], lane);
+  return u.d;
+}
+
 __device__ __forceinline__ double shfl_xor_f64(double v, int m) {
   union {
     double d;
@@ -93,6 +119,28 @@ __device__ __forceinline__ double shfl_xor_f64(double v, int m) {
   u.i[1] = __shfl_xor(u.i[1], m);
   return u.d;
 }
+
+// A row of a matrix as the kernels walk it: 16-byte vectors at 4-byte
+// alignment, with what is left at either end (at most one bf16 element before
+// them, less than a vector after them) element by element.  Reads off 4 bytes
+// cost a quarter of the bandwidth (4.9 against 6.1 TB/s over 50257-column
+// bf16 rows); beyond 4 bytes alignment made no difference.
+template <bool BF16>
+struct Row {
+  int head, vecs, n;
+  __device__ __forceinline__ Row(const void *p, int64_t cols) {
+    head = BF16 && ((uintptr_t)p & 2) ? 1 : 0;
+    n = (int)cols;
+    vecs = (n - head) / Elem<BF16>::N;
+  }
+  // column of a vector's first element
+  __device__ __forceinline__ uint32_t col(int vec) const { return (uint32_t)(head + vec * Elem<BF16>::N); }
+  // single elements, and the column of the i-th
+  __device__ __forceinline__ int singles() const { return n - vecs * Elem<BF16>::N; }
+  __device__ __forceinline__ uint32_t single(int i) const {
+    return (uint32_t)(i < head ? i : vecs * Elem<BF16>::N + i);
+  }
+};
 
 // Sum over a workgroup of WAVES waves in a fixed order; every thread gets
 // it.  `red` holds WAVES doubles and is free again after the call.

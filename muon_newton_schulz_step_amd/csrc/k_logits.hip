@@ -37,7 +37,7 @@ struct Online {
     s *= exp_shift(m, n);
     m = n;
 #pragma unroll
-    for (int k = 0; k < N; ++k) s += exp_shift(v[k], m);
+    for (int k = 0; k < N; ++k) s += exp_term(v[k], m);
   }
   __device__ __forceinline__ void join(float m2, float s2) {
     const float n = fmaxf(m, m2);
@@ -67,16 +67,18 @@ __device__ __forceinline__ Online block_join(Online o, float *red) {
 
 }  // namespace
 
-// One workgroup a row: maximum, sum and the target's log-probability.
+// One workgroup a row: maximum, sum and the target's log-probability.  HBM-
+// bound.  grad (may be NULL) starts as that of a row without a gradient.
 template <bool BF16, int THREADS>
-__global__ __launch_bounds__(THREADS) void kl_rows(LogitArgs a, const float *weights, RowStat *stat, float *logp,
+__global__ __launch_bounds__(THREADS) void kl_rows(LogitArgs a, RowStat *stat, RowGrad *grad, float *logp,
                                                    float *lse) {
   typedef Elem<BF16> E;
   typedef typename E::type T;
   __shared__ float red[2 * THREADS / 64];
   const int64_t r = blockIdx.x;
   const int64_t target = index_at(a.targets, r);
-  if (target < 0 || target >= a.vocab || (weights && weights[r] == 0.f)) {
+  if (grad && threadIdx.x == 0) grad[r] = RowGrad{0.f, 0.f, 0.f, 0};
+  if (target < 0 || target >= a.vocab) {
     if (threadIdx.x == 0) {
       if (stat) stat[r] = RowStat{0.f, 0.f, 0.0};
       if (logp) logp[r] = 0.f;
@@ -85,26 +87,25 @@ __global__ __launch_bounds__(THREADS) void kl_rows(LogitArgs a, const float *wei
     return;
   }
   const T *x = static_cast<const T *>(a.logits) + r * a.ld;
+  const Row<BF16> row(x, a.vocab);
   Online o;
-  const int64_t vecs = a.vocab / E::N;
-  int64_t i = threadIdx.x;
-  for (; i + 3 * THREADS < vecs; i += 4 * THREADS) {
+  int i = threadIdx.x;
+  for (; i + 3 * THREADS < row.vecs; i += 4 * THREADS) {
     uint4 w[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = load16(x + (i + k * THREADS) * E::N);
+    for (int k = 0; k < 4; ++k) w[k] = load16(x + row.col(i + k * THREADS));
     float v[4 * E::N];
 #pragma unroll
     for (int k = 0; k < 4; ++k) E::unpack(w[k], v + k * E::N);
     o.add<4 * E::N>(v);
   }
-  for (; i < vecs; i += THREADS) {
+  for (; i < row.vecs; i += THREADS) {
     float v[E::N];
-    E::unpack(load16(x + i * E::N), v);
+    E::unpack(load16(x + row.col(i)), v);
     o.add<E::N>(v);
   }
-  i = vecs * E::N + threadIdx.x;
-  if (i < a.vocab) {
-    const float v = E::get(x[i]);
+  if ((int)threadIdx.x < row.singles()) {
+    const float v = E::get(x[row.single(threadIdx.x)]);
     o.add<1>(&v);
   }
   o = block_join<THREADS / 64>(o, red);
@@ -117,47 +118,143 @@ __global__ __launch_bounds__(THREADS) void kl_rows(LogitArgs a, const float *wei
   }
 }
 
-// The policy loss of every row and its four sums, in one workgroup.
+namespace {
+
+// Vectors of a row that a thread keeps in registers (64 of the 128 it has
+// with a 1024-thread workgroup on a CU, or several smaller ones).
+constexpr int KEEP = 16;
+
+}  // namespace
+
+// The policy loss and its gradient, one workgroup a row:
 //   ratio = exp(logp - old), J = min(ratio a, clip(ratio) a)
 //   KL estimate exp(d) - 1 - d, d = ref - logp
 // The derivative by logp is -a ratio while the unclipped branch is the
 // smaller, plus kl_coef (1 - exp(d)).
-__global__ __launch_bounds__(1024) void kl_policy(LogitArgs a, PolicyArgs p, const RowStat *stat, RowGrad *grad) {
+//
+// HBM-bound, one read and one write of a row: the row stays in the
+// workgroup's registers between its sum and its gradient (a CU's registers
+// hold 256 KB of it; what a longer row has beyond KEEP vectors a thread is
+// read again).  The row's own arithmetic, in fp64, is two function calls deep
+// in one wave: lanes 0 to 2 share a call of expm1.
+template <bool BF16, int THREADS>
+__global__ __launch_bounds__(THREADS, 4) void kl_policy(LogitArgs a, PolicyArgs p, void *dlogits, int64_t dld,
+                                                        double *terms) {
+  typedef Elem<BF16> E;
+  typedef typename E::type T;
+  __shared__ float red[2 * THREADS / 64];
+  __shared__ float coef[3];
+  const int64_t r = blockIdx.x;
+  const int tid = threadIdx.x;
+  const int64_t target = index_at(a.targets, r);
+  const float w = p.weights[r];
+  T *d = static_cast<T *>(dlogits) + r * dld;
+  if (target < 0 || target >= a.vocab || w == 0.f) {
+    const Row<BF16> out(d, a.vocab);
+    for (int i = tid; i < out.vecs; i += THREADS) store16(d + out.col(i), make_uint4(0, 0, 0, 0));
+    if (tid < out.singles()) d[out.single(tid)] = T(0);
+    if (tid < 4) terms[4 * r + tid] = 0.0;
+    if (tid == 0) p.logp[r] = 0.f;
+    return;
+  }
+  const T *x = static_cast<const T *>(a.logits) + r * a.ld;
+  const Row<BF16> row(x, a.vocab);
+  uint4 keep[KEEP];
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k) {
+    const int i = tid + k * THREADS;
+    keep[k] = i < row.vecs ? load16(x + row.col(i)) : E::none();
+  }
+  const bool lone = tid < row.singles();
+  const float single = lone ? E::get(x[row.single(tid)]) : -INFINITY;
+  const float at_target = E::get(x[target]);
+  Online o;
+#pragma unroll
+  for (int k = 0; k < KEEP; k += 2) {
+    if (k * THREADS < row.vecs) {
+      float v[2 * E::N];
+      E::unpack(keep[k], v);
+      E::unpack(keep[k + 1], v + E::N);
+      o.add<2 * E::N>(v);
+    }
+  }
+  for (int i = tid + KEEP * THREADS; i < row.vecs; i += THREADS) {
+    float v[E::N];
+    E::unpack(load16(x + row.col(i)), v);
+    o.add<E::N>(v);
+  }
+  o.add<1>(&single);
+  o = block_join<THREADS / 64>(o, red);
+  if (tid < 64) {
+    const double logp = (double)at_target - (double)o.m - log((double)o.s);
+    // lane 0: the ratio, lane 1: the KL term, lane 2: the target's own share
+    double arg = 0.0;
+    if (tid == 0 && p.old_logp) arg = logp - (double)p.old_logp[r];
+    if (tid == 1 && p.ref_logp) arg = (double)p.ref_logp[r] - logp;
+    if (tid == 2) arg = logp;
+    const double em1 = expm1(arg);
+    const double ratio = 1.0 + shfl_f64(em1, 0), ed = shfl_f64(em1, 1), share = shfl_f64(em1, 2);
+    const double kl = ed - shfl_f64(arg, 1);
+    const double adv = p.advantages[r];
+    const double clipped = fmin(fmax(ratio, 1.0 - p.clip_low), 1.0 + p.clip_high);
+    const bool active = ratio * adv <= clipped * adv;
+    const double pg = active ? -ratio * adv : -clipped * adv;
+    const double dlogp = (double)w * ((active ? -adv * ratio : 0.0) - p.kl_coef * ed);
+    if (tid == 0) {
+      coef[0] = (float)(-dlogp / (double)o.s);
+      coef[1] = (float)(-dlogp * share);
+      coef[2] = dlogp != 0.0 ? 1.f : 0.f;
+      p.logp[r] = (float)logp;
+      terms[4 * r] = (double)w * (pg + p.kl_coef * kl);
+      terms[4 * r + 1] = (double)w * pg;
+      terms[4 * r + 2] = (double)w * kl;
+      terms[4 * r + 3] = active ? 0.0 : (double)w;
+    }
+  }
+  __syncthreads();
+  // the vectors are unpacked a second time: kept unpacked over the sum, a bf16
+  // row would take twice the registers
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k)
+    asm volatile("" : "+v"(keep[k].x), "+v"(keep[k].y), "+v"(keep[k].z), "+v"(keep[k].w));
+  const float c = coef[0], dt = coef[1], m = o.m;
+  const bool live = coef[2] != 0.f;
+  auto grad = [&](uint4 in, int i) {
+    float v[E::N];
+    E::unpack(in, v);
+#pragma unroll
+    for (int j = 0; j < E::N; ++j) v[j] = live ? c * exp_shift(v[j], m) : 0.f;
+    const int at = (int)target - (int)row.col(i);
+    if (at >= 0 && at < E::N) {
+#pragma unroll
+      for (int j = 0; j < E::N; ++j) v[j] = j == at ? dt : v[j];
+    }
+    store16(d + row.col(i), E::pack(v));
+  };
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k) {
+    const int i = tid + k * THREADS;
+    if (i < row.vecs) grad(keep[k], i);
+  }
+  for (int i = tid + KEEP * THREADS; i < row.vecs; i += THREADS) grad(load16(x + row.col(i)), i);
+  if (lone) {
+    const int j = row.single(tid);
+    d[j] = E::put(!live ? 0.f : j == target ? dt : c * exp_shift(single, m));
+  }
+}
+
+// The four sums over the rows, in a fixed order.
+__global__ __launch_bounds__(1024) void kl_policy_sum(const double *terms, int64_t rows, float *stats) {
   __shared__ double red[16];
   double sum[4] = {};
-  const double lo = 1.0 - p.clip_low, hi = 1.0 + p.clip_high;
-  for (int64_t r = threadIdx.x; r < a.rows; r += 1024) {
-    const int64_t target = index_at(a.targets, r);
-    const float w = p.weights[r];
-    if (target < 0 || target >= a.vocab || w == 0.f) {
-      p.logp[r] = 0.f;
-      grad[r] = RowGrad{0.f, 0.f, 0.f, 0};
-      continue;
-    }
-    const RowStat st = stat[r];
-    const double adv = p.advantages[r];
-    const double ratio = p.old_logp ? exp(st.logp - (double)p.old_logp[r]) : 1.0;
-    const double clipped = fmin(fmax(ratio, lo), hi);
-    const bool active = ratio * adv <= clipped * adv;
-    double kl = 0.0, dkl = 0.0;
-    if (p.ref_logp) {
-      const double d = (double)p.ref_logp[r] - st.logp;
-      dkl = -expm1(d);
-      kl = -dkl - d;
-    }
-    const double pg = active ? -ratio * adv : -clipped * adv;
-    const double dlogp = (double)w * ((active ? -adv * ratio : 0.0) + p.kl_coef * dkl);
-    sum[0] += (double)w * (pg + p.kl_coef * kl);
-    sum[1] += (double)w * pg;
-    sum[2] += (double)w * kl;
-    sum[3] += active ? 0.0 : (double)w;
-    p.logp[r] = (float)st.logp;
-    grad[r] = RowGrad{st.max, (float)(-dlogp / (double)st.total), (float)(-dlogp * expm1(st.logp)), dlogp != 0.0};
+  for (int64_t r = threadIdx.x; r < rows; r += 1024) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum[k] += terms[4 * r + k];
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const double t = block_sum<16>(sum[k], red);
-    if (threadIdx.x == 0) p.stats[k] = (float)t;
+    if (threadIdx.x == 0) stats[k] = (float)t;
   }
 }
 
@@ -177,92 +274,88 @@ __device__ __forceinline__ void sequence(const IndexVec &off, int64_t s, int64_t
 //   gain = sum logp - ref, m = beta (gain_chosen - gain_rejected)
 //   loss = -(1 - s) log sigmoid(m) - s log sigmoid(-m)
 //   d loss / d logp = +- beta (sigmoid(m) - (1 - s)) / pairs
-__global__ __launch_bounds__(256) void kl_pairs(LogitArgs a, PreferenceArgs p, const RowStat *stat, double *coef) {
+__global__ __launch_bounds__(256) void kl_pairs(LogitArgs a, PreferenceArgs p, const RowStat *stat, RowGrad *grad,
+                                                double *losses) {
   __shared__ double red[4];
   const int64_t i = blockIdx.x;
+  int64_t lo[2], hi[2];
   double gain[2];
   for (int side = 0; side < 2; ++side) {
     const int64_t s = i + side * p.pairs;
-    int64_t lo, hi;
-    sequence(p.offsets, s, a.rows, &lo, &hi);
+    sequence(p.offsets, s, a.rows, &lo[side], &hi[side]);
     double t = 0.0;
-    for (int64_t r = lo + threadIdx.x; r < hi; r += 256) t += stat[r].logp;
+    for (int64_t r = lo[side] + threadIdx.x; r < hi[side]; r += 256) t += stat[r].logp;
     gain[side] = block_sum<4>(t, red) - (double)p.ref_logp[s];
     if (threadIdx.x == 0) p.rewards[s] = (float)(p.beta * gain[side]);
   }
+  const double m = p.beta * (gain[0] - gain[1]);
+  const double q = exp(-fabs(m));
+  // softplus(-m), softplus(m) and sigmoid(m) without overflow
   if (threadIdx.x == 0) {
-    const double m = p.beta * (gain[0] - gain[1]);
-    const double q = exp(-fabs(m)), l = log1p(q);
-    // softplus(-m) and softplus(m), and sigmoid(m), without overflow
-    const double up = fmax(-m, 0.0) + l, down = fmax(m, 0.0) + l;
-    const double sig = (m >= 0.0 ? 1.0 : q) / (1.0 + q);
-    coef[2 * i] = (1.0 - p.smoothing) * up + p.smoothing * down;
-    coef[2 * i + 1] = p.beta * (sig - (1.0 - p.smoothing)) / (double)p.pairs;
+    const double l = log1p(q);
+    losses[i] = (1.0 - p.smoothing) * (fmax(-m, 0.0) + l) + p.smoothing * (fmax(m, 0.0) + l);
+  }
+  const double sig = (m >= 0.0 ? 1.0 : q) / (1.0 + q);
+  const double chosen = p.beta * (sig - (1.0 - p.smoothing)) / (double)p.pairs;
+  for (int side = 0; side < 2; ++side) {
+    const double d = side ? -chosen : chosen;
+    for (int64_t r = lo[side] + threadIdx.x; r < hi[side]; r += 256) {
+      const int64_t target = index_at(a.targets, r);
+      if (target < 0 || target >= a.vocab) continue;
+      const RowStat st = stat[r];
+      grad[r] = RowGrad{st.max, (float)(-d / (double)st.total), (float)(-d * expm1(st.logp)), d != 0.0};
+    }
   }
 }
 
-// The mean loss (first workgroup) and every row's gradient coefficients.
-__global__ __launch_bounds__(256) void kl_pair_rows(LogitArgs a, PreferenceArgs p, const RowStat *stat,
-                                                    const double *coef, RowGrad *grad) {
+// The mean of the pairs' losses, by one workgroup of the gradient kernel.
+__device__ __forceinline__ void mean_loss(const double *losses, int64_t pairs, float *loss) {
   __shared__ double red[4];
-  if (blockIdx.x == 0) {
-    double t = 0.0;
-    for (int64_t i = threadIdx.x; i < p.pairs; i += 256) t += coef[2 * i];
-    t = block_sum<4>(t, red);
-    if (threadIdx.x == 0) p.loss[0] = (float)(t / (double)p.pairs);
-  }
-  const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (r >= a.rows) return;
-  // the last sequence that starts at or before the row
-  int64_t lo = 0, hi = 2 * p.pairs - 1;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi + 1) >> 1;
-    if (index_at(p.offsets, mid) <= r) lo = mid;
-    else hi = mid - 1;
-  }
-  int64_t s0, s1;
-  sequence(p.offsets, lo, a.rows, &s0, &s1);
-  const int64_t target = index_at(a.targets, r);
-  RowGrad g{0.f, 0.f, 0.f, 0};
-  if (r >= s0 && r < s1 && target >= 0 && target < a.vocab) {
-    const RowStat st = stat[r];
-    const double d = lo < p.pairs ? coef[2 * lo + 1] : -coef[2 * (lo - p.pairs) + 1];
-    g = RowGrad{st.max, (float)(-d / (double)st.total), (float)(-d * expm1(st.logp)), d != 0.0};
-  }
-  grad[r] = g;
+  double t = 0.0;
+  for (int64_t i = threadIdx.x; i < pairs; i += 256) t += losses[i];
+  t = block_sum<4>(t, red);
+  if (threadIdx.x == 0) *loss = (float)(t / (double)pairs);
 }
 
 // The gradient of the logits, element by element; a row without one gets
-// zeros and is not read.
+// zeros and is not read.  The rows are taken from the last to the first: the
+// last ones that the row sums read are still in the memory-side cache.
 template <bool BF16>
 __global__ __launch_bounds__(256) void kl_grad(LogitArgs a, const RowGrad *grad, void *dlogits, int64_t dld,
-                                               int pieces) {
+                                               int pieces, const double *losses, int64_t pairs, float *loss) {
   typedef Elem<BF16> E;
   typedef typename E::type T;
-  const int64_t r = blockIdx.x;
-  const int piece = blockIdx.y;
+  if (blockIdx.x == 0) mean_loss(losses, pairs, loss);
+  if (a.rows == 0) return;
+  const int64_t r = a.rows - 1 - blockIdx.x / pieces;
+  const int piece = blockIdx.x % pieces;
   const RowGrad g = grad[r];
   const int64_t target = index_at(a.targets, r);
   const T *x = static_cast<const T *>(a.logits) + r * a.ld;
   T *d = static_cast<T *>(dlogits) + r * dld;
-  const int64_t vecs = (a.vocab + E::N - 1) / E::N;
-  const int64_t v0 = vecs * piece / pieces, v1 = vecs * (piece + 1) / pieces;
-  for (int64_t i = v0 + threadIdx.x; i < v1; i += 256) {
-    const int64_t j = i * E::N;
-    if (j + E::N <= a.vocab) {
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (g.live) {
-        float v[E::N];
-        E::unpack(load16(x + j), v);
+  const Row<BF16> row(g.live ? x : d, a.vocab);
+  const int v0 = (int)((int64_t)row.vecs * piece / pieces), v1 = (int)((int64_t)row.vecs * (piece + 1) / pieces);
+  if (!g.live) {
+    for (int i = v0 + threadIdx.x; i < v1; i += 256) store16(d + row.col(i), make_uint4(0, 0, 0, 0));
+    if (piece == 0 && (int)threadIdx.x < row.singles()) d[row.single(threadIdx.x)] = T(0);
+    return;
+  }
+#pragma unroll 4
+  for (int i = v0 + threadIdx.x; i < v1; i += 256) {
+    float v[E::N];
+    E::unpack(load16(x + row.col(i)), v);
 #pragma unroll
-        for (int k = 0; k < E::N; ++k) v[k] = j + k == target ? g.dt : g.c * exp_shift(v[k], g.max);
-        w = E::pack(v);
-      }
-      store16(d + j, w);
-    } else {
-      for (int64_t k = j; k < a.vocab; ++k)
-        d[k] = !g.live ? T(0) : E::put(k == target ? g.dt : g.c * exp_shift(E::get(x[k]), g.max));
+    for (int k = 0; k < E::N; ++k) v[k] = g.c * exp_shift(v[k], g.max);
+    const int at = (int)target - (int)row.col(i);
+    if (at >= 0 && at < E::N) {
+#pragma unroll
+      for (int k = 0; k < E::N; ++k) v[k] = k == at ? g.dt : v[k];
     }
+    store16(d + row.col(i), E::pack(v));
+  }
+  if (piece == 0 && (int)threadIdx.x < row.singles()) {
+    const int j = row.single(threadIdx.x);
+    d[j] = E::put(j == target ? g.dt : g.c * exp_shift(E::get(x[j]), g.max));
   }
 }
 
@@ -270,20 +363,11 @@ __global__ __launch_bounds__(256) void kl_grad(LogitArgs a, const RowGrad *grad,
 
 namespace {
 
-hipError_t rows_launch(const LogitArgs &a, bool bf16, const float *weights, RowStat *stat, float *logp, float *lse,
+hipError_t rows_launch(const LogitArgs &a, bool bf16, RowStat *stat, RowGrad *grad, float *logp, float *lse,
                        hipStream_t s) {
   const dim3 g((unsigned)a.rows);
-  if (bf16) hipLaunchKernelGGL((kl_rows<true, 512>), g, dim3(512), 0, s, a, weights, stat, logp, lse);
-  else hipLaunchKernelGGL((kl_rows<false, 512>), g, dim3(512), 0, s, a, weights, stat, logp, lse);
-  return hipGetLastError();
-}
-
-hipError_t grad_launch(const LogitArgs &a, bool bf16, const RowGrad *grad, void *dlogits, int64_t dld,
-                       hipStream_t s) {
-  const int pieces = (int)std::max<int64_t>(1, std::min<int64_t>(a.vocab / 8192, 64));
-  const dim3 g((unsigned)a.rows, (unsigned)pieces);
-  if (bf16) hipLaunchKernelGGL(kl_grad<true>, g, dim3(256), 0, s, a, grad, dlogits, dld, pieces);
-  else hipLaunchKernelGGL(kl_grad<false>, g, dim3(256), 0, s, a, grad, dlogits, dld, pieces);
+  if (bf16) hipLaunchKernelGGL((kl_rows<true, 512>), g, dim3(512), 0, s, a, stat, grad, logp, lse);
+  else hipLaunchKernelGGL((kl_rows<false, 512>), g, dim3(512), 0, s, a, stat, grad, logp, lse);
   return hipGetLastError();
 }
 
@@ -298,32 +382,45 @@ hipError_t launch_token_logprob(const LogitArgs &a, bool bf16, float *logp, floa
 
 PolicyLayout policy_layout(int64_t rows) {
   PolicyLayout l{};
-  l.stat = 0;
-  l.grad = up256(sizeof(RowStat) * (size_t)rows);
-  l.total = l.grad + up256(sizeof(RowGrad) * (size_t)std::max<int64_t>(rows, 1));
+  l.terms = 0;
+  l.total = up256(4 * sizeof(double) * (size_t)std::max<int64_t>(rows, 1));
   return l;
 }
+
+namespace {
+
+template <bool BF16>
+void policy_launch(const LogitArgs &a, const PolicyArgs &p, void *dlogits, int64_t dld, double *terms, hipStream_t s) {
+  const dim3 g((unsigned)a.rows);
+  const int64_t vecs = a.vocab / Elem<BF16>::N;
+  // the smallest workgroup that holds the row: several rows on a CU at a time
+  if (vecs <= 256 * KEEP) hipLaunchKernelGGL((kl_policy<BF16, 256>), g, dim3(256), 0, s, a, p, dlogits, dld, terms);
+  else if (vecs <= 512 * KEEP) hipLaunchKernelGGL((kl_policy<BF16, 512>), g, dim3(512), 0, s, a, p, dlogits, dld, terms);
+  else hipLaunchKernelGGL((kl_policy<BF16, 1024>), g, dim3(1024), 0, s, a, p, dlogits, dld, terms);
+}
+
+}  // namespace
 
 hipError_t launch_policy(const LogitArgs &a, const PolicyArgs &p, bool bf16, void *dlogits, int64_t dld, char *ws,
                          hipStream_t s) {
   const PolicyLayout l = policy_layout(a.rows);
-  RowStat *stat = reinterpret_cast<RowStat *>(ws + l.stat);
-  RowGrad *grad = reinterpret_cast<RowGrad *>(ws + l.grad);
-  hipError_t e = hipSuccess;
-  if (a.rows > 0) e = rows_launch(a, bf16, p.weights, stat, nullptr, nullptr, s);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kl_policy, dim3(1), dim3(1024), 0, s, a, p, stat, grad);
-  e = hipGetLastError();
-  if (e != hipSuccess || a.rows == 0) return e;
-  return grad_launch(a, bf16, grad, dlogits, dld, s);
+  double *terms = reinterpret_cast<double *>(ws + l.terms);
+  if (a.rows > 0) {
+    if (bf16) policy_launch<true>(a, p, dlogits, dld, terms, s);
+    else policy_launch<false>(a, p, dlogits, dld, terms, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kl_policy_sum, dim3(1), dim3(1024), 0, s, terms, a.rows, p.stats);
+  return hipGetLastError();
 }
 
 PreferenceLayout preference_layout(int64_t rows, int64_t pairs) {
   PreferenceLayout l{};
   l.stat = 0;
   l.grad = up256(sizeof(RowStat) * (size_t)rows);
-  l.coef = l.grad + up256(sizeof(RowGrad) * (size_t)rows);
-  l.total = l.coef + up256(2 * sizeof(double) * (size_t)pairs);
+  l.losses = l.grad + up256(sizeof(RowGrad) * (size_t)rows);
+  l.total = l.losses + up256(sizeof(double) * (size_t)pairs);
   return l;
 }
 
@@ -332,16 +429,19 @@ hipError_t launch_preference(const LogitArgs &a, const PreferenceArgs &p, bool b
   const PreferenceLayout l = preference_layout(a.rows, p.pairs);
   RowStat *stat = reinterpret_cast<RowStat *>(ws + l.stat);
   RowGrad *grad = reinterpret_cast<RowGrad *>(ws + l.grad);
-  double *coef = reinterpret_cast<double *>(ws + l.coef);
+  double *losses = reinterpret_cast<double *>(ws + l.losses);
   hipError_t e = hipSuccess;
-  if (a.rows > 0) e = rows_launch(a, bf16, nullptr, stat, nullptr, nullptr, s);
+  if (a.rows > 0) e = rows_launch(a, bf16, stat, grad, nullptr, nullptr, s);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kl_pairs, dim3((unsigned)p.pairs), dim3(256), 0, s, a, p, stat, coef);
+  hipLaunchKernelGGL(kl_pairs, dim3((unsigned)p.pairs), dim3(256), 0, s, a, p, stat, grad, losses);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  const unsigned blocks = (unsigned)std::max<int64_t>(1, (a.rows + 255) / 256);
-  hipLaunchKernelGGL(kl_pair_rows, dim3(blocks), dim3(256), 0, s, a, p, stat, coef, grad);
-  if ((e = hipGetLastError()) != hipSuccess || a.rows == 0) return e;
-  return grad_launch(a, bf16, grad, dlogits, dld, s);
+  // pieces of a row: 8192 elements or more, and a grid that stays in range
+  int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(a.vocab / 8192, 64));
+  if (a.rows > 0) pieces = std::max<int64_t>(1, std::min(pieces, (((int64_t)1 << 31) - 1) / a.rows));
+  const dim3 g((unsigned)std::max<int64_t>(1, a.rows * pieces));
+  if (bf16) hipLaunchKernelGGL(kl_grad<true>, g, dim3(256), 0, s, a, grad, dlogits, dld, (int)pieces, losses, p.pairs, p.loss);
+  else hipLaunchKernelGGL(kl_grad<false>, g, dim3(256), 0, s, a, grad, dlogits, dld, (int)pieces, losses, p.pairs, p.loss);
+  return hipGetLastError();
 }
 
 }  // namespace muon

@@ -99,7 +99,8 @@ muon_status check_logits(const char *where, const muon_logits *x) {
   if (!known_dtype(x->dtype) || !known_index(x->target_type)) return fail(MUON_ERR_INVALID_ARG, where, "unknown dtype or target type");
   if (x->rows > 0 && (!x->logits || !x->targets)) return fail(MUON_ERR_INVALID_ARG, where, "NULL logits or targets");
   if (x->ld < x->vocab) return fail(MUON_ERR_INVALID_ARG, where, "ld is below the vocabulary");
-  if (x->rows >= kMax || x->vocab >= kMax || !fits(x->rows, x->ld)) return fail(MUON_ERR_UNSUPPORTED, where, "rows and vocab must be below 2^31");
+  if (x->rows >= kMax || x->vocab >= kMax / 4 || !fits(x->rows, x->ld))
+    return fail(MUON_ERR_UNSUPPORTED, where, "rows must be below 2^31 and vocab below 2^29");
   return MUON_OK;
 }
 

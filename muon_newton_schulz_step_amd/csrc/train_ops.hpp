@@ -116,14 +116,14 @@ struct PreferenceArgs {
 hipError_t launch_token_logprob(const LogitArgs &a, bool bf16, float *logp, float *lse, hipStream_t s);
 
 struct PolicyLayout {
-  size_t stat, grad, total;
+  size_t terms, total;
 };
 PolicyLayout policy_layout(int64_t rows);
 hipError_t launch_policy(const LogitArgs &a, const PolicyArgs &p, bool bf16, void *dlogits, int64_t dld, char *ws,
                          hipStream_t s);
 
 struct PreferenceLayout {
-  size_t stat, grad, coef, total;
+  size_t stat, grad, losses, total;
 };
 PreferenceLayout preference_layout(int64_t rows, int64_t pairs);
 hipError_t launch_preference(const LogitArgs &a, const PreferenceArgs &p, bool bf16, void *dlogits, int64_t dld,

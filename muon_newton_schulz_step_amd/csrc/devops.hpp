@@ -80,6 +80,13 @@ template <class T>
 __device__ __forceinline__ void store16(T *p, uint4 v) {
   __builtin_memcpy(p, &v, 16);
 }
+// A store that leaves the caches to what is read again.
+template <class T>
+__device__ __forceinline__ void stream16(T *p, uint4 v) {
+  typedef uint32_t words __attribute__((ext_vector_type(4), aligned(2)));
+  const words w = {v.x, v.y, v.z, v.w};
+  __builtin_nontemporal_store(w, reinterpret_cast<words *>(p));
+}
 
 __device__ __forceinline__ int64_t index_at(const IndexVec &v, int64_t i) {
   return v.is64 ? static_cast<const int64_t *>(v.p)[i] : (int64_t)static_cast<const int32_t *>(v.p)[i];
@@ -95,7 +102,7 @@ __device__ __forceinline__ float exp_shift(float x, float m) { return __builtin_
 // of rows' log-probabilities, so the constant's rest is added back.
 __device__ __forceinline__ float exp_term(float x, float m) {
   const float d = x - m;
-  return __builtin_amdgcn_exp2f(fmaf(d, kLog2eLow, d * kLog2e));
+  return __builtin_amdgcn_exp2f(fmaf(d, kLog2e, d * kLog2eLow));
 }
 
 __device__ __forceinline__ double shfl_f64(double v, int lane) {

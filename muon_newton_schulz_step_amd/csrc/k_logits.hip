@@ -120,9 +120,8 @@ __global__ __launch_bounds__(THREADS) void kl_rows(LogitArgs a, RowStat *stat, R
 
 namespace {
 
-// Vectors of a row that a thread keeps in registers (64 of the 128 it has
-// with a 1024-thread workgroup on a CU, or several smaller ones).
-constexpr int KEEP = 16;
+// Vectors of a row that a thread of the policy kernel keeps in registers.
+constexpr int KEEP = 4;
 
 }  // namespace
 
@@ -132,13 +131,18 @@ constexpr int KEEP = 16;
 // The derivative by logp is -a ratio while the unclipped branch is the
 // smaller, plus kl_coef (1 - exp(d)).
 //
-// HBM-bound, one read and one write of a row: the row stays in the
-// workgroup's registers between its sum and its gradient (a CU's registers
-// hold 256 KB of it; what a longer row has beyond KEEP vectors a thread is
-// read again).  The row's own arithmetic, in fp64, is two function calls deep
-// in one wave: lanes 0 to 2 share a call of expm1.
+// HBM-bound, one read and one write of a row.  The first KEEP vectors of each
+// thread stay in registers between the row's sum and its gradient; the rest
+// is read again, from the caches: two workgroups of 1024 threads on a CU have
+// at most 64 VGPRs a thread, and keep 512 rows of the chip (128 MB at 131072
+// bf16 columns) under way, which the memory-side cache holds, the more so as
+// the gradient is stored past it.  Whole rows in registers (16 vectors, half
+// the waves) hide less: 4.2 against 5.0 TB/s over 4577 x 131072 bf16, 4.2
+// against 5.4 over 50257 columns; nothing kept gives 4.5 and 4.7, ordinary
+// stores 10% less.  The row's own arithmetic, in fp64, is two function calls
+// deep in one wave: lanes 0 to 2 share a call of expm1.
 template <bool BF16, int THREADS>
-__global__ __launch_bounds__(THREADS, 4) void kl_policy(LogitArgs a, PolicyArgs p, void *dlogits, int64_t dld,
+__global__ __launch_bounds__(THREADS, 8) void kl_policy(LogitArgs a, PolicyArgs p, void *dlogits, int64_t dld,
                                                         double *terms) {
   typedef Elem<BF16> E;
   typedef typename E::type T;
@@ -151,7 +155,7 @@ __global__ __launch_bounds__(THREADS, 4) void kl_policy(LogitArgs a, PolicyArgs 
   T *d = static_cast<T *>(dlogits) + r * dld;
   if (target < 0 || target >= a.vocab || w == 0.f) {
     const Row<BF16> out(d, a.vocab);
-    for (int i = tid; i < out.vecs; i += THREADS) store16(d + out.col(i), make_uint4(0, 0, 0, 0));
+    for (int i = tid; i < out.vecs; i += THREADS) stream16(d + out.col(i), make_uint4(0, 0, 0, 0));
     if (tid < out.singles()) d[out.single(tid)] = T(0);
     if (tid < 4) terms[4 * r + tid] = 0.0;
     if (tid == 0) p.logp[r] = 0.f;
@@ -212,8 +216,8 @@ __global__ __launch_bounds__(THREADS, 4) void kl_policy(LogitArgs a, PolicyArgs 
     }
   }
   __syncthreads();
-  // the vectors are unpacked a second time: kept unpacked over the sum, a bf16
-  // row would take twice the registers
+  // the vectors are unpacked a second time: kept unpacked over the sum, bf16
+  // ones would take twice the registers
 #pragma unroll
   for (int k = 0; k < KEEP; ++k)
     asm volatile("" : "+v"(keep[k].x), "+v"(keep[k].y), "+v"(keep[k].z), "+v"(keep[k].w));
@@ -229,7 +233,7 @@ __global__ __launch_bounds__(THREADS, 4) void kl_policy(LogitArgs a, PolicyArgs 
 #pragma unroll
       for (int j = 0; j < E::N; ++j) v[j] = j == at ? dt : v[j];
     }
-    store16(d + row.col(i), E::pack(v));
+    stream16(d + row.col(i), E::pack(v));
   };
 #pragma unroll
   for (int k = 0; k < KEEP; ++k) {
@@ -393,9 +397,7 @@ template <bool BF16>
 void policy_launch(const LogitArgs &a, const PolicyArgs &p, void *dlogits, int64_t dld, double *terms, hipStream_t s) {
   const dim3 g((unsigned)a.rows);
   const int64_t vecs = a.vocab / Elem<BF16>::N;
-  // the smallest workgroup that holds the row: several rows on a CU at a time
   if (vecs <= 256 * KEEP) hipLaunchKernelGGL((kl_policy<BF16, 256>), g, dim3(256), 0, s, a, p, dlogits, dld, terms);
-  else if (vecs <= 512 * KEEP) hipLaunchKernelGGL((kl_policy<BF16, 512>), g, dim3(512), 0, s, a, p, dlogits, dld, terms);
   else hipLaunchKernelGGL((kl_policy<BF16, 1024>), g, dim3(1024), 0, s, a, p, dlogits, dld, terms);
 }
 

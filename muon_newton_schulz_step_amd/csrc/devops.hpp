@@ -127,22 +127,23 @@ __device__ __forceinline__ double shfl_xor_f64(double v, int m) {
   return u.d;
 }
 
-// A row of a matrix as the kernels walk it: 16-byte vectors at 4-byte
-// alignment, with what is left at either end (at most one bf16 element before
-// them, less than a vector after them) element by element.  Reads off 4 bytes
-// cost a quarter of the bandwidth (4.9 against 6.1 TB/s over 50257-column
-// bf16 rows); beyond 4 bytes alignment made no difference.
+// A row of a matrix as the kernels walk it: 16-byte vectors from its first
+// 128-byte line on, and what is left at either end (less than a line before
+// them, less than a vector after them) element by element.  Over 50257-column
+// bf16 rows, reads off 4 bytes cost a quarter of the bandwidth (4.9 against
+// 6.1 TB/s), and streamed stores off their line write it in two parts: the
+// policy loss took 541 us on odd rows, 466 on rows at 4 bytes, 446 at 8.
 template <bool BF16>
 struct Row {
   int head, vecs, n;
   __device__ __forceinline__ Row(const void *p, int64_t cols) {
-    head = BF16 && ((uintptr_t)p & 2) ? 1 : 0;
     n = (int)cols;
+    head = min((int)((0u - (uint32_t)(uintptr_t)p) & 127u) / (int)sizeof(typename Elem<BF16>::type), n);
     vecs = (n - head) / Elem<BF16>::N;
   }
   // column of a vector's first element
   __device__ __forceinline__ uint32_t col(int vec) const { return (uint32_t)(head + vec * Elem<BF16>::N); }
-  // single elements, and the column of the i-th
+  // single elements (fewer than 80), and the column of the i-th
   __device__ __forceinline__ int singles() const { return n - vecs * Elem<BF16>::N; }
   __device__ __forceinline__ uint32_t single(int i) const {
     return (uint32_t)(i < head ? i : vecs * Elem<BF16>::N + i);

@@ -77,11 +77,11 @@ hipError_t launch_embed_backward(const EmbedBwdArgs &a, bool bf16, hipStream_t s
 
 // --------------------------------------------------- losses over logits
 
-// A row's softmax statistics: its maximum, the sum of exp(x - max), and the
-// target's log-probability.
+// A row's softmax statistics: its maximum, the sum of exp(x - max), the
+// target's log-probability and expm1 of that.
 struct RowStat {
   float max, total;
-  double logp;
+  double logp, share;
 };
 
 // What the gradient pass needs of a row: d x_j = c exp(x_j - max) away from

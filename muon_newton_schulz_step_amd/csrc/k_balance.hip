@@ -23,115 +23,196 @@ using namespace dev;
 
 namespace {
 
-constexpr int BH_GROUPS = 64;      // workgroups that count choices
-constexpr int BM_GROUPS = 1024;    // workgroups of the main pass, at most
+constexpr int BH_GROUPS = 64;   // workgroups that count choices, at most
+constexpr int BM_GROUPS = 512;  // workgroups of the main pass, at most: two on a CU
+constexpr int BM_THREADS = 1024;
+// Up to this many logits (and choices) one workgroup does the whole call.
+constexpr int64_t BALANCE_SOLO = 16384;
+
+// Adds the choices of tokens [t0, t1) to h; returns this thread's counted tokens.
+__device__ __forceinline__ int count_choices(const BalanceArgs &a, int64_t t0, int64_t t1, int *h) {
+  int live = 0;
+  if (a.valid) {
+    for (int64_t t = t0 + threadIdx.x; t < t1; t += 1024) live += a.valid[t] != 0;
+  } else if (threadIdx.x == 0) {
+    live = (int)(t1 - t0);
+  }
+  const uint32_t k = (uint32_t)a.k, end = (uint32_t)t1 * k;  // tokens * k stays below 2^31
+#pragma unroll 8
+  for (uint32_t i = (uint32_t)t0 * k + threadIdx.x; i < end; i += 1024) {
+    const int64_t e = index_at(a.experts, i);
+    if (e >= 0 && e < a.n_experts && (!a.valid || a.valid[i / k])) atomicAdd(&h[e], 1);
+  }
+  return live;
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  const int x = __float_as_int(v);
+  return __int_as_float(__builtin_amdgcn_update_dpp(x, x, CTRL, 0xf, 0xf, false));
+}
+
+// Reductions over LANES consecutive lanes (4, 16 or 64); every lane gets the
+// same bits, since each step joins two lanes that hold the same two halves.
+constexpr int QUAD_XOR1 = 0xb1, QUAD_XOR2 = 0x4e, ROW_ROR8 = 0x128, ROW_ROR4 = 0x124;
+template <int LANES, class F>
+__device__ __forceinline__ float group_reduce(float v, F f) {
+  v = f(v, dpp<QUAD_XOR1>(v));
+  v = f(v, dpp<QUAD_XOR2>(v));
+  if constexpr (LANES >= 16) {
+    v = f(v, dpp<ROW_ROR8>(v));
+    v = f(v, dpp<ROW_ROR4>(v));
+  }
+  if constexpr (LANES == 64) {
+    v = f(v, __shfl_xor(v, 16));
+    v = f(v, __shfl_xor(v, 32));
+  }
+  return v;
+}
 
 }  // namespace
 
 // Choices per expert of one part of the tokens: hist[part][e], and the part's
-// counted tokens at hist[part][E].
-__global__ __launch_bounds__(1024) void kb_count(BalanceArgs a, int32_t *hist) {
+// counted tokens at hist[part][E].  Clears the main pass's arrival count.
+__global__ __launch_bounds__(1024) void kb_count(BalanceArgs a, int32_t *hist, int32_t *arrive) {
   __shared__ int h[BAL_MAX_EXPERTS + 1];
   const int parts = gridDim.x;
   for (int e = threadIdx.x; e <= a.n_experts; e += 1024) h[e] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *arrive = 0;
   __syncthreads();
-  const int64_t t0 = a.tokens * blockIdx.x / parts, t1 = a.tokens * (blockIdx.x + 1) / parts;
-  int live = 0;
-  for (int64_t t = t0 + threadIdx.x; t < t1; t += 1024) live += !a.valid || a.valid[t];
+  const int live = count_choices(a, a.tokens * blockIdx.x / parts, a.tokens * (blockIdx.x + 1) / parts, h);
   if (live) atomicAdd(&h[a.n_experts], live);
-  for (int64_t i = t0 * a.k + threadIdx.x; i < t1 * a.k; i += 1024) {
-    const int64_t e = index_at(a.experts, i);
-    if (e >= 0 && e < a.n_experts && (!a.valid || a.valid[i / a.k])) atomicAdd(&h[e], 1);
-  }
   __syncthreads();
   for (int e = threadIdx.x; e <= a.n_experts; e += 1024) hist[(int64_t)blockIdx.x * (a.n_experts + 1) + e] = h[e];
 }
 
-// One wave a token, ITEMS logits a lane (lane, lane + 64, ...).
-template <bool BF16, int ITEMS>
-__global__ __launch_bounds__(256) void kb_main(BalanceArgs a, const int32_t *hist, int parts, double *sums) {
+// A group of LANES lanes takes a token, VECS 16-byte vectors a lane, so that
+// a wave reduces 64 / LANES tokens at a time and most steps stay inside a row
+// of 16 lanes.  HBM-bound: one read and one write of the logits.  The last
+// workgroup to finish adds up the workgroups' sums, in their order.  With
+// parts = 0 the only workgroup counts the choices itself.
+template <bool BF16, int LANES, int VECS>
+__global__ __launch_bounds__(BM_THREADS, 8) void kb_main(BalanceArgs a, const int32_t *hist, int parts, double *sums,
+                                                         int32_t *arrive) {
   typedef Elem<BF16> E;
   typedef typename E::type T;
-  __shared__ float f_of[BAL_MAX_EXPERTS];
-  __shared__ int total;
-  __shared__ double red[4];
-  const int n = a.n_experts, lane = threadIdx.x & 63;
-  for (int e = threadIdx.x; e <= n; e += 256) {
-    int c = 0;
-    for (int i = 0; i < parts; ++i) c += hist[(int64_t)i * (n + 1) + e];
-    if (e == n) total = c;
-    else {
-      f_of[e] = (float)c;
-      if (blockIdx.x == 0) a.counts[e] = c;
-    }
+  constexpr int N = E::N, PER = BM_THREADS / LANES;
+  __shared__ int count[BAL_MAX_EXPERTS + 1];
+  __shared__ __attribute__((aligned(16))) float f_of[LANES * VECS * N];
+  __shared__ double red[BM_THREADS / 64];
+  __shared__ int last;
+  const int n = a.n_experts, tid = threadIdx.x;
+  for (int e = tid; e <= n; e += BM_THREADS) count[e] = 0;
+  __syncthreads();
+  if (parts == 0) {
+    const int live = count_choices(a, 0, a.tokens, count);
+    if (live) atomicAdd(&count[n], live);
+  } else {
+    for (int i = tid; i < parts * (n + 1); i += BM_THREADS) atomicAdd(&count[i % (n + 1)], hist[i]);
   }
   __syncthreads();
+  const int total = count[n];
   const float tokens = (float)max(total, 1);
-  float f[ITEMS];
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) f[i] = lane + 64 * i < n ? f_of[lane + 64 * i] / (tokens * (float)a.k) : 0.f;
+  for (int e = tid; e < LANES * VECS * N; e += BM_THREADS) {
+    f_of[e] = e < n ? (float)count[e] / (tokens * (float)a.k) : 0.f;
+    if (blockIdx.x == 0 && e < n) a.counts[e] = count[e];
+  }
+  __syncthreads();
   const float cb = (float)(a.coef * (double)n / (double)tokens), cz = (float)(2.0 * a.z_coef / (double)tokens);
+  const int l = tid & (LANES - 1);
   double bal = 0.0, zz = 0.0;
-  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.tokens; t += (int64_t)gridDim.x * 4) {
+  const int64_t step = (int64_t)gridDim.x * PER;
+  int64_t t = (int64_t)blockIdx.x * PER + tid / LANES;
+  bool ok = t < a.tokens && (!a.valid || a.valid[t]);
+  for (; t < a.tokens; t += step) {
+    const bool now = ok;
+    ok = t + step < a.tokens && (!a.valid || a.valid[t + step]);
     T *d = static_cast<T *>(a.dlogits) + t * a.dld;
-    if (a.valid && !a.valid[t]) {
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i)
-        if (lane + 64 * i < n) d[lane + 64 * i] = T(0);
-      continue;
-    }
     const T *x = static_cast<const T *>(a.logits) + t * a.ld;
-    float v[ITEMS], m = kLowest, s = 0.f, pf = 0.f;
+    float v[VECS][N];
+    if (now) {
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      v[i] = lane + 64 * i < n ? E::get(x[lane + 64 * i]) : -INFINITY;
-      m = fmaxf(m, v[i]);
+      for (int i = 0; i < VECS; ++i) {
+        const int c = (l + LANES * i) * N;
+        if (c + N <= n) {
+          E::unpack(load16(x + c), v[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < N; ++j) v[i][j] = c + j < n ? E::get(x[c + j]) : -INFINITY;
+        }
+      }
+      float m = kLowest;
+#pragma unroll
+      for (int i = 0; i < VECS; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) m = fmaxf(m, v[i][j]);
+      m = group_reduce<LANES>(m, [](float p, float q) { return fmaxf(p, q); });
+      float s = 0.f, pf = 0.f;
+#pragma unroll
+      for (int i = 0; i < VECS; ++i) {
+        const float *f = f_of + (l + LANES * i) * N;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          v[i][j] = exp_shift(v[i][j], m);
+          s += v[i][j];
+          pf += v[i][j] * f[j];
+        }
+      }
+      s = group_reduce<LANES>(s, [](float p, float q) { return p + q; });
+      pf = group_reduce<LANES>(pf, [](float p, float q) { return p + q; });
+      const float inv = 1.f / s, mean_f = pf * inv, lse = m + logf(s);
+      if (l == 0) {
+        bal += (double)mean_f;
+        zz += (double)lse * (double)lse;
+      }
+      const float base = cz * lse;
+#pragma unroll
+      for (int i = 0; i < VECS; ++i) {
+        const float *f = f_of + (l + LANES * i) * N;
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[i][j] = v[i][j] * inv * (cb * (f[j] - mean_f) + base);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VECS; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[i][j] = 0.f;
     }
 #pragma unroll
-    for (int k = 32; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor(m, k));
+    for (int i = 0; i < VECS; ++i) {
+      const int c = (l + LANES * i) * N;
+      if (c + N <= n) {
+        store16(d + c, E::pack(v[i]));
+      } else {
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      v[i] = exp_shift(v[i], m);
-      s += v[i];
-      pf += v[i] * f[i];
+        for (int j = 0; j < N; ++j)
+          if (c + j < n) d[c + j] = E::put(v[i][j]);
+      }
     }
-#pragma unroll
-    for (int k = 32; k > 0; k >>= 1) {
-      s += __shfl_xor(s, k);
-      pf += __shfl_xor(pf, k);
+  }
+  double tb = block_sum<BM_THREADS / 64>(bal, red), tz = block_sum<BM_THREADS / 64>(zz, red);
+  if (parts != 0) {
+    const int groups = gridDim.x;
+    if (tid == 0) {
+      sums[2 * blockIdx.x] = tb;
+      sums[2 * blockIdx.x + 1] = tz;
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+      last = __hip_atomic_fetch_add(arrive, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == groups - 1;
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
     }
-    const float inv = 1.f / s, mean_f = pf * inv, lse = m + logf(s);
-    bal += (double)mean_f;
-    zz += (double)lse * (double)lse;
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i)
-      if (lane + 64 * i < n) d[lane + 64 * i] = E::put(v[i] * inv * (cb * (f[i] - mean_f) + cz * lse));
+    __syncthreads();
+    if (!last) return;
+    const bool in = tid < groups;
+    tb = block_sum<BM_THREADS / 64>(in ? sums[2 * tid] : 0.0, red);
+    tz = block_sum<BM_THREADS / 64>(in ? sums[2 * tid + 1] : 0.0, red);
   }
-  // every lane of a wave holds the wave's sums
-  const double tb = block_sum<4>(lane == 0 ? bal : 0.0, red), tz = block_sum<4>(lane == 0 ? zz : 0.0, red);
-  if (threadIdx.x == 0) {
-    sums[3 * blockIdx.x] = tb;
-    sums[3 * blockIdx.x + 1] = tz;
-    sums[3 * blockIdx.x + 2] = (double)total;
-  }
-}
-
-__global__ __launch_bounds__(256) void kb_final(BalanceArgs a, const double *sums, int groups) {
-  __shared__ double red[4];
-  double b = 0.0, z = 0.0;
-  for (int i = threadIdx.x; i < groups; i += 256) {
-    b += sums[3 * i];
-    z += sums[3 * i + 1];
-  }
-  b = block_sum<4>(b, red);
-  z = block_sum<4>(z, red);
-  if (threadIdx.x == 0) {
-    const double t = fmax(sums[2], 1.0);
-    b *= (double)a.n_experts / t;
-    z /= t;
-    a.stats[0] = (float)(a.coef * b + a.z_coef * z);
-    a.stats[1] = (float)b;
-    a.stats[2] = (float)z;
+  if (tid == 0) {
+    const double den = (double)max(total, 1);
+    tb *= (double)n / den;
+    tz /= den;
+    a.stats[0] = (float)(a.coef * tb + a.z_coef * tz);
+    a.stats[1] = (float)tb;
+    a.stats[2] = (float)tz;
   }
 }
 
@@ -140,35 +221,56 @@ BalanceLayout balance_layout(int64_t tokens, int32_t n_experts) {
   BalanceLayout l{};
   l.hist = 0;
   l.sums = ((size_t)BH_GROUPS * ((size_t)n_experts + 1) * 4 + 255) / 256 * 256;
-  l.total = l.sums + 3 * sizeof(double) * BM_GROUPS;
+  l.arrive = l.sums + 2 * sizeof(double) * BM_GROUPS;
+  l.total = l.arrive + 256;
   return l;
 }
 
 namespace {
 
-template <bool BF16>
-void main_launch(const BalanceArgs &a, const int32_t *hist, int parts, double *sums, int groups, hipStream_t s) {
-  const dim3 g(groups), b(256);
-  if (a.n_experts <= 64) hipLaunchKernelGGL((kb_main<BF16, 1>), g, b, 0, s, a, hist, parts, sums);
-  else if (a.n_experts <= 256) hipLaunchKernelGGL((kb_main<BF16, 4>), g, b, 0, s, a, hist, parts, sums);
-  else hipLaunchKernelGGL((kb_main<BF16, BAL_MAX_EXPERTS / 64>), g, b, 0, s, a, hist, parts, sums);
-}
+struct MainLaunch {
+  const BalanceArgs &a;
+  const int32_t *hist;
+  int parts;
+  double *sums;
+  int32_t *arrive;
+  hipStream_t s;
+  template <bool BF16, int LANES, int VECS>
+  void go() const {
+    static_assert(BM_GROUPS <= BM_THREADS, "a thread a workgroup in the last sums");
+    const int64_t per = BM_THREADS / LANES;
+    const int64_t g = parts ? std::max<int64_t>(1, std::min<int64_t>(BM_GROUPS, (a.tokens + per - 1) / per)) : 1;
+    hipLaunchKernelGGL((kb_main<BF16, LANES, VECS>), dim3((unsigned)g), dim3(BM_THREADS), 0, s, a, hist, parts, sums, arrive);
+  }
+  // the fewest lanes and vectors that hold a token (four bf16 vectors a lane
+  // would not fit the 64 registers of a full CU)
+  template <bool BF16>
+  void choose() const {
+    constexpr int N = Elem<BF16>::N;
+    const int n = a.n_experts;
+    if (n <= 4 * N) go<BF16, 4, 1>();
+    else if (n <= 16 * N) go<BF16, 16, 1>();
+    else if (n <= 32 * N) go<BF16, 16, 2>();
+    else if (n <= 64 * N) go<BF16, BF16 ? 64 : 16, BF16 ? 1 : 4>();
+    else go<BF16, 64, BAL_MAX_EXPERTS / (64 * N)>();
+  }
+};
 
 }  // namespace
 
 hipError_t launch_balance(const BalanceArgs &a, bool bf16, char *ws, hipStream_t s) {
   const BalanceLayout l = balance_layout(a.tokens, a.n_experts);
-  int32_t *hist = reinterpret_cast<int32_t *>(ws + l.hist);
-  double *sums = reinterpret_cast<double *>(ws + l.sums);
-  const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(BH_GROUPS, a.tokens / 512));
-  hipLaunchKernelGGL(kb_count, dim3(parts), dim3(1024), 0, s, a, hist);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int groups = (int)std::max<int64_t>(1, std::min<int64_t>(BM_GROUPS, (a.tokens + 3) / 4));
-  if (bf16) main_launch<true>(a, hist, parts, sums, groups, s);
-  else main_launch<false>(a, hist, parts, sums, groups, s);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL(kb_final, dim3(1), dim3(256), 0, s, a, sums, groups);
+  int32_t *hist = reinterpret_cast<int32_t *>(ws + l.hist), *arrive = reinterpret_cast<int32_t *>(ws + l.arrive);
+  int parts = 0;
+  if (a.tokens * std::max(a.n_experts, a.k) > BALANCE_SOLO) {
+    parts = (int)std::max<int64_t>(1, std::min<int64_t>(BH_GROUPS, a.tokens * a.k / 2048));
+    hipLaunchKernelGGL(kb_count, dim3(parts), dim3(1024), 0, s, a, hist, arrive);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const MainLaunch m{a, hist, parts, reinterpret_cast<double *>(ws + l.sums), arrive, s};
+  if (bf16) m.choose<true>();
+  else m.choose<false>();
   return hipGetLastError();
 }
 

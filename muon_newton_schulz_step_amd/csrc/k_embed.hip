@@ -11,6 +11,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "devops.hpp"
 #include "train_ops.hpp"
@@ -72,18 +73,34 @@ hipError_t launch_embed_forward(const EmbedFwdArgs &a, bool bf16, hipStream_t s)
 // frequent low ids spread over the buckets).  Every workgroup reads all ids:
 // while it collects its own tokens it counts those of the lower buckets, and
 // so knows where its part of the sorted order starts without a pass between
-// the workgroups.  Inside the bucket the tokens go through a stable
-// least-digit-first radix sort; a digit of 10 bits covers a table of 2^18
+// the workgroups.  A bucket of at most ES_SMALL tokens is sorted by counting,
+// for each token, the smaller keys in LDS; a larger one by a stable
+// least-digit-first radix sort whose digit of 10 bits covers a table of 2^18
 // rows in one pass.
+//
+// At the first call of a step, as many workgroups more write the zeros of the
+// rows without a token, one bucket's each: the sort waits for memory and the
+// zeros for bandwidth, so they fit beside each other on a CU.
 namespace {
 
 constexpr int ES_WAVES = 16, ES_THREADS = 64 * ES_WAVES;
 constexpr int ES_BITS = 10, ES_DIGITS = 1 << ES_BITS;
 constexpr int ES_MAP_BITS = 1 << 17;  // local rows that one presence map covers
+constexpr int ES_HELD = 16;           // ids that a thread reads at a time
+constexpr int ES_SMALL = 512;
 static_assert(ES_DIGITS == ES_THREADS, "one thread a digit in the scan");
 static_assert(ES_MAP_BITS / 32 <= ES_WAVES * ES_DIGITS, "the map shares the counts' memory");
+static_assert((EB_BUCKETS & (EB_BUCKETS - 1)) == 0, "bucket and key are bits of the row");
+constexpr int EB_SHIFT = 8;
+static_assert(EB_BUCKETS == 1 << EB_SHIFT, "");
 
 __device__ __forceinline__ uint64_t lanes_below() { return (1ull << (threadIdx.x & 63)) - 1; }
+
+// A token's table row, -1 if it has none.
+__device__ __forceinline__ int row_of(const EmbedBwdArgs &a, int64_t t) {
+  const int64_t id = index_at(a.ids, t);
+  return id >= 0 && id < a.vocab ? (int)id : -1;
+}
 
 // Exclusive sum over the workgroup; *total gets the sum.
 __device__ __forceinline__ int scan_exclusive(int v, int *wsum, int *total) {
@@ -106,32 +123,73 @@ __device__ __forceinline__ int scan_exclusive(int v, int *wsum, int *total) {
   return base + x - v;
 }
 
+// Zeros into the rows of bucket b that no token meets; map: ES_MAP_BITS bits.
+__device__ void zero_rows(const EmbedBwdArgs &a, int b, uint32_t *map) {
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int rows = (int)((a.vocab - b + EB_BUCKETS - 1) >> EB_SHIFT);
+  for (int r0 = 0; r0 < rows; r0 += ES_MAP_BITS) {
+    const int m = min(rows - r0, ES_MAP_BITS);
+    for (int i = threadIdx.x; i < (m + 31) / 32; i += ES_THREADS) map[i] = 0;
+    __syncthreads();
+#pragma unroll 8
+    for (int64_t t = threadIdx.x; t < a.tokens; t += ES_THREADS) {
+      const int id = row_of(a, t), r = (id >> EB_SHIFT) - r0;
+      if (id >= 0 && (id & (EB_BUCKETS - 1)) == b && r >= 0 && r < m) atomicOr(&map[r >> 5], 1u << (r & 31));
+    }
+    __syncthreads();
+    for (int r = w; r < m; r += ES_WAVES) {
+      if ((map[r >> 5] >> (r & 31)) & 1) continue;
+      float *dst = a.acc + (int64_t)((r0 + r) * EB_BUCKETS + b) * a.acc_ld;
+      const Row<false> row(dst, a.dim);
+#pragma unroll 4
+      for (int i = lane; i < row.vecs; i += 64) stream16(dst + row.col(i), make_uint4(0, 0, 0, 0));
+      if (lane < row.singles()) dst[row.single(lane)] = 0.f;
+    }
+    __syncthreads();
+  }
+}
+
 }  // namespace
 
-__global__ __launch_bounds__(ES_THREADS) void ke_sort(EmbedBwdArgs a, int passes, int col_blocks) {
-  __shared__ int count[ES_WAVES][ES_DIGITS];
+__global__ __launch_bounds__(ES_THREADS, 8) void ke_sort(EmbedBwdArgs a, int passes, int col_blocks) {
+  __shared__ __attribute__((aligned(16))) int count[ES_WAVES][ES_DIGITS];
   __shared__ int base[ES_DIGITS];
   __shared__ int wsum[ES_WAVES], wsum2[ES_WAVES];
-  __shared__ int n_chunks, n_empty;
-  const int b = blockIdx.x, w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t span = (a.tokens + ES_THREADS - 1) / ES_THREADS * 64;
+  __shared__ int n_chunks;
+  const int b = blockIdx.x, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (b >= EB_BUCKETS) {
+    zero_rows(a, b - EB_BUCKETS, reinterpret_cast<uint32_t *>(&count[0][0]));
+    return;
+  }
+  // a wave takes a contiguous span of the tokens, so wave order is token
+  // order; up to 16384 tokens its part of the ids is read once
+  const int span = (int)((a.tokens + ES_THREADS - 1) / ES_THREADS) * 64;
   const int64_t t0 = min((int64_t)w * span, a.tokens), t1 = min(t0 + span, a.tokens);
-
-  // a wave takes a contiguous span of the tokens, so wave order is token order
+  int held[ES_HELD];
+  auto read_ids = [&](int64_t t) {
+#pragma unroll
+    for (int k = 0; k < ES_HELD; ++k) {
+      held[k] = -1;
+      if (t + 64 * k < t1 && t + 64 * k + lane < t1) held[k] = row_of(a, t + 64 * k + lane);
+    }
+  };
   int mine = 0, lower = 0;
-#pragma unroll 4
-  for (int64_t t = t0; t < t1; t += 64) {
-    const int64_t id = t + lane < t1 ? index_at(a.ids, t + lane) : -1;
-    const bool ok = id >= 0 && id < a.vocab;
-    const int bk = (int)(id & (EB_BUCKETS - 1));
-    mine += __popcll(__ballot(ok && bk == b));
-    lower += __popcll(__ballot(ok && bk < b));
+  for (int64_t t = t0; t < t1; t += 64 * ES_HELD) {
+    read_ids(t);
+#pragma unroll
+    for (int k = 0; k < ES_HELD; ++k) {
+      if (t + 64 * k < t1) {
+        const int bk = held[k] & (EB_BUCKETS - 1);
+        mine += __popcll(__ballot(held[k] >= 0 && bk == b));
+        lower += __popcll(__ballot(held[k] >= 0 && bk < b));
+      }
+    }
   }
   if (lane == 0) {
     wsum[w] = mine;
     wsum2[w] = lower;
   }
-  if (threadIdx.x == 0) n_chunks = n_empty = 0;
+  if (threadIdx.x == 0) n_chunks = 0;
   __syncthreads();
   int first = 0, n = 0, at = 0;
   for (int i = 0; i < ES_WAVES; ++i) {
@@ -139,6 +197,8 @@ __global__ __launch_bounds__(ES_THREADS) void ke_sort(EmbedBwdArgs a, int passes
     if (i == w) at = n;
     n += wsum[i];
   }
+  const bool small = n <= ES_SMALL;
+  int *const lkey = &count[0][0], *const ltok = &count[ES_WAVES / 2][0];
   int32_t *key = passes & 1 ? a.key_b : a.key_a, *tok = passes & 1 ? a.tok_b : a.perm;
   int32_t *key2 = passes & 1 ? a.key_a : a.key_b, *tok2 = passes & 1 ? a.perm : a.tok_b;
   key += first;
@@ -146,20 +206,60 @@ __global__ __launch_bounds__(ES_THREADS) void ke_sort(EmbedBwdArgs a, int passes
   key2 += first;
   tok2 += first;
   if (mine) {
-#pragma unroll 4
-    for (int64_t t = t0; t < t1; t += 64) {
-      const int64_t id = t + lane < t1 ? index_at(a.ids, t + lane) : -1;
-      const bool in = id >= 0 && id < a.vocab && (int)(id & (EB_BUCKETS - 1)) == b;
-      const uint64_t m = __ballot(in);
-      if (in) {
-        const int p = at + __popcll(m & lanes_below());
-        key[p] = (int32_t)(id / EB_BUCKETS);
-        tok[p] = (int32_t)(t + lane);
+    for (int64_t t = t0; t < t1; t += 64 * ES_HELD) {
+      if (span > 64 * ES_HELD) read_ids(t);
+#pragma unroll
+      for (int k = 0; k < ES_HELD; ++k) {
+        if (t + 64 * k < t1) {
+          const bool in = held[k] >= 0 && (held[k] & (EB_BUCKETS - 1)) == b;
+          const uint64_t m = __ballot(in);
+          if (in) {
+            const int p = at + __popcll(m & lanes_below());
+            (small ? lkey : key)[p] = held[k] >> EB_SHIFT;
+            (small ? ltok : tok)[p] = (int32_t)(t + 64 * k + lane);
+          }
+          at += __popcll(m);
+        }
       }
-      at += __popcll(m);
     }
   }
+  if (small && threadIdx.x < 4) lkey[n + threadIdx.x] = INT32_MAX;  // no row's key
   __syncthreads();
+
+  // a row's tokens in nearly equal chunks of at most EB_CHUNK (their order in
+  // the list does not touch the results)
+  auto emit = [&](int k, int s, int len, int tok0) {
+    const int parts = (len + EB_CHUNK - 1) / EB_CHUNK;
+    const int slot = atomicAdd(&n_chunks, parts);
+    const int row = k * EB_BUCKETS + b;
+    for (int i = 0; i < parts; ++i) {
+      const int lo = (int)((int64_t)len * i / parts), hi = (int)((int64_t)len * (i + 1) / parts);
+      a.chunks[first + slot + i] = EbChunk{row, first + s + lo, hi - lo, parts, first + s, len, tok0, 0};
+    }
+    if (parts > 1) {
+      for (int j = 0; j < col_blocks; ++j) a.arrive[(int64_t)((first + s) / (EB_CHUNK / 2)) * col_blocks + j] = 0;
+    }
+  };
+
+  if (small) {
+    const int p = threadIdx.x;
+    if (p < n) {
+      const int k = lkey[p];
+      int less = 0, same = 0, before = 0;
+#pragma unroll 4
+      for (int q = 0; q < n; q += 4) {
+        const int4 o = *reinterpret_cast<const int4 *>(lkey + q);
+        less += (o.x < k) + (o.y < k) + (o.z < k) + (o.w < k);
+        same += (o.x == k) + (o.y == k) + (o.z == k) + (o.w == k);
+        before += (o.x == k && q < p) + (o.y == k && q + 1 < p) + (o.z == k && q + 2 < p) + (o.w == k && q + 3 < p);
+      }
+      a.perm[first + less + before] = ltok[p];
+      if (before == 0) emit(k, less, same, ltok[p]);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) a.buckets[b] = EbBucket{first, n_chunks};
+    return;
+  }
 
   const int span2 = (n + ES_THREADS - 1) / ES_THREADS * 64;
   const int p0 = min(w * span2, n), p1 = min(p0 + span2, n);
@@ -229,189 +329,164 @@ __global__ __launch_bounds__(ES_THREADS) void ke_sort(EmbedBwdArgs a, int passes
     hat += __popcll(m);
   }
   __syncthreads();
-
-  // work chunks: a row's tokens in nearly equal parts of at most EB_CHUNK
-  // (their order in the list does not touch the results)
   for (int h = threadIdx.x; h < n_heads; h += ES_THREADS) {
-    const int s = head[h], len = (h + 1 < n_heads ? head[h + 1] : n) - s;
-    const int parts = (len + EB_CHUNK - 1) / EB_CHUNK;
-    const int slot = atomicAdd(&n_chunks, parts);
-    const int row = key[s] * EB_BUCKETS + b;
-    for (int i = 0; i < parts; ++i) {
-      const int lo = (int)((int64_t)len * i / parts), hi = (int)((int64_t)len * (i + 1) / parts);
-      a.chunks[first + slot + i] = EbChunk{row, first + s + lo, hi - lo, parts, first + s, len};
-    }
-    if (parts > 1) {
-      for (int j = 0; j < col_blocks; ++j) a.arrive[(int64_t)((first + s) / (EB_CHUNK / 2)) * col_blocks + j] = 0;
-    }
-  }
-
-  // the bucket's rows without a token
-  if (a.first) {
-    const int per = (int)((a.vocab + EB_BUCKETS - 1) / EB_BUCKETS);
-    const int rows = (int)((a.vocab - b + EB_BUCKETS - 1) / EB_BUCKETS);
-    uint32_t *map = reinterpret_cast<uint32_t *>(&count[0][0]);
-    for (int r0 = 0; r0 < rows; r0 += ES_MAP_BITS) {
-      const int m = min(rows - r0, ES_MAP_BITS);
-      for (int i = threadIdx.x; i < (m + 31) / 32; i += ES_THREADS) map[i] = 0;
-      __syncthreads();
-      for (int h = threadIdx.x; h < n_heads; h += ES_THREADS) {
-        const int r = key[head[h]] - r0;
-        if (r >= 0 && r < m) atomicOr(&map[r >> 5], 1u << (r & 31));
-      }
-      __syncthreads();
-      for (int r = threadIdx.x; r < m; r += ES_THREADS) {
-        if (!((map[r >> 5] >> (r & 31)) & 1)) {
-          a.empty[(int64_t)b * per + atomicAdd(&n_empty, 1)] = (r0 + r) * EB_BUCKETS + b;
-        }
-      }
-      __syncthreads();
-    }
+    const int s = head[h];
+    emit(key[s], s, (h + 1 < n_heads ? head[h + 1] : n) - s, tok[s]);
   }
   __syncthreads();
-  if (threadIdx.x == 0) a.buckets[b] = EbBucket{first, n, n_chunks, n_empty};
+  if (threadIdx.x == 0) a.buckets[b] = EbBucket{first, n_chunks};
 }
 
 // ------------------------------------------------------- adding them up
 
 // Units of work, a wave each: (chunk, column block) adds up to EB_CHUNK rows
-// of dout, (empty row, column block) writes zeros.  HBM-bound: each live
-// dout row is read once, each gradient row written once.
-template <bool BF16>
+// of dout, VECS 16-byte vectors a lane.  HBM-bound: each live dout row is
+// read once, each gradient row with a token written once.
+template <bool BF16, int VECS>
 __global__ __launch_bounds__(256) void ke_add(EmbedBwdArgs a, int col_blocks) {
   typedef Elem<BF16> E;
   typedef typename E::type T;
-  constexpr int COLS = 64 * E::N;   // columns of a wave
-  constexpr int ZCOLS = 2048;       // columns of a wave that writes zeros
-  __shared__ int chunk0[EB_BUCKETS + 1], empty0[EB_BUCKETS + 1];
+  constexpr int N = E::N, AHEAD = 8 / VECS;
+  __shared__ int chunk0[EB_BUCKETS], slot0[EB_BUCKETS];
+  __shared__ int wx[4];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   {
-    // exclusive sums of the buckets' unit counts (256 threads, 256 buckets)
+    // exclusive sums of the buckets' chunk counts (256 threads, 256 buckets)
     const EbBucket k = a.buckets[threadIdx.x];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    int x = k.chunks, y = k.empty;
+    int x = k.chunks;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
-      const int u = __shfl_up(x, d), v = __shfl_up(y, d);
-      if (lane >= d) {
-        x += u;
-        y += v;
-      }
+      const int y = __shfl_up(x, d);
+      if (lane >= d) x += y;
     }
-    __shared__ int wx[4], wy[4];
-    if (lane == 63) {
-      wx[w] = x;
-      wy[w] = y;
-    }
+    if (lane == 63) wx[w] = x;
     __syncthreads();
-    for (int i = 0; i < w; ++i) {
-      x += wx[i];
-      y += wy[i];
-    }
-    chunk0[threadIdx.x + 1] = x;
-    empty0[threadIdx.x + 1] = y;
-    if (threadIdx.x == 0) chunk0[0] = empty0[0] = 0;
+    x -= k.chunks;
+    for (int i = 0; i < w; ++i) x += wx[i];
+    chunk0[threadIdx.x] = x;
+    slot0[threadIdx.x] = k.first - x;  // a bucket's chunks lie from its first token on
     __syncthreads();
   }
-  auto bucket_of = [](const int *start, int i) {
-    int lo = 0, hi = EB_BUCKETS - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (start[mid] <= i) lo = mid;
-      else hi = mid - 1;
-    }
-    return lo;
-  };
-  const int lane = threadIdx.x & 63;
-  const int zblocks = (int)((a.dim + ZCOLS - 1) / ZCOLS);
-  const int64_t n_chunk_units = (int64_t)chunk0[EB_BUCKETS] * col_blocks;
-  const int64_t n_units = n_chunk_units + (int64_t)empty0[EB_BUCKETS] * zblocks;
-  const int per = (int)((a.vocab + EB_BUCKETS - 1) / EB_BUCKETS);
+  const uint32_t n_units = (uint32_t)(wx[0] + wx[1] + wx[2] + wx[3]) * (uint32_t)col_blocks;
+  int start[EB_BUCKETS / 64];
+#pragma unroll
+  for (int k = 0; k < EB_BUCKETS / 64; ++k) start[k] = chunk0[lane + 64 * k];
   const T *dout = static_cast<const T *>(a.dout);
-  for (int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); u < n_units; u += (int64_t)gridDim.x * 4) {
-    if (u >= n_chunk_units) {
-      const int64_t z = u - n_chunk_units;
-      const int i = (int)(z / zblocks);
-      const int bk = bucket_of(empty0, i);
-      float *dst = a.acc + a.empty[(int64_t)bk * per + i - empty0[bk]] * a.acc_ld;
-      const int64_t c0 = z % zblocks * ZCOLS, c1 = min(c0 + ZCOLS, a.dim);
-      for (int64_t c = c0 + 4 * lane; c < c1; c += 256) {
-        if (c + 4 <= c1) store16(dst + c, make_uint4(0, 0, 0, 0));
-        else
-          for (int64_t j = c; j < c1; ++j) dst[j] = 0.f;
-      }
-      continue;
+  for (uint32_t u = blockIdx.x * 4 + w; u < n_units; u += gridDim.x * 4) {
+    const int i = (int)(u / (uint32_t)col_blocks), cb = (int)(u % (uint32_t)col_blocks);
+    int bk = -1;
+#pragma unroll
+    for (int k = 0; k < EB_BUCKETS / 64; ++k) bk += __popcll(__ballot(start[k] <= i));
+    const EbChunk ch = a.chunks[__builtin_amdgcn_readfirstlane(slot0[bk] + i)];
+    const int count = ch.count;
+    const int64_t c0 = (int64_t)cb * (64 * N * VECS) + lane * N;
+    int cols[VECS];
+#pragma unroll
+    for (int v = 0; v < VECS; ++v) cols[v] = (int)max((int64_t)0, min((int64_t)N, a.dim - c0 - v * 64 * N));
+    const int toks = count == 1 ? ch.tok0 : lane < count ? a.perm[ch.start + lane] : 0;
+    float *dst = a.acc + ch.row * a.acc_ld + c0;
+    float sum[VECS][N] = {};
+    uint4 old[VECS][N / 4];
+    const bool add_old = !a.first && ch.parts == 1;
+    if (add_old) {
+#pragma unroll
+      for (int v = 0; v < VECS; ++v)
+        if (cols[v] == N) {
+#pragma unroll
+          for (int j = 0; j < N; j += 4) old[v][j / 4] = load16(dst + v * 64 * N + j);
+        }
     }
-    const int i = (int)(u / col_blocks), cb = (int)(u % col_blocks);
-    const int bk = bucket_of(chunk0, i);
-    const EbChunk ch = a.chunks[a.buckets[bk].first + i - chunk0[bk]];
-    const int64_t c = (int64_t)cb * COLS + lane * E::N;
-    const int cols = (int)max((int64_t)0, min((int64_t)E::N, a.dim - c));
-    float sum[E::N] = {};
-    if (cols == E::N) {
-#pragma unroll 4
-      for (int k = 0; k < ch.count; ++k) {
-        float v[E::N];
-        E::unpack(load16(dout + a.perm[ch.start + k] * a.dout_ld + c), v);
+    auto add = [&](int k, auto steps) {
+      constexpr int STEPS = decltype(steps)::value;
+      uint4 in[STEPS][VECS];
 #pragma unroll
-        for (int j = 0; j < E::N; ++j) sum[j] += v[j];
+      for (int q = 0; q < STEPS; ++q) {
+        const T *row = dout + (int64_t)__builtin_amdgcn_readlane(toks, k + q) * a.dout_ld + c0;
+#pragma unroll
+        for (int v = 0; v < VECS; ++v) {
+          in[q][v] = make_uint4(0, 0, 0, 0);
+          if (cols[v] == N) in[q][v] = load16(row + v * 64 * N);
+        }
       }
-    } else if (cols > 0) {
-      for (int k = 0; k < ch.count; ++k) {
-        const T *row = dout + a.perm[ch.start + k] * a.dout_ld + c;
 #pragma unroll
-        for (int j = 0; j < E::N; ++j)
-          if (j < cols) sum[j] += E::get(row[j]);
+      for (int q = 0; q < STEPS; ++q)
+#pragma unroll
+        for (int v = 0; v < VECS; ++v) {
+          float x[N];
+          E::unpack(in[q][v], x);
+#pragma unroll
+          for (int j = 0; j < N; ++j) sum[v][j] += x[j];
+        }
+    };
+    int k = 0;
+    for (; k + AHEAD <= count; k += AHEAD) add(k, std::integral_constant<int, AHEAD>());
+    for (; k < count; ++k) add(k, std::integral_constant<int, 1>());
+#pragma unroll
+    for (int v = 0; v < VECS; ++v) {
+      if (cols[v] > 0 && cols[v] < N) {  // the row's last elements
+        for (k = 0; k < count; ++k) {
+          const T *row = dout + (int64_t)__builtin_amdgcn_readlane(toks, k) * a.dout_ld + c0 + v * 64 * N;
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (j < cols[v]) sum[v][j] += E::get(row[j]);
+        }
       }
     }
     if (ch.parts > 1) {
       // the row's chunks meet here: each leaves its sum, the last to arrive
       // adds them in their order (which one is last does not matter)
-      const int slot0 = ch.seg / (EB_CHUNK / 2);
-      float *mine = a.partials + (int64_t)(ch.start / (EB_CHUNK / 2)) * a.dim + c;
+      float *mine = a.partials + (int64_t)(ch.start / (EB_CHUNK / 2)) * a.dim + c0;
 #pragma unroll
-      for (int j = 0; j < E::N; ++j)
-        if (j < cols) mine[j] = sum[j];
+      for (int v = 0; v < VECS; ++v)
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (j < cols[v]) mine[v * 64 * N + j] = sum[v][j];
       int before = 0;
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
       if (lane == 0)
-        before = __hip_atomic_fetch_add(&a.arrive[(int64_t)slot0 * col_blocks + cb], 1, __ATOMIC_RELAXED,
-                                        __HIP_MEMORY_SCOPE_AGENT);
+        before = __hip_atomic_fetch_add(&a.arrive[(int64_t)(ch.seg / (EB_CHUNK / 2)) * col_blocks + cb], 1,
+                                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       before = __builtin_amdgcn_readfirstlane(before);
       if (before != ch.parts - 1) continue;
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
 #pragma unroll
-      for (int j = 0; j < E::N; ++j) sum[j] = 0.f;
-      for (int k = 0; k < ch.parts; ++k) {
-        const int st = ch.seg + (int)((int64_t)ch.seg_count * k / ch.parts);
-        const float *p = a.partials + (int64_t)(st / (EB_CHUNK / 2)) * a.dim + c;
+      for (int v = 0; v < VECS; ++v)
 #pragma unroll
-        for (int j = 0; j < E::N; ++j)
-          if (j < cols) sum[j] += p[j];
+        for (int j = 0; j < N; ++j) sum[v][j] = 0.f;
+      for (k = 0; k < ch.parts; ++k) {
+        const int st = ch.seg + (int)((int64_t)ch.seg_count * k / ch.parts);
+        const float *p = a.partials + (int64_t)(st / (EB_CHUNK / 2)) * a.dim + c0;
+#pragma unroll
+        for (int v = 0; v < VECS; ++v)
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (j < cols[v]) sum[v][j] += p[v * 64 * N + j];
       }
     }
-    float *dst = a.acc + ch.row * a.acc_ld + c;
 #pragma unroll
-    for (int j = 0; j < E::N; ++j) sum[j] *= a.scale;
-    if (cols == E::N) {
+    for (int v = 0; v < VECS; ++v) {
+      float *out = dst + v * 64 * N;
 #pragma unroll
-      for (int j = 0; j < E::N; j += 4) {
-        float4 v = make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
-        if (!a.first) {
-          float4 o;
-          __builtin_memcpy(&o, dst + j, 16);
-          v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+      for (int j = 0; j < N; ++j) sum[v][j] *= a.scale;
+      if (cols[v] == N) {
+#pragma unroll
+        for (int j = 0; j < N; j += 4) {
+          float o[4] = {};
+          if (!a.first) Elem<false>::unpack(add_old ? old[v][j / 4] : load16(out + j), o);
+          for (int q = 0; q < 4; ++q) o[q] += sum[v][j + q];
+          store16(out + j, Elem<false>::pack(o));
         }
-        __builtin_memcpy(dst + j, &v, 16);
-      }
-    } else {
+      } else {
 #pragma unroll
-      for (int j = 0; j < E::N; ++j)
-        if (j < cols) dst[j] = a.first ? sum[j] : dst[j] + sum[j];
+        for (int j = 0; j < N; ++j)
+          if (j < cols[v]) out[j] = a.first ? sum[v][j] : out[j] + sum[v][j];
+      }
     }
   }
 }
 
 EbLayout embed_layout(int64_t tokens, int64_t vocab, int64_t dim) {
+  (void)vocab;
   EbLayout l{};
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -426,7 +501,6 @@ EbLayout embed_layout(int64_t tokens, int64_t vocab, int64_t dim) {
   l.key_b = take(4 * n);
   l.tok_b = take(4 * n);
   l.chunks = take(sizeof(EbChunk) * n);
-  l.empty = take(4 * ((size_t)vocab + EB_BUCKETS));
   // a row of at most EB_CHUNK tokens leaves no partial sums
   l.partials = take(n > EB_CHUNK ? slots * (size_t)dim * 4 : 0);
   l.arrive = take(n > EB_CHUNK ? slots * (((size_t)dim + 255) / 256) * 4 : 0);
@@ -434,19 +508,29 @@ EbLayout embed_layout(int64_t tokens, int64_t vocab, int64_t dim) {
   return l;
 }
 
-hipError_t launch_embed_backward(const EmbedBwdArgs &a, bool bf16, hipStream_t s) {
-  const int cols = bf16 ? 512 : 256;
-  const int col_blocks = (int)((a.dim + cols - 1) / cols);
-  int passes = 1;
-  while (((a.vocab - 1) / EB_BUCKETS) >> (passes * ES_BITS)) ++passes;
-  hipLaunchKernelGGL(ke_sort, dim3(EB_BUCKETS), dim3(ES_THREADS), 0, s, a, passes, col_blocks);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int64_t units = a.tokens * col_blocks + (a.first ? a.vocab * ((a.dim + 2047) / 2048) : 0);
-  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((units + 3) / 4, 2048));
-  if (bf16) hipLaunchKernelGGL(ke_add<true>, dim3(grid), dim3(256), 0, s, a, col_blocks);
-  else hipLaunchKernelGGL(ke_add<false>, dim3(grid), dim3(256), 0, s, a, col_blocks);
+namespace {
+
+template <bool BF16>
+hipError_t add_launch(const EmbedBwdArgs &a, int passes, hipStream_t s) {
+  constexpr int WAVE_COLS = 64 * Elem<BF16>::N;
+  const bool wide = a.dim > WAVE_COLS;
+  const int cols = WAVE_COLS * (wide ? 2 : 1), col_blocks = (int)((a.dim + cols - 1) / cols);
+  hipLaunchKernelGGL(ke_sort, dim3(EB_BUCKETS + (a.first ? (unsigned)std::min<int64_t>(a.vocab, EB_BUCKETS) : 0)),
+                     dim3(ES_THREADS), 0, s, a, passes, col_blocks);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.tokens == 0) return e;
+  const unsigned grid = (unsigned)std::min<int64_t>((a.tokens * col_blocks + 3) / 4, 2048);
+  if (wide) hipLaunchKernelGGL((ke_add<BF16, 2>), dim3(grid), dim3(256), 0, s, a, col_blocks);
+  else hipLaunchKernelGGL((ke_add<BF16, 1>), dim3(grid), dim3(256), 0, s, a, col_blocks);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_embed_backward(const EmbedBwdArgs &a, bool bf16, hipStream_t s) {
+  int passes = 1;
+  while (((a.vocab - 1) >> EB_SHIFT) >> (passes * ES_BITS)) ++passes;
+  return bf16 ? add_launch<true>(a, passes, s) : add_launch<false>(a, passes, s);
 }
 
 }  // namespace muon

@@ -189,7 +189,6 @@ muon_status muon_embed_backward(const void *ids, int32_t id_type, int64_t tokens
     a.key_b = reinterpret_cast<int32_t *>(w + l.key_b);
     a.tok_b = reinterpret_cast<int32_t *>(w + l.tok_b);
     a.chunks = reinterpret_cast<EbChunk *>(w + l.chunks);
-    a.empty = reinterpret_cast<int32_t *>(w + l.empty);
     a.partials = reinterpret_cast<float *>(w + l.partials);
     a.arrive = reinterpret_cast<int32_t *>(w + l.arrive);
     return done(launch_embed_backward(a, dtype == MUON_DT_BF16, static_cast<hipStream_t>(stream)), me);

@@ -31,14 +31,11 @@ hipError_t launch_embed_forward(const EmbedFwdArgs &a, bool bf16, hipStream_t s)
 
 constexpr int EB_BUCKETS = 256;  // bucket of a table row = row mod EB_BUCKETS
 constexpr int EB_CHUNK = 64;     // tokens that one workgroup adds up in a row
-constexpr int EB_COLS = 1024;    // columns of a work unit
 
 // What the sort leaves about one bucket.
 struct EbBucket {
-  int32_t first;    // its tokens' first position in the sorted order
-  int32_t tokens;   // their count
-  int32_t chunks;   // its work chunks, at chunk slots [first, first + chunks)
-  int32_t empty;    // its table rows without a token (first call of a step)
+  int32_t first;   // its tokens' first position in the sorted order
+  int32_t chunks;  // its work chunks, at chunk slots [first, first + chunks)
 };
 
 // At most EB_CHUNK consecutive sorted tokens of one table row.  A row with
@@ -49,11 +46,13 @@ struct EbChunk {
   int32_t parts;     // chunks of the row (1: the chunk writes the row itself)
   int32_t seg;       // the row's first sorted position
   int32_t seg_count; // the row's tokens
+  int32_t tok0;      // the row's first token
+  int32_t pad;
 };
 
 // Workspace of the gradient, carved in this order (256-byte aligned parts).
 struct EbLayout {
-  size_t buckets, perm, key_a, key_b, tok_b, chunks, empty, partials, arrive, total;
+  size_t buckets, perm, key_a, key_b, tok_b, chunks, partials, arrive, total;
 };
 EbLayout embed_layout(int64_t tokens, int64_t vocab, int64_t dim);
 
@@ -69,7 +68,6 @@ struct EmbedBwdArgs {
   EbBucket *buckets;
   int32_t *perm, *key_a, *key_b, *tok_b;
   EbChunk *chunks;
-  int32_t *empty;
   float *partials;
   int32_t *arrive;
 };
@@ -145,7 +143,7 @@ struct BalanceArgs {
   void *dlogits;
 };
 struct BalanceLayout {
-  size_t hist, sums, total;
+  size_t hist, sums, arrive, total;
 };
 BalanceLayout balance_layout(int64_t tokens, int32_t n_experts);
 hipError_t launch_balance(const BalanceArgs &a, bool bf16, char *ws, hipStream_t s);

@@ -108,15 +108,14 @@ def _launch(name, call, stream, tensors):
     for t in tensors:
         if t is not None and t.get_device() != dev:
             _refuse(name, "the tensors are on different devices")
-    cuda = _torch.cuda
-    if stream is None:
-        s = cuda.current_stream(dev).cuda_stream
+    if stream is None:  # the handle alone: a Stream object costs a microsecond
+        s = _torch._C._cuda_getCurrentRawStream(dev)
     else:
         s = stream if isinstance(stream, int) else stream.cuda_stream
-    if cuda.current_device() == dev:
+    if _torch._C._cuda_getDevice() == dev:
         st = call(s)
     else:
-        with cuda.device(dev):
+        with _torch.cuda.device(dev):
             st = call(s)
     if st:
         _lib._check(st, "muon_" + name)

@@ -150,6 +150,27 @@ struct Row {
   }
 };
 
+// Values passed between workgroups of one launch, past the caches that are not
+// shared by all of them.  arrive() counts a wave in after its stores have
+// reached memory, and returns how many came before it: whoever learns that
+// all did may read what they put.  (A release and an acquire fence of device
+// scope would write back and invalidate a whole L2: the embedding gradient of
+// 16384 tokens took 193 us so, instead of 70 in its second kernel.)
+template <class T>
+__device__ __forceinline__ void put_shared(T *p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <class T>
+__device__ __forceinline__ T get_shared(const T *p) {
+  return __hip_atomic_load(const_cast<T *>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ int arrive(int32_t *count) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  const int before = __hip_atomic_fetch_add(count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  asm volatile("" ::: "memory");
+  return before;
+}
+
 // Sum over a workgroup of WAVES waves in a fixed order; every thread gets
 // it.  `red` holds WAVES doubles and is free again after the call.
 template <int WAVES>

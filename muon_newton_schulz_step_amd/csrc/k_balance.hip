@@ -33,15 +33,26 @@ constexpr int64_t BALANCE_SOLO = 16384;
 __device__ __forceinline__ int count_choices(const BalanceArgs &a, int64_t t0, int64_t t1, int *h) {
   int live = 0;
   if (a.valid) {
+#pragma unroll 4
     for (int64_t t = t0 + threadIdx.x; t < t1; t += 1024) live += a.valid[t] != 0;
   } else if (threadIdx.x == 0) {
     live = (int)(t1 - t0);
   }
-  const uint32_t k = (uint32_t)a.k, end = (uint32_t)t1 * k;  // tokens * k stays below 2^31
-#pragma unroll 8
-  for (uint32_t i = (uint32_t)t0 * k + threadIdx.x; i < end; i += 1024) {
-    const int64_t e = index_at(a.experts, i);
-    if (e >= 0 && e < a.n_experts && (!a.valid || a.valid[i / k])) atomicAdd(&h[e], 1);
+  // tokens * k stays below 2^31; the loads of a round are under way together
+  constexpr int ROUND = 8;
+  const uint32_t k = (uint32_t)a.k, end = (uint32_t)t1 * k;
+  for (uint32_t i = (uint32_t)t0 * k + threadIdx.x; i < end; i += ROUND * 1024) {
+    int64_t e[ROUND];
+    uint8_t ok[ROUND];
+#pragma unroll
+    for (int q = 0; q < ROUND; ++q) {
+      const uint32_t j = i + q * 1024;
+      e[q] = j < end ? index_at(a.experts, j) : -1;
+      ok[q] = j < end && a.valid ? a.valid[j / k] : 1;
+    }
+#pragma unroll
+    for (int q = 0; q < ROUND; ++q)
+      if (e[q] >= 0 && e[q] < a.n_experts && ok[q]) atomicAdd(&h[e[q]], 1);
   }
   return live;
 }
@@ -101,14 +112,45 @@ __global__ __launch_bounds__(BM_THREADS, 8) void kb_main(BalanceArgs a, const in
   __shared__ __attribute__((aligned(16))) float f_of[LANES * VECS * N];
   __shared__ double red[BM_THREADS / 64];
   __shared__ int last;
-  const int n = a.n_experts, tid = threadIdx.x;
+  const int n = a.n_experts, tid = threadIdx.x, l = tid & (LANES - 1);
+  const int64_t step = (int64_t)gridDim.x * PER;
+  int64_t t = (int64_t)blockIdx.x * PER + tid / LANES;
+  float v[VECS][N];
+  bool ok, next = t < a.tokens && (!a.valid || a.valid[t]);
+  // the token's logits, and whether the next one counts
+  auto fetch = [&](int64_t t) {
+    ok = next;
+    next = t + step < a.tokens && (!a.valid || a.valid[t + step]);
+    if (!ok) return;
+    const T *x = static_cast<const T *>(a.logits) + t * a.ld;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      const int c = (l + LANES * i) * N;
+      if (c + N <= n) {
+        E::unpack(load16(x + c), v[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[i][j] = c + j < n ? E::get(x[c + j]) : -INFINITY;
+      }
+    }
+  };
+  fetch(t);
   for (int e = tid; e <= n; e += BM_THREADS) count[e] = 0;
   __syncthreads();
   if (parts == 0) {
     const int live = count_choices(a, 0, a.tokens, count);
     if (live) atomicAdd(&count[n], live);
   } else {
-    for (int i = tid; i < parts * (n + 1); i += BM_THREADS) atomicAdd(&count[i % (n + 1)], hist[i]);
+    constexpr int ROUND = 8;
+    const int all = parts * (n + 1);
+    for (int i = tid; i < all; i += ROUND * BM_THREADS) {
+      int c[ROUND];
+#pragma unroll
+      for (int q = 0; q < ROUND; ++q) c[q] = i + q * BM_THREADS < all ? hist[i + q * BM_THREADS] : 0;
+#pragma unroll
+      for (int q = 0; q < ROUND; ++q)
+        if (c[q]) atomicAdd(&count[(i + q * BM_THREADS) % (n + 1)], c[q]);
+    }
   }
   __syncthreads();
   const int total = count[n];
@@ -119,28 +161,10 @@ __global__ __launch_bounds__(BM_THREADS, 8) void kb_main(BalanceArgs a, const in
   }
   __syncthreads();
   const float cb = (float)(a.coef * (double)n / (double)tokens), cz = (float)(2.0 * a.z_coef / (double)tokens);
-  const int l = tid & (LANES - 1);
   double bal = 0.0, zz = 0.0;
-  const int64_t step = (int64_t)gridDim.x * PER;
-  int64_t t = (int64_t)blockIdx.x * PER + tid / LANES;
-  bool ok = t < a.tokens && (!a.valid || a.valid[t]);
   for (; t < a.tokens; t += step) {
-    const bool now = ok;
-    ok = t + step < a.tokens && (!a.valid || a.valid[t + step]);
     T *d = static_cast<T *>(a.dlogits) + t * a.dld;
-    const T *x = static_cast<const T *>(a.logits) + t * a.ld;
-    float v[VECS][N];
-    if (now) {
-#pragma unroll
-      for (int i = 0; i < VECS; ++i) {
-        const int c = (l + LANES * i) * N;
-        if (c + N <= n) {
-          E::unpack(load16(x + c), v[i]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < N; ++j) v[i][j] = c + j < n ? E::get(x[c + j]) : -INFINITY;
-        }
-      }
+    if (ok) {
       float m = kLowest;
 #pragma unroll
       for (int i = 0; i < VECS; ++i)
@@ -182,29 +206,28 @@ __global__ __launch_bounds__(BM_THREADS, 8) void kb_main(BalanceArgs a, const in
     for (int i = 0; i < VECS; ++i) {
       const int c = (l + LANES * i) * N;
       if (c + N <= n) {
-        store16(d + c, E::pack(v[i]));
+        stream16(d + c, E::pack(v[i]));
       } else {
 #pragma unroll
         for (int j = 0; j < N; ++j)
           if (c + j < n) d[c + j] = E::put(v[i][j]);
       }
     }
+    fetch(t + step);
   }
   double tb = block_sum<BM_THREADS / 64>(bal, red), tz = block_sum<BM_THREADS / 64>(zz, red);
   if (parts != 0) {
     const int groups = gridDim.x;
     if (tid == 0) {
-      sums[2 * blockIdx.x] = tb;
-      sums[2 * blockIdx.x + 1] = tz;
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-      last = __hip_atomic_fetch_add(arrive, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == groups - 1;
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+      put_shared(&sums[2 * blockIdx.x], tb);
+      put_shared(&sums[2 * blockIdx.x + 1], tz);
+      last = dev::arrive(arrive) == groups - 1;
     }
     __syncthreads();
     if (!last) return;
     const bool in = tid < groups;
-    tb = block_sum<BM_THREADS / 64>(in ? sums[2 * tid] : 0.0, red);
-    tz = block_sum<BM_THREADS / 64>(in ? sums[2 * tid + 1] : 0.0, red);
+    tb = block_sum<BM_THREADS / 64>(in ? get_shared(&sums[2 * tid]) : 0.0, red);
+    tz = block_sum<BM_THREADS / 64>(in ? get_shared(&sums[2 * tid + 1]) : 0.0, red);
   }
   if (tid == 0) {
     const double den = (double)max(total, 1);

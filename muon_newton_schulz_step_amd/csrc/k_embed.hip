@@ -123,23 +123,31 @@ __device__ __forceinline__ int scan_exclusive(int v, int *wsum, int *total) {
   return base + x - v;
 }
 
-// Zeros into the rows of bucket b that no token meets; map: ES_MAP_BITS bits.
-__device__ void zero_rows(const EmbedBwdArgs &a, int b, uint32_t *map) {
+// Zeros into the rows congruent to b modulo 2^SHIFT that no token meets; map:
+// MAP_BITS bits of LDS.
+template <int THREADS, int SHIFT, int MAP_BITS>
+__device__ __forceinline__ void zero_rows(const EmbedBwdArgs &a, int b, uint32_t *map) {
+  constexpr int MASK = (1 << SHIFT) - 1, ROUND = 8;
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int rows = (int)((a.vocab - b + EB_BUCKETS - 1) >> EB_SHIFT);
-  for (int r0 = 0; r0 < rows; r0 += ES_MAP_BITS) {
-    const int m = min(rows - r0, ES_MAP_BITS);
-    for (int i = threadIdx.x; i < (m + 31) / 32; i += ES_THREADS) map[i] = 0;
+  const int rows = (int)((a.vocab - b + MASK) >> SHIFT);
+  for (int r0 = 0; r0 < rows; r0 += MAP_BITS) {
+    const int m = min(rows - r0, MAP_BITS);
+    for (int i = threadIdx.x; i < (m + 31) / 32; i += THREADS) map[i] = 0;
     __syncthreads();
-#pragma unroll 8
-    for (int64_t t = threadIdx.x; t < a.tokens; t += ES_THREADS) {
-      const int id = row_of(a, t), r = (id >> EB_SHIFT) - r0;
-      if (id >= 0 && (id & (EB_BUCKETS - 1)) == b && r >= 0 && r < m) atomicOr(&map[r >> 5], 1u << (r & 31));
+    for (int64_t t = threadIdx.x; t < a.tokens; t += ROUND * THREADS) {
+      int id[ROUND];
+#pragma unroll
+      for (int q = 0; q < ROUND; ++q) id[q] = t + q * THREADS < a.tokens ? row_of(a, t + q * THREADS) : -1;
+#pragma unroll
+      for (int q = 0; q < ROUND; ++q) {
+        const int r = (id[q] >> SHIFT) - r0;
+        if (id[q] >= 0 && (id[q] & MASK) == b && r >= 0 && r < m) atomicOr(&map[r >> 5], 1u << (r & 31));
+      }
     }
     __syncthreads();
-    for (int r = w; r < m; r += ES_WAVES) {
+    for (int r = w; r < m; r += THREADS / 64) {
       if ((map[r >> 5] >> (r & 31)) & 1) continue;
-      float *dst = a.acc + (int64_t)((r0 + r) * EB_BUCKETS + b) * a.acc_ld;
+      float *dst = a.acc + (((int64_t)(r0 + r) << SHIFT) + b) * a.acc_ld;
       const Row<false> row(dst, a.dim);
 #pragma unroll 4
       for (int i = lane; i < row.vecs; i += 64) stream16(dst + row.col(i), make_uint4(0, 0, 0, 0));
@@ -155,10 +163,10 @@ __global__ __launch_bounds__(ES_THREADS, 8) void ke_sort(EmbedBwdArgs a, int pas
   __shared__ __attribute__((aligned(16))) int count[ES_WAVES][ES_DIGITS];
   __shared__ int base[ES_DIGITS];
   __shared__ int wsum[ES_WAVES], wsum2[ES_WAVES];
-  __shared__ int n_chunks;
+  __shared__ int n_heavy, n_light;
   const int b = blockIdx.x, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   if (b >= EB_BUCKETS) {
-    zero_rows(a, b - EB_BUCKETS, reinterpret_cast<uint32_t *>(&count[0][0]));
+    zero_rows<ES_THREADS, EB_SHIFT, ES_MAP_BITS>(a, b - EB_BUCKETS, reinterpret_cast<uint32_t *>(&count[0][0]));
     return;
   }
   // a wave takes a contiguous span of the tokens, so wave order is token
@@ -189,7 +197,7 @@ __global__ __launch_bounds__(ES_THREADS, 8) void ke_sort(EmbedBwdArgs a, int pas
     wsum[w] = mine;
     wsum2[w] = lower;
   }
-  if (threadIdx.x == 0) n_chunks = 0;
+  if (threadIdx.x == 0) n_heavy = n_light = 0;
   __syncthreads();
   int first = 0, n = 0, at = 0;
   for (int i = 0; i < ES_WAVES; ++i) {
@@ -226,15 +234,18 @@ __global__ __launch_bounds__(ES_THREADS, 8) void ke_sort(EmbedBwdArgs a, int pas
   if (small && threadIdx.x < 4) lkey[n + threadIdx.x] = INT32_MAX;  // no row's key
   __syncthreads();
 
-  // a row's tokens in nearly equal chunks of at most EB_CHUNK (their order in
-  // the list does not touch the results)
+  // a row's tokens in nearly equal chunks of at most EB_CHUNK: chunks of many
+  // tokens from the front of the bucket's slots, others from the back (their
+  // order does not touch the results)
   auto emit = [&](int k, int s, int len, int tok0) {
     const int parts = (len + EB_CHUNK - 1) / EB_CHUNK;
-    const int slot = atomicAdd(&n_chunks, parts);
     const int row = k * EB_BUCKETS + b;
+    int slot = first;
+    if (len > EB_LIGHT) slot += atomicAdd(&n_heavy, parts);
+    else slot += n - 1 - atomicAdd(&n_light, 1);
     for (int i = 0; i < parts; ++i) {
       const int lo = (int)((int64_t)len * i / parts), hi = (int)((int64_t)len * (i + 1) / parts);
-      a.chunks[first + slot + i] = EbChunk{row, first + s + lo, hi - lo, parts, first + s, len, tok0, 0};
+      a.chunks[slot + i] = EbChunk{row, first + s + lo, hi - lo, parts, first + s, len, tok0, 0};
     }
     if (parts > 1) {
       for (int j = 0; j < col_blocks; ++j) a.arrive[(int64_t)((first + s) / (EB_CHUNK / 2)) * col_blocks + j] = 0;
@@ -257,7 +268,7 @@ __global__ __launch_bounds__(ES_THREADS, 8) void ke_sort(EmbedBwdArgs a, int pas
       if (before == 0) emit(k, less, same, ltok[p]);
     }
     __syncthreads();
-    if (threadIdx.x == 0) a.buckets[b] = EbBucket{first, n_chunks};
+    if (threadIdx.x == 0) a.buckets[b] = EbBucket{first, n, n_heavy, n_light};
     return;
   }
 
@@ -334,50 +345,41 @@ __global__ __launch_bounds__(ES_THREADS, 8) void ke_sort(EmbedBwdArgs a, int pas
     emit(key[s], s, (h + 1 < n_heads ? head[h + 1] : n) - s, tok[s]);
   }
   __syncthreads();
-  if (threadIdx.x == 0) a.buckets[b] = EbBucket{first, n_chunks};
+  if (threadIdx.x == 0) a.buckets[b] = EbBucket{first, n, n_heavy, n_light};
 }
 
 // ------------------------------------------------------- adding them up
 
 // Units of work, a wave each: (chunk, column block) adds up to EB_CHUNK rows
 // of dout, VECS 16-byte vectors a lane.  HBM-bound: each live dout row is
-// read once, each gradient row with a token written once.
+// read once, each gradient row with a token written once.  The units run over
+// the buckets' first chunks, then over their second ones, and so on: the
+// chunks of many tokens come first and the light ones fill the end.
 template <bool BF16, int VECS>
 __global__ __launch_bounds__(256) void ke_add(EmbedBwdArgs a, int col_blocks) {
   typedef Elem<BF16> E;
   typedef typename E::type T;
   constexpr int N = E::N, AHEAD = 8 / VECS;
-  __shared__ int chunk0[EB_BUCKETS], slot0[EB_BUCKETS];
-  __shared__ int wx[4];
+  __shared__ EbBucket bucket[EB_BUCKETS];
+  __shared__ int most;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  {
-    // exclusive sums of the buckets' chunk counts (256 threads, 256 buckets)
-    const EbBucket k = a.buckets[threadIdx.x];
-    int x = k.chunks;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int y = __shfl_up(x, d);
-      if (lane >= d) x += y;
-    }
-    if (lane == 63) wx[w] = x;
-    __syncthreads();
-    x -= k.chunks;
-    for (int i = 0; i < w; ++i) x += wx[i];
-    chunk0[threadIdx.x] = x;
-    slot0[threadIdx.x] = k.first - x;  // a bucket's chunks lie from its first token on
-    __syncthreads();
-  }
-  const uint32_t n_units = (uint32_t)(wx[0] + wx[1] + wx[2] + wx[3]) * (uint32_t)col_blocks;
-  int start[EB_BUCKETS / 64];
-#pragma unroll
-  for (int k = 0; k < EB_BUCKETS / 64; ++k) start[k] = chunk0[lane + 64 * k];
+  if (threadIdx.x == 0) most = 0;
+  __syncthreads();
+  bucket[threadIdx.x] = a.buckets[threadIdx.x];
+  atomicMax(&most, bucket[threadIdx.x].heavy + bucket[threadIdx.x].light);
+  __syncthreads();
+  const uint64_t n_q = (uint64_t)most * EB_BUCKETS;
   const T *dout = static_cast<const T *>(a.dout);
-  for (uint32_t u = blockIdx.x * 4 + w; u < n_units; u += gridDim.x * 4) {
-    const int i = (int)(u / (uint32_t)col_blocks), cb = (int)(u % (uint32_t)col_blocks);
-    int bk = -1;
-#pragma unroll
-    for (int k = 0; k < EB_BUCKETS / 64; ++k) bk += __popcll(__ballot(start[k] <= i));
-    const EbChunk ch = a.chunks[__builtin_amdgcn_readfirstlane(slot0[bk] + i)];
+  const uint32_t waves = gridDim.x * 4 / (uint32_t)col_blocks * (uint32_t)col_blocks;
+  const uint32_t wave = blockIdx.x * 4 + w;
+  if (wave >= waves) return;
+  const int cb = (int)(wave % (uint32_t)col_blocks);
+  for (uint64_t q = wave / (uint32_t)col_blocks; q < n_q; q += waves / (uint32_t)col_blocks) {
+    const EbBucket bk = bucket[q & (EB_BUCKETS - 1)];
+    const int at = (int)(q >> EB_SHIFT);
+    if (at >= bk.heavy + bk.light) continue;
+    const int slot = bk.first + (at < bk.heavy ? at : bk.tokens - 1 - (at - bk.heavy));
+    const EbChunk ch = a.chunks[__builtin_amdgcn_readfirstlane(slot)];
     const int count = ch.count;
     const int64_t c0 = (int64_t)cb * (64 * N * VECS) + lane * N;
     int cols[VECS];
@@ -435,32 +437,31 @@ __global__ __launch_bounds__(256) void ke_add(EmbedBwdArgs a, int col_blocks) {
     if (ch.parts > 1) {
       // the row's chunks meet here: each leaves its sum, the last to arrive
       // adds them in their order (which one is last does not matter)
-      float *mine = a.partials + (int64_t)(ch.start / (EB_CHUNK / 2)) * a.dim + c0;
+      // (a lane's elements lie 64 apart, so that the lanes' stores touch)
+      const int64_t width = (int64_t)col_blocks * (64 * N * VECS);
+      float *part = a.partials + (int64_t)cb * (64 * N * VECS) + lane;
+      float *mine = part + (int64_t)(ch.start / (EB_CHUNK / 2)) * width;
 #pragma unroll
       for (int v = 0; v < VECS; ++v)
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-          if (j < cols[v]) mine[v * 64 * N + j] = sum[v][j];
+        for (int j = 0; j < N; ++j) put_shared(mine + 64 * (v * N + j), sum[v][j]);
       int before = 0;
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-      if (lane == 0)
-        before = __hip_atomic_fetch_add(&a.arrive[(int64_t)(ch.seg / (EB_CHUNK / 2)) * col_blocks + cb], 1,
-                                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // of all lanes
+      if (lane == 0) before = arrive(&a.arrive[(int64_t)(ch.seg / (EB_CHUNK / 2)) * col_blocks + cb]);
       before = __builtin_amdgcn_readfirstlane(before);
       if (before != ch.parts - 1) continue;
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
 #pragma unroll
       for (int v = 0; v < VECS; ++v)
 #pragma unroll
         for (int j = 0; j < N; ++j) sum[v][j] = 0.f;
+#pragma unroll 2
       for (k = 0; k < ch.parts; ++k) {
         const int st = ch.seg + (int)((int64_t)ch.seg_count * k / ch.parts);
-        const float *p = a.partials + (int64_t)(st / (EB_CHUNK / 2)) * a.dim + c0;
+        const float *p = part + (int64_t)(st / (EB_CHUNK / 2)) * width;
 #pragma unroll
         for (int v = 0; v < VECS; ++v)
 #pragma unroll
-          for (int j = 0; j < N; ++j)
-            if (j < cols[v]) sum[v][j] += p[v * 64 * N + j];
+          for (int j = 0; j < N; ++j) sum[v][j] += get_shared(p + 64 * (v * N + j));
       }
     }
 #pragma unroll
@@ -485,6 +486,159 @@ __global__ __launch_bounds__(256) void ke_add(EmbedBwdArgs a, int col_blocks) {
   }
 }
 
+// ------------------------------------------------------- few tokens
+
+// Up to EB_FEW tokens need no sort: a workgroup takes (token t, column block),
+// finds the tokens of the same row among all ids, ends if one of them comes
+// before t, and otherwise adds them up, each wave those of its quarter of the
+// ids; the waves' sums are joined in their order.  Bound by the latency of
+// its three dependent loads (ids, dout rows, acc).  The other workgroups write
+// the zeros of a first call.
+namespace {
+
+constexpr int EF_IDS = EB_FEW / 256;  // ids that a lane holds
+constexpr int EF_ZERO_SHIFT = 10;     // log2 of the workgroups that write zeros
+
+}  // namespace
+
+template <bool BF16, int VECS>
+__global__ __launch_bounds__(256) void ke_few(EmbedBwdArgs a, int zeros) {
+  typedef Elem<BF16> E;
+  typedef typename E::type T;
+  constexpr int N = E::N, COLS = 64 * N * VECS, AHEAD = 8 / VECS;
+  __shared__ __attribute__((aligned(16))) float part[3][COLS];  // sums of waves 1 to 3
+  __shared__ int before, has[4];
+  if ((int)blockIdx.x < zeros) {
+    __shared__ uint32_t map[1 << 8];
+    zero_rows<256, EF_ZERO_SHIFT, 32 << 8>(a, blockIdx.x, map);
+    return;
+  }
+  const uint32_t i0 = blockIdx.x - zeros;
+  const int t = (int)(i0 % (uint32_t)a.tokens), cb = (int)(i0 / (uint32_t)a.tokens), lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int mine = row_of(a, t);
+  int id[EF_IDS];
+#pragma unroll
+  for (int k = 0; k < EF_IDS; ++k) {
+    const int j = (w * EF_IDS + k) * 64 + lane;
+    id[k] = j < a.tokens ? row_of(a, j) : -1;
+  }
+  if (mine < 0) return;
+  if (threadIdx.x == 0) before = 0;
+  __syncthreads();
+  uint64_t same[EF_IDS];
+  int n = 0;
+  bool late = false;
+#pragma unroll
+  for (int k = 0; k < EF_IDS; ++k) {
+    same[k] = __ballot(id[k] == mine);
+    n += __popcll(same[k]);
+    late = late || (same[k] && (w * EF_IDS + k) * 64 + __builtin_ctzll(same[k]) < t);
+  }
+  if (lane == 0) {
+    has[w] = n;
+    if (late) before = 1;
+  }
+  const int64_t c0 = (int64_t)cb * COLS + lane * N;
+  float *dst = a.acc + mine * a.acc_ld + c0;
+  int cols[VECS];
+  uint4 old[VECS][N / 4];
+#pragma unroll
+  for (int v = 0; v < VECS; ++v) {
+    cols[v] = (int)max((int64_t)0, min((int64_t)N, a.dim - c0 - v * 64 * N));
+    if (w == 0 && !a.first && cols[v] == N) {
+#pragma unroll
+      for (int j = 0; j < N; j += 4) old[v][j / 4] = load16(dst + v * 64 * N + j);
+    }
+  }
+  __syncthreads();
+  if (before) return;
+  float sum[VECS][N] = {};
+  const T *dout = static_cast<const T *>(a.dout) + c0;
+  // the wave's tokens in order: the k-th set bit of the masks
+  int word = 0;
+  uint64_t left = same[0];
+  auto pop = [&]() {
+    while (!left) {
+      ++word;
+#pragma unroll
+      for (int k = 1; k < EF_IDS; ++k)
+        if (word == k) left = same[k];
+    }
+    const int j = (w * EF_IDS + word) * 64 + __builtin_ctzll(left);
+    left &= left - 1;
+    return j;
+  };
+  for (int k = 0; k < n; k += AHEAD) {
+    uint4 in[AHEAD][VECS];
+    const int m = min(AHEAD, n - k);
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) {
+      const T *row = dout;
+      if (q < m) row += (int64_t)pop() * a.dout_ld;
+#pragma unroll
+      for (int v = 0; v < VECS; ++v) {
+        in[q][v] = make_uint4(0, 0, 0, 0);
+        if (q < m) {
+          if (cols[v] == N) {
+            in[q][v] = load16(row + v * 64 * N);
+          } else if (cols[v] > 0) {  // the row's last elements
+            float x[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[j] = j < cols[v] ? E::get(row[v * 64 * N + j]) : 0.f;
+            in[q][v] = E::pack(x);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q)
+#pragma unroll
+      for (int v = 0; v < VECS; ++v) {
+        float x[N];
+        E::unpack(in[q][v], x);
+#pragma unroll
+        for (int j = 0; j < N; ++j) sum[v][j] += x[j];
+      }
+  }
+  if (w > 0 && n > 0) {
+#pragma unroll
+    for (int v = 0; v < VECS; ++v)
+#pragma unroll
+      for (int j = 0; j < N; j += 4)
+        *reinterpret_cast<uint4 *>(&part[w - 1][(v * 64 + lane) * N + j]) = Elem<false>::pack(&sum[v][j]);
+  }
+  __syncthreads();
+  if (w > 0) return;
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    if (!has[i]) continue;
+#pragma unroll
+    for (int v = 0; v < VECS; ++v)
+#pragma unroll
+      for (int j = 0; j < N; ++j) sum[v][j] += part[i - 1][(v * 64 + lane) * N + j];
+  }
+#pragma unroll
+  for (int v = 0; v < VECS; ++v) {
+    float *out = dst + v * 64 * N;
+#pragma unroll
+    for (int j = 0; j < N; ++j) sum[v][j] *= a.scale;
+    if (cols[v] == N) {
+#pragma unroll
+      for (int j = 0; j < N; j += 4) {
+        float o[4] = {};
+        if (!a.first) Elem<false>::unpack(old[v][j / 4], o);
+        for (int q = 0; q < 4; ++q) o[q] += sum[v][j + q];
+        store16(out + j, Elem<false>::pack(o));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (j < cols[v]) out[j] = a.first ? sum[v][j] : out[j] + sum[v][j];
+    }
+  }
+}
+
 EbLayout embed_layout(int64_t tokens, int64_t vocab, int64_t dim) {
   (void)vocab;
   EbLayout l{};
@@ -501,9 +655,11 @@ EbLayout embed_layout(int64_t tokens, int64_t vocab, int64_t dim) {
   l.key_b = take(4 * n);
   l.tok_b = take(4 * n);
   l.chunks = take(sizeof(EbChunk) * n);
-  // a row of at most EB_CHUNK tokens leaves no partial sums
-  l.partials = take(n > EB_CHUNK ? slots * (size_t)dim * 4 : 0);
-  l.arrive = take(n > EB_CHUNK ? slots * (((size_t)dim + 255) / 256) * 4 : 0);
+  // a row of at most EB_CHUNK tokens leaves no partial sums; a slot holds the
+  // columns up to whole column blocks, of either type's width
+  const size_t width = dim > 512 ? ((size_t)dim + 1023) / 1024 * 1024 : 512;
+  l.partials = take(n > EB_CHUNK ? slots * width * 4 : 0);
+  l.arrive = take(n > EB_CHUNK ? slots * (width / 256) * 4 : 0);
   l.total = at;
   return l;
 }
@@ -515,11 +671,19 @@ hipError_t add_launch(const EmbedBwdArgs &a, int passes, hipStream_t s) {
   constexpr int WAVE_COLS = 64 * Elem<BF16>::N;
   const bool wide = a.dim > WAVE_COLS;
   const int cols = WAVE_COLS * (wide ? 2 : 1), col_blocks = (int)((a.dim + cols - 1) / cols);
+  if (a.tokens <= EB_FEW && a.tokens * col_blocks <= (1 << 24)) {
+    const int zeros = a.first ? (int)std::min<int64_t>(a.vocab, 1 << EF_ZERO_SHIFT) : 0;
+    const unsigned grid = (unsigned)(zeros + a.tokens * col_blocks);
+    if (grid == 0) return hipSuccess;
+    if (wide) hipLaunchKernelGGL((ke_few<BF16, 2>), dim3(grid), dim3(256), 0, s, a, zeros);
+    else hipLaunchKernelGGL((ke_few<BF16, 1>), dim3(grid), dim3(256), 0, s, a, zeros);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(ke_sort, dim3(EB_BUCKETS + (a.first ? (unsigned)std::min<int64_t>(a.vocab, EB_BUCKETS) : 0)),
                      dim3(ES_THREADS), 0, s, a, passes, col_blocks);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.tokens == 0) return e;
-  const unsigned grid = (unsigned)std::min<int64_t>((a.tokens * col_blocks + 3) / 4, 2048);
+  const unsigned grid = (unsigned)std::max<int64_t>(col_blocks, std::min<int64_t>((a.tokens * col_blocks + 3) / 4, 2048));
   if (wide) hipLaunchKernelGGL((ke_add<BF16, 2>), dim3(grid), dim3(256), 0, s, a, col_blocks);
   else hipLaunchKernelGGL((ke_add<BF16, 1>), dim3(grid), dim3(256), 0, s, a, col_blocks);
   return hipGetLastError();

@@ -30,12 +30,16 @@ struct EmbedFwdArgs {
 hipError_t launch_embed_forward(const EmbedFwdArgs &a, bool bf16, hipStream_t s);
 
 constexpr int EB_BUCKETS = 256;  // bucket of a table row = row mod EB_BUCKETS
-constexpr int EB_CHUNK = 64;     // tokens that one workgroup adds up in a row
+constexpr int EB_CHUNK = 32;     // tokens of a row that one wave adds up, at most
+constexpr int EB_LIGHT = 2;      // a row of more tokens is added up before one of these
+constexpr int EB_FEW = 1024;     // up to so many tokens need no sort
 
 // What the sort leaves about one bucket.
 struct EbBucket {
   int32_t first;   // its tokens' first position in the sorted order
-  int32_t chunks;  // its work chunks, at chunk slots [first, first + chunks)
+  int32_t tokens;  // their count, and its chunk slots: [first, first + tokens)
+  int32_t heavy;   // chunks of rows with more than EB_LIGHT tokens, from the first slot on
+  int32_t light;   // the other chunks, from the last slot down
 };
 
 // At most EB_CHUNK consecutive sorted tokens of one table row.  A row with

@@ -105,6 +105,12 @@ __device__ __forceinline__ float exp_term(float x, float m) {
   return __builtin_amdgcn_exp2f(fmaf(d, kLog2e, d * kLog2eLow));
 }
 
+// A value that is the same in all lanes of a wave, moved to scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 __device__ __forceinline__ double shfl_f64(double v, int lane) {
   union {
     double d;

@@ -31,7 +31,7 @@ __global__ __launch_bounds__(256) void ke_lookup(EmbedFwdArgs a, int lanes) {
   typedef Elem<BF16> E;
   typedef typename E::type T;
   const int per = 256 / lanes;
-  const int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / lanes;
+  const int64_t t = a.token0 + (int64_t)blockIdx.x * per + threadIdx.x / lanes;
   if (t >= a.tokens) return;
   const int64_t id = index_at(a.ids, t);
   const bool has = id >= 0 && id < a.vocab;
@@ -57,14 +57,21 @@ __global__ __launch_bounds__(256) void ke_lookup(EmbedFwdArgs a, int lanes) {
 }
 
 hipError_t launch_embed_forward(const EmbedFwdArgs &a, bool bf16, hipStream_t s) {
-  if (a.tokens == 0) return hipSuccess;
   const int64_t vecs = (a.dim + (bf16 ? 7 : 3)) / (bf16 ? 8 : 4);
   int lanes = 1;
   while (lanes < 256 && lanes < vecs) lanes *= 2;
-  const int64_t per = 256 / lanes, grid = (a.tokens + per - 1) / per;
-  if (bf16) hipLaunchKernelGGL(ke_lookup<true>, dim3((unsigned)grid), dim3(256), 0, s, a, lanes);
-  else hipLaunchKernelGGL(ke_lookup<false>, dim3((unsigned)grid), dim3(256), 0, s, a, lanes);
-  return hipGetLastError();
+  const int64_t per = 256 / lanes;
+  // a grid holds fewer than 2^32 threads: more tokens take several launches
+  const int64_t most = ((int64_t)1 << 23) * per;
+  EmbedFwdArgs b = a;
+  for (b.token0 = 0; b.token0 < a.tokens; b.token0 += most) {
+    const dim3 grid((unsigned)((std::min(most, a.tokens - b.token0) + per - 1) / per));
+    if (bf16) hipLaunchKernelGGL(ke_lookup<true>, grid, dim3(256), 0, s, b, lanes);
+    else hipLaunchKernelGGL(ke_lookup<false>, grid, dim3(256), 0, s, b, lanes);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // ---------------------------------------------------- sorting the tokens
@@ -375,7 +382,7 @@ __global__ __launch_bounds__(256) void ke_add(EmbedBwdArgs a, int col_blocks) {
   if (wave >= waves) return;
   const int cb = (int)(wave % (uint32_t)col_blocks);
   for (uint64_t q = wave / (uint32_t)col_blocks; q < n_q; q += waves / (uint32_t)col_blocks) {
-    const EbBucket bk = bucket[q & (EB_BUCKETS - 1)];
+    const EbBucket bk = bucket[(q + 37 * (q >> EB_SHIFT)) & (EB_BUCKETS - 1)];
     const int at = (int)(q >> EB_SHIFT);
     if (at >= bk.heavy + bk.light) continue;
     const int slot = bk.first + (at < bk.heavy ? at : bk.tokens - 1 - (at - bk.heavy));
@@ -671,7 +678,7 @@ hipError_t add_launch(const EmbedBwdArgs &a, int passes, hipStream_t s) {
   constexpr int WAVE_COLS = 64 * Elem<BF16>::N;
   const bool wide = a.dim > WAVE_COLS;
   const int cols = WAVE_COLS * (wide ? 2 : 1), col_blocks = (int)((a.dim + cols - 1) / cols);
-  if (a.tokens <= EB_FEW && a.tokens * col_blocks <= (1 << 24)) {
+  if (a.tokens <= EB_FEW && a.tokens * col_blocks <= (1 << 23)) {
     const int zeros = a.first ? (int)std::min<int64_t>(a.vocab, 1 << EF_ZERO_SHIFT) : 0;
     const unsigned grid = (unsigned)(zeros + a.tokens * col_blocks);
     if (grid == 0) return hipSuccess;
@@ -683,7 +690,7 @@ hipError_t add_launch(const EmbedBwdArgs &a, int passes, hipStream_t s) {
                      dim3(ES_THREADS), 0, s, a, passes, col_blocks);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.tokens == 0) return e;
-  const unsigned grid = (unsigned)std::max<int64_t>(col_blocks, std::min<int64_t>((a.tokens * col_blocks + 3) / 4, 2048));
+  const unsigned grid = (unsigned)std::max<int64_t>(col_blocks, std::min<int64_t>((a.tokens * col_blocks + 7) / 8, 4096));
   if (wide) hipLaunchKernelGGL((ke_add<BF16, 2>), dim3(grid), dim3(256), 0, s, a, col_blocks);
   else hipLaunchKernelGGL((ke_add<BF16, 1>), dim3(grid), dim3(256), 0, s, a, col_blocks);
   return hipGetLastError();

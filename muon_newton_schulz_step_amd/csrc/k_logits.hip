@@ -65,30 +65,11 @@ __device__ __forceinline__ Online block_join(Online o, float *red) {
   return t;
 }
 
-}  // namespace
-
-// One workgroup a row: maximum, sum and the target's log-probability.  HBM-
-// bound.  grad (may be NULL) starts as that of a row without a gradient.
-template <bool BF16, int THREADS>
-__global__ __launch_bounds__(THREADS, 8) void kl_rows(LogitArgs a, RowStat *stat, RowGrad *grad, float *logp,
-                                                   float *lse) {
+// Maximum and sum of a row by a workgroup; every thread gets them.
+template <bool BF16, int THREADS, int UNROLL = 4>
+__device__ __forceinline__ Online row_online(const typename Elem<BF16>::type *x, int64_t vocab, float *red) {
   typedef Elem<BF16> E;
-  typedef typename E::type T;
-  __shared__ float red[2 * THREADS / 64];
-  const int64_t r = blockIdx.x;
-  const int64_t target = index_at(a.targets, r);
-  if (grad && threadIdx.x == 0) grad[r] = RowGrad{0.f, 0.f, 0.f, 0};
-  if (target < 0 || target >= a.vocab) {
-    if (threadIdx.x == 0) {
-      if (stat) stat[r] = RowStat{0.f, 0.f, 0.0, 0.0};
-      if (logp) logp[r] = 0.f;
-      if (lse) lse[r] = 0.f;
-    }
-    return;
-  }
-  const T *x = static_cast<const T *>(a.logits) + r * a.ld;
-  const Row<BF16> row(x, a.vocab);
-  constexpr int UNROLL = 4;
+  const Row<BF16> row(x, vocab);
   Online o;
   int i = threadIdx.x;
   for (; i + (UNROLL - 1) * THREADS < row.vecs; i += UNROLL * THREADS) {
@@ -100,22 +81,47 @@ __global__ __launch_bounds__(THREADS, 8) void kl_rows(LogitArgs a, RowStat *stat
       float v[2 * E::N];
       E::unpack(w[k], v);
       E::unpack(w[k + 1], v + E::N);
-      o.add<2 * E::N>(v);
+      o.template add<2 * E::N>(v);
     }
   }
   for (; i < row.vecs; i += THREADS) {
     float v[E::N];
     E::unpack(load16(x + row.col(i)), v);
-    o.add<E::N>(v);
+    o.template add<E::N>(v);
   }
   if ((int)threadIdx.x < row.singles()) {
     const float v = E::get(x[row.single(threadIdx.x)]);
-    o.add<1>(&v);
+    o.template add<1>(&v);
   }
-  o = block_join<THREADS / 64>(o, red);
+  return block_join<THREADS / 64>(o, red);
+}
+
+}  // namespace
+
+// One workgroup a row: maximum, sum and the target's log-probability.  HBM-
+// bound.  grad (may be NULL) starts as that of a row without a gradient.
+template <bool BF16, int THREADS, int UNROLL>
+__global__ __launch_bounds__(THREADS, UNROLL > 4 ? 4 : 8) void kl_rows(LogitArgs a, RowStat *stat, RowGrad *grad,
+                                                                       float *logp, float *lse) {
+  typedef Elem<BF16> E;
+  __shared__ float red[2 * THREADS / 64];
+  const int64_t r = a.row0 + blockIdx.x;
+  const int64_t target = index_at(a.targets, r);
+  if (grad && threadIdx.x == 0) grad[r] = RowGrad{0.f, 0.f, 0.f, 0};
+  if (target < 0 || target >= a.vocab) {
+    if (threadIdx.x == 0) {
+      if (stat) stat[r] = RowStat{0.f, 0.f, 0.0, 0.0};
+      if (logp) logp[r] = 0.f;
+      if (lse) lse[r] = 0.f;
+    }
+    return;
+  }
+  const typename E::type *x = static_cast<const typename E::type *>(a.logits) + r * a.ld;
+  const float at_target = E::get(x[target]);
+  const Online o = row_online<BF16, THREADS, UNROLL>(x, a.vocab, red);
   if (threadIdx.x == 0) {
     const double log_total = log((double)o.s);
-    const double lp = (double)E::get(x[target]) - (double)o.m - log_total;
+    const double lp = (double)at_target - (double)o.m - log_total;
     if (stat) stat[r] = RowStat{o.m, o.s, lp, expm1(lp)};
     if (logp) logp[r] = (float)lp;
     if (lse) lse[r] = (float)((double)o.m + log_total);
@@ -127,6 +133,8 @@ namespace {
 // Vectors of a row that a thread of the policy kernel keeps: the first ones in
 // LDS (64 KB a workgroup of 1024, two of them on a CU), the others in registers.
 constexpr int KEEP_LDS = 4, KEEP_REGS = 2, KEEP = KEEP_LDS + KEEP_REGS;
+// Rows whose terms one workgroup adds up.
+constexpr int64_t SUM_ROWS = 16384;
 // Loads of the rest under way at a time.
 constexpr int AHEAD = 2;
 
@@ -161,7 +169,7 @@ __global__ __launch_bounds__(THREADS, 8) void kl_policy(LogitArgs a, PolicyArgs 
   __shared__ float red[2 * THREADS / 64];
   __shared__ float coef[2];
   __shared__ uint4 held[KEEP_LDS][THREADS];
-  const int64_t r = blockIdx.x;
+  const int64_t r = a.row0 + blockIdx.x;
   const int tid = threadIdx.x;
   const int64_t target = index_at(a.targets, r);
   const float w = p.weights[r];
@@ -170,7 +178,7 @@ __global__ __launch_bounds__(THREADS, 8) void kl_policy(LogitArgs a, PolicyArgs 
     const Row<BF16> out(d, a.vocab);
     for (int i = tid; i < out.vecs; i += THREADS) stream16(d + out.col(i), make_uint4(0, 0, 0, 0));
     if (tid < out.singles()) d[out.single(tid)] = T(0);
-    if (tid < 4) terms[4 * r + tid] = 0.0;
+    if (tid < 4) terms[tid * a.rows + r] = 0.0;
     if (tid == 0) p.logp[r] = 0.f;
     return;
   }
@@ -185,6 +193,11 @@ __global__ __launch_bounds__(THREADS, 8) void kl_policy(LogitArgs a, PolicyArgs 
   const bool lone = tid < row.singles();
   const float single = lone ? E::get(x[row.single(tid)]) : -INFINITY;
   const float at_target = E::get(x[target]);
+  // lane 0: for the ratio, lane 1: for the KL term
+  float other = 0.f;
+  if (tid == 0 && p.old_logp) other = p.old_logp[r];
+  if (tid == 1 && p.ref_logp) other = p.ref_logp[r];
+  const float advantage = p.advantages[r];
   Online o;
 #pragma unroll
   for (int k = 0; k < KEEP; ++k) {
@@ -218,13 +231,13 @@ __global__ __launch_bounds__(THREADS, 8) void kl_policy(LogitArgs a, PolicyArgs 
     const double logp = (double)at_target - (double)o.m - log((double)o.s);
     // lane 0: the ratio, lane 1: the KL term, lane 2: the target's own share
     double arg = 0.0;
-    if (tid == 0 && p.old_logp) arg = logp - (double)p.old_logp[r];
-    if (tid == 1 && p.ref_logp) arg = (double)p.ref_logp[r] - logp;
+    if (tid == 0 && p.old_logp) arg = logp - (double)other;
+    if (tid == 1 && p.ref_logp) arg = (double)other - logp;
     if (tid == 2) arg = logp;
     const double em1 = expm1(arg);
     const double ratio = 1.0 + shfl_f64(em1, 0), ed = shfl_f64(em1, 1), share = shfl_f64(em1, 2);
     const double kl = ed - shfl_f64(arg, 1);
-    const double adv = p.advantages[r];
+    const double adv = advantage;
     const double clipped = fmin(fmax(ratio, 1.0 - p.clip_low), 1.0 + p.clip_high);
     const bool active = !(ratio * adv > clipped * adv);  // a NaN stays one
     const double pg = active ? -ratio * adv : -clipped * adv;
@@ -233,10 +246,10 @@ __global__ __launch_bounds__(THREADS, 8) void kl_policy(LogitArgs a, PolicyArgs 
       coef[0] = (float)(-dlogp / (double)o.s);
       coef[1] = (float)(-dlogp * share);
       p.logp[r] = (float)logp;
-      terms[4 * r] = (double)w * (pg + p.kl_coef * kl);
-      terms[4 * r + 1] = (double)w * pg;
-      terms[4 * r + 2] = (double)w * kl;
-      terms[4 * r + 3] = active ? 0.0 : (double)w;
+      terms[r] = (double)w * (pg + p.kl_coef * kl);
+      terms[a.rows + r] = (double)w * pg;
+      terms[2 * a.rows + r] = (double)w * kl;
+      terms[3 * a.rows + r] = active ? 0.0 : (double)w;
     }
   }
   __syncthreads();
@@ -274,24 +287,69 @@ __global__ __launch_bounds__(THREADS, 8) void kl_policy(LogitArgs a, PolicyArgs 
   if (in_vec ? at / E::N % THREADS == tid : lone && row.single(tid) == (uint32_t)target) d[target] = E::put(dt);
 }
 
-// The four sums over the rows, in a fixed order.
-__global__ __launch_bounds__(1024) void kl_policy_sum(const double *terms, int64_t rows, float *stats) {
+// The four sums over the rows, in a fixed order, SUM_ROWS rows a workgroup and
+// four of its waves a sum; into stats if there is one workgroup, otherwise
+// into part, the next launch's terms.
+__global__ __launch_bounds__(1024) void kl_policy_sum(const double *terms, int64_t rows, double *part, float *stats) {
   __shared__ double red[16];
-  double sum[4] = {};
-  for (int64_t r = threadIdx.x; r < rows; r += 1024) {
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, kind = w & 3;
+  const int64_t r0 = (int64_t)blockIdx.x * SUM_ROWS, r1 = min(r0 + SUM_ROWS, rows);
+  double sum = 0.0;
+#pragma unroll 8
+  for (int64_t r = r0 + (w >> 2) * 64 + lane; r < r1; r += 256) sum += terms[kind * rows + r];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) sum[k] += terms[4 * r + k];
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const double t = block_sum<16>(sum[k], red);
-    if (threadIdx.x == 0) stats[k] = (float)t;
+  for (int d = 32; d > 0; d >>= 1) sum += shfl_xor_f64(sum, d);
+  if (lane == 0) red[w] = sum;
+  __syncthreads();
+  if (threadIdx.x < 4) {
+    sum = red[threadIdx.x] + red[threadIdx.x + 4] + red[threadIdx.x + 8] + red[threadIdx.x + 12];
+    if (stats) stats[threadIdx.x] = (float)sum;
+    else part[threadIdx.x * gridDim.x + blockIdx.x] = sum;
   }
 }
 
+// ------------------------------------------------------- preference loss
+//
+//   gain = sum logp - ref, m = beta (gain_chosen - gain_rejected)
+//   loss = -(1 - s) log sigmoid(m) - s log sigmoid(-m)
+//   d loss / d logp = +- beta (sigmoid(m) - (1 - s)) / pairs
+//
+// A row's gradient needs its whole pair's log-probabilities, so its logits
+// are read twice.  Logits that the memory-side cache (256 MB) holds are walked
+// by three launches: the rows' sums (kl_rows), the pairs (kl_pairs), the
+// gradient (kl_grad).  Larger ones are walked pair by pair in one launch
+// (kp_loss, after kp_plan), the gradient following the sums at a distance of
+// the longest pair and some rows more, so that it finds them in that cache.
+
 namespace {
 
-// Sequence bounds as the kernels use them: whatever the offsets hold, rows
+// A pair's loss, rewards and the coefficient of its chosen rows.
+__device__ __forceinline__ double pair_loss(const PreferenceArgs &p, int64_t i, double chosen, double rejected,
+                                            bool write, double *loss) {
+  const double gain[2] = {chosen - (double)p.ref_logp[i], rejected - (double)p.ref_logp[i + p.pairs]};
+  const double m = p.beta * (gain[0] - gain[1]);
+  const double q = exp(-fabs(m));
+  const double sig = (m >= 0.0 ? 1.0 : q) / (1.0 + q);
+  if (write) {
+    p.rewards[i] = (float)(p.beta * gain[0]);
+    p.rewards[i + p.pairs] = (float)(p.beta * gain[1]);
+    // softplus(-m) and softplus(m) without overflow
+    const double l = log1p(q);
+    put_shared(loss, (1.0 - p.smoothing) * (fmax(-m, 0.0) + l) + p.smoothing * (fmax(m, 0.0) + l));
+  }
+  return p.beta * (sig - (1.0 - p.smoothing)) / (double)p.pairs;
+}
+
+// The mean of the pairs' losses, in a fixed order.
+template <int THREADS>
+__device__ __forceinline__ void mean_loss(const PreferenceArgs &p, const double *losses, double *red) {
+  double t = 0.0;
+  for (int64_t i = threadIdx.x; i < p.pairs; i += THREADS) t += get_shared(&losses[i]);
+  t = block_sum<THREADS / 64>(t, red);
+  if (threadIdx.x == 0) *p.loss = (float)(t / (double)p.pairs);
+}
+
+// Sequence bounds as kl_pairs uses them: whatever the offsets hold, rows
 // outside [0, rows) are never touched.
 __device__ __forceinline__ void sequence(const IndexVec &off, int64_t s, int64_t rows, int64_t *lo, int64_t *hi) {
   *lo = min(max(index_at(off, s), (int64_t)0), rows);
@@ -302,35 +360,24 @@ __device__ __forceinline__ void sequence(const IndexVec &off, int64_t s, int64_t
 
 // Sum of the log-probabilities of each sequence, and from them the pair's
 // loss and its rows' gradient coefficients; one workgroup a pair, half of it
-// a sequence:
-//   gain = sum logp - ref, m = beta (gain_chosen - gain_rejected)
-//   loss = -(1 - s) log sigmoid(m) - s log sigmoid(-m)
-//   d loss / d logp = +- beta (sigmoid(m) - (1 - s)) / pairs
-// Bound by the latency of its few dependent loads.
+// a sequence.  Bound by the latency of its few dependent loads.
 __global__ __launch_bounds__(1024) void kl_pairs(LogitArgs a, PreferenceArgs p, const RowStat *stat, RowGrad *grad,
                                                  double *losses) {
   __shared__ double red[16];
   const int64_t i = blockIdx.x;
   const int side = threadIdx.x >> 9, tid = threadIdx.x & 511;
-  const int64_t s = i + side * p.pairs;
   int64_t lo, hi;
-  sequence(p.offsets, s, a.rows, &lo, &hi);
-  const double ref[2] = {(double)p.ref_logp[i], (double)p.ref_logp[i + p.pairs]};
+  sequence(p.offsets, i + side * p.pairs, a.rows, &lo, &hi);
   double t = 0.0;
   for (int64_t r = lo + tid; r < hi; r += 512) t += stat[r].logp;
 #pragma unroll
   for (int k = 32; k > 0; k >>= 1) t += shfl_xor_f64(t, k);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = t;
   __syncthreads();
-  double gain[2] = {};
+  double sum[2] = {};
 #pragma unroll
-  for (int w = 0; w < 16; ++w) gain[w >> 3] += red[w];
-  gain[0] -= ref[0];
-  gain[1] -= ref[1];
-  const double m = p.beta * (gain[0] - gain[1]);
-  const double q = exp(-fabs(m));
-  const double sig = (m >= 0.0 ? 1.0 : q) / (1.0 + q);
-  const double chosen = p.beta * (sig - (1.0 - p.smoothing)) / (double)p.pairs;
+  for (int w = 0; w < 16; ++w) sum[w >> 3] += red[w];
+  const double chosen = pair_loss(p, i, sum[0], sum[1], threadIdx.x == 0, &losses[i]);
   const double d = side ? -chosen : chosen;
   for (int64_t r = lo + tid; r < hi; r += 512) {
     const int64_t target = index_at(a.targets, r);
@@ -338,21 +385,6 @@ __global__ __launch_bounds__(1024) void kl_pairs(LogitArgs a, PreferenceArgs p, 
     const RowStat st = stat[r];
     grad[r] = RowGrad{st.max, (float)(-d / (double)st.total), (float)(-d * st.share), d != 0.0};
   }
-  if (tid == 0) p.rewards[s] = (float)(p.beta * (side ? gain[1] : gain[0]));
-  if (threadIdx.x == 0) {
-    // softplus(-m) and softplus(m) without overflow
-    const double l = log1p(q);
-    losses[i] = (1.0 - p.smoothing) * (fmax(-m, 0.0) + l) + p.smoothing * (fmax(m, 0.0) + l);
-  }
-}
-
-// The mean of the pairs' losses, by one workgroup of the gradient kernel.
-__device__ __forceinline__ void mean_loss(const double *losses, int64_t pairs, float *loss) {
-  __shared__ double red[4];
-  double t = 0.0;
-  for (int64_t i = threadIdx.x; i < pairs; i += 256) t += losses[i];
-  t = block_sum<4>(t, red);
-  if (threadIdx.x == 0) *loss = (float)(t / (double)pairs);
 }
 
 // The gradient of the logits, element by element; a row without one gets
@@ -360,10 +392,11 @@ __device__ __forceinline__ void mean_loss(const double *losses, int64_t pairs, f
 // last ones that the row sums read are still in the memory-side cache.
 template <bool BF16>
 __global__ __launch_bounds__(256) void kl_grad(LogitArgs a, const RowGrad *grad, void *dlogits, int64_t dld,
-                                               int pieces, const double *losses, int64_t pairs, float *loss) {
+                                               int pieces, PreferenceArgs p, const double *losses) {
   typedef Elem<BF16> E;
   typedef typename E::type T;
-  if (blockIdx.x == 0) mean_loss(losses, pairs, loss);
+  __shared__ double red[4];
+  if (blockIdx.x == 0) mean_loss<256>(p, losses, red);
   if (a.rows == 0) return;
   const int64_t r = a.rows - 1 - blockIdx.x / pieces;
   const int piece = blockIdx.x % pieces;
@@ -397,48 +430,306 @@ __global__ __launch_bounds__(256) void kl_grad(LogitArgs a, const RowGrad *grad,
   }
 }
 
-// ------------------------------------------------------------- launchers
+// One workgroup: the sequences' bounds and the pairs' places in the order of
+// the walk, the counters, and whatever belongs to pairs without a row.
+__global__ __launch_bounds__(1024) void kp_plan(LogitArgs a, PreferenceArgs p, PreferenceWork w, int slack) {
+  __shared__ int wtop[16];
+  __shared__ double red[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // bounds: clamped into the rows and, whatever the offsets hold, never
+  // decreasing, so that every row belongs to one sequence at most
+  int carry = 0;
+  for (int64_t j0 = 0; j0 <= 2 * p.pairs; j0 += 1024) {
+    const int64_t j = j0 + tid;
+    int v = j <= 2 * p.pairs ? (int)min(max(index_at(p.offsets, j), (int64_t)0), a.rows) : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int u = __shfl_up(v, d);
+      if (lane >= d) v = max(v, u);
+    }
+    if (lane == 63) wtop[wave] = v;
+    __syncthreads();
+    int all = carry;
+    for (int i = 0; i < 16; ++i) {
+      if (i == wave) v = max(v, all);
+      all = max(all, wtop[i]);
+    }
+    if (j <= 2 * p.pairs) w.bounds[j] = v;
+    carry = all;
+    __syncthreads();
+  }
+  int sum = 0, most = 0, none = 0;
+  for (int64_t i0 = 0; i0 < p.pairs; i0 += 1024) {
+    const int64_t i = i0 + tid;
+    int n = 0;
+    if (i < p.pairs) {
+      n = w.bounds[i + 1] - w.bounds[i] + w.bounds[i + p.pairs + 1] - w.bounds[i + p.pairs];
+      w.done[i] = w.ready[i] = 0;
+      if (n == 0) {
+        pair_loss(p, i, 0.0, 0.0, true, &w.losses[i]);
+        ++none;
+      }
+      most = max(most, n);
+    }
+    int x = n;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int u = __shfl_up(x, d);
+      if (lane >= d) x += u;
+    }
+    if (lane == 63) wtop[wave] = x;
+    __syncthreads();
+    int base = sum;
+    for (int k = 0; k < 16; ++k) {
+      if (k == wave) x += base;
+      base += wtop[k];
+    }
+    if (i < p.pairs) w.starts[i] = x - n;
+    sum = base;
+    __syncthreads();
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) most = max(most, __shfl_xor(most, d));
+  if (lane == 0) wtop[wave] = most;
+  const int empty = (int)block_sum<16>((double)none, red);
+  if (tid == 0) {
+    for (int i = 0; i < 16; ++i) most = max(most, wtop[i]);
+    w.starts[p.pairs] = sum;
+    w.walk->ticket = 0;
+    w.walk->pairs_done = empty;
+    w.walk->rows = sum;
+    w.walk->lag = (int)min((int64_t)sum, (int64_t)most + slack);
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (empty == p.pairs) mean_loss<1024>(p, w.losses, red);
+}
 
 namespace {
 
-hipError_t rows_launch(const LogitArgs &a, bool bf16, RowStat *stat, RowGrad *grad, float *logp, float *lse,
-                       hipStream_t s) {
-  const dim3 g((unsigned)a.rows);
-  // 256 threads where 512 would have fewer than two rounds of loads: 20000 x
-  // 4096 bf16 take 35 us instead of 56, 4000 x 1000 7 instead of 11; from
-  // there on 512 are as fast or faster (100 x 50257 fp32 6.7 against 8.3)
-  const bool small = a.vocab <= 4096 * (bf16 ? 2 : 1);
-  if (bf16 && small) hipLaunchKernelGGL((kl_rows<true, 256>), g, dim3(256), 0, s, a, stat, grad, logp, lse);
-  else if (bf16) hipLaunchKernelGGL((kl_rows<true, 512>), g, dim3(512), 0, s, a, stat, grad, logp, lse);
-  else if (small) hipLaunchKernelGGL((kl_rows<false, 256>), g, dim3(256), 0, s, a, stat, grad, logp, lse);
-  else hipLaunchKernelGGL((kl_rows<false, 512>), g, dim3(512), 0, s, a, stat, grad, logp, lse);
-  return hipGetLastError();
+struct Place {
+  int64_t row, pair;  // pair -1: a row of no sequence
+};
+
+// The at-th row of the walk: the pairs' rows, then those of no sequence.
+__device__ __forceinline__ Place place(const PreferenceArgs &p, const PreferenceWork &w, int64_t n, int64_t at) {
+  if (at >= n) {
+    const int64_t lead = w.bounds[0];
+    return {uniform(at - n < lead ? at - n : w.bounds[2 * p.pairs] + (at - n - lead)), -1};
+  }
+  // the last pair that starts at or before this place, 64 probes at a time
+  int64_t lo = 0, hi = p.pairs;
+  while (hi - lo > 1) {
+    const int64_t step = (hi - lo + 63) / 64, probe = lo + (threadIdx.x & 63) * step;
+    const int c = __popcll(__ballot(probe < hi && w.starts[min(probe, p.pairs)] <= at));
+    lo += (c - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  const int64_t pair = uniform(lo);
+  const int64_t off = at - w.starts[pair], len = w.bounds[pair + 1] - w.bounds[pair];
+  return {uniform(off < len ? w.bounds[pair] + off : w.bounds[pair + p.pairs] + (off - len)), pair};
 }
+
+}  // namespace
+
+// A workgroup takes a ticket t and does the sum of the walk's t-th row, then
+// the gradient of the row `lag` places before it.  What a gradient waits for
+// are sums of earlier tickets, and a sum waits for nothing, so every wait
+// ends.  The grid has 2 rows' workgroups, as the host does not know the lag;
+// those too many, spread over the grid, end at once.
+//
+// The tickets come from one address, 18 ns apart: 12500 rows take 230 us of
+// them, beside the rows' own 400.
+template <bool BF16>
+__global__ __launch_bounds__(PREF_THREADS, 8) void kp_loss(LogitArgs a, PreferenceArgs p, PreferenceWork w,
+                                                           void *dlogits, int64_t dld) {
+  typedef Elem<BF16> E;
+  typedef typename E::type T;
+  constexpr int THREADS = PREF_THREADS, AHEAD = 4;
+  __shared__ float red[2 * THREADS / 64];
+  __shared__ double red64[THREADS / 64];
+  __shared__ uint64_t unit;
+  __shared__ int last;
+  __shared__ struct {
+    float max, c, dt;
+    int live;
+  } grad;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int64_t n = uniform(w.walk->rows), lag = uniform(w.walk->lag);
+  const uint64_t units = (uint64_t)(a.rows + lag), groups = 2 * (uint64_t)a.rows, group = (uint64_t)a.row0 + blockIdx.x;
+  if (group * units / groups == (group + 1) * units / groups) return;
+  if (tid == 0) unit = atomicAdd((unsigned long long *)&w.walk->ticket, 1ull);
+  __syncthreads();
+  const int64_t t = uniform((int64_t)unit);
+  if (t < n) {
+    const Place at = place(p, w, n, t);
+    const int64_t r = at.row, pair = at.pair;
+    const int64_t target = uniform(index_at(a.targets, r));
+    double logp = 0.0, share = 0.0;
+    Online o;
+    if (target >= 0 && target < a.vocab) {
+      const T *x = static_cast<const T *>(a.logits) + r * a.ld;
+      const float at_target = E::get(x[target]);
+      o = row_online<BF16, THREADS>(x, a.vocab, red);
+      if (tid == 0) {
+        logp = (double)at_target - (double)o.m - log((double)o.s);
+        share = expm1(logp);
+      }
+    }
+    if (tid == 0) {
+      RowStat *st = w.stat + r;
+      put_shared(&st->max, o.m);
+      put_shared(&st->total, o.s);
+      put_shared(&st->logp, logp);
+      put_shared(&st->share, share);
+      last = arrive(&w.done[pair]) == (int)(w.starts[pair + 1] - w.starts[pair]) - 1;
+    }
+    __syncthreads();
+    if (last) {
+      // the pair's sums, half of the workgroup a sequence
+      const int64_t s = pair + tid / (THREADS / 2) * p.pairs;
+      double sum = 0.0;
+      for (int64_t i = w.bounds[s] + tid % (THREADS / 2); i < w.bounds[s + 1]; i += THREADS / 2)
+        sum += get_shared(&w.stat[i].logp);
+#pragma unroll
+      for (int k = 32; k > 0; k >>= 1) sum += shfl_xor_f64(sum, k);
+      if (lane == 0) red64[tid >> 6] = sum;
+      __syncthreads();
+      if (tid == 0) {
+        double of[2] = {};
+#pragma unroll
+        for (int i = 0; i < THREADS / 64; ++i) of[i / (THREADS / 128)] += red64[i];
+        put_shared(&w.coef[pair], pair_loss(p, pair, of[0], of[1], true, &w.losses[pair]));
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        put_shared(&w.ready[pair], 1);
+        last = arrive(&w.walk->pairs_done) == (int)p.pairs - 1;
+      }
+      __syncthreads();
+      if (last) mean_loss<THREADS>(p, w.losses, red64);
+    }
+  }
+  if (t < lag) return;
+  const Place at = place(p, w, n, t - lag);
+  const int64_t r = at.row, pair = at.pair;
+  const int64_t target = uniform(index_at(a.targets, r));
+  const bool live = pair >= 0 && target >= 0 && target < a.vocab;
+  const T *x = static_cast<const T *>(a.logits) + r * a.ld;
+  T *d = static_cast<T *>(dlogits) + r * dld;
+  const Row<BF16> row(live ? x : d, a.vocab);
+  uint4 in[AHEAD];
+  if (live) {  // the first loads are under way while thread 0 waits for the pair
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      in[k] = E::none();
+      if (tid + k * THREADS < row.vecs) in[k] = load16(x + row.col(tid + k * THREADS));
+    }
+    if (tid == 0) {
+      while (get_shared(&w.ready[pair]) == 0) __builtin_amdgcn_s_sleep(2);
+      asm volatile("" ::: "memory");
+      const RowStat *st = w.stat + r;
+      const double coef = get_shared(&w.coef[pair]), total = (double)get_shared(&st->total), share = get_shared(&st->share);
+      const double dl = r >= w.bounds[pair] && r < w.bounds[pair + 1] ? coef : -coef;
+      grad.max = get_shared(&st->max);
+      grad.c = (float)(-dl / total);
+      grad.dt = (float)(-dl * share);
+      grad.live = dl != 0.0;
+    }
+  }
+  __syncthreads();
+  if (!live || !grad.live) {
+    for (int i = tid; i < row.vecs; i += THREADS) stream16(d + row.col(i), make_uint4(0, 0, 0, 0));
+    if (tid < row.singles()) d[row.single(tid)] = T(0);
+    return;
+  }
+  const float c = grad.c, dt = grad.dt, m = grad.max;
+  const int rel = (int)target - row.head;  // the target's place among the vectors
+  auto put = [&](uint4 v4, int i) {
+    float v[E::N];
+    E::unpack(v4, v);
+#pragma unroll
+    for (int k = 0; k < E::N; ++k) v[k] = c * exp_shift(v[k], m);
+    const int k0 = rel - i * E::N;
+    if (k0 >= 0 && k0 < E::N) {
+#pragma unroll
+      for (int k = 0; k < E::N; ++k) v[k] = k == k0 ? dt : v[k];
+    }
+    stream16(d + row.col(i), E::pack(v));
+  };
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k)
+    if (tid + k * THREADS < row.vecs) put(in[k], tid + k * THREADS);
+  int i = tid + AHEAD * THREADS;
+  for (; i + (AHEAD - 1) * THREADS < row.vecs; i += AHEAD * THREADS) {
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) in[k] = load16(x + row.col(i + k * THREADS));
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) put(in[k], i + k * THREADS);
+  }
+  for (; i < row.vecs; i += THREADS) put(load16(x + row.col(i)), i);
+  if (tid < row.singles()) {
+    const int j = row.single(tid);
+    d[j] = E::put(j == target ? dt : c * exp_shift(E::get(x[j]), m));
+  }
+}
+
+// ------------------------------------------------------------- launchers
+
+namespace {
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 }  // namespace
 
+namespace {
+
+// A grid holds fewer than 2^32 threads: more rows take several launches.
+constexpr int64_t ROWS_A_LAUNCH = (int64_t)1 << 21;
+template <class F>
+hipError_t by_rows(LogitArgs a, int64_t rows, F launch) {
+  for (a.row0 = 0; a.row0 < rows; a.row0 += ROWS_A_LAUNCH) {
+    launch(a, dim3((unsigned)std::min(ROWS_A_LAUNCH, rows - a.row0)));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// 256 threads where 512 would have fewer than two rounds of loads: 20000 x
+// 4096 bf16 take 35 us instead of 56, 4000 x 1000 7 instead of 11; from there
+// on 512 are as fast or faster (100 x 50257 fp32 6.7 against 8.3).  Where
+// every row can have a CU to itself, 1024 and eight loads under way.
+template <bool BF16>
+hipError_t rows_launch(const LogitArgs &a, RowStat *stat, RowGrad *grad, float *logp, float *lse, hipStream_t s) {
+  return by_rows(a, a.rows, [&](const LogitArgs &a, dim3 g) {
+    if (a.vocab <= 1024 * Elem<BF16>::N) hipLaunchKernelGGL((kl_rows<BF16, 256, 4>), g, dim3(256), 0, s, a, stat, grad, logp, lse);
+    else if (a.rows <= 256 && a.vocab >= 8192 * Elem<BF16>::N) hipLaunchKernelGGL((kl_rows<BF16, 1024, 8>), g, dim3(1024), 0, s, a, stat, grad, logp, lse);
+    else hipLaunchKernelGGL((kl_rows<BF16, 512, 4>), g, dim3(512), 0, s, a, stat, grad, logp, lse);
+  });
+}
+
+}  // namespace
+
 hipError_t launch_token_logprob(const LogitArgs &a, bool bf16, float *logp, float *lse, hipStream_t s) {
-  if (a.rows == 0) return hipSuccess;
-  return rows_launch(a, bf16, nullptr, nullptr, logp, lse, s);
+  return bf16 ? rows_launch<true>(a, nullptr, nullptr, logp, lse, s) : rows_launch<false>(a, nullptr, nullptr, logp, lse, s);
 }
 
 PolicyLayout policy_layout(int64_t rows) {
   PolicyLayout l{};
+  const size_t n = (size_t)std::max<int64_t>(rows, 1), groups = (n + SUM_ROWS - 1) / SUM_ROWS;
   l.terms = 0;
-  l.total = up256(4 * sizeof(double) * (size_t)std::max<int64_t>(rows, 1));
+  l.part = up256(4 * sizeof(double) * n);
+  l.total = l.part + 2 * up256(4 * sizeof(double) * groups);
   return l;
 }
 
 namespace {
 
 template <bool BF16>
-void policy_launch(const LogitArgs &a, const PolicyArgs &p, void *dlogits, int64_t dld, double *terms, hipStream_t s) {
-  const dim3 g((unsigned)a.rows);
-  const int64_t vecs = a.vocab / Elem<BF16>::N;
-  if (vecs <= 256 * KEEP) hipLaunchKernelGGL((kl_policy<BF16, 256>), g, dim3(256), 0, s, a, p, dlogits, dld, terms);
-  else hipLaunchKernelGGL((kl_policy<BF16, 1024>), g, dim3(1024), 0, s, a, p, dlogits, dld, terms);
+hipError_t policy_launch(const LogitArgs &a, const PolicyArgs &p, void *dlogits, int64_t dld, double *terms, hipStream_t s) {
+  return by_rows(a, a.rows, [&](const LogitArgs &a, dim3 g) {
+    if (a.vocab / Elem<BF16>::N <= 256 * KEEP) hipLaunchKernelGGL((kl_policy<BF16, 256>), g, dim3(256), 0, s, a, p, dlogits, dld, terms);
+    else hipLaunchKernelGGL((kl_policy<BF16, 1024>), g, dim3(1024), 0, s, a, p, dlogits, dld, terms);
+  });
 }
 
 }  // namespace
@@ -447,43 +738,88 @@ hipError_t launch_policy(const LogitArgs &a, const PolicyArgs &p, bool bf16, voi
                          hipStream_t s) {
   const PolicyLayout l = policy_layout(a.rows);
   double *terms = reinterpret_cast<double *>(ws + l.terms);
-  if (a.rows > 0) {
-    if (bf16) policy_launch<true>(a, p, dlogits, dld, terms, s);
-    else policy_launch<false>(a, p, dlogits, dld, terms, s);
+  const hipError_t e = bf16 ? policy_launch<true>(a, p, dlogits, dld, terms, s) : policy_launch<false>(a, p, dlogits, dld, terms, s);
+  if (e != hipSuccess) return e;
+  double *part = reinterpret_cast<double *>(ws + l.part);
+  for (int64_t n = a.rows;;) {
+    const int64_t groups = std::max<int64_t>(1, (n + SUM_ROWS - 1) / SUM_ROWS);
+    hipLaunchKernelGGL(kl_policy_sum, dim3((unsigned)groups), dim3(1024), 0, s, terms, n, part, groups == 1 ? p.stats : nullptr);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || groups == 1) return e;
+    n = groups;
+    terms = part;
+    part += up256(4 * sizeof(double) * (size_t)groups) / sizeof(double);
   }
-  hipLaunchKernelGGL(kl_policy_sum, dim3(1), dim3(1024), 0, s, terms, a.rows, p.stats);
-  return hipGetLastError();
 }
 
 PreferenceLayout preference_layout(int64_t rows, int64_t pairs) {
   PreferenceLayout l{};
-  l.stat = 0;
-  l.grad = up256(sizeof(RowStat) * (size_t)rows);
-  l.losses = l.grad + up256(sizeof(RowGrad) * (size_t)rows);
-  l.total = l.losses + up256(sizeof(double) * (size_t)pairs);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t p = at;
+    at += up256(bytes);
+    return p;
+  };
+  l.walk = take(sizeof(PreferenceWalk));
+  l.stat = take(sizeof(RowStat) * (size_t)rows);
+  l.grad = take(sizeof(RowGrad) * (size_t)rows);
+  l.losses = take(sizeof(double) * (size_t)pairs);
+  l.coef = take(sizeof(double) * (size_t)pairs);
+  l.bounds = take(sizeof(int32_t) * (2 * (size_t)pairs + 1));
+  l.starts = take(sizeof(int32_t) * ((size_t)pairs + 1));
+  l.done = take(sizeof(int32_t) * (size_t)pairs);
+  l.ready = take(sizeof(int32_t) * (size_t)pairs);
+  l.total = at;
   return l;
 }
 
+namespace {
+
+template <bool BF16>
+hipError_t preference_launch(const LogitArgs &a, const PreferenceArgs &p, void *dlogits, int64_t dld, char *ws,
+                             hipStream_t s) {
+  const PreferenceLayout l = preference_layout(a.rows, p.pairs);
+  PreferenceWork w{};
+  w.walk = reinterpret_cast<PreferenceWalk *>(ws + l.walk);
+  w.stat = reinterpret_cast<RowStat *>(ws + l.stat);
+  w.losses = reinterpret_cast<double *>(ws + l.losses);
+  w.coef = reinterpret_cast<double *>(ws + l.coef);
+  w.bounds = reinterpret_cast<int32_t *>(ws + l.bounds);
+  w.starts = reinterpret_cast<int32_t *>(ws + l.starts);
+  w.done = reinterpret_cast<int32_t *>(ws + l.done);
+  w.ready = reinterpret_cast<int32_t *>(ws + l.ready);
+  RowGrad *grad = reinterpret_cast<RowGrad *>(ws + l.grad);
+  hipError_t e;
+  // One walk where the memory-side cache does not hold the logits but does hold
+  // what lies between a sum and its gradient: a pair and the 1024 rows under
+  // way.  In us, walk and three launches, pairs of 768 rows of 50257 bf16:
+  // 5 (195 MB) 149 144, 6 (232 MB) 196 196, 8 (309 MB) 268 297, 16 457 545; 2400
+  // rows of 32000 fp32 (24 pairs, 307 MB) 217 247; 1600 rows of 131072 bf16 (16
+  // pairs, 420 MB, 1124 rows of which are 295 MB) 386 356.
+  const int64_t row = a.vocab * (int64_t)sizeof(typename Elem<BF16>::type);
+  const bool walk = a.rows * row > (256 << 20) && (a.rows / p.pairs + 1024) * row <= (224 << 20);
+  if (walk || a.rows > ROWS_A_LAUNCH || (a.rows > 0 && p.pairs > ROWS_A_LAUNCH)) {
+    hipLaunchKernelGGL(kp_plan, dim3(1), dim3(1024), 0, s, a, p, w, PREF_SLACK);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    return by_rows(a, 2 * a.rows, [&](const LogitArgs &a, dim3 g) {
+      hipLaunchKernelGGL(kp_loss<BF16>, g, dim3(PREF_THREADS), 0, s, a, p, w, dlogits, dld);
+    });
+  }
+  if ((e = rows_launch<BF16>(a, w.stat, grad, nullptr, nullptr, s)) != hipSuccess) return e;
+  hipLaunchKernelGGL(kl_pairs, dim3((unsigned)p.pairs), dim3(1024), 0, s, a, p, w.stat, grad, w.losses);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  // pieces of a row: 8192 elements or more
+  const int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(a.vocab / 8192, 64));
+  hipLaunchKernelGGL(kl_grad<BF16>, dim3((unsigned)std::max<int64_t>(1, a.rows * pieces)), dim3(256), 0, s, a, grad, dlogits, dld,
+                     (int)pieces, p, w.losses);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_preference(const LogitArgs &a, const PreferenceArgs &p, bool bf16, void *dlogits, int64_t dld,
                              char *ws, hipStream_t s) {
-  const PreferenceLayout l = preference_layout(a.rows, p.pairs);
-  RowStat *stat = reinterpret_cast<RowStat *>(ws + l.stat);
-  RowGrad *grad = reinterpret_cast<RowGrad *>(ws + l.grad);
-  double *losses = reinterpret_cast<double *>(ws + l.losses);
-  hipError_t e = hipSuccess;
-  if (a.rows > 0) e = rows_launch(a, bf16, stat, grad, nullptr, nullptr, s);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kl_pairs, dim3((unsigned)p.pairs), dim3(1024), 0, s, a, p, stat, grad, losses);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  // pieces of a row: 8192 elements or more, and a grid that stays in range
-  int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(a.vocab / 8192, 64));
-  if (a.rows > 0) pieces = std::max<int64_t>(1, std::min(pieces, (((int64_t)1 << 31) - 1) / a.rows));
-  const dim3 g((unsigned)std::max<int64_t>(1, a.rows * pieces));
-  if (bf16) hipLaunchKernelGGL(kl_grad<true>, g, dim3(256), 0, s, a, grad, dlogits, dld, (int)pieces, losses, p.pairs, p.loss);
-  else hipLaunchKernelGGL(kl_grad<false>, g, dim3(256), 0, s, a, grad, dlogits, dld, (int)pieces, losses, p.pairs, p.loss);
-  return hipGetLastError();
+  return bf16 ? preference_launch<true>(a, p, dlogits, dld, ws, s) : preference_launch<false>(a, p, dlogits, dld, ws, s);
 }
 
 }  // namespace muon

@@ -105,7 +105,7 @@ muon_status check_logits(const char *where, const muon_logits *x) {
 }
 
 LogitArgs logit_args(const muon_logits *x) {
-  return {x->logits, {x->targets, x->target_type == MUON_IDX_INT64}, x->ld, x->vocab, x->rows};
+  return {x->logits, {x->targets, x->target_type == MUON_IDX_INT64}, x->ld, x->vocab, x->rows, 0};
 }
 
 // dlogits: the logits themselves, or apart from them
@@ -137,7 +137,7 @@ muon_status muon_embed_forward(const void *table, int64_t vocab, int64_t dim, in
     st = no_overlap(me, {matrix(out, tokens, dim, out_ld, e, "out")},
                     {matrix(table, vocab, dim, table_ld, e, "table"), flat(ids, tokens, index_bytes(id_type), "ids")});
     if (st != MUON_OK) return st;
-    const EmbedFwdArgs a{table, out, {ids, id_type == MUON_IDX_INT64}, table_ld, out_ld, vocab, dim, tokens, scale};
+    const EmbedFwdArgs a{table, out, {ids, id_type == MUON_IDX_INT64}, table_ld, out_ld, vocab, dim, tokens, scale, 0};
     return done(launch_embed_forward(a, dtype == MUON_DT_BF16, static_cast<hipStream_t>(stream)), me);
   });
 }

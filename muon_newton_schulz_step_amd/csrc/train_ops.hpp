@@ -26,6 +26,7 @@ struct EmbedFwdArgs {
   int64_t table_ld, out_ld;
   int64_t vocab, dim, tokens;
   float scale;
+  int64_t token0;  // the first token of a launch
 };
 hipError_t launch_embed_forward(const EmbedFwdArgs &a, bool bf16, hipStream_t s);
 
@@ -86,7 +87,7 @@ struct RowStat {
   double logp, share;
 };
 
-// What the gradient pass needs of a row: d x_j = c exp(x_j - max) away from
+// What the gradient of a row's logits needs: d x_j = c exp(x_j - max) away from
 // the target, dt at the target; all of it 0 where live is 0.
 struct RowGrad {
   float max, c, dt;
@@ -97,6 +98,7 @@ struct LogitArgs {
   const void *logits;
   IndexVec targets;
   int64_t ld, vocab, rows;
+  int64_t row0;  // the first row of a launch
 };
 
 struct PolicyArgs {
@@ -118,14 +120,33 @@ struct PreferenceArgs {
 hipError_t launch_token_logprob(const LogitArgs &a, bool bf16, float *logp, float *lse, hipStream_t s);
 
 struct PolicyLayout {
-  size_t terms, total;
+  size_t terms, part, total;
 };
 PolicyLayout policy_layout(int64_t rows);
 hipError_t launch_policy(const LogitArgs &a, const PolicyArgs &p, bool bf16, void *dlogits, int64_t dld, char *ws,
                          hipStream_t s);
 
+constexpr int PREF_THREADS = 512;  // threads of a workgroup of the preference loss
+constexpr int PREF_SLACK = 64;     // rows between a pair's last sum and its first gradient
+
+// The state of a walk over the rows of the pairs.
+struct PreferenceWalk {
+  uint64_t ticket;
+  int32_t pairs_done;
+  int32_t rows;  // rows that belong to a sequence
+  int32_t lag;   // rows whose sums are handed out before the first gradient
+};
+// Workspace of the preference loss.
+struct PreferenceWork {
+  PreferenceWalk *walk;
+  RowStat *stat;         // a row
+  double *losses, *coef; // a pair
+  int32_t *bounds;       // 2 pairs + 1: the sequences' first rows
+  int32_t *starts;       // pairs + 1: a pair's place in the walk
+  int32_t *done, *ready; // a pair: rows summed, coefficient written
+};
 struct PreferenceLayout {
-  size_t stat, grad, losses, total;
+  size_t walk, stat, grad, losses, coef, bounds, starts, done, ready, total;
 };
 PreferenceLayout preference_layout(int64_t rows, int64_t pairs);
 hipError_t launch_preference(const LogitArgs &a, const PreferenceArgs &p, bool bf16, void *dlogits, int64_t dld,

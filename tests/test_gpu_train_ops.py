@@ -167,6 +167,37 @@ def test_embedding_gradient_layouts(torch, n, vocab, dim, kind, dtype, idt, ld, 
     check_embed_grad(torch, n, vocab, dim, kind, dtype, idt, first, ld, shift)
 
 
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("n,vocab,dim", [(3000, 600000, 9), (1024, 600000, 8), (1025, 600000, 8), (40000, 300, 24)])
+def test_embedding_gradient_of_one_bucket(torch, n, vocab, dim, first):
+    # rows a multiple of 256 apart meet in one bucket of the sort: more than it sorts by counting, and keys of more
+    # bits than one radix pass takes
+    rng = np.random.default_rng(n)
+    ids = rng.integers(0, (vocab + 255) // 256, n) * 256
+    dout = torch.from_numpy(rng.integers(-8, 9, (n, dim)).astype(np.float32)).to(DEV)
+    acc = torch.from_numpy(rng.integers(-8, 9, (vocab, dim)).astype(np.float32)).to(DEV)
+    want = torch.zeros_like(acc) if first else acc.clone()
+    iv = vec(torch, ids, "int64")
+    want.index_add_(0, iv, dout)  # small whole numbers: exact in any order
+    M.embed_backward(iv, dout, acc, first, poisoned(torch, M.embed_backward_workspace_bytes(n, vocab, dim)))
+    assert torch.equal(acc, want)
+
+
+@pytest.mark.parametrize("n,vocab", [(5, 9_000_000), (2000, 34_000_000)])
+def test_embedding_gradient_of_a_long_table(torch, n, vocab):
+    # more rows than one presence map of the zeros' workgroups covers
+    rng = np.random.default_rng(n)
+    ids = rng.integers(0, vocab, n)
+    ids[0], ids[1] = vocab - 1, 0
+    dout = torch.from_numpy(rng.integers(-8, 9, (n, 1)).astype(np.float32)).to(DEV)
+    acc = torch.full((vocab, 1), 5.0, device=DEV)
+    iv = vec(torch, ids, "int32")
+    M.embed_backward(iv, dout, acc, True, poisoned(torch, M.embed_backward_workspace_bytes(n, vocab, 1)))
+    want = torch.zeros_like(acc)
+    want.index_add_(0, iv.long(), dout)
+    assert torch.equal(acc, want)
+
+
 def test_embedding_gradient_against_differences(torch):
     # the lookup is linear: <g, lookup(table + u) - lookup(table)> = <gradient, u>, in exact arithmetic; here
     # small whole numbers make every product and sum exact, so the two sides are equal bit for bit
@@ -449,6 +480,148 @@ def test_preference_loss_bad_offsets_touch_no_row_outside(torch):
                           loss, rew, dl, poisoned(torch, M.preference_loss_workspace_bytes(6, 2)))
         torch.cuda.synchronize()
         assert around_untouched(torch, dl, dbuf)
+
+
+def big_pref(torch, lens, lead, tail, v, dtype, ld, seed):
+    """A preference case too large for the host: logits, targets (some of them none), offsets, references."""
+    g = torch.Generator(DEV).manual_seed(seed)
+    off = np.cumsum([lead] + list(lens))
+    n = int(off[-1]) + tail
+    buf = torch.empty(n * ld, dtype=dt(torch, dtype), device=DEV).normal_(0.0, 2.0, generator=g)
+    x = buf.view(n, ld)[:, :v]
+    t = torch.randint(0, v, (n,), generator=g, device=DEV)
+    t[torch.rand(n, generator=g, device=DEV) < 0.3] = -1
+    ref = []
+    for s in range(len(lens)):
+        lp, _, _, _ = big_rows(torch, x[int(off[s]):int(off[s + 1])], t[int(off[s]):int(off[s + 1])])
+        ref.append(float(lp.sum()) + float(torch.randn(1, generator=g, device=DEV)) * np.sqrt(max(1, lens[s])))
+    return x, t, torch.tensor(off, device=DEV), torch.tensor(ref, device=DEV, dtype=torch.float32)
+
+
+def big_rows(torch, x, t):
+    """logp, p, |d| and the row sums' relative tolerance of rows, in fp64 (0 where a row has no target)."""
+    z = x.double()
+    lp = torch.log_softmax(z, 1)
+    live = (t >= 0) & (t < x.shape[1])
+    logp = torch.where(live, lp.gather(1, t.clamp(0, x.shape[1] - 1)[:, None])[:, 0], 0.0)
+    p, d = lp.exp(), (z - z.max(1, keepdim=True).values).abs()
+    tol = torch.where(live, (2 * (p * d).sum(1) + x.shape[1] / 64 + 64) * E, 0.0)
+    return logp, p, d, tol
+
+
+@pytest.mark.parametrize("lens,lead,tail,v,dtype,ld", [
+    # more than 256 MB: ragged pairs, an empty sequence and an empty pair, rows before and after them
+    ([300, 0, 0, 511, 40, 500, 333, 0, 420, 1], 3, 650, 50257, "bf16", 50257),
+    ([150, 700, 260, 10, 600, 520], 0, 0, 32001, "fp32", 32003)])
+def test_preference_loss_in_one_walk(torch, lens, lead, tail, v, dtype, ld):
+    x, t, off, ref = big_pref(torch, lens, lead, tail, v, dtype, ld, 5)
+    n, seqs, beta, smooth = x.shape[0], len(lens), 0.1, 0.05
+    pairs = seqs // 2
+    assert x.numel() * x.element_size() > 256 << 20
+    o = off.tolist()
+
+    def call(x, dl):
+        loss, rew = torch.full((1,), 9.0, device=DEV), torch.full((seqs,), 9.0, device=DEV)
+        M.preference_loss(x, t, off, ref, loss, rew, dl, poisoned(torch, M.preference_loss_workspace_bytes(n, pairs)),
+                          beta=beta, label_smoothing=smooth)
+        return loss, rew, dl
+    loss, rew, dl = call(x, torch.full((n, v), 9.0, dtype=x.dtype, device=DEV))
+    sums, seq_tol = np.zeros(seqs), np.zeros(seqs)
+    for s in range(seqs):
+        lp, _, _, tol = big_rows(torch, x[o[s]:o[s + 1]], t[o[s]:o[s + 1]])
+        sums[s], seq_tol[s] = float(lp.sum()), float(tol.sum())
+    gain = sums - f64(ref)
+    m = beta * (gain[:pairs] - gain[pairs:])
+    want = ((1 - smooth) * np.logaddexp(0, -m) + smooth * np.logaddexp(0, m)).mean()
+    gain_tol = beta * seq_tol + 4 * E * np.abs(beta * gain)
+    pair_tol = gain_tol[:pairs] + gain_tol[pairs:]
+    within(f64(rew), beta * gain, gain_tol, "rewards")
+    within(f64(loss), [want], pair_tol.mean() + 4 * E * (1 + abs(want)), "loss")
+    c = beta / pairs * (1 / (1 + np.exp(-m)) - (1 - smooth))
+    assert not dl[:o[0]].any() and not dl[o[-1]:].any()
+    for s in range(seqs):
+        for r0 in range(o[s], o[s + 1], 128):
+            r = slice(r0, min(r0 + 128, o[s + 1]))
+            _, p, d, tol = big_rows(torch, x[r], t[r])
+            live = ((t[r] >= 0) & (t[r] < v)).double()[:, None]
+            a = live * (c[s] if s < pairs else -c[s - pairs])
+            one = torch.zeros_like(p).scatter_(1, t[r].clamp(0, v - 1)[:, None], 1.0)
+            wd = a * (one - p)
+            a = a.abs()
+            dd = live * beta / pairs / 4 * pair_tol[s % pairs]
+            lim = p * a * ((2 * d + 8) * E + tol[:, None]) + one * (1 - p) * 4 * E * a + 1.01 * HALF[dtype] * wd.abs()
+            lim = lim + (dd + a * tol[:, None]) * (p + one) + TINY
+            assert bool(((dl[r].double() - wd).abs() <= lim).all()), f"dlogits of sequence {s}, rows {r}"
+    again = call(x, torch.full((n, v), 9.0, dtype=x.dtype, device=DEV))
+    assert all(torch.equal(p, q) for p, q in zip(again, (loss, rew, dl))), "a second run gives other bits"
+    place = call(x, x)
+    assert all(torch.equal(p, q) for p, q in zip(place, (loss, rew, dl))), "other bits in place"
+
+
+def test_preference_loss_walk_in_a_graph(torch):
+    n, v, lens = 2700, 50257, [300, 410, 500, 140, 350, 450, 250, 300]
+    x, t, off, ref = big_pref(torch, lens, 0, 0, v, "bf16", v, 1)
+    assert x.shape[0] == n
+    ws = poisoned(torch, M.preference_loss_workspace_bytes(n, 4))
+
+    def outs():
+        return torch.empty(1, device=DEV), torch.empty(8, device=DEV), torch.empty_like(x)
+    one, two = outs(), outs()
+
+    def call(o):
+        M.preference_loss(x, t, off, ref, o[0], o[1], o[2], ws)
+    call(two)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(one)
+    for k in range(1, 4):
+        x.mul_(0.9)
+        ref.add_(0.5 * k)
+        ws.fill_(0x5A + k)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        call(two)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(one, two)), f"replay {k}"
+    graph.reset()
+
+
+def test_more_rows_than_one_launch_takes(torch):
+    n, v = (1 << 21) + 5, 3
+    g = torch.Generator(DEV).manual_seed(2)
+    x = torch.randn(n, v, generator=g, device=DEV)
+    t = torch.randint(0, v, (n,), generator=g, device=DEV, dtype=torch.int32)
+    t[::7] = -1
+    live = t >= 0
+    z = torch.log_softmax(x.double(), 1)
+    lp = torch.where(live, z.gather(1, t.clamp(min=0).long()[:, None])[:, 0], 0.0)
+    logp = torch.empty(n, device=DEV)
+    M.token_logprob(x, t, logp)
+    # three terms a row: the sum's relative error is below (2 |d| + 68) e with |d| < 16
+    tol = 100 * E * (1 + lp.abs())
+    assert bool(((logp.double() - lp).abs() <= tol).all())
+    w = torch.full((n,), 1.0 / n, device=DEV)
+    adv = torch.randn(n, generator=g, device=DEV)
+    stats, lp2, d = torch.empty(4, device=DEV), torch.empty(n, device=DEV), torch.empty_like(x)
+    M.policy_loss(x, t, adv, w, stats, lp2, d, poisoned(torch, M.policy_loss_workspace_bytes(n)))
+    assert torch.equal(lp2, logp)
+    # ratio 1 in every row: the loss is -sum w a over the live rows
+    aw = torch.where(live, adv.double() * w.double(), 0.0)
+    assert float(stats[0]) == pytest.approx(-float(aw.sum()), abs=2 * E * float(aw.abs().sum()))
+    one = torch.zeros_like(z).scatter_(1, t.clamp(min=0).long()[:, None], 1.0)
+    want = -aw[:, None] * (one - z.exp())
+    assert bool(((d.double() - want).abs() <= 200 * E * aw.abs()[:, None] + TINY).all())
+    off = torch.tensor([2, n // 3, n // 2, n - 70, n - 1], device=DEV)
+    sums = [float(lp[a:b].sum()) for a, b in zip(off.tolist(), off.tolist()[1:])]
+    ref = torch.tensor([round(s) for s in sums], device=DEV, dtype=torch.float32)
+    loss, rew = torch.empty(1, device=DEV), torch.empty(4, device=DEV)
+    M.preference_loss(x, t, off, ref, loss, rew, d, poisoned(torch, M.preference_loss_workspace_bytes(n, 2)), beta=1e-3)
+    gain = np.array(sums) - f64(ref)
+    err = np.array([float(tol[a:b].sum()) for a, b in zip(off.tolist(), off.tolist()[1:])])
+    within(f64(rew), 1e-3 * gain, 1e-3 * err + 4 * E * 1e-3 * np.abs(gain), "rewards")
+    assert not d[:2].any() and not d[n - 1:].any()
 
 
 # ------------------------------------------------------------ balance loss

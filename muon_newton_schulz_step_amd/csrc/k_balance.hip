@@ -23,7 +23,7 @@ using namespace dev;
 
 namespace {
 
-constexpr int BH_GROUPS = 64;   // workgroups that count choices, at most
+constexpr int BH_GROUPS = 128;  // workgroups that count choices, at most
 constexpr int BM_GROUPS = 512;  // workgroups of the main pass, at most: two on a CU
 constexpr int BM_THREADS = 1024;
 // Up to this many logits (and choices) one workgroup does the whole call.
@@ -39,7 +39,7 @@ __device__ __forceinline__ int count_choices(const BalanceArgs &a, int64_t t0, i
     live = (int)(t1 - t0);
   }
   // tokens * k stays below 2^31; the loads of a round are under way together
-  constexpr int ROUND = 8;
+  constexpr int ROUND = 4;
   const uint32_t k = (uint32_t)a.k, end = (uint32_t)t1 * k;
   for (uint32_t i = (uint32_t)t0 * k + threadIdx.x; i < end; i += ROUND * 1024) {
     int64_t e[ROUND];

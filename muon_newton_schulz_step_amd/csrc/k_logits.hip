@@ -65,14 +65,15 @@ __device__ __forceinline__ Online block_join(Online o, float *red) {
   return t;
 }
 
-// Maximum and sum of a row by a workgroup; every thread gets them.
+// Maximum and sum of a row's vectors [v0, v1), and of its single elements if
+// asked for, by a workgroup; every thread gets them.
 template <bool BF16, int THREADS, int UNROLL = 4>
-__device__ __forceinline__ Online row_online(const typename Elem<BF16>::type *x, int64_t vocab, float *red) {
+__device__ __forceinline__ Online row_online(const typename Elem<BF16>::type *x, const Row<BF16> &row, int v0, int v1,
+                                             bool singles, float *red) {
   typedef Elem<BF16> E;
-  const Row<BF16> row(x, vocab);
   Online o;
-  int i = threadIdx.x;
-  for (; i + (UNROLL - 1) * THREADS < row.vecs; i += UNROLL * THREADS) {
+  int i = v0 + threadIdx.x;
+  for (; i + (UNROLL - 1) * THREADS < v1; i += UNROLL * THREADS) {
     uint4 w[UNROLL];
 #pragma unroll
     for (int k = 0; k < UNROLL; ++k) w[k] = load16(x + row.col(i + k * THREADS));
@@ -84,16 +85,21 @@ __device__ __forceinline__ Online row_online(const typename Elem<BF16>::type *x,
       o.template add<2 * E::N>(v);
     }
   }
-  for (; i < row.vecs; i += THREADS) {
+  for (; i < v1; i += THREADS) {
     float v[E::N];
     E::unpack(load16(x + row.col(i)), v);
     o.template add<E::N>(v);
   }
-  if ((int)threadIdx.x < row.singles()) {
+  if (singles && (int)threadIdx.x < row.singles()) {
     const float v = E::get(x[row.single(threadIdx.x)]);
     o.template add<1>(&v);
   }
   return block_join<THREADS / 64>(o, red);
+}
+template <bool BF16, int THREADS, int UNROLL = 4>
+__device__ __forceinline__ Online row_online(const typename Elem<BF16>::type *x, int64_t vocab, float *red) {
+  const Row<BF16> row(x, vocab);
+  return row_online<BF16, THREADS, UNROLL>(x, row, 0, row.vecs, true, red);
 }
 
 }  // namespace
@@ -133,10 +139,66 @@ namespace {
 // Vectors of a row that a thread of the policy kernel keeps: the first ones in
 // LDS (64 KB a workgroup of 1024, two of them on a CU), the others in registers.
 constexpr int KEEP_LDS = 4, KEEP_REGS = 2, KEEP = KEEP_LDS + KEEP_REGS;
+// The policy loss of up to FEW_ROWS rows of at least FEW_ROW 16-byte vectors is
+// computed in pieces: at most FEW_GROUPS workgroups, FEW_VECS vectors or more
+// each.  Kernel time in us, in pieces and one workgroup a row: 8 x 50257 fp32
+// 9.3 14.2, 61 x 32000 bf16 10.8 11.5, 20 x 8192 9.4 7.5, 127 x 32000 13.3 12.5;
+// call time, 131072 bf16 columns: 8 rows 15.6 21.4, 64 15.8 22.8, 128 22.7
+// 23.7, 250 38 33.
+constexpr int FEW_ROWS = 128, FEW_ROW = 8192, FEW_GROUPS = 1024, FEW_VECS = 512;
 // Rows whose terms one workgroup adds up.
 constexpr int64_t SUM_ROWS = 16384;
 // Loads of the rest under way at a time.
 constexpr int AHEAD = 2;
+
+}  // namespace
+
+namespace {
+
+// What a policy row has besides its logits: lane 0 holds the old log-
+// probability, lane 1 the reference's.
+struct PolicyRow {
+  float weight, at_target, other, advantage;
+};
+struct PolicyCoef {
+  float c, dt;  // d x_j = c exp(x_j - max) away from the target, dt at the target
+};
+
+__device__ __forceinline__ PolicyRow policy_row(const PolicyArgs &p, int64_t r, float weight, float at_target) {
+  PolicyRow q{weight, at_target, 0.f, p.advantages[r]};
+  if (threadIdx.x == 0 && p.old_logp) q.other = p.old_logp[r];
+  if (threadIdx.x == 1 && p.ref_logp) q.other = p.ref_logp[r];
+  return q;
+}
+
+// A row's loss and derivative, by the first wave in fp64: its lanes 0 to 2
+// share a call of expm1.  Lane 0 writes logp and the four terms if asked to.
+__device__ __forceinline__ PolicyCoef policy_coef(const PolicyArgs &p, const PolicyRow &q, Online o, int64_t r,
+                                                  int64_t rows, bool write, double *terms) {
+  const int lane = threadIdx.x;
+  const double logp = (double)q.at_target - (double)o.m - log((double)o.s);
+  // lane 0: the ratio, lane 1: the KL term, lane 2: the target's own share
+  double arg = 0.0;
+  if (lane == 0 && p.old_logp) arg = logp - (double)q.other;
+  if (lane == 1 && p.ref_logp) arg = (double)q.other - logp;
+  if (lane == 2) arg = logp;
+  const double em1 = expm1(arg);
+  const double ratio = 1.0 + shfl_f64(em1, 0), ed = shfl_f64(em1, 1), share = shfl_f64(em1, 2);
+  const double kl = ed - shfl_f64(arg, 1);
+  const double adv = q.advantage, w = q.weight;
+  const double clipped = fmin(fmax(ratio, 1.0 - p.clip_low), 1.0 + p.clip_high);
+  const bool active = !(ratio * adv > clipped * adv);  // a NaN stays one
+  const double pg = active ? -ratio * adv : -clipped * adv;
+  const double dlogp = w * ((active ? -adv * ratio : 0.0) - p.kl_coef * ed);
+  if (write && lane == 0) {
+    p.logp[r] = (float)logp;
+    put_shared(&terms[r], w * (pg + p.kl_coef * kl));
+    put_shared(&terms[rows + r], w * pg);
+    put_shared(&terms[2 * rows + r], w * kl);
+    put_shared(&terms[3 * rows + r], active ? 0.0 : w);
+  }
+  return {(float)(-dlogp / (double)o.s), (float)(-dlogp * share)};
+}
 
 }  // namespace
 
@@ -159,8 +221,6 @@ constexpr int AHEAD = 2;
 //   whole rows in registers, half the waves  4.2    4.2    4.2         4.2
 //   nothing kept                             4.5    4.7    4.8         4.6
 //   nothing kept, ordinary stores            3.6    4.5    4.7         3.6
-// The row's own arithmetic, in fp64, is two function calls deep in one wave:
-// lanes 0 to 2 share a call of expm1.
 template <bool BF16, int THREADS>
 __global__ __launch_bounds__(THREADS, 8) void kl_policy(LogitArgs a, PolicyArgs p, void *dlogits, int64_t dld,
                                                         double *terms) {
@@ -193,11 +253,7 @@ __global__ __launch_bounds__(THREADS, 8) void kl_policy(LogitArgs a, PolicyArgs 
   const bool lone = tid < row.singles();
   const float single = lone ? E::get(x[row.single(tid)]) : -INFINITY;
   const float at_target = E::get(x[target]);
-  // lane 0: for the ratio, lane 1: for the KL term
-  float other = 0.f;
-  if (tid == 0 && p.old_logp) other = p.old_logp[r];
-  if (tid == 1 && p.ref_logp) other = p.ref_logp[r];
-  const float advantage = p.advantages[r];
+  const PolicyRow q = policy_row(p, r, w, at_target);
   Online o;
 #pragma unroll
   for (int k = 0; k < KEEP; ++k) {
@@ -228,28 +284,10 @@ __global__ __launch_bounds__(THREADS, 8) void kl_policy(LogitArgs a, PolicyArgs 
   o.add<1>(&single);
   o = block_join<THREADS / 64>(o, red);
   if (tid < 64) {
-    const double logp = (double)at_target - (double)o.m - log((double)o.s);
-    // lane 0: the ratio, lane 1: the KL term, lane 2: the target's own share
-    double arg = 0.0;
-    if (tid == 0 && p.old_logp) arg = logp - (double)other;
-    if (tid == 1 && p.ref_logp) arg = (double)other - logp;
-    if (tid == 2) arg = logp;
-    const double em1 = expm1(arg);
-    const double ratio = 1.0 + shfl_f64(em1, 0), ed = shfl_f64(em1, 1), share = shfl_f64(em1, 2);
-    const double kl = ed - shfl_f64(arg, 1);
-    const double adv = advantage;
-    const double clipped = fmin(fmax(ratio, 1.0 - p.clip_low), 1.0 + p.clip_high);
-    const bool active = !(ratio * adv > clipped * adv);  // a NaN stays one
-    const double pg = active ? -ratio * adv : -clipped * adv;
-    const double dlogp = (double)w * ((active ? -adv * ratio : 0.0) - p.kl_coef * ed);
+    const PolicyCoef g = policy_coef(p, q, o, r, a.rows, true, terms);
     if (tid == 0) {
-      coef[0] = (float)(-dlogp / (double)o.s);
-      coef[1] = (float)(-dlogp * share);
-      p.logp[r] = (float)logp;
-      terms[r] = (double)w * (pg + p.kl_coef * kl);
-      terms[a.rows + r] = (double)w * pg;
-      terms[2 * a.rows + r] = (double)w * kl;
-      terms[3 * a.rows + r] = active ? 0.0 : (double)w;
+      coef[0] = g.c;
+      coef[1] = g.dt;
     }
   }
   __syncthreads();
@@ -306,6 +344,121 @@ __global__ __launch_bounds__(1024) void kl_policy_sum(const double *terms, int64
     if (stats) stats[threadIdx.x] = (float)sum;
     else part[threadIdx.x * gridDim.x + blockIdx.x] = sum;
   }
+}
+
+namespace {
+
+// What a piece of a row leaves: its maximum and sum, and the row's target (the
+// gradient of another piece may be written over it, in place, before it is
+// read again).
+struct PieceStat {
+  float max, sum, at_target;
+};
+
+}  // namespace
+
+// Few rows, in pieces, as a CU's arithmetic (44 cycles a wave and element of
+// the sum) is what bounds a row on one CU.  First the pieces' maxima and sums;
+// then every piece's gradient, each workgroup joining its row's pieces and
+// doing the row's arithmetic for itself.  The last row's first piece to finish
+// adds up the rows' terms.
+template <bool BF16>
+__global__ __launch_bounds__(256, 8) void kl_policy_pieces(LogitArgs a, const float *weights, int pieces,
+                                                           PieceStat *part, int32_t *done) {
+  __shared__ float red[8];
+  const int64_t r = blockIdx.x / pieces;
+  const int piece = blockIdx.x % pieces;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *done = 0;
+  const int64_t target = index_at(a.targets, r);
+  if (target < 0 || target >= a.vocab || weights[r] == 0.f) return;
+  typedef Elem<BF16> E;
+  const typename E::type *x = static_cast<const typename E::type *>(a.logits) + r * a.ld;
+  const Row<BF16> row(x, a.vocab);
+  const int v0 = (int)((int64_t)row.vecs * piece / pieces), v1 = (int)((int64_t)row.vecs * (piece + 1) / pieces);
+  const Online o = row_online<BF16, 256>(x, row, v0, v1, piece == 0, red);
+  if (threadIdx.x == 0) part[blockIdx.x] = PieceStat{o.m, o.s, E::get(x[target])};
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(256, 8) void kl_policy_few(LogitArgs a, PolicyArgs p, int pieces, const PieceStat *part,
+                                                        void *dlogits, int64_t dld, double *terms, int32_t *done) {
+  typedef Elem<BF16> E;
+  typedef typename E::type T;
+  constexpr int HELD = 4;
+  __shared__ float coef[3];
+  __shared__ int last;
+  const int64_t r = blockIdx.x / pieces;
+  const int piece = blockIdx.x % pieces, tid = threadIdx.x;
+  const int64_t target = index_at(a.targets, r);
+  const float w = p.weights[r];
+  const bool live = target >= 0 && target < a.vocab && w != 0.f;
+  const T *x = static_cast<const T *>(a.logits) + r * a.ld;
+  T *d = static_cast<T *>(dlogits) + r * dld;
+  const Row<BF16> row(live ? x : d, a.vocab);
+  const int v0 = (int)((int64_t)row.vecs * piece / pieces) + tid, v1 = (int)((int64_t)row.vecs * (piece + 1) / pieces);
+  const bool lone = piece == 0 && tid < row.singles();
+  if (live) {
+    uint4 in[HELD];
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) in[k] = v0 + k * 256 < v1 ? load16(x + row.col(v0 + k * 256)) : E::none();
+    const float single = lone ? E::get(x[row.single(tid)]) : 0.f;
+    if (tid < 64) {
+      const PolicyRow q = policy_row(p, r, w, part[r * pieces].at_target);
+      Online o;
+      if (tid < pieces) {
+        o.m = part[r * pieces + tid].max;
+        o.s = part[r * pieces + tid].sum;
+      }
+#pragma unroll
+      for (int k = 32; k > 0; k >>= 1) {
+        const float m = __shfl_xor(o.m, k), s = __shfl_xor(o.s, k);
+        o.join(m, s);
+      }
+      const PolicyCoef g = policy_coef(p, q, o, r, a.rows, piece == 0, terms);
+      if (tid == 0) {
+        coef[0] = g.c;
+        coef[1] = g.dt;
+        coef[2] = o.m;
+      }
+    }
+    __syncthreads();
+    const float c = coef[0], dt = coef[1], m = coef[2];
+    const int rel = (int)target - row.head;
+    auto grad = [&](uint4 v4, int i) {
+      float v[E::N];
+      E::unpack(v4, v);
+#pragma unroll
+      for (int j = 0; j < E::N; ++j) v[j] = c * exp_shift(v[j], m);
+      const int j0 = rel - i * E::N;
+      if (j0 >= 0 && j0 < E::N) {
+#pragma unroll
+        for (int j = 0; j < E::N; ++j) v[j] = j == j0 ? dt : v[j];
+      }
+      store16(d + row.col(i), E::pack(v));
+    };
+#pragma unroll
+    for (int k = 0; k < HELD; ++k)
+      if (v0 + k * 256 < v1) grad(in[k], v0 + k * 256);
+    for (int i = v0 + HELD * 256; i < v1; i += 256) grad(load16(x + row.col(i)), i);
+    if (lone) d[row.single(tid)] = E::put((int)row.single(tid) == target ? dt : c * exp_shift(single, m));
+  } else {
+    for (int i = v0; i < v1; i += 256) store16(d + row.col(i), make_uint4(0, 0, 0, 0));
+    if (lone) d[row.single(tid)] = T(0);
+    if (piece == 0 && tid == 0) {
+      p.logp[r] = 0.f;
+      for (int k = 0; k < 4; ++k) put_shared(&terms[k * a.rows + r], 0.0);
+    }
+  }
+  if (piece != 0) return;
+  if (tid == 0) last = arrive(done) == (int)a.rows - 1;
+  __syncthreads();
+  if (!last) return;
+  // a wave a sum, in a fixed order
+  double sum = 0.0;
+  for (int64_t i = tid & 63; i < a.rows; i += 64) sum += get_shared(&terms[(tid >> 6) * a.rows + i]);
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) sum += shfl_xor_f64(sum, k);
+  if ((tid & 63) == 0) p.stats[tid >> 6] = (float)sum;
 }
 
 // ------------------------------------------------------- preference loss
@@ -717,39 +870,51 @@ PolicyLayout policy_layout(int64_t rows) {
   PolicyLayout l{};
   const size_t n = (size_t)std::max<int64_t>(rows, 1), groups = (n + SUM_ROWS - 1) / SUM_ROWS;
   l.terms = 0;
-  l.part = up256(4 * sizeof(double) * n);
-  l.total = l.part + 2 * up256(4 * sizeof(double) * groups);
+  l.part = up256(4 * sizeof(double) * n);  // the few rows' pieces and count, or the sums' partial sums
+  l.total = l.part + std::max(2 * up256(4 * sizeof(double) * groups), 256 + up256(sizeof(PieceStat) * FEW_GROUPS));
   return l;
 }
 
 namespace {
 
 template <bool BF16>
-hipError_t policy_launch(const LogitArgs &a, const PolicyArgs &p, void *dlogits, int64_t dld, double *terms, hipStream_t s) {
-  return by_rows(a, a.rows, [&](const LogitArgs &a, dim3 g) {
-    if (a.vocab / Elem<BF16>::N <= 256 * KEEP) hipLaunchKernelGGL((kl_policy<BF16, 256>), g, dim3(256), 0, s, a, p, dlogits, dld, terms);
+hipError_t policy_launch(const LogitArgs &a, const PolicyArgs &p, void *dlogits, int64_t dld, char *ws, hipStream_t s) {
+  const PolicyLayout l = policy_layout(a.rows);
+  double *terms = reinterpret_cast<double *>(ws + l.terms);
+  const int64_t vecs = a.vocab / Elem<BF16>::N;
+  if (a.rows > 0 && a.rows <= FEW_ROWS && vecs >= FEW_ROW) {
+    static_assert(FEW_GROUPS / FEW_ROWS >= 2 && FEW_ROW / FEW_VECS >= 2, "two pieces at least");
+    const int64_t pieces = std::min<int64_t>({FEW_GROUPS / a.rows, vecs / FEW_VECS, 64});  // a lane a piece joins them
+    int32_t *done = reinterpret_cast<int32_t *>(ws + l.part);
+    PieceStat *part = reinterpret_cast<PieceStat *>(ws + l.part + 256);
+    const dim3 g((unsigned)(a.rows * pieces));
+    hipLaunchKernelGGL(kl_policy_pieces<BF16>, g, dim3(256), 0, s, a, p.weights, (int)pieces, part, done);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kl_policy_few<BF16>, g, dim3(256), 0, s, a, p, (int)pieces, part, dlogits, dld, terms, done);
+    return hipGetLastError();
+  }
+  hipError_t e = by_rows(a, a.rows, [&](const LogitArgs &a, dim3 g) {
+    if (vecs <= 256 * KEEP) hipLaunchKernelGGL((kl_policy<BF16, 256>), g, dim3(256), 0, s, a, p, dlogits, dld, terms);
     else hipLaunchKernelGGL((kl_policy<BF16, 1024>), g, dim3(1024), 0, s, a, p, dlogits, dld, terms);
   });
+  if (e != hipSuccess) return e;
+  double *part = reinterpret_cast<double *>(ws + l.part);
+  for (int64_t n = a.rows;;) {
+    const int64_t groups = std::max<int64_t>(1, (n + SUM_ROWS - 1) / SUM_ROWS);
+    hipLaunchKernelGGL(kl_policy_sum, dim3((unsigned)groups), dim3(1024), 0, s, terms, n, part, groups == 1 ? p.stats : nullptr);
+    if ((e = hipGetLastError()) != hipSuccess || groups == 1) return e;
+    n = groups;
+    terms = part;
+    part += up256(4 * sizeof(double) * (size_t)groups) / sizeof(double);
+  }
 }
 
 }  // namespace
 
 hipError_t launch_policy(const LogitArgs &a, const PolicyArgs &p, bool bf16, void *dlogits, int64_t dld, char *ws,
                          hipStream_t s) {
-  const PolicyLayout l = policy_layout(a.rows);
-  double *terms = reinterpret_cast<double *>(ws + l.terms);
-  const hipError_t e = bf16 ? policy_launch<true>(a, p, dlogits, dld, terms, s) : policy_launch<false>(a, p, dlogits, dld, terms, s);
-  if (e != hipSuccess) return e;
-  double *part = reinterpret_cast<double *>(ws + l.part);
-  for (int64_t n = a.rows;;) {
-    const int64_t groups = std::max<int64_t>(1, (n + SUM_ROWS - 1) / SUM_ROWS);
-    hipLaunchKernelGGL(kl_policy_sum, dim3((unsigned)groups), dim3(1024), 0, s, terms, n, part, groups == 1 ? p.stats : nullptr);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || groups == 1) return e;
-    n = groups;
-    terms = part;
-    part += up256(4 * sizeof(double) * (size_t)groups) / sizeof(double);
-  }
+  return bf16 ? policy_launch<true>(a, p, dlogits, dld, ws, s) : policy_launch<false>(a, p, dlogits, dld, ws, s);
 }
 
 PreferenceLayout preference_layout(int64_t rows, int64_t pairs) {

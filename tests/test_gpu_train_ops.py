@@ -374,6 +374,22 @@ def test_policy_loss_many_rows(torch, n, v, dtype):
     check_policy(torch, x, t, adv, w, old, ref, dtype, "int64")
 
 
+@pytest.mark.parametrize("n,v", [(1, 65537), (9, 70001), (128, 65600), (129, 65600)])
+@pytest.mark.parametrize("dtype,ld,shift", [("bf16", 0, 0), ("fp32", 3, 1)])
+def test_policy_loss_few_long_rows(torch, n, v, dtype, ld, shift):
+    rng = np.random.default_rng(n)
+    x, _, t, adv, w, old, ref = policy_inputs(torch, rng, n, v, dtype, "int64", ld, shift)
+    t[0] = v - 1 if n < 9 else 0
+    old[0] = ref[0] = float(T.token_logprob(f64(x[:1]), t[:1])[0][0]) + 0.01
+    dl, dbuf = strided(torch, np.zeros((n, v)), dtype, v + ld, shift)
+    stats, logp, d = check_policy(torch, x, t, adv, w, old, ref, dtype, "int64", dl=dl)
+    assert around_untouched(torch, d, dbuf)
+    again = check_policy(torch, x, t, adv, w, old, ref, dtype, "int64")
+    assert all(torch.equal(a, b) for a, b in zip(again, (stats, logp, d))), "a second run gives other bits"
+    place = check_policy(torch, x, t, adv, w, old, ref, dtype, "int64", in_place=True)
+    assert all(torch.equal(a, b) for a, b in zip(place, (stats, logp, d))), "other bits in place"
+
+
 @pytest.mark.parametrize("have_old,have_ref,kl", [(False, True, 0.05), (True, False, 0.05), (False, False, 0.0),
                                                   (True, True, 0.0)])
 def test_policy_loss_options(torch, have_old, have_ref, kl):

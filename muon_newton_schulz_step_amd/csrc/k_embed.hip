@@ -25,7 +25,9 @@ using namespace dev;
 // HBM-bound: the distinct rows are read once, the rest of the reads hit the
 // caches.  `lanes` (a power of two) consecutive threads copy one row, 16
 // bytes a thread and step, so a narrow table fills a workgroup with several
-// tokens and a wide one gives a token to the whole workgroup.
+// tokens and a wide one gives a token to the whole workgroup.  32768 tokens of
+// 8192 bf16 columns out of 131072 rows: 148 us for the 727 MB it cannot do
+// without, 4.9 TB/s (a large copy: 4.95); 7 tokens of 4096: 3 us, a launch.
 template <bool BF16>
 __global__ __launch_bounds__(256) void ke_lookup(EmbedFwdArgs a, int lanes) {
   typedef Elem<BF16> E;
@@ -369,7 +371,11 @@ __global__ __launch_bounds__(ES_THREADS, 8) void ke_sort(EmbedBwdArgs a, int pas
 // of dout, VECS 16-byte vectors a lane.  HBM-bound: each live dout row is
 // read once, each gradient row with a token written once.  The units run over
 // the buckets' first chunks, then over their second ones, and so on: the
-// chunks of many tokens come first and the light ones fill the end.
+// chunks of many tokens come first and the light ones fill the end.  A wave
+// meets another bucket at each turn (141 us a call against 167 with always the
+// same, at 16384 tokens of 4096 columns, as the frequent rows' buckets are
+// fuller).  At that size the kernel takes 80 us beside half of the zeros, for
+// 440 MB: 5.5 TB/s.
 template <bool BF16, int VECS>
 __global__ __launch_bounds__(256) void ke_add(EmbedBwdArgs a, int col_blocks, int zeros) {
   typedef Elem<BF16> E;
@@ -513,8 +519,11 @@ __global__ __launch_bounds__(256) void ke_add(EmbedBwdArgs a, int col_blocks, in
 // finds the tokens of the same row among all ids, ends if one of them comes
 // before t, and otherwise adds them up, each wave those of its quarter of the
 // ids; the waves' sums are joined in their order.  Bound by the latency of
-// its three dependent loads (ids, dout rows, acc).  The other workgroups write
-// the zeros of a first call.
+// its dependent loads (ids, then dout rows) and the launch.  The other
+// workgroups write the zeros of a first call.  In us, so and with a sort: 1021
+// tokens of 1024 fp32 columns 7.3 15.3, 1000 tokens into a first call's 32000
+// rows of 1024 30 39, 1024 tokens of 8192 bf16 columns 21.3 23.5; every
+// workgroup reads all ids, so twice the tokens are four times the reads.
 namespace {
 
 constexpr int EF_IDS = EB_FEW / 256;  // ids that a lane holds

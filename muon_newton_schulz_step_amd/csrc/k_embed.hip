@@ -25,10 +25,13 @@ using namespace dev;
 // HBM-bound: the distinct rows are read once, the rest of the reads hit the
 // caches.  `lanes` (a power of two) consecutive threads copy one row, 16
 // bytes a thread and step, so a narrow table fills a workgroup with several
-// tokens and a wide one gives a token to the whole workgroup.  32768 tokens of
-// 8192 bf16 columns out of 131072 rows: 148 us for the 727 MB it cannot do
-// without, 4.9 TB/s (a large copy: 4.95); 7 tokens of 4096: 3 us, a launch.
-template <bool BF16>
+// tokens and a wide one gives a token to the whole workgroup.  An output that
+// the memory-side cache could not hold beside the table is streamed past it:
+// 32768 tokens of 8192 bf16 columns out of 131072 rows take 137 us for the 727
+// MB they cannot do without, 5.3 TB/s (a large copy: 4.95), with ordinary
+// stores 149; 32768 of 1024 fp32 columns out of 32000 rows 29 and 49.  7 tokens
+// of 4096: 3 us, a launch.
+template <bool BF16, bool STREAM>
 __global__ __launch_bounds__(256) void ke_lookup(EmbedFwdArgs a, int lanes) {
   typedef Elem<BF16> E;
   typedef typename E::type T;
@@ -51,7 +54,8 @@ __global__ __launch_bounds__(256) void ke_lookup(EmbedFwdArgs a, int lanes) {
         for (int k = 0; k < E::N; ++k) v[k] *= a.scale;
         w = E::pack(v);
       }
-      store16(dst + c, w);
+      if constexpr (STREAM) stream16(dst + c, w);
+      else store16(dst + c, w);
     } else {
       for (int64_t j = c; j < a.dim; ++j) dst[j] = has ? E::put(E::get(src[j]) * a.scale) : T(0);
     }
@@ -65,11 +69,15 @@ hipError_t launch_embed_forward(const EmbedFwdArgs &a, bool bf16, hipStream_t s)
   const int64_t per = 256 / lanes;
   // a grid holds fewer than 2^32 threads: more tokens take several launches
   const int64_t most = ((int64_t)1 << 23) * per;
+  // (smaller outputs take the same time either way, and their reader finds them in the cache)
+  const bool stream = a.tokens * a.dim * (bf16 ? 2 : 4) >= (64 << 20);
   EmbedFwdArgs b = a;
   for (b.token0 = 0; b.token0 < a.tokens; b.token0 += most) {
     const dim3 grid((unsigned)((std::min(most, a.tokens - b.token0) + per - 1) / per));
-    if (bf16) hipLaunchKernelGGL(ke_lookup<true>, grid, dim3(256), 0, s, b, lanes);
-    else hipLaunchKernelGGL(ke_lookup<false>, grid, dim3(256), 0, s, b, lanes);
+    if (bf16 && stream) hipLaunchKernelGGL((ke_lookup<true, true>), grid, dim3(256), 0, s, b, lanes);
+    else if (bf16) hipLaunchKernelGGL((ke_lookup<true, false>), grid, dim3(256), 0, s, b, lanes);
+    else if (stream) hipLaunchKernelGGL((ke_lookup<false, true>), grid, dim3(256), 0, s, b, lanes);
+    else hipLaunchKernelGGL((ke_lookup<false, false>), grid, dim3(256), 0, s, b, lanes);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -106,6 +106,11 @@ constexpr int ES_BITS = 10, ES_DIGITS = 1 << ES_BITS;
 constexpr int ES_MAP_BITS = 1 << 17;  // local rows that one presence map covers
 constexpr int ES_HELD = 16;           // ids that a thread reads at a time
 constexpr int ES_SMALL = 512;
+constexpr int ES_LARGE = 32;          // rows of a bucket that the workgroup cuts into chunks together
+
+struct EsLarge {
+  int32_t slot, row, start, len, parts, slot0, tok0;
+};
 static_assert(ES_DIGITS == ES_THREADS, "one thread a digit in the scan");
 static_assert(ES_MAP_BITS / 32 <= ES_WAVES * ES_DIGITS, "the map shares the counts' memory");
 static_assert((EB_BUCKETS & (EB_BUCKETS - 1)) == 0, "bucket and key are bits of the row");
@@ -188,7 +193,8 @@ __global__ __launch_bounds__(ES_THREADS, 8) void ke_sort(EmbedBwdArgs a, int pas
   __shared__ __attribute__((aligned(16))) int count[ES_WAVES][ES_DIGITS];
   __shared__ int base[ES_DIGITS];
   __shared__ int wsum[ES_WAVES], wsum2[ES_WAVES];
-  __shared__ int n_heavy, n_light;
+  __shared__ int n_heavy, n_light, n_parts, n_large;
+  __shared__ EsLarge large[ES_LARGE];
   const int b = blockIdx.x, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   if (b >= EB_BUCKETS) {
     zero_rows<ES_THREADS, EB_SHIFT, ES_MAP_BITS>(a, b - EB_BUCKETS, 0, zeros_beside_sort(a.vocab), reinterpret_cast<uint32_t *>(&count[0][0]));
@@ -222,7 +228,7 @@ __global__ __launch_bounds__(ES_THREADS, 8) void ke_sort(EmbedBwdArgs a, int pas
     wsum[w] = mine;
     wsum2[w] = lower;
   }
-  if (threadIdx.x == 0) n_heavy = n_light = 0;
+  if (threadIdx.x == 0) n_heavy = n_light = n_parts = n_large = 0;
   __syncthreads();
   int first = 0, n = 0, at = 0;
   for (int i = 0; i < ES_WAVES; ++i) {
@@ -259,22 +265,43 @@ __global__ __launch_bounds__(ES_THREADS, 8) void ke_sort(EmbedBwdArgs a, int pas
   if (small && threadIdx.x < 4) lkey[n + threadIdx.x] = INT32_MAX;  // no row's key
   __syncthreads();
 
-  // a row's tokens in nearly equal chunks of at most EB_CHUNK: chunks of many
-  // tokens from the front of the bucket's slots, others from the back (their
-  // order does not touch the results)
-  auto emit = [&](int k, int s, int len, int tok0) {
-    const int parts = (len + EB_CHUNK - 1) / EB_CHUNK;
-    const int row = k * EB_BUCKETS + b;
-    int slot = first;
-    if (len > EB_LIGHT) slot += atomicAdd(&n_heavy, parts);
-    else slot += n - 1 - atomicAdd(&n_light, 1);
-    for (int i = 0; i < parts; ++i) {
-      const int lo = (int)((int64_t)len * i / parts), hi = (int)((int64_t)len * (i + 1) / parts);
-      a.chunks[slot + i] = EbChunk{row, first + s + lo, hi - lo, parts, first + s, len, tok0, 0};
-    }
+  // a row's tokens in chunks of EB_CHUNK: chunks of rows with many tokens from
+  // the front of the bucket's slots, others from the back.  Neither their
+  // order nor that of the slots for partial sums touches the results.  (A row
+  // of several chunks has 33 tokens or more and so at most tokens / 16 of
+  // them: the bucket's slots are its own from first / 16 on.)
+  auto chunk = [&](int slot, int row, int s, int len, int parts, int slot0, int tok0, int i) {
+    a.chunks[slot + i] = EbChunk{row, first + s + i * EB_CHUNK, min(EB_CHUNK, len - i * EB_CHUNK), parts, i, slot0, tok0, 0};
     if (parts > 1) {
-      for (int j = 0; j < col_blocks; ++j) a.arrive[(int64_t)((first + s) / (EB_CHUNK / 2)) * col_blocks + j] = 0;
+      for (int j = 0; j < col_blocks; ++j) {
+        a.arrive[((int64_t)slot0 + i) * 2 * col_blocks + j] = 0;
+        a.arrive[((int64_t)slot0 + i) * 2 * col_blocks + col_blocks + j] = 0;
+      }
     }
+  };
+  auto emit = [&](int k, int s, int len, int tok0) {
+    const int parts = (len + EB_CHUNK - 1) / EB_CHUNK, row = k * EB_BUCKETS + b;
+    if (len <= EB_LIGHT) {
+      chunk(first + n - 1 - atomicAdd(&n_light, 1), row, s, len, 1, 0, tok0, 0);
+      return;
+    }
+    const int slot = first + atomicAdd(&n_heavy, parts);
+    const int slot0 = parts > 1 ? first / (EB_CHUNK / 2) + atomicAdd(&n_parts, parts) : 0;
+    // a row of very many tokens is left to the whole workgroup
+    const int at = parts > 4 ? atomicAdd(&n_large, 1) : ES_LARGE;
+    if (at < ES_LARGE) {
+      large[at] = EsLarge{slot, row, s, len, parts, slot0, tok0};
+    } else {
+      for (int i = 0; i < parts; ++i) chunk(slot, row, s, len, parts, slot0, tok0, i);
+    }
+  };
+  auto finish = [&]() {
+    __syncthreads();
+    for (int j = 0; j < min(n_large, ES_LARGE); ++j) {
+      const EsLarge l = large[j];
+      for (int i = threadIdx.x; i < l.parts; i += ES_THREADS) chunk(l.slot, l.row, l.start, l.len, l.parts, l.slot0, l.tok0, i);
+    }
+    if (threadIdx.x == 0) a.buckets[b] = EbBucket{first, n, n_heavy, n_light};
   };
 
   if (small) {
@@ -292,8 +319,7 @@ __global__ __launch_bounds__(ES_THREADS, 8) void ke_sort(EmbedBwdArgs a, int pas
       a.perm[first + less + before] = ltok[p];
       if (before == 0) emit(k, less, same, ltok[p]);
     }
-    __syncthreads();
-    if (threadIdx.x == 0) a.buckets[b] = EbBucket{first, n, n_heavy, n_light};
+    finish();
     return;
   }
 
@@ -369,8 +395,7 @@ __global__ __launch_bounds__(ES_THREADS, 8) void ke_sort(EmbedBwdArgs a, int pas
     const int s = head[h];
     emit(key[s], s, (h + 1 < n_heads ? head[h + 1] : n) - s, tok[s]);
   }
-  __syncthreads();
-  if (threadIdx.x == 0) a.buckets[b] = EbBucket{first, n, n_heavy, n_light};
+  finish();
 }
 
 // ------------------------------------------------------- adding them up
@@ -420,7 +445,7 @@ __global__ __launch_bounds__(256) void ke_add(EmbedBwdArgs a, int col_blocks, in
     int cols[VECS];
 #pragma unroll
     for (int v = 0; v < VECS; ++v) cols[v] = (int)max((int64_t)0, min((int64_t)N, a.dim - c0 - v * 64 * N));
-    const int toks = count == 1 ? ch.tok0 : lane < count ? a.perm[ch.start + lane] : 0;
+    const int toks = count == 1 && ch.parts == 1 ? ch.tok0 : lane < count ? a.perm[ch.start + lane] : 0;
     float *dst = a.acc + ch.row * a.acc_ld + c0;
     float sum[VECS][N] = {};
     uint4 old[VECS][N / 4];
@@ -470,33 +495,48 @@ __global__ __launch_bounds__(256) void ke_add(EmbedBwdArgs a, int col_blocks, in
       }
     }
     if (ch.parts > 1) {
-      // the row's chunks meet here: each leaves its sum, the last to arrive
-      // adds them in their order (which one is last does not matter)
-      // (a lane's elements lie 64 apart, so that the lanes' stores touch)
+      // the row's chunks meet here: each leaves its sum, the last of a group
+      // adds the group's in their order, and the last of the groups the
+      // groups' (which one is last does not matter).  A lane's elements lie
+      // 64 apart, so that the lanes' stores touch.
       const int64_t width = (int64_t)col_blocks * (64 * N * VECS);
-      float *part = a.partials + (int64_t)cb * (64 * N * VECS) + lane;
-      float *mine = part + (int64_t)(ch.start / (EB_CHUNK / 2)) * width;
-#pragma unroll
-      for (int v = 0; v < VECS; ++v)
-#pragma unroll
-        for (int j = 0; j < N; ++j) put_shared(mine + 64 * (v * N + j), sum[v][j]);
-      int before = 0;
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // of all lanes
-      if (lane == 0) before = arrive(&a.arrive[(int64_t)(ch.seg / (EB_CHUNK / 2)) * col_blocks + cb]);
-      before = __builtin_amdgcn_readfirstlane(before);
-      if (before != ch.parts - 1) continue;
-#pragma unroll
-      for (int v = 0; v < VECS; ++v)
-#pragma unroll
-        for (int j = 0; j < N; ++j) sum[v][j] = 0.f;
-#pragma unroll 2
-      for (k = 0; k < ch.parts; ++k) {
-        const int st = ch.seg + (int)((int64_t)ch.seg_count * k / ch.parts);
-        const float *p = part + (int64_t)(st / (EB_CHUNK / 2)) * width;
+      float *part = a.partials + ch.slot0 * width + (int64_t)cb * (64 * N * VECS) + lane;
+      int32_t *count2 = a.arrive + ((int64_t)ch.slot0 * 2 * col_blocks + cb);
+      auto leave = [&](int slot) {
 #pragma unroll
         for (int v = 0; v < VECS; ++v)
 #pragma unroll
-          for (int j = 0; j < N; ++j) sum[v][j] += get_shared(p + 64 * (v * N + j));
+          for (int j = 0; j < N; ++j) put_shared(part + slot * width + 64 * (v * N + j), sum[v][j]);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // of all lanes
+      };
+      auto join = [&](int slot, int slots, int step) {
+#pragma unroll
+        for (int v = 0; v < VECS; ++v)
+#pragma unroll
+          for (int j = 0; j < N; ++j) sum[v][j] = 0.f;
+#pragma unroll 2
+        for (int i = 0; i < slots; ++i) {
+          const float *p = part + (int64_t)(slot + i * step) * width;
+#pragma unroll
+          for (int v = 0; v < VECS; ++v)
+#pragma unroll
+            for (int j = 0; j < N; ++j) sum[v][j] += get_shared(p + 64 * (v * N + j));
+        }
+      };
+      auto count_in = [&](int32_t *c) {
+        int before = 0;
+        if (lane == 0) before = arrive(c);
+        return __builtin_amdgcn_readfirstlane(before);
+      };
+      const int g0 = ch.index / EB_GROUP * EB_GROUP, members = min(EB_GROUP, ch.parts - g0);
+      const int groups = (ch.parts + EB_GROUP - 1) / EB_GROUP;
+      leave(ch.index);
+      if (count_in(count2 + (int64_t)g0 * 2 * col_blocks) != members - 1) continue;
+      join(g0, members, 1);
+      if (groups > 1) {
+        leave(g0);
+        if (count_in(count2 + col_blocks) != groups - 1) continue;
+        join(0, groups, EB_GROUP);
       }
     }
 #pragma unroll
@@ -685,7 +725,7 @@ EbLayout embed_layout(int64_t tokens, int64_t vocab, int64_t dim) {
     at += (bytes + 255) / 256 * 256;
     return p;
   };
-  const size_t n = (size_t)tokens, slots = n / (EB_CHUNK / 2) + 1;
+  const size_t n = (size_t)tokens, slots = n / (EB_CHUNK / 2) + 1;  // of partial sums
   l.buckets = take(EB_BUCKETS * sizeof(EbBucket));
   l.perm = take(4 * n);
   l.key_a = take(4 * n);
@@ -696,7 +736,7 @@ EbLayout embed_layout(int64_t tokens, int64_t vocab, int64_t dim) {
   // columns up to whole column blocks, of either type's width
   const size_t width = dim > 512 ? ((size_t)dim + 1023) / 1024 * 1024 : 512;
   l.partials = take(n > EB_CHUNK ? slots * width * 4 : 0);
-  l.arrive = take(n > EB_CHUNK ? slots * (width / 256) * 4 : 0);
+  l.arrive = take(n > EB_CHUNK ? slots * 2 * (width / 256) * 4 : 0);  // a chunk's group, and its row's groups
   l.total = at;
   return l;
 }

@@ -25,7 +25,8 @@ using namespace dev;
 
 namespace {
 
-// Running maximum and sum of exp(x - max) of one thread's elements.
+// Running maximum and sum of exp(x - max) of one thread's elements.  (fmaf is
+// spelled out so that the same order gives the same bits in every kernel.)
 struct Online {
   float m = kLowest, s = 0.f;
   template <int N>
@@ -34,25 +35,30 @@ struct Online {
 #pragma unroll
     for (int k = 1; k < N; ++k) t = fmaxf(t, v[k]);
     const float n = fmaxf(m, t);
-    s *= exp_term(m, n);
+    s = fmaf(s, exp_term(m, n), exp_term(v[0], n));
     m = n;
 #pragma unroll
-    for (int k = 0; k < N; ++k) s += exp_term(v[k], m);
+    for (int k = 1; k < N; ++k) s += exp_term(v[k], m);
   }
   __device__ __forceinline__ void join(float m2, float s2) {
     const float n = fmaxf(m, m2);
-    s = s * exp_term(m, n) + s2 * exp_term(m2, n);
+    s = fmaf(s, exp_term(m, n), s2 * exp_term(m2, n));
     m = n;
   }
 };
 
-template <int WAVES>
-__device__ __forceinline__ Online block_join(Online o, float *red) {
+__device__ __forceinline__ Online wave_join(Online o) {
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) {
     const float m = __shfl_xor(o.m, d), s = __shfl_xor(o.s, d);
     o.join(m, s);
   }
+  return o;
+}
+
+template <int WAVES>
+__device__ __forceinline__ Online block_join(Online o, float *red) {
+  o = wave_join(o);
   const int w = threadIdx.x >> 6;
   if ((threadIdx.x & 63) == 0) {
     red[2 * w] = o.m;
@@ -139,6 +145,68 @@ __global__ __launch_bounds__(THREADS, UNROLL > 4 ? 4 : 8) void kl_rows(LogitArgs
 
 namespace {
 
+// A short row in the registers of one wave: VECS 16-byte vectors a lane, and
+// up to two of the single elements (fewer than 80) at the row's ends.
+template <bool BF16, int VECS>
+struct ShortRow {
+  typedef Elem<BF16> E;
+  uint4 in[VECS];
+  float lone[2];
+  __device__ __forceinline__ ShortRow(const typename E::type *x, const Row<BF16> &row) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int k = 0; k < VECS; ++k) in[k] = lane + 64 * k < row.vecs ? load16(x + row.col(lane + 64 * k)) : E::none();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) lone[k] = lane + 64 * k < row.singles() ? E::get(x[row.single(lane + 64 * k)]) : -INFINITY;
+  }
+  __device__ __forceinline__ Online sum() const {
+    Online o;
+#pragma unroll
+    for (int k = 0; k < VECS; ++k) {
+      float v[E::N];
+      E::unpack(in[k], v);
+      o.template add<E::N>(v);
+    }
+    o.template add<2>(lone);
+    return wave_join(o);
+  }
+};
+
+}  // namespace
+
+// Short rows, a wave each: no barrier, and the row's own arithmetic of one wave
+// runs beside the others' loads.
+template <bool BF16, int VECS>
+__global__ __launch_bounds__(256) void kl_rows_short(LogitArgs a, RowStat *stat, RowGrad *grad, float *logp, float *lse) {
+  typedef Elem<BF16> E;
+  const int lane = threadIdx.x & 63;
+  const int64_t r = a.row0 + (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (r >= a.rows) return;
+  const int64_t target = index_at(a.targets, r);
+  if (grad && lane == 0) grad[r] = RowGrad{0.f, 0.f, 0.f, 0};
+  if (target < 0 || target >= a.vocab) {
+    if (lane == 0) {
+      if (stat) stat[r] = RowStat{0.f, 0.f, 0.0, 0.0};
+      if (logp) logp[r] = 0.f;
+      if (lse) lse[r] = 0.f;
+    }
+    return;
+  }
+  const typename E::type *x = static_cast<const typename E::type *>(a.logits) + r * a.ld;
+  const float at_target = E::get(x[target]);
+  const Row<BF16> row(x, a.vocab);
+  const Online o = ShortRow<BF16, VECS>(x, row).sum();
+  if (lane == 0) {
+    const double log_total = log((double)o.s);
+    const double lp = (double)at_target - (double)o.m - log_total;
+    if (stat) stat[r] = RowStat{o.m, o.s, lp, expm1(lp)};
+    if (logp) logp[r] = (float)lp;
+    if (lse) lse[r] = (float)((double)o.m + log_total);
+  }
+}
+
+namespace {
+
 // Vectors of a row that a thread of the policy kernel keeps: the first ones in
 // LDS (64 KB a workgroup of 1024, two of them on a CU), the others in registers.
 constexpr int KEEP_LDS = 4, KEEP_REGS = 2, KEEP = KEEP_LDS + KEEP_REGS;
@@ -149,8 +217,8 @@ constexpr int KEEP_LDS = 4, KEEP_REGS = 2, KEEP = KEEP_LDS + KEEP_REGS;
 // call time, 131072 bf16 columns: 8 rows 15.6 21.4, 64 15.8 22.8, 128 22.7
 // 23.7, 250 38 33.
 constexpr int FEW_ROWS = 128, FEW_ROW = 8192, FEW_GROUPS = 1024, FEW_VECS = 512;
-// Rows whose terms one workgroup adds up.
-constexpr int64_t SUM_ROWS = 16384;
+// Workgroups that add up the rows' terms, at most; one for every SUM_ROWS rows.
+constexpr int SUM_GROUPS = 256, SUM_ROWS = 1024;
 // Loads of the rest under way at a time.
 constexpr int AHEAD = 2;
 
@@ -168,17 +236,18 @@ struct PolicyCoef {
 };
 
 __device__ __forceinline__ PolicyRow policy_row(const PolicyArgs &p, int64_t r, float weight, float at_target) {
+  const int lane = threadIdx.x & 63;
   PolicyRow q{weight, at_target, 0.f, p.advantages[r]};
-  if (threadIdx.x == 0 && p.old_logp) q.other = p.old_logp[r];
-  if (threadIdx.x == 1 && p.ref_logp) q.other = p.ref_logp[r];
+  if (lane == 0 && p.old_logp) q.other = p.old_logp[r];
+  if (lane == 1 && p.ref_logp) q.other = p.ref_logp[r];
   return q;
 }
 
-// A row's loss and derivative, by the first wave in fp64: its lanes 0 to 2
+// A row's loss and derivative, by one wave in fp64: its lanes 0 to 2
 // share a call of expm1.  Lane 0 writes logp and the four terms if asked to.
 __device__ __forceinline__ PolicyCoef policy_coef(const PolicyArgs &p, const PolicyRow &q, Online o, int64_t r,
                                                   int64_t rows, bool write, double *terms) {
-  const int lane = threadIdx.x;
+  const int lane = threadIdx.x & 63;
   const double logp = (double)q.at_target - (double)o.m - log((double)o.s);
   // lane 0: the ratio, lane 1: the KL term, lane 2: the target's own share
   double arg = 0.0;
@@ -226,7 +295,7 @@ __device__ __forceinline__ PolicyCoef policy_coef(const PolicyArgs &p, const Pol
 //   nothing kept, ordinary stores            3.6    4.5    4.7         3.6
 template <bool BF16, int THREADS>
 __global__ __launch_bounds__(THREADS, 8) void kl_policy(LogitArgs a, PolicyArgs p, void *dlogits, int64_t dld,
-                                                        double *terms) {
+                                                        double *terms, int32_t *done) {
   typedef Elem<BF16> E;
   typedef typename E::type T;
   __shared__ float red[2 * THREADS / 64];
@@ -234,6 +303,7 @@ __global__ __launch_bounds__(THREADS, 8) void kl_policy(LogitArgs a, PolicyArgs 
   __shared__ uint4 held[KEEP_LDS][THREADS];
   const int64_t r = a.row0 + blockIdx.x;
   const int tid = threadIdx.x;
+  if (r == 0 && tid == 0) *done = 0;
   const int64_t target = index_at(a.targets, r);
   const float w = p.weights[r];
   T *d = static_cast<T *>(dlogits) + r * dld;
@@ -328,25 +398,88 @@ __global__ __launch_bounds__(THREADS, 8) void kl_policy(LogitArgs a, PolicyArgs 
   if (in_vec ? at / E::N % THREADS == tid : lone && row.single(tid) == (uint32_t)target) d[target] = E::put(dt);
 }
 
-// The four sums over the rows, in a fixed order, SUM_ROWS rows a workgroup and
-// four of its waves a sum; into stats if there is one workgroup, otherwise
-// into part, the next launch's terms.
-__global__ __launch_bounds__(1024) void kl_policy_sum(const double *terms, int64_t rows, double *part, float *stats) {
+// The same for short rows, a wave each.
+template <bool BF16, int VECS>
+__global__ __launch_bounds__(256) void kl_policy_short(LogitArgs a, PolicyArgs p, void *dlogits, int64_t dld,
+                                                       double *terms, int32_t *done) {
+  typedef Elem<BF16> E;
+  typedef typename E::type T;
+  const int lane = threadIdx.x & 63;
+  const int64_t r = a.row0 + (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (r >= a.rows) return;
+  if (r == 0 && lane == 0) *done = 0;
+  const int64_t target = index_at(a.targets, r);
+  const float w = p.weights[r];
+  T *d = static_cast<T *>(dlogits) + r * dld;
+  if (target < 0 || target >= a.vocab || w == 0.f) {
+    const Row<BF16> out(d, a.vocab);
+    for (int i = lane; i < out.vecs; i += 64) stream16(d + out.col(i), make_uint4(0, 0, 0, 0));
+    for (int i = lane; i < out.singles(); i += 64) d[out.single(i)] = T(0);
+    if (lane < 4) terms[lane * a.rows + r] = 0.0;
+    if (lane == 0) p.logp[r] = 0.f;
+    return;
+  }
+  const T *x = static_cast<const T *>(a.logits) + r * a.ld;
+  const PolicyRow q = policy_row(p, r, w, E::get(x[target]));
+  const Row<BF16> row(x, a.vocab);
+  const ShortRow<BF16, VECS> held(x, row);
+  const Online o = held.sum();
+  const PolicyCoef own = policy_coef(p, q, o, r, a.rows, true, terms);
+  const float c = __shfl(own.c, 0), dt = __shfl(own.dt, 0);
+  const int rel = (int)target - row.head;
+#pragma unroll
+  for (int k = 0; k < VECS; ++k) {
+    const int i = lane + 64 * k;
+    if (i >= row.vecs) continue;
+    float v[E::N];
+    E::unpack(held.in[k], v);
+#pragma unroll
+    for (int j = 0; j < E::N; ++j) v[j] = rel - i * E::N == j ? dt : c * exp_shift(v[j], o.m);
+    stream16(d + row.col(i), E::pack(v));
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (lane + 64 * k >= row.singles()) continue;
+    const int j = row.single(lane + 64 * k);
+    d[j] = E::put(j == target ? dt : c * exp_shift(held.lone[k], o.m));
+  }
+}
+
+// The four sums over the rows, in a fixed order, four of a workgroup's waves a
+// sum; the last workgroup to finish adds up the workgroups' sums.  done was
+// cleared by the rows' kernel.
+__global__ __launch_bounds__(1024) void kl_policy_sum(const double *terms, int64_t rows, double *part, int32_t *done,
+                                                      float *stats) {
   __shared__ double red[16];
-  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, kind = w & 3;
-  const int64_t r0 = (int64_t)blockIdx.x * SUM_ROWS, r1 = min(r0 + SUM_ROWS, rows);
+  __shared__ int last;
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, kind = w & 3, groups = gridDim.x;
+  const int64_t r0 = rows * blockIdx.x / groups, r1 = rows * (blockIdx.x + 1) / groups;
+  auto four = [&](double sum) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) sum += shfl_xor_f64(sum, d);
+    if (lane == 0) red[w] = sum;
+    __syncthreads();
+    const int k = threadIdx.x & 3;
+    sum = red[k] + red[k + 4] + red[k + 8] + red[k + 12];
+    __syncthreads();
+    return sum;  // thread k has sum k
+  };
   double sum = 0.0;
 #pragma unroll 8
   for (int64_t r = r0 + (w >> 2) * 64 + lane; r < r1; r += 256) sum += terms[kind * rows + r];
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) sum += shfl_xor_f64(sum, d);
-  if (lane == 0) red[w] = sum;
-  __syncthreads();
-  if (threadIdx.x < 4) {
-    sum = red[threadIdx.x] + red[threadIdx.x + 4] + red[threadIdx.x + 8] + red[threadIdx.x + 12];
-    if (stats) stats[threadIdx.x] = (float)sum;
-    else part[threadIdx.x * gridDim.x + blockIdx.x] = sum;
+  sum = four(sum);
+  if (groups > 1) {
+    if (threadIdx.x < 4) put_shared(&part[threadIdx.x * groups + blockIdx.x], sum);
+    if (threadIdx.x < 64) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // of all lanes
+      if (threadIdx.x == 0) last = arrive(done) == groups - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    const int i = (w >> 2) * 64 + lane;
+    sum = four(i < groups ? get_shared(&part[kind * groups + i]) : 0.0);
   }
+  if (threadIdx.x < 4) stats[threadIdx.x] = (float)sum;
 }
 
 namespace {
@@ -412,11 +545,7 @@ __global__ __launch_bounds__(256, 8) void kl_policy_few(LogitArgs a, PolicyArgs 
         o.m = part[r * pieces + tid].max;
         o.s = part[r * pieces + tid].sum;
       }
-#pragma unroll
-      for (int k = 32; k > 0; k >>= 1) {
-        const float m = __shfl_xor(o.m, k), s = __shfl_xor(o.s, k);
-        o.join(m, s);
-      }
+      o = wave_join(o);
       const PolicyCoef g = policy_coef(p, q, o, r, a.rows, piece == 0, terms);
       if (tid == 0) {
         coef[0] = g.c;
@@ -583,6 +712,48 @@ __global__ __launch_bounds__(256) void kl_grad(LogitArgs a, const RowGrad *grad,
   if (piece == 0 && (int)threadIdx.x < row.singles()) {
     const int j = row.single(threadIdx.x);
     d[j] = E::put(j == target ? g.dt : g.c * exp_shift(E::get(x[j]), g.max));
+  }
+}
+
+// The same for short rows, a wave each.
+template <bool BF16, int VECS>
+__global__ __launch_bounds__(256) void kl_grad_short(LogitArgs a, const RowGrad *grad, void *dlogits, int64_t dld,
+                                                     PreferenceArgs p, const double *losses) {
+  typedef Elem<BF16> E;
+  typedef typename E::type T;
+  __shared__ double red[4];
+  if (blockIdx.x == 0) mean_loss<256>(p, losses, red);
+  const int lane = threadIdx.x & 63;
+  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (r >= a.rows) return;
+  const RowGrad g = grad[r];
+  T *d = static_cast<T *>(dlogits) + r * dld;
+  if (!g.live) {
+    const Row<BF16> out(d, a.vocab);
+    for (int i = lane; i < out.vecs; i += 64) stream16(d + out.col(i), make_uint4(0, 0, 0, 0));
+    for (int i = lane; i < out.singles(); i += 64) d[out.single(i)] = T(0);
+    return;
+  }
+  const int64_t target = index_at(a.targets, r);
+  const T *x = static_cast<const T *>(a.logits) + r * a.ld;
+  const Row<BF16> row(x, a.vocab);
+  const ShortRow<BF16, VECS> held(x, row);
+  const int rel = (int)target - row.head;
+#pragma unroll
+  for (int k = 0; k < VECS; ++k) {
+    const int i = lane + 64 * k;
+    if (i >= row.vecs) continue;
+    float v[E::N];
+    E::unpack(held.in[k], v);
+#pragma unroll
+    for (int j = 0; j < E::N; ++j) v[j] = rel - i * E::N == j ? g.dt : g.c * exp_shift(v[j], g.max);
+    stream16(d + row.col(i), E::pack(v));
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (lane + 64 * k >= row.singles()) continue;
+    const int j = row.single(lane + 64 * k);
+    d[j] = E::put(j == target ? g.dt : g.c * exp_shift(held.lone[k], g.max));
   }
 }
 
@@ -854,14 +1025,31 @@ hipError_t by_rows(LogitArgs a, int64_t rows, F launch) {
   return hipSuccess;
 }
 
-// 256 threads where 512 would have fewer than two rounds of loads: 20000 x
-// 4096 bf16 take 35 us instead of 56, 4000 x 1000 7 instead of 11; from there
-// on 512 are as fast or faster (100 x 50257 fp32 6.7 against 8.3).  Where
-// every row can have a CU to itself, 1024 and eight loads under way.
+// Vectors a lane of a row that one wave holds; 0: the row is too long for that.
+// 8192 rows, in us, a wave and a workgroup of 256 a row: log-probability, 1000
+// bf16 columns 8.3 12.4, 4096 15.7 17.3, 2000 fp32 13.2 15.9; policy loss
+// 18.8 28.3, 29.5 32.7, 27.9 29.6; preference loss 20.4 30.4, 42.8 43.0, 39.4
+// 41.5; 300 rows the same either way.
+template <bool BF16>
+int short_vecs(int64_t vocab) {
+  for (int vecs = 2; vecs <= 8; vecs *= 2)
+    if (vocab <= 64 * vecs * Elem<BF16>::N) return vecs;
+  return 0;
+}
+
+// 256 threads where 512 would have fewer than two rounds of loads (20000 x
+// 4096 bf16: 35 us instead of 56); from there on 512 are as fast or faster
+// (100 x 50257 fp32 6.7 against 8.3).  Where every row can have a CU to itself,
+// 1024 and eight loads under way (32 x 131072: 10.3 us instead of 11.0).
 template <bool BF16>
 hipError_t rows_launch(const LogitArgs &a, RowStat *stat, RowGrad *grad, float *logp, float *lse, hipStream_t s) {
+  const int vecs = short_vecs<BF16>(a.vocab);
   return by_rows(a, a.rows, [&](const LogitArgs &a, dim3 g) {
-    if (a.vocab <= 1024 * Elem<BF16>::N) hipLaunchKernelGGL((kl_rows<BF16, 256, 4>), g, dim3(256), 0, s, a, stat, grad, logp, lse);
+    const dim3 g4((g.x + 3) / 4);
+    if (vecs == 2) hipLaunchKernelGGL((kl_rows_short<BF16, 2>), g4, dim3(256), 0, s, a, stat, grad, logp, lse);
+    else if (vecs == 4) hipLaunchKernelGGL((kl_rows_short<BF16, 4>), g4, dim3(256), 0, s, a, stat, grad, logp, lse);
+    else if (vecs == 8) hipLaunchKernelGGL((kl_rows_short<BF16, 8>), g4, dim3(256), 0, s, a, stat, grad, logp, lse);
+    else if (a.vocab <= 1024 * Elem<BF16>::N) hipLaunchKernelGGL((kl_rows<BF16, 256, 4>), g, dim3(256), 0, s, a, stat, grad, logp, lse);
     else if (a.rows <= 256 && a.vocab >= 8192 * Elem<BF16>::N) hipLaunchKernelGGL((kl_rows<BF16, 1024, 8>), g, dim3(1024), 0, s, a, stat, grad, logp, lse);
     else hipLaunchKernelGGL((kl_rows<BF16, 512, 4>), g, dim3(512), 0, s, a, stat, grad, logp, lse);
   });
@@ -875,10 +1063,10 @@ hipError_t launch_token_logprob(const LogitArgs &a, bool bf16, float *logp, floa
 
 PolicyLayout policy_layout(int64_t rows) {
   PolicyLayout l{};
-  const size_t n = (size_t)std::max<int64_t>(rows, 1), groups = (n + SUM_ROWS - 1) / SUM_ROWS;
-  l.terms = 0;
-  l.part = up256(4 * sizeof(double) * n);  // the few rows' pieces and count, or the sums' partial sums
-  l.total = l.part + std::max(2 * up256(4 * sizeof(double) * groups), 256 + up256(sizeof(PieceStat) * FEW_GROUPS));
+  l.done = 0;
+  l.part = 256;  // the few rows' pieces, or the workgroups' sums
+  l.terms = l.part + up256(std::max(sizeof(PieceStat) * FEW_GROUPS, 4 * sizeof(double) * SUM_GROUPS));
+  l.total = l.terms + up256(4 * sizeof(double) * (size_t)std::max<int64_t>(rows, 1));
   return l;
 }
 
@@ -888,12 +1076,12 @@ template <bool BF16>
 hipError_t policy_launch(const LogitArgs &a, const PolicyArgs &p, void *dlogits, int64_t dld, char *ws, hipStream_t s) {
   const PolicyLayout l = policy_layout(a.rows);
   double *terms = reinterpret_cast<double *>(ws + l.terms);
+  int32_t *done = reinterpret_cast<int32_t *>(ws + l.done);
   const int64_t vecs = a.vocab / Elem<BF16>::N;
   if (a.rows > 0 && a.rows <= FEW_ROWS && vecs >= FEW_ROW) {
     static_assert(FEW_GROUPS / FEW_ROWS >= 2 && FEW_ROW / FEW_VECS >= 2, "two pieces at least");
     const int64_t pieces = std::min<int64_t>({FEW_GROUPS / a.rows, vecs / FEW_VECS, 64});  // a lane a piece joins them
-    int32_t *done = reinterpret_cast<int32_t *>(ws + l.part);
-    PieceStat *part = reinterpret_cast<PieceStat *>(ws + l.part + 256);
+    PieceStat *part = reinterpret_cast<PieceStat *>(ws + l.part);
     const dim3 g((unsigned)(a.rows * pieces));
     hipLaunchKernelGGL(kl_policy_pieces<BF16>, g, dim3(256), 0, s, a, p.weights, (int)pieces, part, done);
     const hipError_t e = hipGetLastError();
@@ -901,20 +1089,20 @@ hipError_t policy_launch(const LogitArgs &a, const PolicyArgs &p, void *dlogits,
     hipLaunchKernelGGL(kl_policy_few<BF16>, g, dim3(256), 0, s, a, p, (int)pieces, part, dlogits, dld, terms, done);
     return hipGetLastError();
   }
+  const int held = short_vecs<BF16>(a.vocab);
   hipError_t e = by_rows(a, a.rows, [&](const LogitArgs &a, dim3 g) {
-    if (vecs <= 256 * KEEP) hipLaunchKernelGGL((kl_policy<BF16, 256>), g, dim3(256), 0, s, a, p, dlogits, dld, terms);
-    else hipLaunchKernelGGL((kl_policy<BF16, 1024>), g, dim3(1024), 0, s, a, p, dlogits, dld, terms);
+    const dim3 g4((g.x + 3) / 4);
+    if (held == 2) hipLaunchKernelGGL((kl_policy_short<BF16, 2>), g4, dim3(256), 0, s, a, p, dlogits, dld, terms, done);
+    else if (held == 4) hipLaunchKernelGGL((kl_policy_short<BF16, 4>), g4, dim3(256), 0, s, a, p, dlogits, dld, terms, done);
+    else if (held == 8) hipLaunchKernelGGL((kl_policy_short<BF16, 8>), g4, dim3(256), 0, s, a, p, dlogits, dld, terms, done);
+    else if (vecs <= 256 * KEEP) hipLaunchKernelGGL((kl_policy<BF16, 256>), g, dim3(256), 0, s, a, p, dlogits, dld, terms, done);
+    else hipLaunchKernelGGL((kl_policy<BF16, 1024>), g, dim3(1024), 0, s, a, p, dlogits, dld, terms, done);
   });
   if (e != hipSuccess) return e;
-  double *part = reinterpret_cast<double *>(ws + l.part);
-  for (int64_t n = a.rows;;) {
-    const int64_t groups = std::max<int64_t>(1, (n + SUM_ROWS - 1) / SUM_ROWS);
-    hipLaunchKernelGGL(kl_policy_sum, dim3((unsigned)groups), dim3(1024), 0, s, terms, n, part, groups == 1 ? p.stats : nullptr);
-    if ((e = hipGetLastError()) != hipSuccess || groups == 1) return e;
-    n = groups;
-    terms = part;
-    part += up256(4 * sizeof(double) * (size_t)groups) / sizeof(double);
-  }
+  const int64_t groups = std::min<int64_t>(SUM_GROUPS, std::max<int64_t>(1, a.rows / SUM_ROWS));
+  hipLaunchKernelGGL(kl_policy_sum, dim3((unsigned)groups), dim3(1024), 0, s, terms, a.rows, reinterpret_cast<double *>(ws + l.part), done,
+                     p.stats);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -980,6 +1168,13 @@ hipError_t preference_launch(const LogitArgs &a, const PreferenceArgs &p, void *
   if ((e = rows_launch<BF16>(a, w.stat, grad, nullptr, nullptr, s)) != hipSuccess) return e;
   hipLaunchKernelGGL(kl_pairs, dim3((unsigned)p.pairs), dim3(1024), 0, s, a, p, w.stat, grad, w.losses);
   if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (const int held = short_vecs<BF16>(a.vocab)) {
+    const dim3 g((unsigned)std::max<int64_t>(1, (a.rows + 3) / 4));
+    if (held == 2) hipLaunchKernelGGL((kl_grad_short<BF16, 2>), g, dim3(256), 0, s, a, grad, dlogits, dld, p, w.losses);
+    else if (held == 4) hipLaunchKernelGGL((kl_grad_short<BF16, 4>), g, dim3(256), 0, s, a, grad, dlogits, dld, p, w.losses);
+    else hipLaunchKernelGGL((kl_grad_short<BF16, 8>), g, dim3(256), 0, s, a, grad, dlogits, dld, p, w.losses);
+    return hipGetLastError();
+  }
   // pieces of a row: 8192 elements or more
   const int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(a.vocab / 8192, 64));
   hipLaunchKernelGGL(kl_grad<BF16>, dim3((unsigned)std::max<int64_t>(1, a.rows * pieces)), dim3(256), 0, s, a, grad, dlogits, dld,

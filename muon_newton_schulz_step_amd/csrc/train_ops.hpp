@@ -32,6 +32,7 @@ hipError_t launch_embed_forward(const EmbedFwdArgs &a, bool bf16, hipStream_t s)
 
 constexpr int EB_BUCKETS = 256;  // bucket of a table row = row mod EB_BUCKETS
 constexpr int EB_CHUNK = 32;     // tokens of a row that one wave adds up, at most
+constexpr int EB_GROUP = 32;     // chunks whose sums are joined at a time
 constexpr int EB_LIGHT = 2;      // a row of more tokens is added up before one of these
 constexpr int EB_FEW = 1024;     // up to so many tokens need no sort
 
@@ -44,14 +45,15 @@ struct EbBucket {
 };
 
 // At most EB_CHUNK consecutive sorted tokens of one table row.  A row with
-// more tokens has several chunks, whose sums meet in the workspace.
+// more tokens has several chunks, whose sums meet in the workspace: EB_GROUP
+// chunks at a time, then the groups.
 struct EbChunk {
   int32_t row, start;
-  int32_t count;     // tokens of this chunk
-  int32_t parts;     // chunks of the row (1: the chunk writes the row itself)
-  int32_t seg;       // the row's first sorted position
-  int32_t seg_count; // the row's tokens
-  int32_t tok0;      // the row's first token
+  int32_t count;  // tokens of this chunk
+  int32_t parts;  // chunks of the row (1: the chunk writes the row itself)
+  int32_t index;  // this chunk's place among them
+  int32_t slot0;  // the first chunk's slot in the partial sums, the others' follow
+  int32_t tok0;   // the row's first token
   int32_t pad;
 };
 
@@ -120,7 +122,7 @@ struct PreferenceArgs {
 hipError_t launch_token_logprob(const LogitArgs &a, bool bf16, float *logp, float *lse, hipStream_t s);
 
 struct PolicyLayout {
-  size_t terms, part, total;
+  size_t done, part, terms, total;
 };
 PolicyLayout policy_layout(int64_t rows);
 hipError_t launch_policy(const LogitArgs &a, const PolicyArgs &p, bool bf16, void *dlogits, int64_t dld, char *ws,

@@ -25,8 +25,9 @@ using namespace dev;
 
 namespace {
 
-// Running maximum and sum of exp(x - max) of one thread's elements.  (fmaf is
-// spelled out so that the same order gives the same bits in every kernel.)
+// Running maximum and sum of exp(x - max) of one thread's elements.  (Which
+// products are fused is spelled out, so that the same order gives the same
+// bits in every kernel.)
 struct Online {
   float m = kLowest, s = 0.f;
   template <int N>
@@ -40,9 +41,12 @@ struct Online {
 #pragma unroll
     for (int k = 1; k < N; ++k) s += exp_term(v[k], m);
   }
+  // symmetric in its halves: lanes that join the same two get the same bits
   __device__ __forceinline__ void join(float m2, float s2) {
+#pragma clang fp contract(off)
     const float n = fmaxf(m, m2);
-    s = fmaf(s, exp_term(m, n), s2 * exp_term(m2, n));
+    const float mine = s * exp_term(m, n), other = s2 * exp_term(m2, n);
+    s = mine + other;
     m = n;
   }
 };

@@ -93,7 +93,8 @@ hipError_t launch_embed_forward(const EmbedFwdArgs &a, bool bf16, hipStream_t s)
 // the workgroups.  A bucket of at most ES_SMALL tokens is sorted by counting,
 // for each token, the smaller keys in LDS; a larger one by a stable
 // least-digit-first radix sort whose digit of 10 bits covers a table of 2^18
-// rows in one pass.
+// rows in one pass.  Bound by the latency of its dependent steps: 27 us at
+// 16384 tokens, 46 with half of the zeros of 32000 x 4096 beside it.
 //
 // At the first call of a step, as many workgroups more write zeros into rows
 // without a token, one bucket's each: the sort waits for memory and the zeros
@@ -408,7 +409,10 @@ __global__ __launch_bounds__(ES_THREADS, 8) void ke_sort(EmbedBwdArgs a, int pas
 // meets another bucket at each turn (141 us a call against 167 with always the
 // same, at 16384 tokens of 4096 columns, as the frequent rows' buckets are
 // fuller).  At that size the kernel takes 80 us beside half of the zeros, for
-// 440 MB: 5.5 TB/s.
+// 440 MB: 5.5 TB/s.  Chunk sums of one row are joined 32 at a time and then the
+// groups: of 32768 tokens of 4096 columns with 30% in one row a call takes 265
+// us, 410 if its last chunk adds up all the others (and one thread of the sort
+// lists them).
 template <bool BF16, int VECS>
 __global__ __launch_bounds__(256) void ke_add(EmbedBwdArgs a, int col_blocks, int zeros) {
   typedef Elem<BF16> E;

@@ -179,7 +179,9 @@ struct ShortRow {
 }  // namespace
 
 // Short rows, a wave each: no barrier, and the row's own arithmetic of one wave
-// runs beside the others' loads.
+// runs beside the others' loads.  Bound by the latency of target, row and join
+// (8192 x 1000 bf16: 7.7 us, the policy loss's 13); two to four rows a wave,
+// whose fp64 functions are then called once, take as long.
 template <bool BF16, int VECS>
 __global__ __launch_bounds__(256) void kl_rows_short(LogitArgs a, RowStat *stat, RowGrad *grad, float *logp, float *lse) {
   typedef Elem<BF16> E;

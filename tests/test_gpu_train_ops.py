@@ -123,6 +123,20 @@ def test_lookup(torch, n, vocab, dim, kind, dtype, idt, ld, shift):
     assert around_untouched(torch, out, obuf)
 
 
+@pytest.mark.parametrize("dtype,dim,ld", [("bf16", 4096, 4096), ("bf16", 4099, 4101), ("fp32", 2050, 2051)])
+def test_lookup_of_many_tokens(torch, dtype, dim, ld):
+    # outputs of 64 MB and more take another way to memory
+    n, vocab = 9000, 700
+    g = torch.Generator(DEV).manual_seed(1)
+    tab = torch.empty(vocab, ld, dtype=dt(torch, dtype), device=DEV).normal_(generator=g)[:, :dim]
+    ids = torch.randint(-30, vocab + 30, (n,), generator=g, device=DEV)
+    buf = torch.full((n, ld), 7.0, dtype=tab.dtype, device=DEV)
+    M.embed_forward(tab, ids, buf[:, :dim], scale=2.0)  # twice a value: exact
+    has = (ids >= 0) & (ids < vocab)
+    assert torch.equal(buf[:, :dim], torch.where(has[:, None], tab[ids.clamp(0, vocab - 1)] * 2.0, 0.0).to(tab.dtype))
+    assert bool((buf[:, dim:] == 7.0).all())
+
+
 def check_embed_grad(torch, n, vocab, dim, kind, dtype, idt, first, ld=0, shift=0, scale=1.75, seed=0):
     rng = np.random.default_rng(1000 + n + vocab + seed)
     ids = make_ids(rng, n, vocab, kind)
@@ -168,7 +182,8 @@ def test_embedding_gradient_layouts(torch, n, vocab, dim, kind, dtype, idt, ld, 
 
 
 @pytest.mark.parametrize("first", [True, False])
-@pytest.mark.parametrize("n,vocab,dim", [(3000, 600000, 9), (1024, 600000, 8), (1025, 600000, 8), (40000, 300, 24)])
+@pytest.mark.parametrize("n,vocab,dim", [(3000, 600000, 9), (1024, 600000, 8), (1025, 600000, 8), (40000, 300, 24),
+                                         (9000, 10240, 24)])  # the last: 40 rows of many chunks in one bucket
 def test_embedding_gradient_of_one_bucket(torch, n, vocab, dim, first):
     # rows a multiple of 256 apart meet in one bucket of the sort: more than it sorts by counting, and keys of more
     # bits than one radix pass takes

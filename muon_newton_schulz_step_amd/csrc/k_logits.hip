@@ -1181,8 +1181,9 @@ hipError_t preference_launch(const LogitArgs &a, const PreferenceArgs &p, void *
     else hipLaunchKernelGGL((kl_grad_short<BF16, 8>), g, dim3(256), 0, s, a, grad, dlogits, dld, p, w.losses);
     return hipGetLastError();
   }
-  // pieces of a row: 8192 elements or more
-  const int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(a.vocab / 8192, 64));
+  // pieces of a row: 8192 elements or more, and a grid that stays in range
+  const int64_t most = 4 * ROWS_A_LAUNCH / std::max<int64_t>(a.rows, 1);
+  const int64_t pieces = std::max<int64_t>(1, std::min<int64_t>({a.vocab / 8192, 64, most}));
   hipLaunchKernelGGL(kl_grad<BF16>, dim3((unsigned)std::max<int64_t>(1, a.rows * pieces)), dim3(256), 0, s, a, grad, dlogits, dld,
                      (int)pieces, p, w.losses);
   return hipGetLastError();

@@ -397,7 +397,9 @@ muon_status muon_embed_backward(const void *ids, int32_t id_type, int64_t tokens
  * [0, vocab) has none: it is not read, its log-probability is 0 and so is
  * its gradient.  -inf logits are probabilities of 0; a row with a target
  * and nothing but -inf has lse = -inf and a NaN log-probability; NaN and
- * +inf propagate within their row and the sums it enters.
+ * +inf propagate within their row and the sums it enters.  A term of a loss
+ * whose factor is 0 is 0 also where a target of probability 0 makes the
+ * rest of it infinite.
  * Limits: rows < 2^31, vocab < 2^29. */
 typedef struct {
   const void *logits;

@@ -75,6 +75,10 @@ __device__ __forceinline__ Online block_join(Online o, float *red) {
   return t;
 }
 
+// c v, where a factor of 0 leaves nothing of an infinite value (a target of
+// probability 0); NaN stays NaN.
+__device__ __forceinline__ double times(double c, double v) { return c == 0.0 && fabs(v) == INFINITY ? 0.0 : c * v; }
+
 // Maximum and sum of a row's vectors [v0, v1), and of its single elements if
 // asked for, by a workgroup; every thread gets them.
 template <bool BF16, int THREADS, int UNROLL = 4>
@@ -626,7 +630,7 @@ __device__ __forceinline__ double pair_loss(const PreferenceArgs &p, int64_t i, 
     p.rewards[i + p.pairs] = (float)(p.beta * gain[1]);
     // softplus(-m) and softplus(m) without overflow
     const double l = log1p(q);
-    put_shared(loss, (1.0 - p.smoothing) * (fmax(-m, 0.0) + l) + p.smoothing * (fmax(m, 0.0) + l));
+    put_shared(loss, times(1.0 - p.smoothing, fmax(-m, 0.0) + l) + times(p.smoothing, fmax(m, 0.0) + l));
   }
   return p.beta * (sig - (1.0 - p.smoothing)) / (double)p.pairs;
 }

@@ -47,6 +47,12 @@ def token_logprob(x, targets):
     return np.where(has, lp[np.arange(len(at)), at], 0.0), np.where(has, lse, 0.0)
 
 
+def times(c, v):
+    """c v, where a factor of 0 leaves nothing of an infinite value."""
+    with np.errstate(invalid="ignore"):
+        return np.where((np.asarray(c) == 0.0) & np.isinf(v), 0.0, np.multiply(c, v))
+
+
 def logit_grad(x, targets, dlogp):
     """sum_r dlogp[r] logp[r] by the logits; rows whose dlogp is 0 get 0."""
     x = np.asarray(x, dtype=np.float64)
@@ -94,7 +100,7 @@ def preference_loss(x, targets, offsets, ref_logp, beta=0.1, label_smoothing=0.0
     pairs = seqs // 2
     gain = np.array([logp[offsets[s]:offsets[s + 1]].sum() - float(ref_logp[s]) for s in range(seqs)])
     m = beta * (gain[:pairs] - gain[pairs:])
-    loss = ((1.0 - label_smoothing) * np.logaddexp(0.0, -m) + label_smoothing * np.logaddexp(0.0, m)).mean()
+    loss = (times(1.0 - label_smoothing, np.logaddexp(0.0, -m)) + times(label_smoothing, np.logaddexp(0.0, m))).mean()
     sig = np.exp(-np.logaddexp(0.0, -m))
     c = beta / pairs * (sig - (1.0 - label_smoothing))
     dlogp = np.zeros(n)

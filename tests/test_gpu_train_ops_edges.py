@@ -1,0 +1,68 @@
+"""The losses at the ends of their range, on the GPU: terms whose factor is 0 beside infinities, margins of any size,
+rows that hold NaN.  Expected values are written out from the formulas in fp64; tolerances as in
+test_gpu_train_ops.py (e = 2^-24, half a step of fp32; h = half a step of the output's type)."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import muon_newton_schulz_step_amd as M
+from test_gpu_train_ops import DEV, E, HALF, TINY, dt, f64, poisoned, torch, vec, within  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+def preference(torch, x, t, ref, beta, smooth, off=None):
+    """(loss, rewards, dlogits) of a call."""
+    seqs = len(ref)
+    off = np.arange(seqs + 1) if off is None else off
+    loss, rew = torch.full((1,), 9.0, device=DEV), torch.full((seqs,), 9.0, device=DEV)
+    d = torch.full_like(x, 9.0)
+    M.preference_loss(x, vec(torch, np.asarray(t), "int64"), vec(torch, np.asarray(off), "int64"),
+                      vec(torch, np.asarray(ref, dtype=np.float32)), loss, rew, d,
+                      poisoned(torch, M.preference_loss_workspace_bytes(x.shape[0], seqs // 2)), beta=beta,
+                      label_smoothing=smooth)
+    return f64(loss)[0], f64(rew), f64(d)
+
+
+def policy(torch, x, t, adv, old, ref, kl):
+    """(stats, logp, dlogits) of a call with weights 1 and clips 0.2 and 0.28."""
+    n = x.shape[0]
+    stats, logp, d = torch.full((4,), 9.0, device=DEV), torch.full((n,), 9.0, device=DEV), torch.full_like(x, 9.0)
+    opt = dict(old_logp=None if old is None else vec(torch, np.asarray(old, dtype=np.float32)),
+               ref_logp=None if ref is None else vec(torch, np.asarray(ref, dtype=np.float32)))
+    M.policy_loss(x, vec(torch, np.asarray(t), "int64"), vec(torch, np.asarray(adv, dtype=np.float32)),
+                  torch.ones(n, device=DEV), stats, logp, d, poisoned(torch, M.policy_loss_workspace_bytes(n)),
+                  clip_low=0.2, clip_high=0.28, kl_coef=kl, **opt)
+    return f64(stats), f64(logp), f64(d)
+
+
+def masked_pair(torch, dtype, side):
+    """Two pairs of one-row sequences over 8 equal logits; the target of pair 0's sequence on `side` (0: chosen) is
+    masked.  Rows: chosen 0, chosen 1, rejected 0, rejected 1."""
+    x = torch.zeros((4, 8), dtype=dt(torch, dtype), device=DEV)
+    x[2 * side, 2 * side] = -INF
+    return x, [0, 1, 2, 3]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("smooth", [0.0, 1.0])
+def test_preference_masked_target_without_the_other_label(torch, dtype, smooth):
+    # the masked sequence has log-probability -inf, so the margin is infinite on the side whose weight is 1: that
+    # pair's loss and gradient are 0, and the other label's infinite term has weight 0
+    side = 1 if smooth == 0.0 else 0
+    x, t = masked_pair(torch, dtype, side)
+    loss, rew, d = preference(torch, x, t, [0.0] * 4, 0.5, smooth)
+    within(loss, np.log(2) / 2, 100 * E, "loss")
+    want = np.full(4, -0.5 * np.log(8))
+    want[2 * side] = -INF
+    within(rew, want, 100 * E * 0.5, "rewards")
+    assert not d[0].any() and not d[2].any()
+    c = 0.5 / 2 * (0.5 - (1.0 - smooth))
+    for r, a in ((1, c), (3, -c)):
+        g = -a / 8 * np.ones(8)
+        g[r] += a
+        within(d[r], g, 100 * E * abs(c) + HALF[dtype] * np.abs(g) * 1.01, "dlogits")

@@ -68,6 +68,15 @@ def test_preference_definition_against_differences_and_by_hand():
     assert loss == pytest.approx(np.log(2)) and dl == pytest.approx([-0.15, 0.15])
 
 
+@pytest.mark.parametrize("smooth", [0.0, 1.0])
+def test_preference_definition_at_an_infinite_margin(smooth):
+    # the sequence that should lose has probability 0: loss and gradient 0, whatever the other label would cost
+    x = np.zeros((2, 4))
+    x[int(smooth == 0.0), 1] = -np.inf
+    loss, rew, d, _ = T.preference_loss(x, np.array([1, 1]), np.array([0, 1, 2]), np.zeros(2), 0.5, smooth)
+    assert loss == 0.0 and not d.any() and rew[int(smooth == 0.0)] == -np.inf
+
+
 def test_balance_definition_against_differences_and_by_hand():
     rng = np.random.default_rng(5)
     x, ch = rng.standard_normal((11, 5)), rng.integers(0, 5, (11, 2))

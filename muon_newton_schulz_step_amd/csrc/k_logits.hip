@@ -622,12 +622,13 @@ namespace {
 __device__ __forceinline__ double pair_loss(const PreferenceArgs &p, int64_t i, double chosen, double rejected,
                                             bool write, double *loss) {
   const double gain[2] = {chosen - (double)p.ref_logp[i], rejected - (double)p.ref_logp[i + p.pairs]};
-  const double m = p.beta * (gain[0] - gain[1]);
+  const double reward[2] = {times(p.beta, gain[0]), times(p.beta, gain[1])};
+  const double m = p.beta == 0.0 ? reward[0] - reward[1] : p.beta * (gain[0] - gain[1]);
   const double q = exp(-fabs(m));
   const double sig = (m >= 0.0 ? 1.0 : q) / (1.0 + q);
   if (write) {
-    p.rewards[i] = (float)(p.beta * gain[0]);
-    p.rewards[i + p.pairs] = (float)(p.beta * gain[1]);
+    p.rewards[i] = (float)reward[0];
+    p.rewards[i + p.pairs] = (float)reward[1];
     // softplus(-m) and softplus(m) without overflow
     const double l = log1p(q);
     put_shared(loss, times(1.0 - p.smoothing, fmax(-m, 0.0) + l) + times(p.smoothing, fmax(m, 0.0) + l));

@@ -99,7 +99,8 @@ def preference_loss(x, targets, offsets, ref_logp, beta=0.1, label_smoothing=0.0
     seqs = len(ref_logp)
     pairs = seqs // 2
     gain = np.array([logp[offsets[s]:offsets[s + 1]].sum() - float(ref_logp[s]) for s in range(seqs)])
-    m = beta * (gain[:pairs] - gain[pairs:])
+    rewards = times(beta, gain)
+    m = rewards[:pairs] - rewards[pairs:] if beta == 0.0 else beta * (gain[:pairs] - gain[pairs:])
     loss = (times(1.0 - label_smoothing, np.logaddexp(0.0, -m)) + times(label_smoothing, np.logaddexp(0.0, m))).mean()
     sig = np.exp(-np.logaddexp(0.0, -m))
     c = beta / pairs * (sig - (1.0 - label_smoothing))
@@ -107,7 +108,7 @@ def preference_loss(x, targets, offsets, ref_logp, beta=0.1, label_smoothing=0.0
     for s in range(seqs):
         dlogp[offsets[s]:offsets[s + 1]] = c[s] if s < pairs else -c[s - pairs]
     dlogp = np.where((targets >= 0) & (targets < v), dlogp, 0.0)
-    return loss, beta * gain, logit_grad(x, targets, dlogp), dlogp
+    return loss, rewards, logit_grad(x, targets, dlogp), dlogp
 
 
 def balance_loss(x, choices, valid=None, coef=0.01, z_coef=0.0):

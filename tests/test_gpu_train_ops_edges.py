@@ -66,3 +66,16 @@ def test_preference_masked_target_without_the_other_label(torch, dtype, smooth):
         g = -a / 8 * np.ones(8)
         g[r] += a
         within(d[r], g, 100 * E * abs(c) + HALF[dtype] * np.abs(g) * 1.01, "dlogits")
+
+
+@pytest.mark.parametrize("side", [0, 1])
+def test_preference_of_beta_zero(torch, side):
+    # beta 0: margins and rewards are 0, also of a sequence of log-probability -inf
+    x, t = masked_pair(torch, "fp32", side)
+    loss, rew, d = preference(torch, x, t, [0.0] * 4, 0.0, 0.1)
+    within(loss, np.log(2), 2 * E, "loss")
+    assert not rew.any() and not d.any()
+    # but NaN is not a factor's business
+    x[1, 5] = float("nan")
+    loss, rew, d = preference(torch, x, t, [0.0] * 4, 0.0, 0.1)
+    assert np.isnan(loss) and np.isnan(rew[1]) and not rew[[0, 2, 3]].any()

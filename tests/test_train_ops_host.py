@@ -77,6 +77,13 @@ def test_preference_definition_at_an_infinite_margin(smooth):
     assert loss == 0.0 and not d.any() and rew[int(smooth == 0.0)] == -np.inf
 
 
+def test_preference_definition_of_beta_zero():
+    x = np.zeros((2, 4))
+    x[1, 1] = -np.inf
+    loss, rew, d, _ = T.preference_loss(x, np.array([1, 1]), np.array([0, 1, 2]), np.zeros(2), 0.0, 0.1)
+    assert loss == pytest.approx(np.log(2)) and not rew.any() and not d.any()
+
+
 def test_balance_definition_against_differences_and_by_hand():
     rng = np.random.default_rng(5)
     x, ch = rng.standard_normal((11, 5)), rng.integers(0, 5, (11, 2))

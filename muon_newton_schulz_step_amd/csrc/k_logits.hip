@@ -266,7 +266,7 @@ __device__ __forceinline__ PolicyCoef policy_coef(const PolicyArgs &p, const Pol
   if (lane == 2) arg = logp;
   const double em1 = expm1(arg);
   const double ratio = 1.0 + shfl_f64(em1, 0), ed = shfl_f64(em1, 1), share = shfl_f64(em1, 2);
-  const double kl = ed - shfl_f64(arg, 1);
+  const double d = shfl_f64(arg, 1), kl = ed == INFINITY ? ed : ed - d;  // (d may be +inf too)
   const double adv = q.advantage, w = q.weight;
   const double clipped = fmin(fmax(ratio, 1.0 - p.clip_low), 1.0 + p.clip_high);
   const bool active = !(ratio * adv > clipped * adv);  // a NaN stays one

@@ -79,3 +79,14 @@ def test_preference_of_beta_zero(torch, side):
     x[1, 5] = float("nan")
     loss, rew, d = preference(torch, x, t, [0.0] * 4, 0.0, 0.1)
     assert np.isnan(loss) and np.isnan(rew[1]) and not rew[[0, 2, 3]].any()
+
+
+def test_policy_kl_of_a_target_of_probability_zero(torch):
+    # exp(d) - 1 - d at d = +inf is +inf, not inf - inf; at d = -inf likewise
+    x = torch.zeros((2, 8), device=DEV)
+    x[1, 4] = -INF
+    lp = -np.log(8)
+    for ref in ([lp, lp], [-INF, lp]):
+        stats, _, _ = policy(torch, x, [0, 4], [1.0, 1.0], [lp, lp], ref, 0.1)
+        assert stats[0] == INF and stats[2] == INF
+        within(stats[1], -1.0, 100 * E, "policy part")

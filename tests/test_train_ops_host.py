@@ -52,6 +52,15 @@ def test_policy_definition_by_hand():
     assert dl == pytest.approx([0.0, 2.0]) and d == pytest.approx(np.array([[0, 0], [-1.0, 1.0]]))
 
 
+def test_policy_definition_of_an_infinite_kl():
+    x = np.zeros((1, 4))
+    x[0, 1] = -np.inf
+    lp = np.full(1, -np.log(4))
+    with np.errstate(over="ignore"):
+        stats, _, _, _ = T.policy_loss(x, np.array([1]), np.ones(1), np.ones(1), lp, lp, kl_coef=0.1)
+    assert stats[0] == np.inf and stats[2] == np.inf and stats[1] == 0.0
+
+
 def test_preference_definition_against_differences_and_by_hand():
     rng = np.random.default_rng(3)
     x, t = rng.standard_normal((12, 7)), rng.integers(0, 7, 12)

@@ -271,10 +271,10 @@ __device__ __forceinline__ PolicyCoef policy_coef(const PolicyArgs &p, const Pol
   const double clipped = fmin(fmax(ratio, 1.0 - p.clip_low), 1.0 + p.clip_high);
   const bool active = !(ratio * adv > clipped * adv);  // a NaN stays one
   const double pg = active ? -ratio * adv : -clipped * adv;
-  const double dlogp = w * ((active ? -adv * ratio : 0.0) - p.kl_coef * ed);
+  const double dlogp = w * ((active ? -adv * ratio : 0.0) - times(p.kl_coef, ed));
   if (write && lane == 0) {
     p.logp[r] = (float)logp;
-    put_shared(&terms[r], w * (pg + p.kl_coef * kl));
+    put_shared(&terms[r], w * (pg + times(p.kl_coef, kl)));
     put_shared(&terms[rows + r], w * pg);
     put_shared(&terms[2 * rows + r], w * kl);
     put_shared(&terms[3 * rows + r], active ? 0.0 : w);

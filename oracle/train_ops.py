@@ -86,8 +86,8 @@ def policy_loss(x, targets, advantages, weights, old_logp=None, ref_logp=None, c
         if ref_logp is not None:
             d = float(ref_logp[r]) - logp[r]
             kl, dkl = np.expm1(d) - (d if d < np.inf else 0.0), -np.expm1(d)
-        stats += np.array([w * (pg + kl_coef * kl), w * pg, w * kl, w if flat else 0.0])
-        dlogp[r] = w * ((0.0 if flat else -a * ratio) + kl_coef * dkl)
+        stats += np.array([w * (pg + times(kl_coef, kl)), w * pg, w * kl, w if flat else 0.0])
+        dlogp[r] = w * ((0.0 if flat else -a * ratio) + times(kl_coef, dkl))
     return stats, out, logit_grad(x, targets, dlogp), dlogp
 
 

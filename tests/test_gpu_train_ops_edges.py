@@ -90,3 +90,28 @@ def test_policy_kl_of_a_target_of_probability_zero(torch):
         stats, _, _ = policy(torch, x, [0, 4], [1.0, 1.0], [lp, lp], ref, 0.1)
         assert stats[0] == INF and stats[2] == INF
         within(stats[1], -1.0, 100 * E, "policy part")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,v", [(3, 8), (3, 5000), (3, 70000)])  # a wave a row, a workgroup a row, pieces (bf16)
+@pytest.mark.parametrize("has_old", [True, False])
+def test_policy_masked_target_with_a_reference_but_no_kl(torch, dtype, n, v, has_old):
+    # kl_coef 0 with a reference to look at: the KL of a target of probability 0 is infinite and its factor 0
+    x = torch.zeros((n, v), dtype=dt(torch, dtype), device=DEV)
+    x[1, 4] = -INF
+    lp = -np.log(v)
+    adv = np.array([1.0, 2.0, -0.5])
+    stats, logp, d = policy(torch, x, [0, 4, 2], adv, [lp] * n if has_old else None, [lp] * n, 0.0)
+    ratio = np.array([1.0, 0.0 if has_old else 1.0, 1.0])
+    tol = (v / 64 + 64) * E
+    within(logp, [lp, -INF, lp], tol + 2 * E * (1 - lp) * 12, "logp")
+    within(stats[:2], np.full(2, -(ratio * adv).sum()), 3.5 * (tol + 20 * E), "loss")
+    for r, t in ((0, 0), (1, 4), (2, 2)):
+        dl = -adv[r] * ratio[r]
+        p = np.full(v, 1.0 / v)
+        if r == 1:
+            p = np.full(v, 1.0 / (v - 1))
+            p[4] = 0.0
+        g = -dl * p
+        g[t] += dl
+        within(d[r], g, np.abs(dl) * (p + (np.arange(v) == t)) * (2 * tol + 30 * E) + 1.01 * HALF[dtype] * np.abs(g), "dlogits")

@@ -61,6 +61,14 @@ def test_policy_definition_of_an_infinite_kl():
     assert stats[0] == np.inf and stats[2] == np.inf and stats[1] == 0.0
 
 
+def test_policy_definition_with_a_reference_but_no_kl():
+    x = np.zeros((2, 4))
+    x[1, 1] = -np.inf
+    lp = np.full(2, -np.log(4))
+    stats, logp, d, dl = T.policy_loss(x, np.array([0, 1]), np.ones(2), np.ones(2), lp, lp, kl_coef=0.0)
+    assert stats[:2] == pytest.approx([-1.0, -1.0]) and dl == pytest.approx([-1.0, 0.0]) and not d[1].any()
+
+
 def test_preference_definition_against_differences_and_by_hand():
     rng = np.random.default_rng(3)
     x, t = rng.standard_normal((12, 7)), rng.integers(0, 7, 12)

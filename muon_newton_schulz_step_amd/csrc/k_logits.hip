@@ -269,9 +269,10 @@ __device__ __forceinline__ PolicyCoef policy_coef(const PolicyArgs &p, const Pol
   const double d = shfl_f64(arg, 1), kl = ed == INFINITY ? ed : ed - d;  // (d may be +inf too)
   const double adv = q.advantage, w = q.weight;
   const double clipped = fmin(fmax(ratio, 1.0 - p.clip_low), 1.0 + p.clip_high);
-  const bool active = !(ratio * adv > clipped * adv);  // a NaN stays one
-  const double pg = active ? -ratio * adv : -clipped * adv;
-  const double dlogp = w * ((active ? -adv * ratio : 0.0) - times(p.kl_coef, ed));
+  const double plain = times(adv, ratio);  // (the ratio may be infinite, and the advantage 0)
+  const bool active = !(plain > clipped * adv);  // a NaN stays one
+  const double pg = active ? -plain : -clipped * adv;
+  const double dlogp = w * ((active ? -plain : 0.0) - times(p.kl_coef, ed));
   if (write && lane == 0) {
     p.logp[r] = (float)logp;
     put_shared(&terms[r], w * (pg + times(p.kl_coef, kl)));

@@ -80,14 +80,15 @@ def policy_loss(x, targets, advantages, weights, old_logp=None, ref_logp=None, c
         out[r] = logp[r]
         ratio = 1.0 if old_logp is None else np.exp(logp[r] - float(old_logp[r]))
         clipped = min(max(ratio, 1.0 - clip_low), 1.0 + clip_high)
-        flat = ratio * a > clipped * a
-        pg = -a * (clipped if flat else ratio)
+        plain = float(times(a, ratio))
+        flat = plain > clipped * a
+        pg = -(clipped * a if flat else plain)
         kl = dkl = 0.0
         if ref_logp is not None:
             d = float(ref_logp[r]) - logp[r]
             kl, dkl = np.expm1(d) - (d if d < np.inf else 0.0), -np.expm1(d)
         stats += np.array([w * (pg + times(kl_coef, kl)), w * pg, w * kl, w if flat else 0.0])
-        dlogp[r] = w * ((0.0 if flat else -a * ratio) + times(kl_coef, dkl))
+        dlogp[r] = w * ((0.0 if flat else -plain) + times(kl_coef, dkl))
     return stats, out, logit_grad(x, targets, dlogp), dlogp
 
 

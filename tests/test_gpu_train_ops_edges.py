@@ -115,3 +115,15 @@ def test_policy_masked_target_with_a_reference_but_no_kl(torch, dtype, n, v, has
         g = -dl * p
         g[t] += dl
         within(d[r], g, np.abs(dl) * (p + (np.arange(v) == t)) * (2 * tol + 30 * E) + 1.01 * HALF[dtype] * np.abs(g), "dlogits")
+
+
+@pytest.mark.parametrize("n,v", [(3, 8), (3, 5000), (3, 70000)])
+def test_policy_without_advantage_at_an_infinite_ratio(torch, n, v):
+    # a target that the old policy gave probability 0 (or far less than now): the ratio is infinite, and with
+    # advantage 0 both branches are 0
+    x = torch.zeros((n, v), dtype=torch.bfloat16, device=DEV)
+    lp = -np.log(v)
+    stats, _, d = policy(torch, x, [0, 1, 2], [0.0, 0.0, 1.0], [-INF, -2000.0, lp], None, 0.0)
+    within(stats[:2], [-1.0, -1.0], (v / 64 + 90) * E, "loss")
+    assert stats[2] == 0.0 and stats[3] == 0.0
+    assert not d[:2].any() and d[2].any()

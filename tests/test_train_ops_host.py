@@ -69,6 +69,12 @@ def test_policy_definition_with_a_reference_but_no_kl():
     assert stats[:2] == pytest.approx([-1.0, -1.0]) and dl == pytest.approx([-1.0, 0.0]) and not d[1].any()
 
 
+def test_policy_definition_without_advantage_at_an_infinite_ratio():
+    with np.errstate(over="ignore"):
+        stats, _, d, _ = T.policy_loss(np.zeros((2, 4)), np.array([0, 1]), np.zeros(2), np.ones(2), np.array([-np.inf, -2000.0]))
+    assert not stats.any() and not d.any()
+
+
 def test_preference_definition_against_differences_and_by_hand():
     rng = np.random.default_rng(3)
     x, t = rng.standard_normal((12, 7)), rng.integers(0, 7, 12)

@@ -259,9 +259,10 @@ __device__ __forceinline__ PolicyCoef policy_coef(const PolicyArgs &p, const Pol
                                                   int64_t rows, bool write, double *terms) {
   const int lane = threadIdx.x & 63;
   const double logp = (double)q.at_target - (double)o.m - log((double)o.s);
-  // lane 0: the ratio, lane 1: the KL term, lane 2: the target's own share
+  // lane 0: the ratio (1 without old_logp, if there is a logp at all), lane 1:
+  // the KL term, lane 2: the target's own share
   double arg = 0.0;
-  if (lane == 0 && p.old_logp) arg = logp - (double)q.other;
+  if (lane == 0) arg = p.old_logp ? logp - (double)q.other : logp != logp ? logp : 0.0;
   if (lane == 1 && p.ref_logp) arg = (double)q.other - logp;
   if (lane == 2) arg = logp;
   const double em1 = expm1(arg);

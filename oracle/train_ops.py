@@ -78,7 +78,7 @@ def policy_loss(x, targets, advantages, weights, old_logp=None, ref_logp=None, c
         if not 0 <= targets[r] < v or w == 0.0:
             continue
         out[r] = logp[r]
-        ratio = 1.0 if old_logp is None else np.exp(logp[r] - float(old_logp[r]))
+        ratio = (logp[r] if np.isnan(logp[r]) else 1.0) if old_logp is None else np.exp(logp[r] - float(old_logp[r]))
         clipped = min(max(ratio, 1.0 - clip_low), 1.0 + clip_high)
         plain = float(times(a, ratio))
         flat = plain > clipped * a

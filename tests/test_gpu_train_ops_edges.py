@@ -127,3 +127,17 @@ def test_policy_without_advantage_at_an_infinite_ratio(torch, n, v):
     within(stats[:2], [-1.0, -1.0], (v / 64 + 90) * E, "loss")
     assert stats[2] == 0.0 and stats[3] == 0.0
     assert not d[:2].any() and d[2].any()
+
+
+@pytest.mark.parametrize("v", [8, 5000, 70000])
+def test_policy_nan_without_old_logp_reaches_the_loss(torch, v):
+    # the ratio is 1 by value, but of a row without a log-probability there is none
+    for bad, row in (("nan", 0), ("all masked", 1)):
+        x = torch.zeros((2, v), dtype=torch.bfloat16, device=DEV)
+        if row == 0:
+            x[0, 5] = float("nan")
+        else:
+            x[1] = -INF
+        stats, logp, d = policy(torch, x, [0, 1], [1.0, 1.0], None, None, 0.0)
+        assert np.isnan(logp[row]) and np.isnan(stats[0]) and np.isnan(stats[1]), bad
+        assert np.isnan(d[row]).any() and not np.isnan(d[1 - row]).any()

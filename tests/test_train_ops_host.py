@@ -75,6 +75,13 @@ def test_policy_definition_without_advantage_at_an_infinite_ratio():
     assert not stats.any() and not d.any()
 
 
+def test_policy_definition_of_nan_without_old_logp():
+    x = np.zeros((2, 4))
+    x[1, 2] = np.nan
+    stats, logp, _, _ = T.policy_loss(x, np.array([0, 1]), np.ones(2), np.ones(2))
+    assert np.isnan(logp[1]) and np.isnan(stats[0]) and np.isnan(stats[1]) and not np.isnan(logp[0])
+
+
 def test_preference_definition_against_differences_and_by_hand():
     rng = np.random.default_rng(3)
     x, t = rng.standard_normal((12, 7)), rng.integers(0, 7, 12)

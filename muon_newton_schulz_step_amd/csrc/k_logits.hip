@@ -609,7 +609,7 @@ __global__ __launch_bounds__(256, 8) void kl_policy_few(LogitArgs a, PolicyArgs 
 //
 //   gain = sum logp - ref, m = beta (gain_chosen - gain_rejected)
 //   loss = -(1 - s) log sigmoid(m) - s log sigmoid(-m)
-//   d loss / d logp = +- beta (sigmoid(m) - (1 - s)) / pairs
+//   d loss / d logp = +- beta (s sigmoid(m) - (1 - s) sigmoid(-m)) / pairs
 //
 // A row's gradient needs its whole pair's log-probabilities, so its logits
 // are read twice.  Logits that the memory-side cache (256 MB) holds are walked
@@ -626,8 +626,10 @@ __device__ __forceinline__ double pair_loss(const PreferenceArgs &p, int64_t i, 
   const double gain[2] = {chosen - (double)p.ref_logp[i], rejected - (double)p.ref_logp[i + p.pairs]};
   const double reward[2] = {times(p.beta, gain[0]), times(p.beta, gain[1])};
   const double m = p.beta == 0.0 ? reward[0] - reward[1] : p.beta * (gain[0] - gain[1]);
+  // sigmoid(m) and sigmoid(-m) each from exp(-|m|): as 1 minus the other, the
+  // far one would be 0 from |m| = 37 on, and no longer accurate to fp32 from 20
   const double q = exp(-fabs(m));
-  const double sig = (m >= 0.0 ? 1.0 : q) / (1.0 + q);
+  const double up = (m >= 0.0 ? 1.0 : q) / (1.0 + q), down = (m >= 0.0 ? q : 1.0) / (1.0 + q);
   if (write) {
     p.rewards[i] = (float)reward[0];
     p.rewards[i + p.pairs] = (float)reward[1];
@@ -635,7 +637,7 @@ __device__ __forceinline__ double pair_loss(const PreferenceArgs &p, int64_t i, 
     const double l = log1p(q);
     put_shared(loss, times(1.0 - p.smoothing, fmax(-m, 0.0) + l) + times(p.smoothing, fmax(m, 0.0) + l));
   }
-  return p.beta * (sig - (1.0 - p.smoothing)) / (double)p.pairs;
+  return p.beta * (p.smoothing * up - (1.0 - p.smoothing) * down) / (double)p.pairs;
 }
 
 // The mean of the pairs' losses, in a fixed order.

@@ -103,8 +103,8 @@ def preference_loss(x, targets, offsets, ref_logp, beta=0.1, label_smoothing=0.0
     rewards = times(beta, gain)
     m = rewards[:pairs] - rewards[pairs:] if beta == 0.0 else beta * (gain[:pairs] - gain[pairs:])
     loss = (times(1.0 - label_smoothing, np.logaddexp(0.0, -m)) + times(label_smoothing, np.logaddexp(0.0, m))).mean()
-    sig = np.exp(-np.logaddexp(0.0, -m))
-    c = beta / pairs * (sig - (1.0 - label_smoothing))
+    up, down = np.exp(-np.logaddexp(0.0, -m)), np.exp(-np.logaddexp(0.0, m))  # neither as 1 minus the other
+    c = beta / pairs * (label_smoothing * up - (1.0 - label_smoothing) * down)
     dlogp = np.zeros(n)
     for s in range(seqs):
         dlogp[offsets[s]:offsets[s + 1]] = c[s] if s < pairs else -c[s - pairs]

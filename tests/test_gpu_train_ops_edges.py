@@ -141,3 +141,28 @@ def test_policy_nan_without_old_logp_reaches_the_loss(torch, v):
         stats, logp, d = policy(torch, x, [0, 1], [1.0, 1.0], None, None, 0.0)
         assert np.isnan(logp[row]) and np.isnan(stats[0]) and np.isnan(stats[1]), bad
         assert np.isnan(d[row]).any() and not np.isnan(d[1 - row]).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("smooth", [0.0, 1.0])
+@pytest.mark.parametrize("margin", [3.0, 20.0, 30.0, 36.0, 40.0, 80.0])
+def test_preference_gradient_at_large_margins(torch, dtype, smooth, margin):
+    # sigmoid's far side is exp(-|m|) there, a normal number of either type: the coefficient keeps its relative
+    # accuracy on the side that is already right, and is near -+1 on the other.  The margin comes from the reference
+    # alone: the logits are equal, so gains are -log 8 - ref, whose own error (64 e of log 8, and the reference's
+    # rounding) moves the coefficient by as much again.
+    beta, v = 0.5, 8
+    x = torch.zeros((4, v), dtype=dt(torch, dtype), device=DEV)
+    ref = np.array([-margin / beta, margin / beta, 0.0, 0.0], dtype=np.float32)  # pair 0: +margin, pair 1: -margin
+    loss, _, d = preference(torch, x, [0, 1, 2, 3], ref, beta, smooth)
+    m = np.array([margin, -margin])
+    q = np.exp(-margin) / (1.0 + np.exp(-margin))
+    far = {1.0: q, -1.0: 1.0 / (1.0 + np.exp(-margin))}  # sigmoid(-m) by the margin's sign
+    c = np.array([beta / 2 * (smooth * far[-s] - (1.0 - smooth) * far[s]) for s in np.sign(m)])
+    rel = 2 * beta * 200 * E + 40 * E
+    for r, a in ((0, c[0]), (1, c[1]), (2, -c[0]), (3, -c[1])):
+        g = -a / v * np.ones(v)
+        g[r] += a
+        within(d[r], g, np.abs(g) * (rel + 1.01 * HALF[dtype]), f"dlogits of row {r}")
+    want = np.mean([(1 - smooth) * np.logaddexp(0, -a) + smooth * np.logaddexp(0, a) for a in m])
+    within(loss, want, 100 * E * (1 + want), "loss")

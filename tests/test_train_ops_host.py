@@ -98,6 +98,14 @@ def test_preference_definition_against_differences_and_by_hand():
     assert loss == pytest.approx(np.log(2)) and dl == pytest.approx([-0.15, 0.15])
 
 
+@pytest.mark.parametrize("margin", [1.0, 20.0, 40.0, 80.0])
+def test_preference_definition_at_large_margins(margin):
+    # d log(1 + exp(-m)) / d m = -exp(-m) / (1 + exp(-m)) to full accuracy, however small
+    _, _, _, dl = T.preference_loss(np.zeros((2, 4)), np.array([0, 1]), np.array([0, 1, 2]), np.array([-margin, 0.0]), 1.0)
+    want = np.exp(-margin) / (1.0 + np.exp(-margin))
+    assert dl == pytest.approx([-want, want], rel=1e-13)
+
+
 @pytest.mark.parametrize("smooth", [0.0, 1.0])
 def test_preference_definition_at_an_infinite_margin(smooth):
     # the sequence that should lose has probability 0: loss and gradient 0, whatever the other label would cost

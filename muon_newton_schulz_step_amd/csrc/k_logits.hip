@@ -646,7 +646,7 @@ __device__ __forceinline__ void mean_loss(const PreferenceArgs &p, const double 
   double t = 0.0;
   for (int64_t i = threadIdx.x; i < p.pairs; i += THREADS) t += get_shared(&losses[i]);
   t = block_sum<THREADS / 64>(t, red);
-  if (threadIdx.x == 0) *p.loss = (float)(t / (double)p.pairs);
+  if (threadIdx.x == 0) put_shared(p.loss, (float)(t / (double)p.pairs));
 }
 
 // Sequence bounds as kl_pairs uses them: whatever the offsets hold, rows
@@ -841,6 +841,7 @@ __global__ __launch_bounds__(1024) void kp_plan(LogitArgs a, PreferenceArgs p, P
     w.walk->pairs_done = empty;
     w.walk->rows = sum;
     w.walk->lag = (int)min((int64_t)sum, (int64_t)most + slack);
+    w.walk->late = 0;
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
@@ -854,22 +855,24 @@ struct Place {
 };
 
 // The at-th row of the walk: the pairs' rows, then those of no sequence.
-__device__ __forceinline__ Place place(const PreferenceArgs &p, const PreferenceWork &w, int64_t n, int64_t at) {
+__device__ __forceinline__ Place place(const PreferenceArgs &p, const PreferenceWork &w, int64_t rows, int64_t n,
+                                       int64_t at) {
+  auto inside = [&](int64_t row) { return min(max(uniform(row), (int64_t)0), rows - 1); };
   if (at >= n) {
     const int64_t lead = w.bounds[0];
-    return {uniform(at - n < lead ? at - n : w.bounds[2 * p.pairs] + (at - n - lead)), -1};
+    return {inside(at - n < lead ? at - n : w.bounds[2 * p.pairs] + (at - n - lead)), -1};
   }
   // the last pair that starts at or before this place, 64 probes at a time
   int64_t lo = 0, hi = p.pairs;
   while (hi - lo > 1) {
     const int64_t step = (hi - lo + 63) / 64, probe = lo + (threadIdx.x & 63) * step;
-    const int c = __popcll(__ballot(probe < hi && w.starts[min(probe, p.pairs)] <= at));
+    const int c = max(__popcll(__ballot(probe < hi && w.starts[min(probe, p.pairs)] <= at)), 1);
     lo += (c - 1) * step;
     hi = min(hi, lo + step);
   }
   const int64_t pair = uniform(lo);
   const int64_t off = at - w.starts[pair], len = w.bounds[pair + 1] - w.bounds[pair];
-  return {uniform(off < len ? w.bounds[pair] + off : w.bounds[pair + p.pairs] + (off - len)), pair};
+  return {inside(off < len ? w.bounds[pair] + off : w.bounds[pair + p.pairs] + (off - len)), pair};
 }
 
 }  // namespace
@@ -879,6 +882,11 @@ __device__ __forceinline__ Place place(const PreferenceArgs &p, const Preference
 // are sums of earlier tickets, and a sum waits for nothing, so every wait
 // ends.  The grid has 2 rows' workgroups, as the host does not know the lag;
 // those too many, spread over the grid, end at once.
+//
+// Should a wait not end all the same (another call running on the same
+// workspace), it is given up after max_polls looks, and so are those that
+// would follow: their rows' gradients and the loss become NaN, and tickets and
+// rows beyond the walk are not taken.
 //
 // 12500 rows of 50257 bf16 in 16 pairs: 457 us, 4.6 TB/s; the second reads that
 // the cache still holds are what it gains over three launches (545).  The
@@ -907,8 +915,9 @@ __global__ __launch_bounds__(PREF_THREADS, 8) void kp_loss(LogitArgs a, Preferen
   if (tid == 0) unit = atomicAdd((unsigned long long *)&w.walk->ticket, 1ull);
   __syncthreads();
   const int64_t t = uniform((int64_t)unit);
+  if ((uint64_t)t >= units) return;
   if (t < n) {
-    const Place at = place(p, w, n, t);
+    const Place at = place(p, w, a.rows, n, t);
     const int64_t r = at.row, pair = at.pair;
     const int64_t target = uniform(index_at(a.targets, r));
     double logp = 0.0, share = 0.0;
@@ -951,11 +960,17 @@ __global__ __launch_bounds__(PREF_THREADS, 8) void kp_loss(LogitArgs a, Preferen
         last = arrive(&w.walk->pairs_done) == (int)p.pairs - 1;
       }
       __syncthreads();
-      if (last) mean_loss<THREADS>(p, w.losses, red64);
+      if (last) {
+        mean_loss<THREADS>(p, w.losses, red64);
+        if (tid == 0) {  // the loss is NaN if a gradient gives up, whichever comes last
+          asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+          if (get_shared(&w.walk->late)) put_shared(p.loss, __builtin_nanf(""));
+        }
+      }
     }
   }
   if (t < lag) return;
-  const Place at = place(p, w, n, t - lag);
+  const Place at = place(p, w, a.rows, n, t - lag);
   const int64_t r = at.row, pair = at.pair;
   const int64_t target = uniform(index_at(a.targets, r));
   const bool live = pair >= 0 && target >= 0 && target < a.vocab;
@@ -970,7 +985,12 @@ __global__ __launch_bounds__(PREF_THREADS, 8) void kp_loss(LogitArgs a, Preferen
       if (tid + k * THREADS < row.vecs) in[k] = load16(x + row.col(tid + k * THREADS));
     }
     if (tid == 0) {
-      while (get_shared(&w.ready[pair]) == 0) __builtin_amdgcn_s_sleep(2);
+      bool late = false;
+      for (int left = w.max_polls; !(left >= 0 && get_shared(&w.ready[pair])); --left) {
+        late = left <= 0 || get_shared(&w.walk->late);
+        if (late) break;
+        __builtin_amdgcn_s_sleep(2);
+      }
       asm volatile("" ::: "memory");
       const RowStat *st = w.stat + r;
       const double coef = get_shared(&w.coef[pair]), total = (double)get_shared(&st->total), share = get_shared(&st->share);
@@ -979,6 +999,13 @@ __global__ __launch_bounds__(PREF_THREADS, 8) void kp_loss(LogitArgs a, Preferen
       grad.c = (float)(-dl / total);
       grad.dt = (float)(-dl * share);
       grad.live = dl != 0.0;
+      if (late) {
+        grad.c = grad.dt = __builtin_nanf("");
+        grad.live = 1;
+        put_shared(&w.walk->late, 1);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        put_shared(p.loss, __builtin_nanf(""));
+      }
     }
   }
   __syncthreads();
@@ -1019,6 +1046,13 @@ __global__ __launch_bounds__(PREF_THREADS, 8) void kp_loss(LogitArgs a, Preferen
 }
 
 // ------------------------------------------------------------- launchers
+
+// Looks, about a microsecond apart, that a gradient takes at its pair before it
+// gives up: four seconds and more.  Not in the header; a test sets it to -1 to
+// see every wait given up.
+extern "C" {
+int muon_preference_max_polls = 1 << 22;
+}
 
 namespace {
 
@@ -1155,6 +1189,7 @@ hipError_t preference_launch(const LogitArgs &a, const PreferenceArgs &p, void *
                              hipStream_t s) {
   const PreferenceLayout l = preference_layout(a.rows, p.pairs);
   PreferenceWork w{};
+  w.max_polls = muon_preference_max_polls;
   w.walk = reinterpret_cast<PreferenceWalk *>(ws + l.walk);
   w.stat = reinterpret_cast<RowStat *>(ws + l.stat);
   w.losses = reinterpret_cast<double *>(ws + l.losses);

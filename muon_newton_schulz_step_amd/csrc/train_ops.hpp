@@ -137,9 +137,11 @@ struct PreferenceWalk {
   int32_t pairs_done;
   int32_t rows;  // rows that belong to a sequence
   int32_t lag;   // rows whose sums are handed out before the first gradient
+  alignas(128) int32_t late;  // a gradient gave up waiting (a line of its own: the first one takes the tickets)
 };
 // Workspace of the preference loss.
 struct PreferenceWork {
+  int32_t max_polls;     // of a gradient's wait
   PreferenceWalk *walk;
   RowStat *stat;         // a row
   double *losses, *coef; // a pair

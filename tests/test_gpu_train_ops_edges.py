@@ -1,14 +1,16 @@
 """The losses at the ends of their range, on the GPU: terms whose factor is 0 beside infinities, margins of any size,
-rows that hold NaN.  Expected values are written out from the formulas in fp64; tolerances as in
+rows that hold NaN, waits that are given up.  Expected values are written out from the formulas in fp64; tolerances as in
 test_gpu_train_ops.py (e = 2^-24, half a step of fp32; h = half a step of the output's type)."""
 
 from __future__ import annotations
+
+import ctypes as C
 
 import numpy as np
 import pytest
 
 import muon_newton_schulz_step_amd as M
-from test_gpu_train_ops import DEV, E, HALF, TINY, dt, f64, poisoned, torch, vec, within  # noqa: F401
+from test_gpu_train_ops import DEV, E, HALF, big_pref, dt, f64, poisoned, torch, vec, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -166,3 +168,36 @@ def test_preference_gradient_at_large_margins(torch, dtype, smooth, margin):
         within(d[r], g, np.abs(g) * (rel + 1.01 * HALF[dtype]), f"dlogits of row {r}")
     want = np.mean([(1 - smooth) * np.logaddexp(0, -a) + smooth * np.logaddexp(0, a) for a in m])
     within(loss, want, 100 * E * (1 + want), "loss")
+
+
+def test_preference_walk_gives_up_a_wait_that_does_not_end(torch):
+    # with no look allowed every gradient gives up: the call ends, rows with a gradient and the loss are NaN, rewards
+    # and rows without one are as ever; with one look each row is right or NaN; with the default all are right
+    lens, lead, tail, v = [300, 410, 0, 500, 140, 350, 450, 250], 3, 400, 50257
+    x, t, off, ref = big_pref(torch, lens, lead, tail, v, "bf16", v, 7)
+    n, seqs = x.shape[0], len(lens)
+    assert x.numel() * 2 > 256 << 20
+    polls = C.c_int.in_dll(M.load(), "muon_preference_max_polls")
+
+    def call(most):
+        before, polls.value = polls.value, most
+        try:
+            loss, rew, d = torch.full((1,), 9.0, device=DEV), torch.full((seqs,), 9.0, device=DEV), torch.full_like(x, 9.0)
+            M.preference_loss(x, t, off, ref, loss, rew, d, poisoned(torch, M.preference_loss_workspace_bytes(n, seqs // 2)))
+            torch.cuda.synchronize()
+            return loss, rew, d
+        finally:
+            polls.value = before
+    loss, rew, d = call(polls.value)
+    assert not loss.isnan().any() and not d.isnan().any()
+    at = torch.arange(n, device=DEV)
+    live = (t >= 0) & (at >= lead) & (at < n - tail)
+    none, rew0, d0 = call(-1)
+    assert none.isnan().all() and torch.equal(rew0, rew)
+    assert d0[live].isnan().all() and not d0[~live].any()
+    one, rew1, d1 = call(0)
+    bad = d1.isnan().all(1)
+    assert torch.equal(rew1, rew) and torch.equal(d1[~bad], d[~bad]) and not (bad & ~live).any()
+    assert bool(one.isnan()) == bool(bad.any()) and (bad.any() or torch.equal(one, loss))
+    again = call(polls.value)
+    assert all(torch.equal(a, b) for a, b in zip(again, (loss, rew, d)))

@@ -1208,7 +1208,7 @@ hipError_t preference_launch(const LogitArgs &a, const PreferenceArgs &p, void *
   // pairs, 420 MB, 1124 rows of which are 295 MB) 386 356.
   const int64_t row = a.vocab * (int64_t)sizeof(typename Elem<BF16>::type);
   const bool walk = a.rows * row > (256 << 20) && (a.rows / p.pairs + 1024) * row <= (224 << 20);
-  if (walk || a.rows > ROWS_A_LAUNCH || (a.rows > 0 && p.pairs > ROWS_A_LAUNCH)) {
+  if (walk || a.rows > ROWS_A_LAUNCH || p.pairs > ROWS_A_LAUNCH) {
     hipLaunchKernelGGL(kp_plan, dim3(1), dim3(1024), 0, s, a, p, w, PREF_SLACK);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     return by_rows(a, 2 * a.rows, [&](const LogitArgs &a, dim3 g) {

@@ -10,7 +10,7 @@ import numpy as np
 import pytest
 
 import muon_newton_schulz_step_amd as M
-from test_gpu_train_ops import DEV, E, HALF, big_pref, dt, f64, poisoned, torch, vec, within  # noqa: F401
+from test_gpu_train_ops import DEV, E, HALF, TINY, big_pref, dt, f64, poisoned, torch, vec, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -201,3 +201,20 @@ def test_preference_walk_gives_up_a_wait_that_does_not_end(torch):
     assert bool(one.isnan()) == bool(bad.any()) and (bad.any() or torch.equal(one, loss))
     again = call(polls.value)
     assert all(torch.equal(a, b) for a, b in zip(again, (loss, rew, d)))
+
+
+def test_preference_of_more_pairs_than_a_launch_has_workgroups(torch):
+    # no rows at all: every pair is empty, its margin is its references'
+    pairs, v = (1 << 22) + 5, 8
+    g = torch.Generator(DEV).manual_seed(3)
+    ref = torch.randn(2 * pairs, generator=g, device=DEV)
+    gain = -ref.double()
+    m = 0.1 * (gain[:pairs] - gain[pairs:])
+    want = float(torch.nn.functional.softplus(-m).mean())
+    x, t = torch.empty((0, v), device=DEV), torch.empty(0, dtype=torch.int64, device=DEV)
+    off = torch.zeros(2 * pairs + 1, dtype=torch.int32, device=DEV)
+    loss, rew = torch.full((1,), 9.0, device=DEV), torch.full((2 * pairs,), 9.0, device=DEV)
+    M.preference_loss(x, t, off, ref, loss, rew, torch.empty_like(x),
+                      poisoned(torch, M.preference_loss_workspace_bytes(0, pairs)), beta=0.1)
+    assert bool(((rew.double() - 0.1 * gain).abs() <= 2 * E * 0.1 * gain.abs() + TINY).all())
+    within(f64(loss), [want], 2 * E * want, "loss")

@@ -105,6 +105,13 @@ __device__ __forceinline__ float exp_term(float x, float m) {
   return __builtin_amdgcn_exp2f(fmaf(d, kLog2e, d * kLog2eLow));
 }
 
+// And for the elements of a gradient of either type: a bf16 result's rounding
+// (2^-8) hides the constant's rest, fp32 ones would all be off to one side.
+template <bool BF16>
+__device__ __forceinline__ float exp_grad(float x, float m) {
+  return BF16 ? exp_shift(x, m) : exp_term(x, m);
+}
+
 // A value that is the same in all lanes of a wave, moved to scalar registers.
 __device__ __forceinline__ int64_t uniform(int64_t v) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));

@@ -386,7 +386,7 @@ __global__ __launch_bounds__(THREADS, 8) void kl_policy(LogitArgs a, PolicyArgs 
     float v[E::N];
     E::unpack(in, v);
 #pragma unroll
-    for (int j = 0; j < E::N; ++j) v[j] = c * exp_shift(v[j], m);
+    for (int j = 0; j < E::N; ++j) v[j] = c * exp_grad<BF16>(v[j], m);
     stream16(d + row.col(i), E::pack(v));
   };
 #pragma unroll
@@ -403,7 +403,7 @@ __global__ __launch_bounds__(THREADS, 8) void kl_policy(LogitArgs a, PolicyArgs 
     for (int k = 0; k < AHEAD; ++k) grad(in[k], far + k * THREADS);
   }
   for (; far < row.vecs; far += THREADS) grad(load16(x + row.col(far)), far);
-  if (lone) d[row.single(tid)] = E::put(c * exp_shift(single, m));
+  if (lone) d[row.single(tid)] = E::put(c * exp_grad<BF16>(single, m));
   // the target's own element, by the thread that wrote over it
   const int at = (int)target - row.head;
   const bool in_vec = at >= 0 && at / E::N < row.vecs;
@@ -446,14 +446,14 @@ __global__ __launch_bounds__(256) void kl_policy_short(LogitArgs a, PolicyArgs p
     float v[E::N];
     E::unpack(held.in[k], v);
 #pragma unroll
-    for (int j = 0; j < E::N; ++j) v[j] = rel - i * E::N == j ? dt : c * exp_shift(v[j], o.m);
+    for (int j = 0; j < E::N; ++j) v[j] = rel - i * E::N == j ? dt : c * exp_grad<BF16>(v[j], o.m);
     stream16(d + row.col(i), E::pack(v));
   }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (lane + 64 * k >= row.singles()) continue;
     const int j = row.single(lane + 64 * k);
-    d[j] = E::put(j == target ? dt : c * exp_shift(held.lone[k], o.m));
+    d[j] = E::put(j == target ? dt : c * exp_grad<BF16>(held.lone[k], o.m));
   }
 }
 
@@ -572,7 +572,7 @@ __global__ __launch_bounds__(256, 8) void kl_policy_few(LogitArgs a, PolicyArgs 
       float v[E::N];
       E::unpack(v4, v);
 #pragma unroll
-      for (int j = 0; j < E::N; ++j) v[j] = c * exp_shift(v[j], m);
+      for (int j = 0; j < E::N; ++j) v[j] = c * exp_grad<BF16>(v[j], m);
       const int j0 = rel - i * E::N;
       if (j0 >= 0 && j0 < E::N) {
 #pragma unroll
@@ -584,7 +584,7 @@ __global__ __launch_bounds__(256, 8) void kl_policy_few(LogitArgs a, PolicyArgs 
     for (int k = 0; k < HELD; ++k)
       if (v0 + k * 256 < v1) grad(in[k], v0 + k * 256);
     for (int i = v0 + HELD * 256; i < v1; i += 256) grad(load16(x + row.col(i)), i);
-    if (lone) d[row.single(tid)] = E::put((int)row.single(tid) == target ? dt : c * exp_shift(single, m));
+    if (lone) d[row.single(tid)] = E::put((int)row.single(tid) == target ? dt : c * exp_grad<BF16>(single, m));
   } else {
     for (int i = v0; i < v1; i += 256) store16(d + row.col(i), make_uint4(0, 0, 0, 0));
     if (lone) d[row.single(tid)] = T(0);
@@ -716,7 +716,7 @@ __global__ __launch_bounds__(256) void kl_grad(LogitArgs a, const RowGrad *grad,
     float v[E::N];
     E::unpack(load16(x + row.col(i)), v);
 #pragma unroll
-    for (int k = 0; k < E::N; ++k) v[k] = g.c * exp_shift(v[k], g.max);
+    for (int k = 0; k < E::N; ++k) v[k] = g.c * exp_grad<BF16>(v[k], g.max);
     const int at = (int)target - (int)row.col(i);
     if (at >= 0 && at < E::N) {
 #pragma unroll
@@ -726,7 +726,7 @@ __global__ __launch_bounds__(256) void kl_grad(LogitArgs a, const RowGrad *grad,
   }
   if (piece == 0 && (int)threadIdx.x < row.singles()) {
     const int j = row.single(threadIdx.x);
-    d[j] = E::put(j == target ? g.dt : g.c * exp_shift(E::get(x[j]), g.max));
+    d[j] = E::put(j == target ? g.dt : g.c * exp_grad<BF16>(E::get(x[j]), g.max));
   }
 }
 
@@ -761,14 +761,14 @@ __global__ __launch_bounds__(256) void kl_grad_short(LogitArgs a, const RowGrad 
     float v[E::N];
     E::unpack(held.in[k], v);
 #pragma unroll
-    for (int j = 0; j < E::N; ++j) v[j] = rel - i * E::N == j ? g.dt : g.c * exp_shift(v[j], g.max);
+    for (int j = 0; j < E::N; ++j) v[j] = rel - i * E::N == j ? g.dt : g.c * exp_grad<BF16>(v[j], g.max);
     stream16(d + row.col(i), E::pack(v));
   }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (lane + 64 * k >= row.singles()) continue;
     const int j = row.single(lane + 64 * k);
-    d[j] = E::put(j == target ? g.dt : g.c * exp_shift(held.lone[k], g.max));
+    d[j] = E::put(j == target ? g.dt : g.c * exp_grad<BF16>(held.lone[k], g.max));
   }
 }
 
@@ -1020,7 +1020,7 @@ __global__ __launch_bounds__(PREF_THREADS, 8) void kp_loss(LogitArgs a, Preferen
     float v[E::N];
     E::unpack(v4, v);
 #pragma unroll
-    for (int k = 0; k < E::N; ++k) v[k] = c * exp_shift(v[k], m);
+    for (int k = 0; k < E::N; ++k) v[k] = c * exp_grad<BF16>(v[k], m);
     const int k0 = rel - i * E::N;
     if (k0 >= 0 && k0 < E::N) {
 #pragma unroll
@@ -1041,7 +1041,7 @@ __global__ __launch_bounds__(PREF_THREADS, 8) void kp_loss(LogitArgs a, Preferen
   for (; i < row.vecs; i += THREADS) put(load16(x + row.col(i)), i);
   if (tid < row.singles()) {
     const int j = row.single(tid);
-    d[j] = E::put(j == target ? dt : c * exp_shift(E::get(x[j]), m));
+    d[j] = E::put(j == target ? dt : c * exp_grad<BF16>(E::get(x[j]), m));
   }
 }
 

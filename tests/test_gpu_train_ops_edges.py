@@ -218,3 +218,37 @@ def test_preference_of_more_pairs_than_a_launch_has_workgroups(torch):
                       poisoned(torch, M.preference_loss_workspace_bytes(0, pairs)), beta=0.1)
     assert bool(((rew.double() - 0.1 * gain).abs() <= 2 * E * 0.1 * gain.abs() + TINY).all())
     within(f64(loss), [want], 2 * E * want, "loss")
+
+
+@pytest.mark.parametrize("v", [2000, 6000, 70000])
+def test_fp32_gradients_without_a_bias_in_the_exponent(torch, v):
+    # Away from its target a gradient is dlogp exp(x - lse).  The relative error may be up to (2 |d| + 8) e an
+    # element, but of either sign: fitted to d = x - max over 10^6 elements its slope is 0 within the noise, whose
+    # deviation is below e (|d| + 4) / (10^3 std(d)) = 3.3e-10 (logits of deviation 4, |d| around 18; six of those
+    # are 2e-9).  log2(e) rounded to fp32 alone is low by 1.3e-8 of itself, and that is the slope without its rest.
+    n = 1 + 10 ** 6 // v
+    g = torch.Generator(DEV).manual_seed(v)
+    x = torch.empty((n, v), device=DEV).normal_(0.0, 4.0, generator=g)
+    t = np.zeros(n, dtype=np.int64)
+    z = x.double()
+    want = torch.log_softmax(z, 1)
+    shift = z - z.max(1, keepdim=True).values
+    seqs = 2 * (n // 2)
+    off = np.arange(seqs + 1)
+    lp = want[:, 0].float()
+
+    def slope(d, rows):
+        # ratios of the elements to the first one after the target take the row's own factor (and its rounding) out
+        rel = (d[:rows, 1:].double().abs().log() - want[:rows, 1:])
+        s = shift[:rows, 1:]
+        rel, s = rel - rel.mean(1, keepdim=True), s - s.mean(1, keepdim=True)
+        keep = want[:rows, 1:] > -60.0  # away from the smallest numbers
+        return float((rel * s)[keep].sum() / (s * s)[keep].sum())
+    d, stats, logp = torch.empty_like(x), torch.empty(4, device=DEV), torch.empty(n, device=DEV)
+    M.policy_loss(x, vec(torch, t, "int64"), torch.ones(n, device=DEV), torch.ones(n, device=DEV), stats, logp, d,
+                  poisoned(torch, M.policy_loss_workspace_bytes(n)))
+    assert abs(slope(d, n)) < 2e-9, "policy loss"
+    loss, rew = torch.empty(1, device=DEV), torch.empty(seqs, device=DEV)
+    M.preference_loss(x, vec(torch, t, "int64"), vec(torch, off, "int64"), lp[:seqs].contiguous(), loss, rew, d,
+                      poisoned(torch, M.preference_loss_workspace_bytes(n, seqs // 2)), beta=1.0)
+    assert abs(slope(d, seqs)) < 2e-9, "preference loss"

@@ -612,11 +612,12 @@ __global__ __launch_bounds__(256, 8) void kl_policy_few(LogitArgs a, PolicyArgs 
 //   d loss / d logp = +- beta (s sigmoid(m) - (1 - s) sigmoid(-m)) / pairs
 //
 // A row's gradient needs its whole pair's log-probabilities, so its logits
-// are read twice.  Logits that the memory-side cache (256 MB) holds are walked
-// by three launches: the rows' sums (kl_rows), the pairs (kl_pairs), the
-// gradient (kl_grad).  Larger ones are walked pair by pair in one launch
-// (kp_loss, after kp_plan), the gradient following the sums at a distance of
-// the longest pair and some rows more, so that it finds them in that cache.
+// are read twice.  Logits that the memory-side cache (256 MB) holds or nearly
+// holds, and short rows, are walked by three launches: the rows' sums
+// (kl_rows), the pairs (kl_pairs), the gradient (kl_grad).  Larger ones are
+// walked pair by pair in one launch (kp_loss, after kp_plan), the gradient
+// following the sums at a distance of the longest pair and some rows more, so
+// that it finds them in that cache.
 
 namespace {
 
@@ -1201,13 +1202,20 @@ hipError_t preference_launch(const LogitArgs &a, const PreferenceArgs &p, void *
   RowGrad *grad = reinterpret_cast<RowGrad *>(ws + l.grad);
   hipError_t e;
   // One walk where the memory-side cache does not hold the logits but does hold
-  // what lies between a sum and its gradient: a pair and the 1024 rows under
-  // way.  In us, walk and three launches, pairs of 768 rows of 50257 bf16:
-  // 5 (195 MB) 149 144, 6 (232 MB) 196 196, 8 (309 MB) 268 297, 16 457 545; 2400
-  // rows of 32000 fp32 (24 pairs, 307 MB) 217 247; 1600 rows of 131072 bf16 (16
-  // pairs, 420 MB, 1124 rows of which are 295 MB) 386 356.
+  // what lies between a sum and its gradient (a pair, here the average one, and
+  // the 1024 rows under way), and where a row takes longer than its tickets.
+  // In us, walk and three launches:
+  //   total, pairs of 768 rows of 50257 bf16: 294 MB 168 161, 368 MB 206 206,
+  //     441 MB 236 249, 588 MB 306 338, 1325 MB 652 791
+  //   row, at about 600 MB and 1200 MB: 8 KB (4096 bf16) 1101 338; 16 KB 584 310;
+  //     32 KB 479 383, 772 764; 44 KB 340 340, 643 672 (but 48 KB at 457 MB 288
+  //     251); 64 KB 358 349, 649 770 (468 MB: 257 264); 80 KB 297 322, 606 727;
+  //     128 KB (fp32, pairs of 300) 292 339, 560 726
+  //   what lies between, at about 600 MB: 212 MB (80 rows of 200 KB a pair) 316
+  //     343, 215 MB (700 of 128 KB) 336 326, 223 MB (1300 of 100 KB) 348 360, 306
+  //     MB (200 of 256 KB) 353 329
   const int64_t row = a.vocab * (int64_t)sizeof(typename Elem<BF16>::type);
-  const bool walk = a.rows * row > (256 << 20) && (a.rows / p.pairs + 1024) * row <= (224 << 20);
+  const bool walk = row >= (56 << 10) && a.rows * row > (400 << 20) && (a.rows / p.pairs + 1024) * row <= (224 << 20);
   if (walk || a.rows > ROWS_A_LAUNCH || p.pairs > ROWS_A_LAUNCH) {
     hipLaunchKernelGGL(kp_plan, dim3(1), dim3(1024), 0, s, a, p, w, PREF_SLACK);
     if ((e = hipGetLastError()) != hipSuccess) return e;

@@ -1,15 +1,18 @@
 """The preference loss where it walks pair by pair: over several launches, with more pairs than workgroups of a
-launch, with bad offsets.  Definitions and tolerances are those of test_gpu_train_ops.py."""
+launch, with bad offsets; and which calls do.  Definitions and tolerances are those of test_gpu_train_ops.py."""
 
 from __future__ import annotations
+
+import ctypes as C
 
 import numpy as np
 import pytest
 
 import muon_newton_schulz_step_amd as M
 import oracle.train_ops as T
-from test_gpu_train_ops import (DEV, E, TINY, around_untouched, dt, f64, grad_tol, poisoned, row_tol, strided,  # noqa: F401
-                                torch, vec, within)
+from test_gpu_train_ops import (DEV, E, TINY, around_untouched, big_pref, dt, f64, grad_tol, poisoned,  # noqa: F401
+                                row_tol, strided, torch, vec, within)
+from test_gpu_train_ops import test_preference_loss_in_one_walk as one_walk
 
 pytestmark = pytest.mark.gpu
 
@@ -102,3 +105,69 @@ def test_preference_walk_of_bad_offsets_touches_no_row_outside(torch):
                           poisoned(torch, M.preference_loss_workspace_bytes(n, pairs)))
         torch.cuda.synchronize()
         assert around_untouched(torch, dl, dbuf)
+
+
+# (a call takes the walk from 400 MB of logits on, as test_which_way pins)
+@pytest.mark.parametrize("lens,lead,tail,v,dtype,ld", [
+    # ragged pairs, an empty sequence and an empty pair, rows before and after them
+    ([600, 0, 0, 1011, 40, 1000, 633, 0, 820, 1], 3, 650, 50257, "bf16", 50257),
+    ([300, 400, 260, 10, 400, 320, 290, 350, 290, 310, 250, 300], 0, 0, 32001, "fp32", 32003)])
+def test_preference_walk_of_large_logits(torch, lens, lead, tail, v, dtype, ld):
+    one_walk(torch, lens, lead, tail, v, dtype, ld)
+
+
+def test_preference_walk_of_large_logits_in_a_graph(torch):
+    v, lens = 50257, [500, 610, 700, 340, 650, 650, 450, 400]
+    x, t, off, ref = big_pref(torch, lens, 0, 0, v, "bf16", v, 1)
+    ws = poisoned(torch, M.preference_loss_workspace_bytes(x.shape[0], 4))
+
+    def outs():
+        return torch.empty(1, device=DEV), torch.empty(8, device=DEV), torch.empty_like(x)
+    one, two = outs(), outs()
+
+    def call(o):
+        M.preference_loss(x, t, off, ref, o[0], o[1], o[2], ws)
+    call(two)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(one)
+    for k in range(1, 4):
+        x.mul_(0.9)
+        ref.add_(0.5 * k)
+        ws.fill_(0x5A + k)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        call(two)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(one, two)), f"replay {k}"
+    graph.reset()
+
+
+@pytest.mark.parametrize("n,v,pairs,dtype,walk", [
+    (34000, 4000, 40, "bf16", False),    # 272 MB of short rows
+    (14000, 16000, 18, "bf16", False),   # 448 MB of 32 KB rows: the tickets would take longer than the rows
+    (3000, 50257, 4, "bf16", False),     # 302 MB: the second read is half out of the cache anyway
+    (4500, 50257, 6, "bf16", True),      # 452 MB of 100 KB rows
+    (7000, 32000, 9, "bf16", True),      # 448 MB of 64 KB rows
+    (2400, 50257, 30, "fp32", True),     # 482 MB of 200 KB rows in short pairs
+    (2400, 50257, 3, "fp32", False),     # the same in long ones, which the cache does not hold
+    (1700, 131072, 17, "bf16", False)])  # nor these rows
+def test_which_way(torch, n, v, pairs, dtype, walk):
+    # with no look allowed at its pair a gradient of the walk is given up, so its loss is NaN; three launches wait
+    # for nothing
+    g = torch.Generator(DEV).manual_seed(n)
+    x = torch.empty((n, v), dtype=dt(torch, dtype), device=DEV).normal_(0.0, 2.0, generator=g)
+    t = torch.randint(0, v, (n,), generator=g, device=DEV)
+    off = torch.arange(2 * pairs + 1, device=DEV) * n // (2 * pairs)
+    loss, rew, d = torch.full((1,), 9.0, device=DEV), torch.empty(2 * pairs, device=DEV), torch.empty_like(x)
+    polls = C.c_int.in_dll(M.load(), "muon_preference_max_polls")
+    before, polls.value = polls.value, -1
+    try:
+        M.preference_loss(x, t, off, torch.zeros(2 * pairs, device=DEV), loss, rew, d,
+                          poisoned(torch, M.preference_loss_workspace_bytes(n, pairs)))
+        torch.cuda.synchronize()
+    finally:
+        polls.value = before
+    assert bool(loss.isnan()) == walk

@@ -357,9 +357,10 @@ const char *muon_last_error(void);
  *    the row length); elements are fp32 or bf16 (muon_dtype), whole numbers
  *    int32 or int64 (muon_index_type).  Only element alignment is required.
  *    A buffer of zero elements may be NULL.
- *  - Arithmetic is fp32 an element and fp64 a row; bf16 results are rounded
- *    once, to nearest even.  No float atomics: results are bitwise the same
- *    from run to run.
+ *  - Arithmetic is fp32 an element and fp64 a row (in the balance loss, whose
+ *    rows are short, fp32 a token and fp64 the sums over the tokens); bf16
+ *    results are rounded once, to nearest even.  No float atomics: results
+ *    are bitwise the same from run to run.
  *  - They enqueue kernels only (no copy, memset, event or allocation), so
  *    they can be captured into a graph.
  *  - A workspace is scratch for one call: its contents need not be set
@@ -368,8 +369,9 @@ const char *muon_last_error(void);
  *  - Errors of all of them: INVALID_ARG (NULL pointer, negative size, ld
  *    below the row length, unknown enum, non-finite factor), UNSUPPORTED (a
  *    size beyond a stated limit), ALIAS (an output overlaps another buffer
- *    of the call, except where in place is allowed), WORKSPACE (missing,
- *    not 256-byte aligned, too small), HIP.
+ *    of the call, except where in place is allowed; a matrix counts from its
+ *    first to its last element, with what lies between its rows), WORKSPACE
+ *    (missing, not 256-byte aligned, too small), HIP.
  * ---------------------------------------------------------------------- */
 
 typedef enum { MUON_IDX_INT32 = 0, MUON_IDX_INT64 = 1 } muon_index_type;
@@ -468,7 +470,9 @@ muon_status muon_preference_loss(const muon_logits *x, const void *offsets, int3
  * p is the softmax of a token's logits, lse its log-sum-exp; the counts
  * carry no gradient.  choices is tokens x k, dense; a choice outside
  * [0, experts) is counted nowhere.  Tokens that are not valid get a zero
- * gradient and are not read.
+ * gradient and are not read.  -inf logits are probabilities of 0; a valid
+ * token with nothing else has no softmax: its gradient, the balance and the
+ * loss are NaN, and z is infinite.
  *   counts  int32, one an expert;  stats[0..3)  loss, balance, z
  *   dlogits tokens x experts of type `dtype`; may be the logits themselves
  *           (same pointer and ld).

@@ -2,7 +2,7 @@
 //
 //   lookup     out[t] = scale * table[ids[t]]
 //   gradient   acc[v] (+)= scale * sum of dout[t] over the tokens t with
-//              ids[t] = v, added in token order
+//              ids[t] = v, added in a fixed order
 //
 // An id outside the table (padding) has no row: its output is 0 and it adds
 // nothing.  The gradient uses no float atomics: the tokens are sorted by row
@@ -120,7 +120,10 @@ static_assert(EB_BUCKETS == 1 << EB_SHIFT, "");
 
 // Rows from here on get their zeros beside the sums.  16384 tokens of 4096
 // columns into 32000 rows take 157 us so; with a quarter beside the sort 165,
-// with two thirds 164, with all 162.
+// with two thirds 164, with all 162.  (Every workgroup that sorts or writes
+// zeros reads all ids: 256, and in a first call 256 and 1024 more.  2^20 tokens
+// of 1024 bf16 columns take 1.7 ms, in a first call 3.1; the bytes that they
+// cannot do without 0.5 at a copy's rate.)
 __device__ __forceinline__ int64_t zeros_beside_sort(int64_t vocab) { return vocab / 2; }
 
 constexpr int EF_ZERO_SHIFT = 10;  // log2 of the workgroups that write zeros beside sums
@@ -572,10 +575,16 @@ __global__ __launch_bounds__(256) void ke_add(EmbedBwdArgs a, int col_blocks, in
 // before t, and otherwise adds them up, each wave those of its quarter of the
 // ids; the waves' sums are joined in their order.  Bound by the latency of
 // its dependent loads (ids, then dout rows) and the launch.  The other
-// workgroups write the zeros of a first call.  In us, so and with a sort: 1021
-// tokens of 1024 fp32 columns 7.3 15.3, 1000 tokens into a first call's 32000
-// rows of 1024 30 39, 1024 tokens of 8192 bf16 columns 21.3 23.5; every
-// workgroup reads all ids, so twice the tokens are four times the reads.
+// workgroups write the zeros of a first call.  In us, so and with a sort, ids
+// at word frequencies: 1021 tokens of 64 bf16 columns 8.3 16.6, of 1024 fp32
+// ones 8.8 17.6, of 4096 bf16 14.3 24.6, of 8192 21.9 26.9; 1000 tokens into a
+// first call's 32000 rows of 1024 30 33.  Every workgroup reads all ids, so
+// twice the tokens are four times the reads, and more ids a lane slow the
+// smaller calls too: with 2048 as the limit 2000 tokens of 64 columns take 9.6
+// (sorted 19.5) and of 1024 14.7 (23.2), but of 4096 29.6 (28.9), 1500 of 8192
+// 38.8 (29.7), and 1021 of 8192 29.2.  One workgroup a column block adds up a
+// row's tokens however many they are: 1000 tokens of 4096 bf16 columns take 31
+// (sorted 35) with 30% of them in one row, 74 (32) with all.
 namespace {
 
 constexpr int EF_IDS = EB_FEW / 256;  // ids that a lane holds

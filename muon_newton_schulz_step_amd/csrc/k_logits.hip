@@ -8,10 +8,12 @@
 //
 // where dlogp_r is the loss's derivative by the row's log-probability.  A row
 // whose target is outside the vocabulary has none: it is not read, its
-// log-probability and its gradient are 0.  Row sums are fp32 a thread (at
-// most a few hundred terms) joined in a fixed tree; everything a row has one
-// of is computed in fp64.  No float atomics: results are bitwise the same
-// from run to run.
+// log-probability and its gradient are 0.  Row sums are fp32 a thread, joined
+// in a fixed tree.  A thread has up to 64 terms in short rows and vocab / 512
+// or fewer in long ones, and each addition rounds by at most 2^-24: 131072
+// columns are off by at most 2^-16 (the largest vocabulary, 2^29, by 2^-4 if
+// all its roundings had one sign).  Everything a row has one of is computed in
+// fp64.  No float atomics: results are bitwise the same from run to run.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -223,9 +225,9 @@ constexpr int KEEP_LDS = 4, KEEP_REGS = 2, KEEP = KEEP_LDS + KEEP_REGS;
 // The policy loss of up to FEW_ROWS rows of at least FEW_ROW 16-byte vectors is
 // computed in pieces: at most FEW_GROUPS workgroups, FEW_VECS vectors or more
 // each.  Kernel time in us, in pieces and one workgroup a row: 8 x 50257 fp32
-// 9.3 14.2, 61 x 32000 bf16 10.8 11.5, 20 x 8192 9.4 7.5, 127 x 32000 13.3 12.5;
-// call time, 131072 bf16 columns: 8 rows 15.6 21.4, 64 15.8 22.8, 128 22.7
-// 23.7, 250 38 33.
+// (12564 vectors) 9.3 14.2; 4000 vectors (32000 bf16) either way, 61 rows 10.8
+// 11.5, 127 rows 13.3 12.5; 20 x 8192 bf16 (1024) 9.4 7.5.  Call time, 131072
+// bf16 columns: 8 rows 15.6 21.4, 64 15.8 22.8, 128 22.7 23.7, 250 38 33.
 constexpr int FEW_ROWS = 128, FEW_ROW = 8192, FEW_GROUPS = 1024, FEW_VECS = 512;
 // Workgroups that add up the rows' terms, at most; one for every SUM_ROWS rows.
 constexpr int SUM_GROUPS = 256, SUM_ROWS = 1024;

@@ -252,3 +252,25 @@ def test_fp32_gradients_without_a_bias_in_the_exponent(torch, v):
     M.preference_loss(x, vec(torch, t, "int64"), vec(torch, off, "int64"), lp[:seqs].contiguous(), loss, rew, d,
                       poisoned(torch, M.preference_loss_workspace_bytes(n, seqs // 2)), beta=1.0)
     assert abs(slope(d, seqs)) < 2e-9, "preference loss"
+
+
+@pytest.mark.parametrize("n,e", [(5, 8), (3000, 8), (100, 256)])
+def test_balance_of_a_valid_token_with_everything_masked(torch, n, e):
+    # it has no softmax, and says so: NaN in its gradient and the sums; the same token without its mark counts nowhere
+    x = torch.zeros((n, e), device=DEV)
+    x[2] = -INF
+    ch = torch.zeros((n, 1), dtype=torch.int64, device=DEV)
+    for counted in (True, False):
+        valid = torch.ones(n, dtype=torch.bool, device=DEV)
+        valid[2] = counted
+        counts, stats = torch.empty(e, dtype=torch.int32, device=DEV), torch.empty(3, device=DEV)
+        d = torch.full_like(x, 9.0)
+        M.balance_loss(x, ch, counts, stats, d, poisoned(torch, M.balance_loss_workspace_bytes(n, e)), valid=valid,
+                       coef=0.1, z_coef=0.01)
+        got = f64(stats)
+        assert int(counts[0]) == n - 1 + counted and not counts[1:].any()
+        assert not d[:2].isnan().any() and not d[3:].isnan().any()
+        if counted:
+            assert d[2].isnan().all() and np.isnan(got[0]) and np.isnan(got[1]) and got[2] == INF
+        else:
+            assert not d[2].any() and np.isfinite(got).all()

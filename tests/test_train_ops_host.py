@@ -310,3 +310,12 @@ def test_tensor_checks():
            torch.zeros(2), x.clone(), ws)
     refuse("logits: a host", M.balance_loss, x, torch.zeros(4, 2, dtype=torch.int64),
            torch.zeros(6, dtype=torch.int32), torch.zeros(3), x.clone(), ws)
+
+
+def test_a_matrix_counts_with_what_lies_between_its_rows():
+    # two column ranges of one allocation: the second is refused as an output, its rows lie between the first's
+    _expect("muon_embed_forward", "MUON_ERR_ALIAS", BASE, 10, 8, 16, 0, BASE + BIG, 0, 5, 1.0, BASE + 8 * 4, 16, None,
+            text="out and table")
+    _expect("muon_balance_loss", "MUON_ERR_ALIAS", BASE, 4, 8, 16, 0, BASE + BIG, 0, 2, None,
+            C.byref(_lib.muon_balance_options(0.1, 0.0)), BASE + 2 * BIG, BASE + 3 * BIG, BASE + 32, 16, WS,
+            M.balance_loss_workspace_bytes(4, 8), None, text="dlogits and logits")

@@ -9,8 +9,10 @@ the logits themselves.  Matrices may have any row stride; their elements in a
 row have to be adjacent.  The calls check every tensor (device, type, shape,
 strides) and raise ``ValueError`` before anything is enqueued; what the
 library itself refuses raises ``MuonError``.  Work is ordered on ``stream``
-(the current one of the tensors' device by default); nothing synchronises the
-host, and nothing is allocated, so the calls can be captured into a graph.
+(the current one of the tensors' device by default); on another stream than a
+tensor's own, keeping the tensor until the work is done is the caller's part
+(``Tensor.record_stream``).  Nothing synchronises the host, and nothing is
+allocated, so the calls can be captured into a graph.
 """
 
 from __future__ import annotations

@@ -27,47 +27,47 @@ ACTS = ("none", "relu", "silu", "gelu", "gelu_tanh")
 def listed():
     return [
         # one short micro-batch through a small model's residual branch: latency counts
-        {"name": "dropout, 33 x 1024", "op": "dropout", "rows": 33, "cols": 1024, "dtype": "fp32", "p": 0.1,
+        {"name": "dropout 33 x 1024", "op": "dropout", "rows": 33, "cols": 1024, "dtype": "fp32", "p": 0.1,
          "residual": True},
         # a training batch of a wide model, added to the residual stream
-        {"name": "dropout, 16384 x 8192", "op": "dropout", "rows": 16384, "cols": 8192, "dtype": "bf16", "p": 0.1,
+        {"name": "dropout 16384 x 8192", "op": "dropout", "rows": 16384, "cols": 8192, "dtype": "bf16", "p": 0.1,
          "residual": True},
         # a few tokens of a small mixture: softmax, the two best of eight, odd count
-        {"name": "route, 61 x 8", "op": "route", "tokens": 61, "experts": 8, "k": 2, "dtype": "bf16", "ids": "int64",
+        {"name": "route 61 x 8", "op": "route", "tokens": 61, "experts": 8, "k": 2, "dtype": "bf16", "ids": "int64",
          "scoring": "softmax", "bias": False, "groups": 1, "keep": 1, "top": 1, "renorm": True, "scale": 1.0,
          "pad": 0.0, "first": True},
         # a global batch of a fine-grained mixture: sigmoid scores, a balancing bias, half of eight groups, eight
         # choices; padded tokens route nowhere
-        {"name": "route, 131072 x 256", "op": "route", "tokens": 131072, "experts": 256, "k": 8, "dtype": "fp32",
+        {"name": "route 131072 x 256", "op": "route", "tokens": 131072, "experts": 256, "k": 8, "dtype": "fp32",
          "ids": "int32", "scoring": "sigmoid", "bias": True, "groups": 8, "keep": 4, "top": 2, "renorm": True,
          "scale": 2.5, "pad": 0.1, "first": True},
         # the tokens of a small mixture sorted by expert, and the experts' rows summed, forwards and backwards
-        {"name": "order and combine, 509 x 2", "op": "combine", "tokens": 509, "experts": 8, "k": 2, "dim": 1024,
+        {"name": "order and combine 509 x 2", "op": "combine", "tokens": 509, "experts": 8, "k": 2, "dim": 1024,
          "dtype": "fp32", "ids": "int64", "pad": 0.0, "residual": True},
         # the same of a fine-grained mixture
-        {"name": "order and combine, 16384 x 8", "op": "combine", "tokens": 16384, "experts": 256, "k": 8,
+        {"name": "order and combine 16384 x 8", "op": "combine", "tokens": 16384, "experts": 256, "k": 8,
          "dim": 4096, "dtype": "bf16", "ids": "int32", "pad": 0.05, "residual": True},
         # one token through a wide layer: the weights' way through memory
-        {"name": "linear, 1 token", "op": "linear", "rows": 1, "in": 4096, "out": 11008, "groups": 1, "dtype": "bf16",
+        {"name": "linear 1 token", "op": "linear", "rows": 1, "in": 4096, "out": 11008, "groups": 1, "dtype": "bf16",
          "layout": "in_out", "act": "silu", "bias": True, "residual": False, "pre": False, "pad": 0.0},
         # a training batch through the first matrix of a block; what the gradient needs is kept
-        {"name": "linear, 8192 tokens", "op": "linear", "rows": 8192, "in": 4096, "out": 11008, "groups": 1,
+        {"name": "linear 8192 tokens", "op": "linear", "rows": 8192, "in": 4096, "out": 11008, "groups": 1,
          "dtype": "bf16", "layout": "in_out", "act": "gelu_tanh", "bias": True, "residual": False, "pre": True,
          "pad": 0.0},
         # 32 experts of a mixture on their sorted tokens: very uneven groups, empty ones among them
-        {"name": "linear, 32 experts", "op": "linear", "rows": 32768, "in": 1024, "out": 4096, "groups": 32,
+        {"name": "linear 32 experts", "op": "linear", "rows": 32768, "in": 1024, "out": 4096, "groups": 32,
          "dtype": "bf16", "layout": "out_in", "act": "silu", "bias": True, "residual": False, "pre": True,
          "pad": 0.05},
         # both gradients of the second matrix of a block, through the activation before it; odd count
-        {"name": "linear gradients, 4091 tokens", "op": "linear_grad", "rows": 4091, "in": 11008, "out": 4096,
+        {"name": "linear gradients 4091 tokens", "op": "linear_grad", "rows": 4091, "in": 11008, "out": 4096,
          "groups": 1, "dtype": "bf16", "layout": "in_out", "act": "gelu_tanh", "bias": True, "residual": False,
          "first": True, "pad": 0.0},
         # both gradients of the experts' second matrices
-        {"name": "linear gradients, 32 experts", "op": "linear_grad", "rows": 32768, "in": 4096, "out": 1024,
+        {"name": "linear gradients 32 experts", "op": "linear_grad", "rows": 32768, "in": 4096, "out": 1024,
          "groups": 32, "dtype": "bf16", "layout": "out_in", "act": "silu", "bias": True, "residual": False,
          "first": True, "pad": 0.05},
         # a small model in 32 bits, odd sizes, with the skip connection's gradient
-        {"name": "linear gradients, 1021 x 1000 fp32", "op": "linear_grad", "rows": 1021, "in": 1000, "out": 257,
+        {"name": "linear gradients 1021 x 1000 fp32", "op": "linear_grad", "rows": 1021, "in": 1000, "out": 257,
          "groups": 1, "dtype": "fp32", "layout": "in_out", "act": "gelu", "bias": True, "residual": True,
          "first": True, "pad": 0.0},
     ]

@@ -487,6 +487,103 @@ muon_status muon_balance_loss(const void *logits, int64_t tokens, int64_t expert
                               const muon_balance_options *opt, int32_t *counts, float *stats, void *dlogits,
                               int64_t dlogits_ld, void *ws, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of a trained layer: dropout, a router's choice of experts, the
+ * order of the tokens by expert, the experts' weighted sum, and the product
+ * with a weight matrix, or with one a group of rows, each with its
+ * gradient.  Conventions and errors as above; what else lies in a matrix's
+ * allocation, and rows that a call's definition leaves out, keep their
+ * contents.
+ * ---------------------------------------------------------------------- */
+
+/* Dropout: out = residual + (kept ? x / (1 - p) : 0), rounded once; residual
+ * may be NULL (none).  Element (r, c) is kept if word c mod 4 of
+ *   Philox4x32-10, counter (c / 4, r, site, step), key (seed, low half first)
+ * is at least round(p 2^32): the mask depends on where an element stands and
+ * on seed, site and step alone, and is never stored.  The gradient by x is
+ * the same call on the gradient by out, without a residual.  A dropped
+ * element adds nothing, also where x is not finite.  If device_step is not
+ * NULL its low 32 bits are read on the device instead of step, so that a
+ * captured call draws anew whenever the program raises it.  0 <= p < 1.  out
+ * may be x or the residual (same pointer and ld). */
+muon_status muon_dropout(const void *x, int64_t rows, int64_t cols, int64_t ld, int32_t dtype, double p, uint64_t seed,
+                         uint32_t site, uint32_t step, const int64_t *device_step, const void *residual,
+                         int64_t residual_ld, void *out, int64_t out_ld, void *stream);
+
+/* A router's choice of k experts a token.
+ *   s = softmax or sigmoid of the token's logits, rank = s + bias
+ *   With groups > 1 the experts are cut into equal consecutive groups; a
+ *   group's value is the sum of its group_top best ranks, and only experts
+ *   of the keep_groups groups of highest value can be chosen.
+ *   choices[t]  the k experts of highest rank, highest first
+ *   weights[t]  scale s_j / (sum of the chosen s + 1e-20), or scale s_j if
+ *               renormalize is 0
+ * Of equal ranks or values the lower index goes first.  The choice is that
+ * of the exact ranks: ranks that fp32 does not tell apart are computed again
+ * in fp64.  Without a bias (NULL), and with group_top 1 or one group, experts
+ * are ranked by their logits.  An expert whose logit or bias is -inf is never
+ * chosen; where a token has fewer than k experts left, and in tokens that are
+ * not valid (valid NULL: all are), the choice is -1 and its weight 0.  A NaN
+ * ranks below every number.
+ * The gradient by the logits, for the gradient dweights by the weights, is
+ * written (first != 0) or added to what dlogits holds; the choice itself
+ * carries none, nor does the bias.  Choices outside [0, experts) add nothing;
+ * tokens that are not valid get zeros, or keep what they hold.  It takes the
+ * scoring, renormalize and scale of the choice, and no notice of the groups.
+ * Limits: experts <= MUON_BALANCE_MAX_EXPERTS, k <= MUON_ROUTE_MAX_CHOICES,
+ * groups <= MUON_ROUTE_MAX_GROUPS, tokens * k < 2^31. */
+typedef enum { MUON_SCORE_SOFTMAX = 0, MUON_SCORE_SIGMOID = 1 } muon_scoring;
+#define MUON_ROUTE_MAX_CHOICES 32
+#define MUON_ROUTE_MAX_GROUPS 32
+typedef struct {
+  int32_t scoring;     /* muon_scoring                                    */
+  int32_t renormalize;
+  int32_t groups, keep_groups;
+  int32_t group_top;   /* 1 or 2                                          */
+  int32_t reserved;
+  double scale;
+} muon_route_options;
+muon_status muon_route(const void *logits, int64_t tokens, int64_t experts, int64_t ld, int32_t dtype, const float *bias,
+                       const uint8_t *valid, const muon_route_options *opt, void *choices, int32_t choice_type,
+                       int64_t k, float *weights, void *stream);
+muon_status muon_route_backward(const void *logits, int64_t tokens, int64_t experts, int64_t ld, int32_t dtype,
+                                const uint8_t *valid, const muon_route_options *opt, const void *choices,
+                                int32_t choice_type, int64_t k, const float *dweights, void *dlogits,
+                                int64_t dlogits_ld, int32_t first, void *stream);
+
+/* The order of the tokens by expert.  Every choice in [0, experts) gets a
+ * slot: those of expert e have the slots [offsets[e], offsets[e + 1]), in the
+ * order of their tokens and of a token's choices.
+ *   slot_tokens  tokens * k: the slots' tokens, -1 behind the last slot
+ *   offsets      experts + 1
+ *   place        tokens x k: the choices' slots, -1 for a choice outside
+ * With slot_tokens as ids, muon_embed_forward gathers the experts' rows.
+ * Limits: experts <= MUON_BALANCE_MAX_EXPERTS, tokens * k < 2^31. */
+muon_status muon_expert_order_workspace_bytes(int64_t tokens, int64_t k, int64_t experts, size_t *bytes);
+muon_status muon_expert_order(const void *choices, int32_t choice_type, int64_t tokens, int64_t k, int64_t experts,
+                              int32_t *slot_tokens, int32_t *offsets, int32_t *place, void *ws, size_t ws_bytes,
+                              void *stream);
+
+/* What the experts return, summed up a token:
+ *   out[t] = residual[t] + sum_j weights[t][j] y[place[t][j]]
+ * y is rows x dim, out and residual tokens x dim, of type `dtype`; place and
+ * weights are tokens x k, dense; a place outside [0, rows) adds nothing.
+ * weights NULL: 1 each (the gradient of the gather); residual NULL: none.
+ * out may be the residual (same pointer and ld).
+ * The gradients, for the gradient dout by out:
+ *   dy[place[t][j]] = weights[t][j] dout[t]       rows of no place are kept
+ *   dweights[t][j]  = sum dout[t] y[place[t][j]]  0 for a place outside
+ * Either may be NULL; y is read for dweights only.  dy may be y (same pointer
+ * and ld).  No two places may be equal (muon_expert_order gives none).
+ * Limits: tokens * k, rows, dim < 2^31, tokens < 2^26, tokens * dim < 2^34. */
+muon_status muon_expert_combine(const void *y, int64_t rows, int64_t dim, int64_t y_ld, int32_t dtype,
+                                const int32_t *place, int64_t tokens, int64_t k, const float *weights,
+                                const void *residual, int64_t residual_ld, void *out, int64_t out_ld, void *stream);
+muon_status muon_expert_combine_backward(const void *dout, int64_t tokens, int64_t dim, int64_t dout_ld, int32_t dtype,
+                                         const int32_t *place, int64_t k, const float *weights, const void *y,
+                                         int64_t y_ld, int64_t rows, void *dy, int64_t dy_ld, float *dweights,
+                                         void *stream);
+
 #ifdef __cplusplus
 }
 #endif

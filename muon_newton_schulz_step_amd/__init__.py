@@ -5,7 +5,8 @@ This package is the Python face of that library: ``_lib`` binds the C entry
 points by name; ``MuonGroup`` is a small convenience wrapper that owns a plan;
 ``train_ops`` holds the operators around the step on torch tensors (embedding
 lookup and gradient, token log-probability, policy, preference and balance
-losses).
+losses), ``layer_ops`` those of a trained layer (dropout, routing to experts,
+the tokens' order by expert and the experts' weighted sum).
 Device memory and streams come from the caller (e.g. torch tensors).
 """
 
@@ -20,13 +21,18 @@ from ._lib import (DTYPE, EXPORTS, NS_METHOD, PRECISION, SCHEDULE, MuonError, lo
                    INDEX_TYPE, muon_balance_loss, muon_balance_loss_workspace_bytes, muon_balance_options,
                    muon_embed_backward, muon_embed_backward_workspace_bytes, muon_embed_forward, muon_logits,
                    muon_policy_loss, muon_policy_loss_workspace_bytes, muon_policy_options, muon_preference_loss,
-                   muon_preference_loss_workspace_bytes, muon_preference_options, muon_token_logprob)
-from . import train_ops
+                   muon_preference_loss_workspace_bytes, muon_preference_options, muon_token_logprob,
+                   SCORING, muon_dropout, muon_expert_combine, muon_expert_combine_backward, muon_expert_order,
+                   muon_expert_order_workspace_bytes, muon_route, muon_route_backward, muon_route_options)
+from . import layer_ops, train_ops
+from .layer_ops import (dropout, expert_combine, expert_combine_backward, expert_order,  # noqa: F401
+                        expert_order_workspace_bytes, route_backward, route_experts)
 from .train_ops import (balance_loss, balance_loss_workspace_bytes, embed_backward,  # noqa: F401
                         embed_backward_workspace_bytes, embed_forward, policy_loss, policy_loss_workspace_bytes,
                         preference_loss, preference_loss_workspace_bytes, token_logprob)
 
-__all__ = ["MuonGroup", "pack_layout", "MuonError", "load"] + list(train_ops.__all__) + list(EXPORTS)
+__all__ = ["MuonGroup", "pack_layout", "MuonError", "load"] + list(train_ops.__all__) + list(layer_ops.__all__) + list(
+    EXPORTS)
 
 
 def pack_layout(shapes, num_partitions: int, align: int = 16, interior_align: bool = False):

@@ -25,6 +25,7 @@ PRECISION = {"fp32": 0, "bf16": 1}
 DTYPE = {"fp32": 0, "bf16": 1}
 SCHEDULE = {"launches": 0, "persistent": 1}
 INDEX_TYPE = {"int32": 0, "int64": 1}
+SCORING = {"softmax": 0, "sigmoid": 1}
 
 # every symbol include/muon.h declares
 EXPORTS = ("muon_default_options", "muon_plan_create", "muon_plan_workspace_bytes", "muon_accumulate",
@@ -33,7 +34,9 @@ EXPORTS = ("muon_default_options", "muon_plan_create", "muon_plan_workspace_byte
            "muon_plan_phase_ms", "muon_plan_destroy", "muon_status_string", "muon_last_error",
            "muon_embed_forward", "muon_embed_backward_workspace_bytes", "muon_embed_backward", "muon_token_logprob",
            "muon_policy_loss_workspace_bytes", "muon_policy_loss", "muon_preference_loss_workspace_bytes",
-           "muon_preference_loss", "muon_balance_loss_workspace_bytes", "muon_balance_loss")
+           "muon_preference_loss", "muon_balance_loss_workspace_bytes", "muon_balance_loss",
+           "muon_dropout", "muon_route", "muon_route_backward", "muon_expert_order_workspace_bytes",
+           "muon_expert_order", "muon_expert_combine", "muon_expert_combine_backward")
 
 
 class muon_matrix(C.Structure):
@@ -84,6 +87,11 @@ class muon_balance_options(C.Structure):
     _fields_ = [("coef", C.c_double), ("z_coef", C.c_double)]
 
 
+class muon_route_options(C.Structure):
+    _fields_ = [("scoring", C.c_int32), ("renormalize", C.c_int32), ("groups", C.c_int32), ("keep_groups", C.c_int32),
+                ("group_top", C.c_int32), ("reserved", C.c_int32), ("scale", C.c_double)]
+
+
 _lib = None
 
 
@@ -132,6 +140,15 @@ def load(path: str | None = None) -> C.CDLL:
                                     vp, vp, i64, vp, sz, vp]),
         "muon_status_string": (C.c_char_p, [i32]),
         "muon_last_error": (C.c_char_p, []),
+        "muon_dropout": (i32, [vp, i64, i64, i64, i32, C.c_double, C.c_uint64, C.c_uint32, C.c_uint32, vp, vp, i64, vp,
+                               i64, vp]),
+        "muon_route": (i32, [vp, i64, i64, i64, i32, vp, vp, C.POINTER(muon_route_options), vp, i32, i64, vp, vp]),
+        "muon_route_backward": (i32, [vp, i64, i64, i64, i32, vp, C.POINTER(muon_route_options), vp, i32, i64, vp, vp,
+                                      i64, i32, vp]),
+        "muon_expert_order_workspace_bytes": (i32, [i64, i64, i64, C.POINTER(sz)]),
+        "muon_expert_order": (i32, [vp, i32, i64, i64, i64, vp, vp, vp, vp, sz, vp]),
+        "muon_expert_combine": (i32, [vp, i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, vp, i64, vp]),
+        "muon_expert_combine_backward": (i32, [vp, i64, i64, i64, i32, vp, i64, vp, vp, i64, i64, vp, i64, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -435,3 +452,60 @@ def muon_balance_loss(logits, tokens: int, experts: int, ld: int, dtype, choices
                                   dlogits_ld, _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream))
     if st:
         _check(st, "muon_balance_loss")
+
+
+# ---------------------------------------------- operators of a trained layer
+
+
+def muon_dropout(x, rows: int, cols: int, ld: int, dtype, p: float, seed: int, site: int, step: int, device_step,
+                 residual, residual_ld: int, out, out_ld: int, stream=None) -> None:
+    st = load().muon_dropout(_ptr(x), rows, cols, ld, _dt(dtype), p, seed, site, step, _ptr(device_step),
+                             _ptr(residual), residual_ld, _ptr(out), out_ld, _stream(stream))
+    if st:
+        _check(st, "muon_dropout")
+
+
+def muon_route(logits, tokens: int, experts: int, ld: int, dtype, bias, valid, options: muon_route_options, choices,
+               choice_type, k: int, weights, stream=None) -> None:
+    st = load().muon_route(_ptr(logits), tokens, experts, ld, _dt(dtype), _ptr(bias), _ptr(valid), C.byref(options),
+                           _ptr(choices), _it(choice_type), k, _ptr(weights), _stream(stream))
+    if st:
+        _check(st, "muon_route")
+
+
+def muon_route_backward(logits, tokens: int, experts: int, ld: int, dtype, valid, options: muon_route_options, choices,
+                        choice_type, k: int, dweights, dlogits, dlogits_ld: int, first: bool, stream=None) -> None:
+    st = load().muon_route_backward(_ptr(logits), tokens, experts, ld, _dt(dtype), _ptr(valid), C.byref(options),
+                                    _ptr(choices), _it(choice_type), k, _ptr(dweights), _ptr(dlogits), dlogits_ld,
+                                    1 if first else 0, _stream(stream))
+    if st:
+        _check(st, "muon_route_backward")
+
+
+def muon_expert_order_workspace_bytes(tokens: int, k: int, experts: int) -> int:
+    return _bytes_of("muon_expert_order_workspace_bytes", tokens, k, experts)
+
+
+def muon_expert_order(choices, choice_type, tokens: int, k: int, experts: int, slot_tokens, offsets, place, ws,
+                      ws_bytes: int, stream=None) -> None:
+    st = load().muon_expert_order(_ptr(choices), _it(choice_type), tokens, k, experts, _ptr(slot_tokens),
+                                  _ptr(offsets), _ptr(place), _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream))
+    if st:
+        _check(st, "muon_expert_order")
+
+
+def muon_expert_combine(y, rows: int, dim: int, y_ld: int, dtype, place, tokens: int, k: int, weights, residual,
+                        residual_ld: int, out, out_ld: int, stream=None) -> None:
+    st = load().muon_expert_combine(_ptr(y), rows, dim, y_ld, _dt(dtype), _ptr(place), tokens, k, _ptr(weights),
+                                    _ptr(residual), residual_ld, _ptr(out), out_ld, _stream(stream))
+    if st:
+        _check(st, "muon_expert_combine")
+
+
+def muon_expert_combine_backward(dout, tokens: int, dim: int, dout_ld: int, dtype, place, k: int, weights, y,
+                                 y_ld: int, rows: int, dy, dy_ld: int, dweights, stream=None) -> None:
+    st = load().muon_expert_combine_backward(_ptr(dout), tokens, dim, dout_ld, _dt(dtype), _ptr(place), k,
+                                             _ptr(weights), _ptr(y), y_ld, rows, _ptr(dy), dy_ld, _ptr(dweights),
+                                             _stream(stream))
+    if st:
+        _check(st, "muon_expert_combine_backward")

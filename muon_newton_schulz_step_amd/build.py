@@ -23,7 +23,8 @@ LIB_NAME = "libmuon_mi355x.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["plan.cpp", "abi.cpp", "noalloc.hip", "k_elem.hip", "k_gemm.hip", "k_gemm256.hip", "k_head.hip",
-           "train_abi.cpp", "k_embed.hip", "k_logits.hip", "k_balance.hip"]
+           "train_abi.cpp", "k_embed.hip", "k_logits.hip", "k_balance.hip", "layer_abi.cpp", "k_dropout.hip", "k_route.hip",
+           "k_order.hip"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops: keep the compiler from emitting packed fp32 VALU ops.

@@ -1,0 +1,516 @@
+// A router's choice of experts and its gradient, on gfx950.
+//
+//   s = softmax(x) or sigmoid(x),  rank = s + bias
+//   a group's value = the sum of its `top` best ranks; the `keep` best groups
+//   stay, and of their experts the k of best rank are chosen (equal ranks: the
+//   lower index first)
+//   w_j = scale s_j / (sum of the chosen s + 1e-20), or scale s_j
+//
+//   d s_j = scale (dw_j - sum_i dw_i s_i / S) / S, or scale dw_j
+//   softmax: d x_e = [e chosen] s_e ds_e - s_e sum_j s_j ds_j
+//   sigmoid: d x_e = [e chosen] s_e (1 - s_e) ds_e
+//
+// Ranks are computed in fp32; a token in which two ranks that decide about the
+// choice or its order are closer than fp32 tells apart is decided again in
+// fp64 (route_exact), so that the choice is that of the definition.  Without a
+// bias the logits themselves order the experts, and nothing is ever close.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "devops.hpp"
+#include "layer_ops.hpp"
+
+namespace muon {
+
+using namespace dev;
+
+namespace {
+
+constexpr int RT = 256;  // threads of a workgroup
+constexpr float NORM_EPS = 1e-20f;
+constexpr int QUAD_XOR1 = 0xb1, QUAD_XOR2 = 0x4e, ROW_ROR8 = 0x128, ROW_ROR4 = 0x124;
+
+template <int CTRL>
+__device__ __forceinline__ int dpp_i(int x) {
+  return __builtin_amdgcn_update_dpp(x, x, CTRL, 0xf, 0xf, false);
+}
+__device__ __forceinline__ float as_f(int x) { return __int_as_float(x); }
+
+// Reduction over LANES consecutive lanes (4, 16 or 64); every lane gets it.
+template <int LANES, class F>
+__device__ __forceinline__ float reduce_f(float v, F f) {
+  v = f(v, as_f(dpp_i<QUAD_XOR1>(__float_as_int(v))));
+  v = f(v, as_f(dpp_i<QUAD_XOR2>(__float_as_int(v))));
+  if constexpr (LANES >= 16) {
+    v = f(v, as_f(dpp_i<ROW_ROR8>(__float_as_int(v))));
+    v = f(v, as_f(dpp_i<ROW_ROR4>(__float_as_int(v))));
+  }
+  if constexpr (LANES == 64) {
+    v = f(v, __shfl_xor(v, 16));
+    v = f(v, __shfl_xor(v, 32));
+  }
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ int reduce_min(int v) {
+  v = min(v, dpp_i<QUAD_XOR1>(v));
+  v = min(v, dpp_i<QUAD_XOR2>(v));
+  if constexpr (LANES >= 16) {
+    v = min(v, dpp_i<ROW_ROR8>(v));
+    v = min(v, dpp_i<ROW_ROR4>(v));
+  }
+  if constexpr (LANES == 64) {
+    v = min(v, __shfl_xor(v, 16));
+    v = min(v, __shfl_xor(v, 32));
+  }
+  return v;
+}
+struct Max {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct Sum {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+
+// of a row's sum; a row of -inf has none
+__device__ __forceinline__ float inverse(float s) { return s == 0.f ? 0.f : 1.f / s; }
+__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + exp_term(0.f, x)); }  // exp(0 - x)
+
+template <bool BF16>
+__device__ __forceinline__ float logit(const RouteArgs &a, int64_t t, int e) {
+  typedef typename Elem<BF16>::type T;
+  return Elem<BF16>::get(static_cast<const T *>(a.logits)[t * a.ld + e]);
+}
+
+// rank as it is compared: -inf is never chosen, a NaN comes last
+__device__ __forceinline__ float orderly(float r) { return r != r ? kLowest : r; }
+
+// A token's choice in fp64, by a whole wave: expert e belongs to lane e % 64,
+// its rank to rank[e] in LDS.  Writes k experts (-1 where there are no more)
+// to chosen.
+template <bool BF16>
+__device__ __forceinline__ void route_exact(const RouteArgs &a, int64_t t, double *rank, int32_t *chosen) {
+  const int lane = threadIdx.x & 63;
+  const double ninf = -INFINITY;
+  auto wave_max = [](double v) {
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) v = fmax(v, shfl_xor_f64(v, m));
+    return v;
+  };
+  double top = ninf, total = 0.0;
+  for (int e = lane; e < a.experts; e += 64) {
+    rank[e] = (double)logit<BF16>(a, t, e);
+    top = fmax(top, rank[e]);
+  }
+  top = wave_max(top);
+  // exp(x - max) for the softmax, exp(-x) for the sigmoid
+  for (int e = lane; e < a.experts; e += 64) {
+    const double x = rank[e];
+    if (x == ninf) continue;
+    const double y = exp(a.softmax ? x - top : -x);
+    total += y;
+    rank[e] = a.softmax ? y : 1.0 / (1.0 + y);
+  }
+  if (a.softmax) {
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) total += shfl_xor_f64(total, m);
+  } else {
+    total = 1.0;
+  }
+  for (int e = lane; e < a.experts; e += 64) {
+    if (rank[e] == ninf) continue;
+    const double r = rank[e] / total + (a.bias ? (double)a.bias[e] : 0.0);
+    rank[e] = r != r ? (double)kLowest : r;
+  }
+  // the best rank in [lo, hi) but for expert `but`, and the expert (or INT_MAX)
+  auto best = [&](int lo, int hi, int but, double &v) {
+    double m = ninf;
+    int at = INT32_MAX;
+    for (int e = lane; e < hi; e += 64)
+      if (e >= lo && e != but && rank[e] > m) {
+        m = rank[e];
+        at = e;
+      }
+    v = wave_max(m);
+    at = m == v ? at : INT32_MAX;
+#pragma unroll
+    for (int q = 32; q > 0; q >>= 1) at = min(at, __shfl_xor(at, q));
+    return at;
+  };
+  if (a.groups > 1) {
+    const int size = a.experts / a.groups;
+    double value = ninf;  // of group `lane`
+    for (int g = 0; g < a.groups; ++g) {
+      double v1, v2;
+      const int e = best(g * size, (g + 1) * size, -1, v1);
+      if (a.top > 1 && best(g * size, (g + 1) * size, e, v2) != INT32_MAX) v1 += v2;
+      if (lane == g) value = v1;
+    }
+    int before = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const double v = shfl_f64(value, g);
+      before += v > value || (v == value && g < lane);
+    }
+    const uint64_t open = __ballot(lane < a.groups && before < a.keep);
+    for (int e = lane; e < a.experts; e += 64)
+      if (!(open >> (e / size) & 1)) rank[e] = ninf;
+  }
+  for (int j = 0; j < a.k; ++j) {
+    double v;
+    const int e = best(0, a.experts, -1, v);
+    if (lane == 0) chosen[j] = e == INT32_MAX ? -1 : e;
+    if (e != INT32_MAX && (e & 63) == lane) rank[e] = ninf;
+  }
+}
+
+// LANES lanes take a token, V consecutive experts a lane.
+template <bool BF16, int LANES, int V>
+__global__ __launch_bounds__(RT) void kr_route(RouteArgs a) {
+  typedef Elem<BF16> E;
+  typedef typename E::type T;
+  constexpr int PER = RT / LANES, N = E::N < V ? E::N : V;
+  __shared__ int32_t chosen[PER][ROUTE_MAX_CHOICES + 1];
+  __shared__ double exact[RT / 64][LANES * V];
+  const int l = threadIdx.x & (LANES - 1), slot = threadIdx.x / LANES;
+  const int64_t t = (int64_t)blockIdx.x * PER + slot;
+  const bool in = t < a.tokens;
+  const bool ok = in && (!a.valid || a.valid[t]);
+  const int e0 = l * V;
+  const bool by_logit = !a.bias && (a.groups == 1 || a.top == 1);
+  float r[V];
+  {
+    const T *x = static_cast<const T *>(a.logits) + (ok ? t : 0) * a.ld + e0;
+#pragma unroll
+    for (int i = 0; i < V; i += N) {
+      if (ok && N == E::N && e0 + i + N <= a.experts) {
+        E::unpack(load16(x + i), r + i);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) r[i + j] = ok && e0 + i + j < a.experts ? E::get(x[i + j]) : -INFINITY;
+      }
+    }
+  }
+  float m = 0.f, inv = 0.f;  // softmax: the row's maximum, 1 / sum
+  if (a.softmax) {
+    m = kLowest;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, r[i]);
+    m = reduce_f<LANES>(m, Max());
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) s += exp_term(r[i], m);
+    inv = inverse(reduce_f<LANES>(s, Sum()));
+  }
+  if (!by_logit) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float s = a.softmax ? exp_term(r[i], m) * inv : sigmoid(r[i]);
+      const float b = a.bias ? a.bias[min(e0 + i, a.experts - 1)] : 0.f;
+      r[i] = r[i] == -INFINITY ? r[i] : s + b;
+    }
+  }
+  float size_max = 0.f;  // the largest finite rank's magnitude, for the bound on its rounding
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    r[i] = orderly(r[i]);
+    if (fabsf(r[i]) < 3e38f) size_max = fmaxf(size_max, fabsf(r[i]));
+  }
+  bool close = false;
+  float tol = 0.f;
+  if (!by_logit) {
+    // What a score may be off by, in units of 2^-24: an exponential of d carries |d| + 2 of itself, which moves a
+    // sigmoid by at most 3 in all; a softmax's sum carries sum p (|d| + 2) <= 7 + 2 for 1024 experts, at most 22 for
+    // its additions and 4 for the quotient and the product, its term s (|d| + 2) < 3.  The bias adds a rounding of
+    // the rank.  Twice that for the difference of two ranks, twice again for values that are sums of two.
+    size_max = reduce_f<LANES>(size_max, Max());
+    tol = (40.f + size_max) * (4.f * 5.9604645e-8f);
+  }
+  if (a.groups > 1) {
+    // every lane goes through the groups' values, group by group
+    const int size = a.experts / a.groups;
+    uint32_t open = 0;
+    float value[ROUTE_MAX_GROUPS / 4];  // of group l + LANES i, i < groups / LANES
+#pragma unroll
+    for (int i = 0; i < ROUTE_MAX_GROUPS / 4; ++i) value[i] = -INFINITY;
+    for (int g = 0; g < a.groups; ++g) {
+      const int lo = g * size - e0, hi = lo + size;
+      float v1 = -INFINITY, v2 = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float x = i >= lo && i < hi ? r[i] : -INFINITY;
+        v2 = fmaxf(v2, fminf(v1, x));
+        v1 = fmaxf(v1, x);
+      }
+      const float best = reduce_f<LANES>(v1, Max());
+      if (a.top > 1) {
+        // the second: of the lane that holds the best, its second; of the others, their first
+        const int who = reduce_min<LANES>(v1 == best ? l : LANES);
+        const float second = reduce_f<LANES>(l == who ? v2 : v1, Max());
+        v1 = second == -INFINITY ? best : fmaxf(best + second, kLowest);
+      } else {
+        v1 = best;
+      }
+#pragma unroll
+      for (int i = 0; i < ROUTE_MAX_GROUPS / 4; ++i)
+        if (g == l + LANES * i) value[i] = v1;
+    }
+    // the `keep` best, one at a time; the first that stays outside tells how close it was
+    float last = INFINITY;
+    for (int q = 0; q <= a.keep && q < a.groups; ++q) {
+      float v = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < ROUTE_MAX_GROUPS / 4; ++i) v = fmaxf(v, value[i]);
+      const float best = reduce_f<LANES>(v, Max());
+      if (q == a.keep) {
+        close |= !by_logit && last - best <= tol;
+        break;
+      }
+      last = best;
+      int at = INT32_MAX;
+#pragma unroll
+      for (int i = ROUTE_MAX_GROUPS / 4 - 1; i >= 0; --i)
+        if (value[i] == best && best != -INFINITY) at = l + LANES * i;
+      at = reduce_min<LANES>(at);
+      if (at == INT32_MAX) break;
+      open |= 1u << at;
+#pragma unroll
+      for (int i = 0; i < ROUTE_MAX_GROUPS / 4; ++i)
+        if (l + LANES * i == at) value[i] = -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (!(open >> min((e0 + i) / size, 31) & 1)) r[i] = -INFINITY;
+  }
+  // the k best, one at a time, and the first that stays outside
+  float last = INFINITY;
+  for (int j = 0; j <= a.k; ++j) {
+    if (j == a.k && by_logit) break;
+    float v = r[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) v = fmaxf(v, r[i]);
+    const float best = reduce_f<LANES>(v, Max());
+    if (!by_logit && best != -INFINITY && last - best <= tol) close = true;
+    last = best;
+    if (j == a.k) break;
+    int at = INT32_MAX;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i)
+      if (r[i] == best && best != -INFINITY) at = e0 + i;
+    at = reduce_min<LANES>(at);
+    if (l == 0) chosen[slot][j] = at == INT32_MAX ? -1 : at;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (e0 + i == at) r[i] = -INFINITY;
+  }
+  uint64_t redo = __ballot(close && ok && l == 0);
+  while (redo) {
+    const int lane = __ffsll((unsigned long long)redo) - 1;
+    redo &= redo - 1;
+    const int who = (threadIdx.x & ~63) / LANES + lane / LANES;
+    route_exact<BF16>(a, (int64_t)blockIdx.x * PER + who, exact[threadIdx.x >> 6], chosen[who]);
+  }
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  if (!in) return;
+  float sum = 0.f, s[(ROUTE_MAX_CHOICES + LANES - 1) / LANES];
+  int e[(ROUTE_MAX_CHOICES + LANES - 1) / LANES];
+#pragma unroll
+  for (int q = 0; q < (ROUTE_MAX_CHOICES + LANES - 1) / LANES; ++q) {
+    const int j = l + LANES * q;
+    e[q] = ok && j < a.k ? chosen[slot][j] : -1;
+    s[q] = 0.f;
+    if (e[q] >= 0) {
+      const float x = logit<BF16>(a, t, e[q]);
+      s[q] = a.softmax ? exp_term(x, m) * inv : sigmoid(x);
+    }
+    sum += s[q];
+  }
+  sum = reduce_f<LANES>(sum, Sum());
+  const float f = a.renormalize ? a.scale / (sum + NORM_EPS) : a.scale;
+#pragma unroll
+  for (int q = 0; q < (ROUTE_MAX_CHOICES + LANES - 1) / LANES; ++q) {
+    const int j = l + LANES * q;
+    if (j >= a.k) continue;
+    const int64_t at = t * a.k + j;
+    if (a.choices.is64) static_cast<int64_t *>(const_cast<void *>(a.choices.p))[at] = e[q];
+    else static_cast<int32_t *>(const_cast<void *>(a.choices.p))[at] = e[q];
+    a.weights[at] = e[q] >= 0 ? s[q] * f : 0.f;
+  }
+}
+
+// LANES lanes take a token, VECS 16-byte vectors a lane.
+template <bool BF16, int LANES, int VECS>
+__global__ __launch_bounds__(RT) void kr_backward(RouteArgs a) {
+  typedef Elem<BF16> E;
+  typedef typename E::type T;
+  constexpr int PER = RT / LANES, N = E::N;
+  const int l = threadIdx.x & (LANES - 1);
+  const int64_t t = (int64_t)blockIdx.x * PER + threadIdx.x / LANES;
+  const bool in = t < a.tokens;
+  const bool ok = in && (!a.valid || a.valid[t]);
+  const int64_t row = ok ? t : 0;
+  const T *x = static_cast<const T *>(a.logits) + row * a.ld;
+  float v[VECS][N];
+  float m = 0.f, inv = 0.f;
+  if (a.softmax) {
+    m = kLowest;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      const int c = (l + LANES * i) * N;
+      if (ok && c + N <= a.experts) {
+        E::unpack(load16(x + c), v[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[i][j] = ok && c + j < a.experts ? E::get(x[c + j]) : -INFINITY;
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) m = fmaxf(m, v[i][j]);
+    }
+    m = reduce_f<LANES>(m, Max());
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        v[i][j] = exp_term(v[i][j], m);
+        s += v[i][j];
+      }
+    inv = inverse(reduce_f<LANES>(s, Sum()));
+  }
+  // the chosen experts' scores, their sum S and sum_i dw_i s_i
+  float total = 0.f, dot = 0.f;
+  for (int j0 = 0; j0 < a.k; j0 += LANES) {
+    const int j = j0 + l;
+    float s = 0.f, dw = 0.f;
+    if (ok && j < a.k) {
+      const int64_t e = index_at(a.choices, t * a.k + j);
+      if (e >= 0 && e < a.experts) {
+        const float z = E::get(x[e]);
+        s = a.softmax ? exp_term(z, m) * inv : sigmoid(z);
+        dw = a.dweights[t * a.k + j];
+        dot += dw * s;
+      }
+    }
+    total += s;
+  }
+  total = reduce_f<LANES>(total, Sum());
+  dot = reduce_f<LANES>(dot, Sum());
+  const float S = a.renormalize ? total + NORM_EPS : 1.f;
+  const float f = a.scale / S;
+  const float mean = a.renormalize ? dot / S : 0.f;
+  // sum_j s_j ds_j; renormalised it is scale / S dot (1 - total / S), all but 0
+  const float inner = a.renormalize ? f * dot * (NORM_EPS / S) : f * dot;
+  if (a.softmax) {
+#pragma unroll
+    for (int i = 0; i < VECS; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[i][j] = -(v[i][j] * inv) * inner;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VECS; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[i][j] = 0.f;
+  }
+  for (int j = 0; j < a.k; ++j) {
+    if (!ok) break;
+    const int64_t e64 = index_at(a.choices, t * a.k + j);
+    if (e64 < 0 || e64 >= a.experts) continue;
+    const int e = (int)e64;
+    const float z = E::get(x[e]);
+    const float s = a.softmax ? exp_term(z, m) * inv : sigmoid(z);
+    const float ds = f * (a.dweights[t * a.k + j] - mean);
+    const float add = a.softmax ? s * ds : s * (1.f - s) * ds;
+    const int at = e - l * N;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i)
+#pragma unroll
+      for (int q = 0; q < N; ++q)
+        if (at == LANES * N * i + q) v[i][q] += add;
+  }
+  if (!in) return;
+  T *d = static_cast<T *>(a.dlogits) + t * a.dld;
+#pragma unroll
+  for (int i = 0; i < VECS; ++i) {
+    const int c = (l + LANES * i) * N;
+    if (!ok) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[i][j] = 0.f;
+    }
+    if (c + N <= a.experts) {
+      if (!a.first) {
+        if (!ok) continue;
+        float w[N];
+        E::unpack(load16(d + c), w);
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[i][j] += w[j];
+        store16(d + c, E::pack(v[i]));
+      } else {
+        stream16(d + c, E::pack(v[i]));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (c + j < a.experts && (a.first || ok)) d[c + j] = E::put(a.first ? v[i][j] : E::get(d[c + j]) + v[i][j]);
+    }
+  }
+}
+
+template <bool BF16>
+hipError_t route(const RouteArgs &a, hipStream_t s) {
+  auto go = [&](auto lanes, auto per) {
+    constexpr int L = decltype(lanes)::value, V = decltype(per)::value;
+    const int64_t grid = (a.tokens + RT / L - 1) / (RT / L);
+    hipLaunchKernelGGL((kr_route<BF16, L, V>), dim3((unsigned)grid), dim3(RT), 0, s, a);
+    return hipGetLastError();
+  };
+  typedef std::integral_constant<int, 4> c4;
+  typedef std::integral_constant<int, 8> c8;
+  typedef std::integral_constant<int, 16> c16;
+  typedef std::integral_constant<int, 64> c64;
+  const int n = a.experts;
+  if (n <= 16) return go(c4(), c4());
+  if (n <= 32) return go(c4(), c8());
+  if (n <= 64) return go(c16(), c4());
+  if (n <= 128) return go(c16(), c8());
+  if (n <= 256) return go(c16(), c16());
+  if (n <= 512) return go(c64(), c8());
+  return go(c64(), c16());
+}
+
+template <bool BF16>
+hipError_t route_backward(const RouteArgs &a, hipStream_t s) {
+  auto go = [&](auto lanes, auto per) {
+    constexpr int L = decltype(lanes)::value, V = decltype(per)::value;
+    const int64_t grid = (a.tokens + RT / L - 1) / (RT / L);
+    hipLaunchKernelGGL((kr_backward<BF16, L, V>), dim3((unsigned)grid), dim3(RT), 0, s, a);
+    return hipGetLastError();
+  };
+  constexpr int N = Elem<BF16>::N;
+  typedef std::integral_constant<int, 1> c1;
+  typedef std::integral_constant<int, 2> c2;
+  typedef std::integral_constant<int, 4> c4;
+  typedef std::integral_constant<int, 16> c16;
+  typedef std::integral_constant<int, 64> c64;
+  const int n = a.experts;
+  if (n <= 4 * N) return go(c4(), c1());
+  if (n <= 16 * N) return go(c16(), c1());
+  if (n <= 32 * N) return go(c16(), c2());
+  if (n <= 64 * N) return go(c16(), c4());
+  return go(c64(), std::integral_constant<int, ROUTE_MAX_EXPERTS / (64 * N)>());
+}
+
+}  // namespace
+
+hipError_t launch_route(const RouteArgs &a, bool bf16, hipStream_t s) {
+  if (a.tokens == 0) return hipSuccess;
+  return bf16 ? route<true>(a, s) : route<false>(a, s);
+}
+
+hipError_t launch_route_backward(const RouteArgs &a, bool bf16, hipStream_t s) {
+  if (a.tokens == 0) return hipSuccess;
+  return bf16 ? route_backward<true>(a, s) : route_backward<false>(a, s);
+}
+
+}  // namespace muon

@@ -1,0 +1,178 @@
+"""The operators of a trained layer of experts, on torch tensors: dropout, a
+router's choice of experts, the order of the tokens by expert and the weighted
+sum of what the experts return, each with its gradient (include/muon.h states
+each formula).
+
+Outputs, checks, streams and errors are as in ``train_ops``: every output is
+the caller's tensor, ``ValueError`` comes before anything is enqueued, nothing
+is allocated and nothing synchronises the host.
+"""
+
+from __future__ import annotations
+
+import ctypes as C
+
+from . import _lib
+from .train_ops import _launch, _matrix, _refuse, _same, _vector, _workspace
+
+__all__ = ["dropout", "route_experts", "route_backward", "expert_order", "expert_order_workspace_bytes",
+           "expert_combine", "expert_combine_backward"]
+
+expert_order_workspace_bytes = _lib.muon_expert_order_workspace_bytes
+
+
+def _like(x, what, rows, cols, dt):
+    """(address, ld) of an optional matrix of that shape and type."""
+    if x is None:
+        return None, 0
+    r, c, ld, _ = _matrix(x, what, dt)
+    _same(what, (r, c), (rows, cols))
+    return x.data_ptr(), ld
+
+
+def _p(x):
+    return None if x is None else x.data_ptr()
+
+
+def dropout(x, out, p: float, seed: int, site: int = 0, step=0, residual=None, stream=None) -> None:
+    """out = residual + (kept ? x / (1 - p) : 0); an element is kept or not by its row, its column, seed, site and
+    step alone, so the gradient by x is the same call on the gradient by out.
+
+    x, out, residual (None: none): rows x cols of one type; out may be x or the residual.  seed: 64 bits; site (a
+    layer's number) and step: 32 bits.  step may be an int64 tensor of one element, read on the device."""
+    rows, cols, ld, dt = _matrix(x, "x")
+    op, old = _like(out, "out", rows, cols, dt)
+    rp, rld = _like(residual, "residual", rows, cols, dt)
+    device_step = None
+    if not isinstance(step, int):
+        _vector(step, "step", 1, dtype="int64")
+        device_step, step = step, 0
+    if not 0 <= seed < 1 << 64 or not 0 <= site < 1 << 32 or not 0 <= step < 1 << 32:
+        _refuse("dropout", "seed is not of 64 bits, or site or step not of 32")
+    f = _lib.load().muon_dropout
+    _launch("dropout", lambda s: f(x.data_ptr(), rows, cols, ld, dt, p, seed, site, step, _p(device_step), rp, rld, op,
+                                   old, s), stream, (x, out, residual, device_step))
+
+
+def _choices(choices, tokens):
+    if choices.dim() != 2 or choices.shape[0] != tokens or choices.shape[1] < 1:
+        _refuse("choices", f"shape {tuple(choices.shape)}, expected ({tokens}, k)")
+    return choices.shape[1], _vector(choices, "choices", choices.numel(), index=True)
+
+
+def _scoring(name):
+    if name not in _lib.SCORING:
+        _refuse("scoring", f"{name!r}, expected one of {', '.join(_lib.SCORING)}")
+    return _lib.SCORING[name]
+
+
+def route_experts(logits, choices, weights, scoring: str = "softmax", bias=None, valid=None, groups: int = 1,
+                  keep_groups: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+                  stream=None) -> None:
+    """choices[t]: the k experts of highest rank, highest first, where rank = score + bias, score = the softmax or
+    sigmoid of logits[t]; weights[t] = scale * their scores, divided by the scores' sum if renormalize.
+
+    logits: tokens x E; choices: tokens x k, int32 or int64; weights: fp32, tokens x k; bias: fp32[E] or None;
+    valid: bool, one a token, or None.  With groups > 1 only experts of the keep_groups groups with the highest sum
+    of their group_top (1 or 2) best ranks can be chosen.  -1 and weight 0 where there is no expert to choose."""
+    tokens, experts, ld, dt = _matrix(logits, "logits")
+    k, ct = _choices(choices, tokens)
+    _vector(weights, "weights", tokens * k)
+    if bias is not None:
+        _vector(bias, "bias", experts)
+    if valid is not None:
+        _vector(valid, "valid", tokens, dtype="bool")
+    o = _lib.muon_route_options(_scoring(scoring), 1 if renormalize else 0, groups, keep_groups, group_top, 0, scale)
+    f = _lib.load().muon_route
+    _launch("route", lambda s: f(logits.data_ptr(), tokens, experts, ld, dt, _p(bias), _p(valid), C.byref(o),
+                                 choices.data_ptr(), ct, k, weights.data_ptr(), s), stream,
+            (logits, choices, weights, bias, valid))
+
+
+def route_backward(logits, choices, dweights, dlogits, first: bool, scoring: str = "softmax", valid=None,
+                   renormalize: bool = True, scale: float = 1.0, stream=None) -> None:
+    """dlogits = (0 if first else dlogits) + the gradient by the logits for the gradient dweights (fp32, tokens x k)
+    by the weights of route_experts; choices as it gave them, scoring, valid, renormalize and scale as it took them.
+    dlogits: like logits."""
+    tokens, experts, ld, dt = _matrix(logits, "logits")
+    k, ct = _choices(choices, tokens)
+    _vector(dweights, "dweights", tokens * k)
+    if valid is not None:
+        _vector(valid, "valid", tokens, dtype="bool")
+    dp, dld = _like(dlogits, "dlogits", tokens, experts, dt)
+    o = _lib.muon_route_options(_scoring(scoring), 1 if renormalize else 0, 1, 1, 1, 0, scale)
+    f = _lib.load().muon_route_backward
+    _launch("route_backward", lambda s: f(logits.data_ptr(), tokens, experts, ld, dt, _p(valid), C.byref(o),
+                                          choices.data_ptr(), ct, k, dweights.data_ptr(), dp, dld, 1 if first else 0,
+                                          s), stream, (logits, choices, dweights, dlogits, valid))
+
+
+def expert_order(choices, tokens, offsets, place, ws, stream=None) -> None:
+    """Sorts the choices (T x k, int32 or int64) by expert, in the order of their tokens: expert e has the slots
+    [offsets[e], offsets[e + 1]), slot s belongs to token tokens[s] (-1 behind the last), and choice (t, j) has the
+    slot place[t, j] (-1 if it is outside [0, E)).
+
+    tokens: int32[T * k]; offsets: int32[E + 1]; place: int32, T x k; ws: at least
+    expert_order_workspace_bytes(T, k, E) bytes, 256-byte aligned."""
+    if choices.dim() != 2 or choices.shape[1] < 1:
+        _refuse("choices", f"shape {tuple(choices.shape)}, expected (tokens, k)")
+    t, k = choices.shape
+    ct = _vector(choices, "choices", t * k, index=True)
+    _vector(tokens, "tokens", t * k, dtype="int32")
+    _vector(place, "place", t * k, dtype="int32")
+    experts = offsets.numel() - 1
+    _vector(offsets, "offsets", experts + 1, dtype="int32")
+    wp, wb = _workspace(ws)
+    f = _lib.load().muon_expert_order
+    _launch("expert_order", lambda s: f(choices.data_ptr(), ct, t, k, experts, tokens.data_ptr(), offsets.data_ptr(),
+                                        place.data_ptr(), wp, wb, s), stream, (choices, tokens, offsets, place, ws))
+
+
+def _place(place, tokens):
+    if place.dim() != 2 or place.shape[0] != tokens or place.shape[1] < 1:
+        _refuse("place", f"shape {tuple(place.shape)}, expected ({tokens}, k)")
+    _vector(place, "place", place.numel(), dtype="int32")
+    return place.shape[1]
+
+
+def expert_combine(y, place, out, weights=None, residual=None, stream=None) -> None:
+    """out[t] = residual[t] + sum_j weights[t, j] * y[place[t, j]]; a place outside y's rows adds nothing.
+    place: int32, T x k; weights: fp32, T x k, or None (1 each); residual: like out, may be out, or None."""
+    rows, dim, yld, dt = _matrix(y, "y")
+    tokens, cols, old, _ = _matrix(out, "out", dt)
+    _same("out columns", cols, dim)
+    k = _place(place, tokens)
+    if weights is not None:
+        _vector(weights, "weights", tokens * k)
+    rp, rld = _like(residual, "residual", tokens, dim, dt)
+    f = _lib.load().muon_expert_combine
+    _launch("expert_combine", lambda s: f(y.data_ptr(), rows, dim, yld, dt, place.data_ptr(), tokens, k, _p(weights),
+                                          rp, rld, out.data_ptr(), old, s), stream, (y, place, out, weights, residual))
+
+
+def expert_combine_backward(dout, place, dy=None, weights=None, y=None, dweights=None, stream=None) -> None:
+    """dy[place[t, j]] = weights[t, j] * dout[t] (rows of no place are kept) and dweights[t, j] = the sum of dout[t] *
+    y[place[t, j]] (0 for a place outside); either may be None.  y is needed for dweights only; dy may be y."""
+    tokens, dim, dold, dt = _matrix(dout, "dout")
+    k = _place(place, tokens)
+    rows = yld = dyld = 0
+    if dy is None and dweights is None:
+        _refuse("expert_combine_backward", "neither dy nor dweights is asked for")
+    if dweights is not None:
+        if y is None:
+            _refuse("dweights", "needs y")
+        rows, cols, yld, _ = _matrix(y, "y", dt)
+        _same("y columns", cols, dim)
+        _vector(dweights, "dweights", tokens * k)
+    if dy is not None:
+        n, cols, dyld, _ = _matrix(dy, "dy", dt)
+        _same("dy columns", cols, dim)
+        if dweights is not None:
+            _same("dy rows", n, rows)
+        rows = n
+    if weights is not None:
+        _vector(weights, "weights", tokens * k)
+    f = _lib.load().muon_expert_combine_backward
+    _launch("expert_combine_backward",
+            lambda s: f(dout.data_ptr(), tokens, dim, dold, dt, place.data_ptr(), k, _p(weights), _p(y), yld, rows,
+                        _p(dy), dyld, _p(dweights), s), stream, (dout, place, dy, weights, y, dweights))

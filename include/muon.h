@@ -584,6 +584,71 @@ muon_status muon_expert_combine_backward(const void *dout, int64_t tokens, int64
                                          int64_t y_ld, int64_t rows, void *dy, int64_t dy_ld, float *dweights,
                                          void *stream);
 
+/* The product with a weight matrix and what usually stands around it:
+ *   pre = x w + bias,  out = act(pre) + residual
+ * x is rows x in, out, pre and residual rows x out, of the weights' type.
+ * bias (out numbers a group, dense), pre and residual may be NULL; out may be
+ * the residual (same pointer and ld).  act: max(v, 0), v / (1 + exp(-v)), v
+ * Phi(v), or v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2.
+ * Every group of rows may have a matrix of its own (a layer's experts): group
+ * g has the rows [offsets[g], offsets[g + 1]) (non-decreasing, on the device;
+ * what falls outside [0, rows) is cut off).  Rows of no group are not
+ * touched.  offsets may be NULL for one group of all rows.
+ * Sums are fp32, of bf16 products or of fp32 ones; what leaves is rounded
+ * once. */
+typedef enum {
+  MUON_ACT_NONE = 0, MUON_ACT_RELU = 1, MUON_ACT_SILU = 2, MUON_ACT_GELU = 3, MUON_ACT_GELU_TANH = 4
+} muon_activation;
+typedef enum { MUON_W_IN_OUT = 0, MUON_W_OUT_IN = 1 } muon_w_layout;
+#define MUON_LINEAR_MAX_GROUPS 1024
+typedef struct {
+  const void *w;
+  int64_t in, out;
+  int64_t ld;           /* of a row: of an input's weights (MUON_W_IN_OUT) or an output's */
+  int64_t stride;       /* from a group's matrix to the next one's, in elements           */
+  int32_t layout;       /* muon_w_layout                                                  */
+  int32_t groups;
+  const void *offsets;  /* DEVICE, groups + 1 whole numbers, or NULL                      */
+  int32_t offset_type;  /* muon_index_type                                                */
+  int32_t dtype;        /* muon_dtype                                                     */
+} muon_weights;
+muon_status muon_linear_workspace_bytes(int64_t rows, int64_t in, int64_t out, int64_t groups, size_t *bytes);
+muon_status muon_linear_forward(const void *x, int64_t rows, int64_t x_ld, const muon_weights *w, const void *bias,
+                                int32_t activation, void *pre, int64_t pre_ld, const void *residual,
+                                int64_t residual_ld, void *out, int64_t out_ld, void *ws, size_t ws_bytes,
+                                void *stream);
+
+/* Its gradient by x, for the gradient dy by the pre of the product:
+ *   dx = (dy w') act'(pre) + residual
+ * where pre is what the activation before the product took (x = act(pre):
+ * the chain reaches the product before without a pass of its own), and the
+ * residual a gradient that joins, such as the skip connection's.  dy is rows
+ * x out, dx, pre and residual rows x in.  pre is not read without an
+ * activation; residual may be NULL, or dx itself (same pointer and ld).
+ * Workspace: muon_linear_workspace_bytes(rows, out, in, groups). */
+muon_status muon_linear_input_grad(const void *dy, int64_t rows, int64_t dy_ld, const muon_weights *w,
+                                   int32_t activation, const void *pre, int64_t pre_ld, const void *residual,
+                                   int64_t residual_ld, void *dx, int64_t dx_ld, void *ws, size_t ws_bytes,
+                                   void *stream);
+
+/* Its gradients by the weights and the bias, accumulated in fp32 as
+ * muon_accumulate does:
+ *   dw[g] = (first != 0 ? 0 : dw[g]) + the group's x' dy,  dbias[g] likewise
+ * the sums of dy's columns.  dw is laid out by dw_ld, dw_stride and dw_layout
+ * as muon_weights; dbias is dense, and may be NULL.  Every element is
+ * written, also of groups without rows. */
+muon_status muon_linear_weight_grad_workspace_bytes(int64_t rows, int64_t in, int64_t out, int64_t groups, size_t *bytes);
+muon_status muon_linear_weight_grad(const void *x, int64_t rows, int64_t in, int64_t x_ld, const void *dy, int64_t out,
+                                    int64_t dy_ld, int32_t dtype, const void *offsets, int32_t offset_type,
+                                    int64_t groups, float *dw, int64_t dw_ld, int64_t dw_stride, int32_t dw_layout,
+                                    float *dbias, int32_t first, void *ws, size_t ws_bytes, void *stream);
+
+/* dpre = dy act'(pre), where a product's activation is not followed by
+ * another product.  dpre may be dy or pre (same pointer and ld). */
+muon_status muon_activation_grad(const void *dy, int64_t rows, int64_t cols, int64_t dy_ld, int32_t dtype,
+                                 int32_t activation, const void *pre, int64_t pre_ld, void *dpre, int64_t dpre_ld,
+                                 void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -6,7 +6,8 @@ points by name; ``MuonGroup`` is a small convenience wrapper that owns a plan;
 ``train_ops`` holds the operators around the step on torch tensors (embedding
 lookup and gradient, token log-probability, policy, preference and balance
 losses), ``layer_ops`` those of a trained layer (dropout, routing to experts,
-the tokens' order by expert and the experts' weighted sum).
+the tokens' order by expert, the experts' weighted sum, the product with
+weights a group of rows), each with its gradient.
 Device memory and streams come from the caller (e.g. torch tensors).
 """
 
@@ -23,10 +24,14 @@ from ._lib import (DTYPE, EXPORTS, NS_METHOD, PRECISION, SCHEDULE, MuonError, lo
                    muon_policy_loss, muon_policy_loss_workspace_bytes, muon_policy_options, muon_preference_loss,
                    muon_preference_loss_workspace_bytes, muon_preference_options, muon_token_logprob,
                    SCORING, muon_dropout, muon_expert_combine, muon_expert_combine_backward, muon_expert_order,
-                   muon_expert_order_workspace_bytes, muon_route, muon_route_backward, muon_route_options)
+                   muon_expert_order_workspace_bytes, muon_route, muon_route_backward, muon_route_options,
+                   ACTIVATION, W_LAYOUT, muon_activation_grad, muon_linear_forward, muon_linear_input_grad,
+                   muon_linear_weight_grad, muon_linear_weight_grad_workspace_bytes, muon_linear_workspace_bytes,
+                   muon_weights)
 from . import layer_ops, train_ops
-from .layer_ops import (dropout, expert_combine, expert_combine_backward, expert_order,  # noqa: F401
-                        expert_order_workspace_bytes, route_backward, route_experts)
+from .layer_ops import (activation_grad, dropout, expert_combine, expert_combine_backward, expert_order,  # noqa: F401
+                        expert_order_workspace_bytes, linear_forward, linear_input_grad, linear_weight_grad,
+                        linear_weight_grad_workspace_bytes, linear_workspace_bytes, route_backward, route_experts)
 from .train_ops import (balance_loss, balance_loss_workspace_bytes, embed_backward,  # noqa: F401
                         embed_backward_workspace_bytes, embed_forward, policy_loss, policy_loss_workspace_bytes,
                         preference_loss, preference_loss_workspace_bytes, token_logprob)

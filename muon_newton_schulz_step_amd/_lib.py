@@ -26,6 +26,8 @@ DTYPE = {"fp32": 0, "bf16": 1}
 SCHEDULE = {"launches": 0, "persistent": 1}
 INDEX_TYPE = {"int32": 0, "int64": 1}
 SCORING = {"softmax": 0, "sigmoid": 1}
+ACTIVATION = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+W_LAYOUT = {"in_out": 0, "out_in": 1}
 
 # every symbol include/muon.h declares
 EXPORTS = ("muon_default_options", "muon_plan_create", "muon_plan_workspace_bytes", "muon_accumulate",
@@ -36,7 +38,9 @@ EXPORTS = ("muon_default_options", "muon_plan_create", "muon_plan_workspace_byte
            "muon_policy_loss_workspace_bytes", "muon_policy_loss", "muon_preference_loss_workspace_bytes",
            "muon_preference_loss", "muon_balance_loss_workspace_bytes", "muon_balance_loss",
            "muon_dropout", "muon_route", "muon_route_backward", "muon_expert_order_workspace_bytes",
-           "muon_expert_order", "muon_expert_combine", "muon_expert_combine_backward")
+           "muon_expert_order", "muon_expert_combine", "muon_expert_combine_backward", "muon_linear_workspace_bytes",
+           "muon_linear_forward", "muon_linear_input_grad", "muon_linear_weight_grad_workspace_bytes",
+           "muon_linear_weight_grad", "muon_activation_grad")
 
 
 class muon_matrix(C.Structure):
@@ -90,6 +94,12 @@ class muon_balance_options(C.Structure):
 class muon_route_options(C.Structure):
     _fields_ = [("scoring", C.c_int32), ("renormalize", C.c_int32), ("groups", C.c_int32), ("keep_groups", C.c_int32),
                 ("group_top", C.c_int32), ("reserved", C.c_int32), ("scale", C.c_double)]
+
+
+class muon_weights(C.Structure):
+    _fields_ = [("w", C.c_void_p), ("in_", C.c_int64), ("out", C.c_int64), ("ld", C.c_int64), ("stride", C.c_int64),
+                ("layout", C.c_int32), ("groups", C.c_int32), ("offsets", C.c_void_p), ("offset_type", C.c_int32),
+                ("dtype", C.c_int32)]
 
 
 _lib = None
@@ -148,6 +158,15 @@ def load(path: str | None = None) -> C.CDLL:
         "muon_expert_order_workspace_bytes": (i32, [i64, i64, i64, C.POINTER(sz)]),
         "muon_expert_order": (i32, [vp, i32, i64, i64, i64, vp, vp, vp, vp, sz, vp]),
         "muon_expert_combine": (i32, [vp, i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, vp, i64, vp]),
+        "muon_linear_workspace_bytes": (i32, [i64, i64, i64, i64, C.POINTER(sz)]),
+        "muon_linear_forward": (i32, [vp, i64, i64, C.POINTER(muon_weights), vp, i32, vp, i64, vp, i64, vp, i64, vp, sz,
+                                      vp]),
+        "muon_linear_input_grad": (i32, [vp, i64, i64, C.POINTER(muon_weights), i32, vp, i64, vp, i64, vp, i64, vp, sz,
+                                         vp]),
+        "muon_linear_weight_grad_workspace_bytes": (i32, [i64, i64, i64, i64, C.POINTER(sz)]),
+        "muon_linear_weight_grad": (i32, [vp, i64, i64, i64, vp, i64, i64, i32, vp, i32, i64, vp, i64, i64, i32, vp,
+                                          i32, vp, sz, vp]),
+        "muon_activation_grad": (i32, [vp, i64, i64, i64, i32, i32, vp, i64, vp, i64, vp]),
         "muon_expert_combine_backward": (i32, [vp, i64, i64, i64, i32, vp, i64, vp, vp, i64, i64, vp, i64, vp, vp]),
     }
     for name, (res, args) in sig.items():
@@ -509,3 +528,52 @@ def muon_expert_combine_backward(dout, tokens: int, dim: int, dout_ld: int, dtyp
                                              _stream(stream))
     if st:
         _check(st, "muon_expert_combine_backward")
+
+
+def _act(x) -> int:
+    return x if isinstance(x, int) else ACTIVATION[x]
+
+
+def muon_linear_workspace_bytes(rows: int, in_: int, out: int, groups: int = 1) -> int:
+    return _bytes_of("muon_linear_workspace_bytes", rows, in_, out, groups)
+
+
+def muon_linear_forward(x, rows: int, x_ld: int, weights: muon_weights, bias, activation, pre, pre_ld: int, residual,
+                        residual_ld: int, out, out_ld: int, ws, ws_bytes: int, stream=None) -> None:
+    st = load().muon_linear_forward(_ptr(x), rows, x_ld, C.byref(weights), _ptr(bias), _act(activation), _ptr(pre),
+                                    pre_ld, _ptr(residual), residual_ld, _ptr(out), out_ld, _ptr(ws),
+                                    _ws_bytes(ws, ws_bytes), _stream(stream))
+    if st:
+        _check(st, "muon_linear_forward")
+
+
+def muon_linear_input_grad(dy, rows: int, dy_ld: int, weights: muon_weights, activation, pre, pre_ld: int, residual,
+                           residual_ld: int, dx, dx_ld: int, ws, ws_bytes: int, stream=None) -> None:
+    st = load().muon_linear_input_grad(_ptr(dy), rows, dy_ld, C.byref(weights), _act(activation), _ptr(pre), pre_ld,
+                                       _ptr(residual), residual_ld, _ptr(dx), dx_ld, _ptr(ws),
+                                       _ws_bytes(ws, ws_bytes), _stream(stream))
+    if st:
+        _check(st, "muon_linear_input_grad")
+
+
+def muon_linear_weight_grad_workspace_bytes(rows: int, in_: int, out: int, groups: int = 1) -> int:
+    return _bytes_of("muon_linear_weight_grad_workspace_bytes", rows, in_, out, groups)
+
+
+def muon_linear_weight_grad(x, rows: int, in_: int, x_ld: int, dy, out: int, dy_ld: int, dtype, offsets, offset_type,
+                            groups: int, dw, dw_ld: int, dw_stride: int, dw_layout, dbias, first: bool, ws,
+                            ws_bytes: int, stream=None) -> None:
+    layout = dw_layout if isinstance(dw_layout, int) else W_LAYOUT[dw_layout]
+    st = load().muon_linear_weight_grad(_ptr(x), rows, in_, x_ld, _ptr(dy), out, dy_ld, _dt(dtype), _ptr(offsets),
+                                        _it(offset_type), groups, _ptr(dw), dw_ld, dw_stride, layout, _ptr(dbias),
+                                        1 if first else 0, _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream))
+    if st:
+        _check(st, "muon_linear_weight_grad")
+
+
+def muon_activation_grad(dy, rows: int, cols: int, dy_ld: int, dtype, activation, pre, pre_ld: int, dpre, dpre_ld: int,
+                         stream=None) -> None:
+    st = load().muon_activation_grad(_ptr(dy), rows, cols, dy_ld, _dt(dtype), _act(activation), _ptr(pre), pre_ld,
+                                     _ptr(dpre), dpre_ld, _stream(stream))
+    if st:
+        _check(st, "muon_activation_grad")

@@ -1,0 +1,331 @@
+// The product with a weight matrix, or with one a group of rows, and its
+// gradients, on gfx950: 128 x 128 tiles, any size, type and alignment.
+//
+//   forwards       out = act(x w + bias) + residual
+//   input          dx = (dy w') act'(pre) + residual
+//   weights        dw (+)= x' dy,  dbias (+)= the sums of dy's columns
+//
+// A workgroup of 4 waves (2 x 2, each 64 x 64) walks K in stages of 128 bytes
+// a row, double buffered in LDS: with loads straight into LDS where rows keep
+// 16-byte alignment, through registers otherwise.  bf16 on
+// v_mfma_f32_16x16x32_bf16, fp32 on v_mfma_f32_16x16x4_f32, sums in fp32.
+// Few tiles with a long K are cut along K into parts, whose sums meet in the
+// workspace and are added up in the order of the parts by a second launch.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "linear_dev.hpp"
+
+namespace muon {
+
+using namespace dev;
+
+namespace {
+
+constexpr int BT = 128;
+constexpr int OPB = BT * STAGE_BYTES;  // an operand's stage in LDS
+
+template <bool BF16, bool AX, bool BX, bool DMA>
+__global__ __launch_bounds__(LIN_THREADS, 2) void kl_linear128(LinearArgs a) {
+  typedef Operand<BF16, BT, AX> OA;
+  typedef Operand<BF16, BT, BX> OB;
+  typedef typename OA::T T;
+  constexpr int KS = OA::KS, L = OA::LOADS;
+  __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * OPB];
+  LinTile x;
+  if (!find_tile<BT>(a, (int)blockIdx.x, KS, x)) return;
+  const OA oa{static_cast<const T *>(a.a) + (AX ? x.row0 : x.row0 * a.lda), a.lda, x.rows, x.k1};
+  const OB ob{static_cast<const T *>(a.b) + x.group * a.bstride + (BX ? x.col0 : x.col0 * a.ldb), a.ldb,
+              (int)min<int64_t>(BT, a.N - x.col0), x.k1};
+  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  f32x4_v acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+  const int nk = (int)((x.k1 - x.k0 + KS - 1) / KS);
+  uint32_t offa[L], offb[L];
+  uint4 ra[L], rb[L];
+  if constexpr (DMA) {
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      offa[j] = oa.offset(j);
+      offb[j] = ob.offset(j);
+    }
+  }
+  auto fetch = [&](int kt, int st) {
+    const int64_t k = x.k0 + (int64_t)kt * KS;
+    char *la = lds + st * 2 * OPB, *lb = la + OPB;
+    if constexpr (DMA) {
+      const auto ars = oa.rsrc(k);
+      const auto brs = ob.rsrc(k);
+#pragma unroll
+      for (int j = 0; j < L; ++j) {
+        oa.dma(ars, k, offa[j], la, j);
+        ob.dma(brs, k, offb[j], lb, j);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < L; ++j) {
+        ra[j] = oa.load(k, j);
+        rb[j] = ob.load(k, j);
+      }
+    }
+  };
+  auto land = [&](int st) {
+    if constexpr (!DMA) {
+#pragma unroll
+      for (int j = 0; j < L; ++j) {
+        OA::put(lds + st * 2 * OPB, j, ra[j]);
+        OB::put(lds + st * 2 * OPB + OPB, j, rb[j]);
+      }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+  };
+  if (nk > 0) {
+    fetch(0, 0);
+    land(0);
+  }
+  for (int kt = 0; kt < nk; ++kt) {
+    const int st = kt & 1;
+    const char *la = lds + st * 2 * OPB, *lb = la + OPB;
+    if (kt + 1 < nk) fetch(kt + 1, st ^ 1);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      if constexpr (BF16) {
+        bf16x8_v fa[4], fb[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          fa[i] = read_fragment<BT, AX>(la, wm * 64 + i * 16, ks);
+          fb[i] = read_fragment<BT, BX>(lb, wn * 64 + i * 16, ks);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+      } else {
+        f32x4_v fa[4], fb[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          fa[i] = read_fragment_f32<BT, AX>(la, wm * 64 + i * 16, ks);
+          fb[i] = read_fragment_f32<BT, BX>(lb, wn * 64 + i * 16, ks);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fb[j][c], fa[i][c], acc[i][j], 0, 0, 0);
+      }
+    }
+    if (kt + 1 < nk) land(st ^ 1);
+  }
+  finish_tile<BF16, 4>(a, x, acc, lds);
+}
+
+// Group of a row, by bisection; -1 for a row of none.
+__device__ __forceinline__ int group_of(const LinearArgs &a, int64_t row) {
+  if (!a.offsets.p) return 0;
+  int lo = 0, hi = a.groups;  // start(lo) <= row < start(hi)
+  if (row < group_start(a.offsets, 0, a.M) || row >= group_start(a.offsets, a.groups, a.M)) return -1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (group_start(a.offsets, mid, a.M) <= row) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Adds up the parts of the sums, in their order: a thread eight neighbours.
+template <bool BF16>
+__global__ __launch_bounds__(256) void kl_join(LinearArgs a, int64_t rows) {
+  const int64_t chunks = (a.N + 7) / 8, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  int64_t row = id / chunks;
+  const int64_t col = (id - row * chunks) * 8;
+  if (row >= rows) return;
+  const int n = (int)min<int64_t>(8, a.N - col);
+  int g;
+  if (a.mode == LIN_WEIGHT) {
+    g = (int)(row / a.M);
+  } else {
+    g = group_of(a, row);
+    if (g < 0) return;
+  }
+  float v[8], w[8];
+  load8<false>(a.partial, row * a.N + col, n, v);
+  for (int s = 1; s < a.splits; ++s) {
+    load8<false>(a.partial, (s * rows + row) * a.N + col, n, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += w[i];
+  }
+  finish8<BF16>(a, g, a.mode == LIN_WEIGHT ? row - g * a.M : row, col, n, v);
+}
+
+// -------------------------------------------------------- sums of columns
+
+constexpr int CS_THREADS = 256;
+
+// A thread takes 16 bytes of columns over part of a group's rows.
+template <bool BF16>
+__global__ __launch_bounds__(CS_THREADS) void kl_column_sums(ColumnSumArgs a) {
+  typedef Elem<BF16> E;
+  typedef typename E::type T;
+  constexpr int N = E::N;
+  // 16 lanes across (256 bytes), 16 rows a round
+  __shared__ float red[16][16 * N + 1];
+  const int lx = threadIdx.x & 15, ly = threadIdx.x >> 4;
+  const int64_t col = ((int64_t)blockIdx.x * 16 + lx) * N;
+  const int g = (int)blockIdx.y / a.splits, part = (int)blockIdx.y % a.splits;
+  int64_t lo = 0, hi = a.rows;
+  if (a.offsets.p) {
+    lo = group_start(a.offsets, g, a.rows);
+    hi = max(lo, group_start(a.offsets, g + 1, a.rows));
+  }
+  const int64_t r0 = lo + (hi - lo) * part / a.splits, r1 = lo + (hi - lo) * (part + 1) / a.splits;
+  const int n = (int)min<int64_t>(N, a.cols - col);
+  float sum[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) sum[i] = 0.f;
+  const T *p = static_cast<const T *>(a.dy) + col;
+  if (n == N) {
+#pragma unroll 4
+    for (int64_t r = r0 + ly; r < r1; r += 16) {
+      float v[N];
+      E::unpack(load16(p + r * a.ld), v);
+#pragma unroll
+      for (int i = 0; i < N; ++i) sum[i] += v[i];
+    }
+  } else if (n > 0) {
+    for (int64_t r = r0 + ly; r < r1; r += 16)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < n) sum[i] += E::get(p[r * a.ld + i]);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) red[ly][lx * N + i] = sum[i];
+  __syncthreads();
+  const int c = threadIdx.x;
+  const int64_t at = (int64_t)blockIdx.x * 16 * N + c;
+  if (c >= 16 * N || at >= a.cols) return;
+  float v = 0.f;
+#pragma unroll
+  for (int y = 0; y < 16; ++y) v += red[y][c];
+  if (a.splits > 1) a.partial[((int64_t)g * a.splits + part) * a.cols + at] = v;
+  else a.out[g * a.cols + at] = a.first ? v : a.out[g * a.cols + at] + v;
+}
+
+__global__ __launch_bounds__(CS_THREADS) void kl_column_join(ColumnSumArgs a) {
+  const int64_t at = (int64_t)blockIdx.x * CS_THREADS + threadIdx.x;
+  if (at >= a.cols) return;
+  const int g = (int)blockIdx.y;
+  double v = 0.0;
+  for (int s = 0; s < a.splits; ++s) v += (double)a.partial[((int64_t)g * a.splits + s) * a.cols + at];
+  a.out[g * a.cols + at] = a.first ? (float)v : (float)((double)a.out[g * a.cols + at] + v);
+}
+
+// dy act'(pre)
+template <bool BF16>
+__global__ __launch_bounds__(256) void kl_activation_grad(ActivationGradArgs a, int64_t chunks) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, row = id / chunks, col = (id - row * chunks) * 8;
+  if (row >= a.rows) return;
+  const int n = (int)min<int64_t>(8, a.cols - col);
+  float v[8], w[8];
+  load8<BF16>(a.dy, row * a.dld + col, n, v);
+  load8<BF16>(a.pre, row * a.pld + col, n, w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= slope<BF16>(a.act, w[i]);
+  store8<BF16>(a.out, row * a.old + col, n, v);
+}
+
+// ---------------------------------------------------------------- launches
+
+bool aligned(const void *p, int64_t ld, int64_t extent, int64_t stride, int e) {
+  return (uintptr_t)p % 16 == 0 && ld * e % 16 == 0 && extent * e % 16 == 0 && stride * e % 16 == 0 && ld < ((int64_t)1 << 20);
+}
+
+template <bool BF16, bool AX, bool BX>
+void go128(const LinearArgs &a, bool dma, unsigned grid, hipStream_t s) {
+  if (dma) hipLaunchKernelGGL((kl_linear128<BF16, AX, BX, true>), dim3(grid), dim3(LIN_THREADS), 0, s, a);
+  else hipLaunchKernelGGL((kl_linear128<BF16, AX, BX, false>), dim3(grid), dim3(LIN_THREADS), 0, s, a);
+}
+
+int64_t tiles_along(int64_t M, int32_t groups, bool grouped, int bt) {
+  return (M + bt - 1) / bt + (grouped ? groups - 1 : 0);
+}
+
+// Parts of K: enough for two workgroups a CU, of four stages each and more,
+// as far as their sums take no more than 64 MB.
+int32_t parts_of(int64_t M, int64_t N, int64_t K, int32_t groups, bool weight) {
+  const int64_t tn = (N + BT - 1) / BT, per = weight ? groups : 1;
+  const int64_t tiles = (weight ? (M + BT - 1) / BT : std::max<int64_t>(1, (M + BT - 1) / BT)) * tn * per;
+  const int64_t stages = (K / (weight ? groups : 1) + 63) / 64;
+  const int64_t bytes = std::max<int64_t>(1, M * per * N * 4);
+  int64_t parts = std::min<int64_t>({512 / std::max<int64_t>(1, tiles), stages / 4, ((int64_t)64 << 20) / bytes, 32});
+  return (int32_t)std::max<int64_t>(1, parts);
+}
+
+}  // namespace
+
+size_t linear_partial_bytes(int64_t M, int64_t N, int64_t K, int32_t groups, bool weight) {
+  const int32_t parts = parts_of(M, N, K, groups, weight);
+  return parts > 1 ? (size_t)parts * (size_t)(M * (weight ? groups : 1)) * (size_t)N * 4 : 0;
+}
+
+hipError_t launch_linear(LinearArgs a, bool bf16, int la, int lb, hipStream_t s) {
+  const int e = bf16 ? 2 : 4;
+  const bool ax = la == LIN_K_ACROSS, bx = lb == LIN_K_ACROSS, weight = a.mode == LIN_WEIGHT;
+  const bool dma = aligned(a.a, a.lda, ax ? a.M : a.K, 0, e) && aligned(a.b, a.ldb, bx ? a.N : a.K, a.groups > 1 ? a.bstride : 0, e);
+  a.splits = parts_of(a.M, a.N, a.K, a.groups, weight);
+  a.tiles_m = (int32_t)tiles_along(a.M, a.groups, !weight && a.offsets.p, BT);
+  a.tiles_n = (int32_t)((a.N + BT - 1) / BT);
+  const int64_t grid = (int64_t)a.tiles_m * a.tiles_n * (weight ? a.groups : 1) * a.splits;
+  const unsigned g = (unsigned)grid;
+  if (bf16) {
+    if (ax) go128<true, true, true>(a, dma, g, s);
+    else if (bx) go128<true, false, true>(a, dma, g, s);
+    else go128<true, false, false>(a, dma, g, s);
+  } else {
+    if (ax) go128<false, true, true>(a, dma, g, s);
+    else if (bx) go128<false, false, true>(a, dma, g, s);
+    else go128<false, false, false>(a, dma, g, s);
+  }
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess || a.splits == 1) return err;
+  const int64_t rows = a.M * (weight ? a.groups : 1), threads = rows * ((a.N + 7) / 8);
+  if (bf16) hipLaunchKernelGGL(kl_join<true>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a, rows);
+  else hipLaunchKernelGGL(kl_join<false>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a, rows);
+  return hipGetLastError();
+}
+
+// Parts of a group's rows for the sums of columns: enough for four workgroups
+// a CU, of 64 rows each and more.
+int32_t column_sum_splits(int64_t rows, int64_t cols, int32_t groups) {
+  const int64_t wide = (cols + 127) / 128 * groups;
+  return (int32_t)std::max<int64_t>(1, std::min<int64_t>({1024 / std::max<int64_t>(1, wide), rows / groups / 64, 64}));
+}
+
+hipError_t launch_column_sums(const ColumnSumArgs &a, bool bf16, hipStream_t s) {
+  const int n = bf16 ? 128 : 64;
+  const dim3 grid((unsigned)((a.cols + n - 1) / n), (unsigned)(a.groups * a.splits));
+  if (bf16) hipLaunchKernelGGL(kl_column_sums<true>, grid, dim3(CS_THREADS), 0, s, a);
+  else hipLaunchKernelGGL(kl_column_sums<false>, grid, dim3(CS_THREADS), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  hipLaunchKernelGGL(kl_column_join, dim3((unsigned)((a.cols + CS_THREADS - 1) / CS_THREADS), (unsigned)a.groups),
+                     dim3(CS_THREADS), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_activation_grad(const ActivationGradArgs &a, bool bf16, hipStream_t s) {
+  if (a.rows == 0) return hipSuccess;
+  const int64_t chunks = (a.cols + 7) / 8;
+  const unsigned grid = (unsigned)((a.rows * chunks + 255) / 256);
+  if (bf16) hipLaunchKernelGGL(kl_activation_grad<true>, dim3(grid), dim3(256), 0, s, a, chunks);
+  else hipLaunchKernelGGL(kl_activation_grad<false>, dim3(grid), dim3(256), 0, s, a, chunks);
+  return hipGetLastError();
+}
+
+}  // namespace muon

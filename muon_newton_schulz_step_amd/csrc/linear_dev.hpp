@@ -1,0 +1,401 @@
+// Device parts that the kernels of the product with a weight matrix share:
+// where a workgroup's tile lies, how a stage of an operand is laid out in LDS,
+// activations, and the way of a tile's sums from registers to memory.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "devops.hpp"
+#include "linear.hpp"
+
+namespace muon {
+namespace dev {
+
+typedef __bf16 bf16x8_v __attribute__((ext_vector_type(8)));
+typedef float f32x4_v __attribute__((ext_vector_type(4)));
+typedef short i16x4_v __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4_v lds_i16x4;
+typedef __attribute__((address_space(3))) void lds_any;
+
+constexpr int LIN_THREADS = 256;
+constexpr int STAGE_BYTES = 128;  // of K a stage holds: 64 bf16 or 32 fp32
+
+// ------------------------------------------------------------- activations
+
+enum : int32_t { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4 };
+
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// Phi(v) = (1 + erf(v / sqrt 2)) / 2.  For bf16 results by Abramowitz and
+// Stegun 7.1.26, off by at most 0.8e-7 (a tenth of the instructions of
+// erfcf, of which a tile's thread would spend 256); fp32 results take erfcf,
+// which keeps the small values of negative v accurate.
+template <bool BF16>
+__device__ __forceinline__ float normal_cdf(float v) {
+  if constexpr (BF16) {
+    const float x = fabsf(v) * 0.70710678f;
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
+    const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+    const float tail = 0.5f * p * exp_fast(-x * x);
+    return v < 0.f ? tail : 1.f - tail;
+  } else {
+    return 0.5f * erfcf(-0.70710678f * v);
+  }
+}
+// (1 + tanh(c (v + 0.044715 v^3))) / 2 = 1 / (1 + exp(-2 c (...)))
+template <bool BF16>
+__device__ __forceinline__ float quotient(float d) {
+  return BF16 ? __builtin_amdgcn_rcpf(d) : 1.f / d;
+}
+template <bool BF16>
+__device__ __forceinline__ float tanh_gate(float v) {
+  const float u = v * fmaf(0.0713548163f, v * v, 1.5957691216f);  // 2 sqrt(2 / pi) (v + 0.044715 v^3)
+  return quotient<BF16>(1.f + exp_fast(-u));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float activate(int32_t act, float v) {
+  switch (act) {
+    case ACT_RELU: return v < 0.f ? 0.f : v;
+    case ACT_SILU: return v * quotient<BF16>(1.f + exp_fast(-v));
+    case ACT_GELU: return v * normal_cdf<BF16>(v);
+    case ACT_GELU_TANH: return v * tanh_gate<BF16>(v);
+    default: return v;
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ float slope(int32_t act, float v) {
+  switch (act) {
+    case ACT_RELU: return v > 0.f ? 1.f : 0.f;
+    case ACT_SILU: {
+      const float q = quotient<BF16>(1.f + exp_fast(-v));
+      return q * fmaf(v, 1.f - q, 1.f);
+    }
+    case ACT_GELU: return fmaf(v * 0.39894228f, exp_fast(-0.5f * v * v), normal_cdf<BF16>(v));
+    case ACT_GELU_TANH: {
+      const float q = tanh_gate<BF16>(v);
+      return fmaf(v * q * (1.f - q), fmaf(0.2140644489f, v * v, 1.5957691216f), q);
+    }
+    default: return 1.f;
+  }
+}
+
+// -------------------------------------------------------------------- tiles
+
+__device__ __forceinline__ int uni32(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// First row of group g, and of group `groups` the end; what falls outside
+// [0, rows] is cut off.
+__device__ __forceinline__ int64_t group_start(const IndexVec &o, int g, int64_t rows) {
+  const int64_t v = index_at(o, g);
+  return v < 0 ? 0 : v > rows ? rows : v;
+}
+
+struct LinTile {
+  int64_t row0, col0;  // of C (in LIN_WEIGHT: of its group's C)
+  int64_t k0, k1;
+  int rows;            // of the tile that exist
+  int group, split;
+};
+
+// Tile t of a launch of BT x BT tiles; false if there is none.  Tiles are
+// counted in panels of 8 tile rows, column by column, so that 32 consecutive
+// ones, which the 32 CUs of an XCD take, share 8 + 4 panels of operands.  A
+// product's tile rows are those of its groups one after the other, found by a
+// scan over the groups' tile counts.
+template <int BT>
+__device__ __forceinline__ bool find_tile(const LinearArgs &a, int t, int stage_k, LinTile &x) {
+  const int lane = threadIdx.x & 63;
+  const int per_split = a.tiles_m * a.tiles_n * (a.mode == LIN_WEIGHT ? a.groups : 1);
+  x.split = t / per_split;
+  t -= x.split * per_split;
+  if (x.split >= a.splits) return false;
+  x.group = 0;
+  if (a.mode == LIN_WEIGHT) {
+    x.group = t / (a.tiles_m * a.tiles_n);
+    t -= x.group * a.tiles_m * a.tiles_n;
+  }
+  const int panel = t / (8 * a.tiles_n), in = t - panel * 8 * a.tiles_n;
+  const int high = min(8, a.tiles_m - panel * 8);
+  const int tn = in / high, tm = panel * 8 + in - tn * high;
+  x.col0 = (int64_t)tn * BT;
+  x.k0 = 0;
+  x.k1 = a.K;
+  if (a.mode == LIN_WEIGHT) {
+    x.row0 = (int64_t)tm * BT;
+    x.rows = (int)min<int64_t>(BT, a.M - x.row0);
+    if (a.offsets.p) {
+      x.k0 = uniform(group_start(a.offsets, x.group, a.K));
+      x.k1 = max(x.k0, uniform(group_start(a.offsets, x.group + 1, a.K)));
+    }
+  } else if (!a.offsets.p) {
+    x.row0 = (int64_t)tm * BT;
+    x.rows = (int)min<int64_t>(BT, a.M - x.row0);
+  } else {
+    int before = 0;
+    bool found = false;
+    for (int g0 = 0; g0 < a.groups && !found; g0 += 64) {
+      const int g = g0 + lane;
+      int64_t lo = 0, hi = 0;
+      if (g < a.groups) {
+        lo = group_start(a.offsets, g, a.M);
+        hi = group_start(a.offsets, g + 1, a.M);
+      }
+      const int tiles = hi > lo ? (int)((hi - lo + BT - 1) / BT) : 0;
+      int sum = tiles;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int y = __shfl_up(sum, d);
+        if (lane >= d) sum += y;
+      }
+      const int mine = before + sum - tiles;  // this group's first tile row
+      const uint64_t has = __ballot(tm >= mine && tm < mine + tiles);
+      if (has) {
+        const int who = __ffsll((unsigned long long)has) - 1;
+        x.group = g0 + who;
+        const int first = uni32(__shfl(mine, who));
+        const int64_t l = uniform((int64_t)__shfl((long long)lo, who)), h = uniform((int64_t)__shfl((long long)hi, who));
+        x.row0 = l + (int64_t)(tm - first) * BT;
+        x.rows = (int)min<int64_t>(BT, h - x.row0);
+        found = true;
+      }
+      before += uni32(__shfl(sum, 63));
+    }
+    if (!found) return false;
+  }
+  if (a.splits > 1) {
+    const int64_t stages = (x.k1 - x.k0 + stage_k - 1) / stage_k, start = x.k0, end = x.k1;
+    x.k0 = min(end, start + stages * x.split / a.splits * stage_k);
+    x.k1 = min(end, start + stages * (x.split + 1) / a.splits * stage_k);
+  }
+  return true;
+}
+
+// ----------------------------------------------------- operands in LDS
+//
+// K adjacent: a row of the tile is 128 bytes of a stage, 16-byte chunk c of
+// row r at position c ^ (r / 2 % 8): the 16 rows that a quarter of a fragment
+// read touches spread over all banks.
+// K across: a row is one k of the stage with the tile's BT elements.  bf16
+// fragments are read with transposing reads (ds_read_b64_tr_b16: lane i of 16
+// gets element i % 4 of the 8 bytes that lanes i / 4, 4 + i / 4, ... address),
+// four k x 16 elements a group of 16 lanes: 32-byte pieces are XORed with
+// f(k) = k % 4 + 4 (k / 8 % 2), so that the eight k of half a wave fall on
+// different banks.  fp32 elements are read one by one, 64-byte pieces XORed
+// with k / 4 % 4.
+
+__device__ __forceinline__ int adjacent_chunk(int r, int c) { return c ^ (r >> 1 & 7); }
+template <bool BF16>
+__device__ __forceinline__ int across_chunk(int k, int c) {
+  return BF16 ? c ^ ((k & 3) << 1 | (k >> 3 & 1) << 3) : c ^ (k >> 2 & 3) << 2;
+}
+
+// One operand of a BT-wide tile as a stage's loads see it: BT / 32 loads of 16
+// bytes a thread, load j of wave w covering the LDS bytes from (w BT / 32 + j)
+// KB on, lane l its 16 bytes l.
+template <bool BF16, int BT, bool ACROSS>
+struct Operand {
+  typedef typename Elem<BF16>::type T;
+  static constexpr int E = (int)sizeof(T), N = 16 / E, LOADS = BT / 32, KS = STAGE_BYTES / E;
+  static constexpr int CPR = ACROSS ? BT * E / 16 : 8;  // 16-byte chunks of a row in LDS
+  static constexpr int RPL = 64 / CPR;                  // rows of a load
+  const T *p;       // the operand's element (tile, k = 0)
+  int64_t ld;
+  int extent;       // elements of the tile that exist
+  int64_t k1;
+
+  static __device__ __forceinline__ int row(int j) { return ((threadIdx.x >> 6) * LOADS + j) * RPL + (threadIdx.x & 63) / CPR; }
+  static __device__ __forceinline__ int chunk(int j) {
+    const int r = row(j), c = (threadIdx.x & 63) % CPR;
+    return ACROSS ? across_chunk<BF16>(r, c) : adjacent_chunk(r, c);
+  }
+  // 32-bit byte offset of load j from the stage's first element
+  __device__ __forceinline__ uint32_t offset(int j) const { return (uint32_t)(row(j) * ld * E) + chunk(j) * 16; }
+
+  // A descriptor whose range ends with the operand's last element: what lies
+  // behind it (rows of the tile or k that do not exist) loads as 0.
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(int64_t k) const {
+    const T *base = p + (ACROSS ? k * ld : k);
+    const int64_t bytes = ACROSS ? ((k1 - k - 1) * ld + extent) * E : ((int64_t)(extent - 1) * ld + (k1 - k)) * E;
+    const uint64_t v = reinterpret_cast<uint64_t>(base);
+    const uint64_t b = (uint64_t)uni32((int)(v >> 32)) << 32 | (uint32_t)uni32((int)v);
+    const int limit = uni32((int)min<int64_t>(bytes, 0x7fffffff));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(b), (short)0, limit, 0x00020000);
+  }
+  // Load j of the stage that starts at k, into LDS.
+  __device__ __forceinline__ void dma(__amdgpu_buffer_rsrc_t rs, int64_t k, uint32_t off, char *lds, int j) const {
+    // the last stage of adjacent K: chunks behind k1 are no rows' ends but the last one's
+    if (!ACROSS && (int64_t)chunk(j) * N >= k1 - k) off = 0x80000000u;
+    const int w = uni32((int)(threadIdx.x >> 6));
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_any *)(lds + (w * LOADS + j) * 1024), 16, off, 0, 0, 0);
+  }
+  // The same through registers, at any alignment and with any end.
+  __device__ __forceinline__ uint4 load(int64_t k, int j) const {
+    const int r = row(j), c = chunk(j) * N;
+    const int64_t have = ACROSS ? (k + r < k1 ? (int64_t)extent - c : 0) : (r < extent ? k1 - k - c : 0);
+    const T *q = p + (ACROSS ? (k + r) * ld + c : r * ld + k + c);
+    if (have >= N) return load16(q);
+    T e[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] = i < have ? q[i] : T(0);
+    uint4 v;
+    __builtin_memcpy(&v, e, 16);
+    return v;
+  }
+  static __device__ __forceinline__ void put(char *lds, int j, uint4 v) {
+    *reinterpret_cast<uint4 *>(lds + ((threadIdx.x >> 6) * LOADS + j) * 1024 + (threadIdx.x & 63) * 16) = v;
+  }
+};
+
+// bf16 fragment of 16 tile elements from `at` on and 32 k from 32 ks on: lane l
+// holds element l % 16, k 8 (l / 16) to + 7.
+template <int BT, bool ACROSS>
+__device__ __forceinline__ bf16x8_v read_fragment(const char *lds, int at, int ks) {
+  const int lr = threadIdx.x & 15, lg = threadIdx.x >> 4 & 3;
+  if constexpr (!ACROSS) {
+    return *reinterpret_cast<const bf16x8_v *>(lds + (at + lr) * STAGE_BYTES + adjacent_chunk(lr, 4 * ks + lg) * 16);
+  } else {
+    const int k = 32 * ks + 8 * lg + (lr >> 2);
+    const char *q = lds + k * (BT * 2) + across_chunk<true>(k, at >> 3) * 16 + (lr & 3) * 8;
+    union {
+      i16x4_v h[2];
+      bf16x8_v v;
+    } u;
+    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(q));
+    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(q + 4 * (BT * 2)));
+    return u.v;
+  }
+}
+
+// fp32 fragment of 16 tile elements and 16 k from 16 ks on: lane l holds
+// element l % 16, k 4 (l / 16) to + 3 (of which product c takes the c-th).
+template <int BT, bool ACROSS>
+__device__ __forceinline__ f32x4_v read_fragment_f32(const char *lds, int at, int ks) {
+  const int lr = threadIdx.x & 15, lg = threadIdx.x >> 4 & 3;
+  if constexpr (!ACROSS) {
+    return *reinterpret_cast<const f32x4_v *>(lds + (at + lr) * STAGE_BYTES + adjacent_chunk(lr, 4 * ks + lg) * 16);
+  } else {
+    f32x4_v v;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int k = 16 * ks + 4 * lg + c;
+      v[c] = *reinterpret_cast<const float *>(lds + k * (BT * 4) + across_chunk<false>(k, (at + lr) >> 2) * 16 + (lr & 3) * 4);
+    }
+    return v;
+  }
+}
+
+// ------------------------------------------------------ sums to memory
+
+// Eight neighbours of a row, n of which exist, as fp32.
+template <bool BF16>
+__device__ __forceinline__ void load8(const void *base, int64_t at, int n, float *v) {
+  typedef typename Elem<BF16>::type T;
+  const T *p = static_cast<const T *>(base) + at;
+  if (n >= 8) {
+    constexpr int N = Elem<BF16>::N;
+#pragma unroll
+    for (int i = 0; i < 8; i += N) Elem<BF16>::unpack(load16(p + i), v + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? Elem<BF16>::get(p[i]) : 0.f;
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void store8(void *base, int64_t at, int n, const float *v) {
+  typedef typename Elem<BF16>::type T;
+  T *p = static_cast<T *>(base) + at;
+  if (n >= 8) {
+    constexpr int N = Elem<BF16>::N;
+#pragma unroll
+    for (int i = 0; i < 8; i += N) store16(p + i, Elem<BF16>::pack(v + i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = Elem<BF16>::put(v[i]);
+  }
+}
+
+// Eight sums of row `row` (in LIN_WEIGHT: of the group's C), columns col to
+// col + 7, n of which exist: bias, activation, residual; rounded once.
+template <bool BF16>
+__device__ __forceinline__ void finish8(const LinearArgs &a, int group, int64_t row, int64_t col, int n, float *v) {
+  if (a.mode == LIN_WEIGHT) {
+    const int64_t at = group * a.out_stride + row * a.out_ld + col;
+    if (!a.first) {
+      float w[8];
+      load8<false>(a.out, at, n, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += w[i];
+    }
+    store8<false>(a.out, at, n, v);
+    return;
+  }
+  float w[8];
+  if (a.mode == LIN_FORWARD) {
+    if (a.bias) {
+      load8<BF16>(a.bias, group * a.N + col, n, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += w[i];
+    }
+    if (a.pre) store8<BF16>(a.pre, row * a.pre_ld + col, n, v);
+    if (a.act != ACT_NONE) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = activate<BF16>(a.act, v[i]);
+    }
+  } else if (a.act != ACT_NONE) {
+    load8<BF16>(a.pre, row * a.pre_ld + col, n, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= slope<BF16>(a.act, w[i]);
+  }
+  if (a.residual) {
+    load8<BF16>(a.residual, row * a.res_ld + col, n, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += w[i];
+  }
+  store8<BF16>(a.out, row * a.out_ld + col, n, v);
+}
+
+// The accumulators of a workgroup of 2 x 2 waves, each W x W blocks of 16 x 16
+// (lane l of block (i, j) holds row l % 16, columns 4 (l / 16) to + 3), leave
+// through LDS in passes of 64 rows, so that a thread gets eight neighbours of
+// a row.  Rows in LDS are BT + 4 floats apart: the 16 rows of a write fall on
+// different banks.
+template <bool BF16, int W>
+__device__ __forceinline__ void finish_tile(const LinearArgs &a, const LinTile &x, const f32x4_v (&acc)[W][W], char *lds) {
+  constexpr int BT = 32 * W, SLD = BT + 4, CH = BT / 8, STEP = LIN_THREADS / CH;
+  float *stg = reinterpret_cast<float *>(lds);
+  const int tid = threadIdx.x, wave = tid >> 6, lr = tid & 15, lg = tid >> 4 & 3, wm = wave >> 1, wn = wave & 1;
+  const int64_t col = x.col0 + (tid % CH) * 8;
+  const int n = (int)min<int64_t>(8, a.N - col);
+  const int64_t rows_all = a.mode == LIN_WEIGHT ? a.M * a.groups : a.M;
+  float *part = nullptr;
+  if (a.splits > 1) part = a.partial + ((int64_t)x.split * rows_all + (a.mode == LIN_WEIGHT ? x.group * a.M : 0)) * a.N;
+#pragma unroll 1
+  for (int p = 0; p < W / 2; ++p) {
+    __syncthreads();
+#pragma unroll
+    for (int pp = 0; pp < W / 2; ++pp)
+      if (p == pp) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < W; ++j)
+            *reinterpret_cast<f32x4_v *>(stg + (wm * 32 + h * 16 + lr) * SLD + wn * (BT / 2) + j * 16 + lg * 4) = acc[2 * pp + h][j];
+      }
+    __syncthreads();
+#pragma unroll 2
+    for (int r = tid / CH; r < 64; r += STEP) {
+      const int tr = (r >> 5) * (BT / 2) + p * 32 + (r & 31);
+      if (tr >= x.rows || n <= 0) continue;
+      const float *src = stg + r * SLD + (tid % CH) * 8;
+      const f32x4_v lo = *reinterpret_cast<const f32x4_v *>(src), hi = *reinterpret_cast<const f32x4_v *>(src + 4);
+      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      if (part) store8<false>(part, (x.row0 + tr) * a.N + col, n, v);
+      else finish8<BF16>(a, x.group, x.row0 + tr, col, n, v);
+    }
+  }
+}
+
+}  // namespace dev
+}  // namespace muon

@@ -1,7 +1,8 @@
 """The operators of a trained layer of experts, on torch tensors: dropout, a
 router's choice of experts, the order of the tokens by expert and the weighted
-sum of what the experts return, each with its gradient (include/muon.h states
-each formula).
+sum of what the experts return, and the product with a weight matrix or with
+one a group of rows, each with its gradient (include/muon.h states each
+formula).
 
 Outputs, checks, streams and errors are as in ``train_ops``: every output is
 the caller's tensor, ``ValueError`` comes before anything is enqueued, nothing
@@ -16,9 +17,12 @@ from . import _lib
 from .train_ops import _launch, _matrix, _refuse, _same, _vector, _workspace
 
 __all__ = ["dropout", "route_experts", "route_backward", "expert_order", "expert_order_workspace_bytes",
-           "expert_combine", "expert_combine_backward"]
+           "expert_combine", "expert_combine_backward", "linear_forward", "linear_input_grad", "linear_weight_grad",
+           "linear_workspace_bytes", "linear_weight_grad_workspace_bytes", "activation_grad"]
 
 expert_order_workspace_bytes = _lib.muon_expert_order_workspace_bytes
+linear_workspace_bytes = _lib.muon_linear_workspace_bytes
+linear_weight_grad_workspace_bytes = _lib.muon_linear_weight_grad_workspace_bytes
 
 
 def _like(x, what, rows, cols, dt):
@@ -176,3 +180,107 @@ def expert_combine_backward(dout, place, dy=None, weights=None, y=None, dweights
     _launch("expert_combine_backward",
             lambda s: f(dout.data_ptr(), tokens, dim, dold, dt, place.data_ptr(), k, _p(weights), _p(y), yld, rows,
                         _p(dy), dyld, _p(dweights), s), stream, (dout, place, dy, weights, y, dweights))
+
+
+def _weights(w, what, offsets, dtype=None):
+    """(groups, in, out, ld, stride, layout, muon_dtype, index type) of a matrix, in x out, or of one a group, groups x
+    in x out; either of in and out may be the adjacent one in memory."""
+    if w.dim() != (2 if offsets is None else 3):
+        _refuse(what, f"{w.dim()} dimensions, expected " + ("2 without offsets" if offsets is None else "3 with offsets"))
+    one = w if offsets is None else w[0] if w.shape[0] > 0 else _refuse(what, "no groups")
+    a, b = one.shape
+    layout = 0 if one.stride(1) == 1 or b == 1 else 1
+    _, _, ld, dt = _matrix(one if layout == 0 else one.t(), what, dtype)
+    groups = 1 if offsets is None else w.shape[0]
+    it = 0
+    if offsets is not None:
+        it = _vector(offsets, "offsets", groups + 1, index=True)
+    return groups, a, b, ld, 0 if groups == 1 else w.stride(0), layout, dt, it
+
+
+def _activation(name):
+    if name not in _lib.ACTIVATION:
+        _refuse("activation", f"{name!r}, expected one of {', '.join(_lib.ACTIVATION)}")
+    return _lib.ACTIVATION[name]
+
+
+def linear_forward(x, w, out, ws, bias=None, activation: str = "none", pre=None, residual=None, offsets=None,
+                   stream=None) -> None:
+    """out = act(x w + bias) + residual, and pre = x w + bias if asked for.
+
+    x: rows x in; w: in x out (a transposed view of out x in will do), or with offsets groups x in x out: group g has
+    the rows [offsets[g], offsets[g + 1]), rows of no group are left alone; out, pre, residual (may be out): rows x
+    out; bias: out or groups x out numbers; all of one type.  offsets: int32 or int64, groups + 1, on the device.
+    activation: none, relu, silu, gelu or gelu_tanh.  ws: at least linear_workspace_bytes(rows, in, out, groups)
+    bytes, 256-byte aligned."""
+    groups, a, b, ld, stride, layout, dt, it = _weights(w, "w", offsets)
+    rows, cols, xld, _ = _matrix(x, "x", dt)
+    _same("x columns", cols, a)
+    op, old = _like(out, "out", rows, b, dt)
+    pp, pld = _like(pre, "pre", rows, b, dt)
+    rp, rld = _like(residual, "residual", rows, b, dt)
+    if bias is not None:
+        _vector(bias, "bias", groups * b, dtype="bfloat16" if dt else "float32")
+    act = _activation(activation)
+    wp, wb = _workspace(ws)
+    o = _lib.muon_weights(w.data_ptr(), a, b, ld, stride, layout, groups, _p(offsets), it, dt)
+    f = _lib.load().muon_linear_forward
+    _launch("linear_forward", lambda s: f(x.data_ptr(), rows, xld, C.byref(o), _p(bias), act, pp, pld, rp, rld, op, old,
+                                          wp, wb, s), stream, (x, w, out, ws, bias, pre, residual, offsets))
+
+
+def linear_input_grad(dy, w, dx, ws, pre=None, activation: str = "none", residual=None, offsets=None,
+                      stream=None) -> None:
+    """dx = (dy w') act'(pre) + residual: the gradient by the product's input, through the activation that made it
+    (pre: what that took, rows x in), with a gradient that joins (residual, may be dx).
+
+    dy: rows x out; w, offsets: as linear_forward took them; ws: at least linear_workspace_bytes(rows, out, in,
+    groups) bytes, 256-byte aligned."""
+    groups, a, b, ld, stride, layout, dt, it = _weights(w, "w", offsets)
+    rows, cols, yld, _ = _matrix(dy, "dy", dt)
+    _same("dy columns", cols, b)
+    act = _activation(activation)
+    if act and pre is None:
+        _refuse("pre", "an activation needs it")
+    if not act:
+        pre = None
+    xp, xld = _like(dx, "dx", rows, a, dt)
+    pp, pld = _like(pre, "pre", rows, a, dt)
+    rp, rld = _like(residual, "residual", rows, a, dt)
+    wp, wb = _workspace(ws)
+    o = _lib.muon_weights(w.data_ptr(), a, b, ld, stride, layout, groups, _p(offsets), it, dt)
+    f = _lib.load().muon_linear_input_grad
+    _launch("linear_input_grad", lambda s: f(dy.data_ptr(), rows, yld, C.byref(o), act, pp, pld, rp, rld, xp, xld, wp,
+                                             wb, s), stream, (dy, w, dx, ws, pre, residual, offsets))
+
+
+def linear_weight_grad(x, dy, dw, first: bool, ws, dbias=None, offsets=None, stream=None) -> None:
+    """dw = (0 if first else dw) + x' dy and dbias = (0 if first else dbias) + the sums of dy's columns, a group of
+    rows each if there are offsets.
+
+    x: rows x in; dy: rows x out, of one type; dw: fp32, in x out or groups x in x out, either adjacent; dbias: fp32,
+    out or groups x out numbers; ws: at least linear_weight_grad_workspace_bytes(rows, in, out, groups) bytes,
+    256-byte aligned."""
+    groups, a, b, ld, stride, layout, _, it = _weights(dw, "dw", offsets, 0)
+    rows, cols, xld, dt = _matrix(x, "x")
+    _same("x columns", cols, a)
+    n, cols, yld, _ = _matrix(dy, "dy", dt)
+    _same("dy", (n, cols), (rows, b))
+    if dbias is not None:
+        _vector(dbias, "dbias", groups * b)
+    wp, wb = _workspace(ws)
+    f = _lib.load().muon_linear_weight_grad
+    _launch("linear_weight_grad", lambda s: f(x.data_ptr(), rows, a, xld, dy.data_ptr(), b, yld, dt, _p(offsets), it,
+                                              groups, dw.data_ptr(), ld, stride, layout, _p(dbias), 1 if first else 0,
+                                              wp, wb, s), stream, (x, dy, dw, ws, dbias, offsets))
+
+
+def activation_grad(dy, pre, dpre, activation: str, stream=None) -> None:
+    """dpre = dy act'(pre), for an activation that no product follows; dpre may be dy or pre."""
+    rows, cols, yld, dt = _matrix(dy, "dy")
+    pp, pld = _like(pre, "pre", rows, cols, dt)
+    op, old = _like(dpre, "dpre", rows, cols, dt)
+    act = _activation(activation)
+    f = _lib.load().muon_activation_grad
+    _launch("activation_grad", lambda s: f(dy.data_ptr(), rows, cols, yld, dt, act, pp, pld, op, old, s), stream,
+            (dy, pre, dpre))

@@ -112,6 +112,10 @@ __device__ __forceinline__ float exp_grad(float x, float m) {
   return BF16 ? exp_shift(x, m) : exp_term(x, m);
 }
 
+// HIP's min and max of 64-bit whole numbers go through fp64.
+__device__ __forceinline__ int64_t lesser(int64_t a, int64_t b) { return a < b ? a : b; }
+__device__ __forceinline__ int64_t greater(int64_t a, int64_t b) { return a > b ? a : b; }
+
 // A value that is the same in all lanes of a wave, moved to scalar registers.
 __device__ __forceinline__ int64_t uniform(int64_t v) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));

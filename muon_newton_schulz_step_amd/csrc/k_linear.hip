@@ -22,6 +22,8 @@ namespace muon {
 
 using namespace dev;
 
+hipError_t launch_linear256(const LinearArgs &a, int tiles, bool ax, bool bx, hipStream_t s);
+
 namespace {
 
 constexpr int BT = 128;
@@ -38,7 +40,7 @@ __global__ __launch_bounds__(LIN_THREADS, 2) void kl_linear128(LinearArgs a) {
   if (!find_tile<BT>(a, (int)blockIdx.x, KS, x)) return;
   const OA oa{static_cast<const T *>(a.a) + (AX ? x.row0 : x.row0 * a.lda), a.lda, x.rows, x.k1};
   const OB ob{static_cast<const T *>(a.b) + x.group * a.bstride + (BX ? x.col0 : x.col0 * a.ldb), a.ldb,
-              (int)min<int64_t>(BT, a.N - x.col0), x.k1};
+              (int)lesser(BT, a.N - x.col0), x.k1};
   const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
   f32x4_v acc[4][4];
 #pragma unroll
@@ -146,7 +148,7 @@ __global__ __launch_bounds__(256) void kl_join(LinearArgs a, int64_t rows) {
   int64_t row = id / chunks;
   const int64_t col = (id - row * chunks) * 8;
   if (row >= rows) return;
-  const int n = (int)min<int64_t>(8, a.N - col);
+  const int n = (int)lesser(8, a.N - col);
   int g;
   if (a.mode == LIN_WEIGHT) {
     g = (int)(row / a.M);
@@ -182,10 +184,10 @@ __global__ __launch_bounds__(CS_THREADS) void kl_column_sums(ColumnSumArgs a) {
   int64_t lo = 0, hi = a.rows;
   if (a.offsets.p) {
     lo = group_start(a.offsets, g, a.rows);
-    hi = max(lo, group_start(a.offsets, g + 1, a.rows));
+    hi = greater(lo, group_start(a.offsets, g + 1, a.rows));
   }
   const int64_t r0 = lo + (hi - lo) * part / a.splits, r1 = lo + (hi - lo) * (part + 1) / a.splits;
-  const int n = (int)min<int64_t>(N, a.cols - col);
+  const int n = (int)lesser(N, a.cols - col);
   float sum[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) sum[i] = 0.f;
@@ -231,7 +233,7 @@ template <bool BF16>
 __global__ __launch_bounds__(256) void kl_activation_grad(ActivationGradArgs a, int64_t chunks) {
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, row = id / chunks, col = (id - row * chunks) * 8;
   if (row >= a.rows) return;
-  const int n = (int)min<int64_t>(8, a.cols - col);
+  const int n = (int)lesser(8, a.cols - col);
   float v[8], w[8];
   load8<BF16>(a.dy, row * a.dld + col, n, v);
   load8<BF16>(a.pre, row * a.pld + col, n, w);
@@ -267,6 +269,12 @@ int32_t parts_of(int64_t M, int64_t N, int64_t K, int32_t groups, bool weight) {
   return (int32_t)std::max<int64_t>(1, parts);
 }
 
+// Whether 256 x 256 tiles are many enough to fill the chip.
+bool large_tiles(const LinearArgs &a, bool weight) {
+  const int64_t tiles = (a.M + 255) / 256 * ((a.N + 255) / 256) * (weight ? a.groups : 1);
+  return tiles >= 192 && a.N >= 256 && (weight ? a.M >= 256 : a.M / a.groups >= 256);
+}
+
 }  // namespace
 
 size_t linear_partial_bytes(int64_t M, int64_t N, int64_t K, int32_t groups, bool weight) {
@@ -278,6 +286,12 @@ hipError_t launch_linear(LinearArgs a, bool bf16, int la, int lb, hipStream_t s)
   const int e = bf16 ? 2 : 4;
   const bool ax = la == LIN_K_ACROSS, bx = lb == LIN_K_ACROSS, weight = a.mode == LIN_WEIGHT;
   const bool dma = aligned(a.a, a.lda, ax ? a.M : a.K, 0, e) && aligned(a.b, a.ldb, bx ? a.N : a.K, a.groups > 1 ? a.bstride : 0, e);
+  if (bf16 && dma && large_tiles(a, weight)) {
+    a.splits = 1;
+    a.tiles_m = (int32_t)tiles_along(a.M, a.groups, !weight && a.offsets.p, 256);
+    a.tiles_n = (int32_t)((a.N + 255) / 256);
+    return launch_linear256(a, a.tiles_m * a.tiles_n * (weight ? a.groups : 1), ax, bx, s);
+  }
   a.splits = parts_of(a.M, a.N, a.K, a.groups, weight);
   a.tiles_m = (int32_t)tiles_along(a.M, a.groups, !weight && a.offsets.p, BT);
   a.tiles_n = (int32_t)((a.N + BT - 1) / BT);

@@ -1,0 +1,177 @@
+// The product with a weight matrix and its gradients on 256 x 256 tiles, for
+// large bf16 products whose rows keep 16-byte alignment, on gfx950.
+//
+// A workgroup of 4 waves (2 x 2), each 128 x 128 = 8 x 8 blocks of
+// v_mfma_f32_16x16x32_bf16 with 256 fp32 sums a lane: 16 fragments of LDS feed
+// 64 products, half of what 64 x 64 a wave needs, which is bound by LDS.  K in
+// stages of 64, double buffered, loaded straight into LDS (buffer_load_dwordx4
+// ... lds) with 16 loads a wave and stage, spread one a group of four products:
+// issued together they stall the wave until the address unit has taken them.
+// A stage has two barriers: one when every wave has read the stage's last
+// fragments, which frees its buffer for the stage after the next, and one
+// between its two k-steps, which waits for the next stage's loads alone.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "linear_dev.hpp"
+
+namespace muon {
+
+using namespace dev;
+
+namespace {
+
+constexpr int BT = 256;
+constexpr int OPB = BT * STAGE_BYTES;  // 32 KB an operand and stage
+
+// c += b' a with the sums tied in place: left to itself the compiler rotates
+// the 64 blocks through copies.  It does not see the latency of an asm
+// product, so the last one of every block (the tile's final k-step, LAST) goes
+// through the builtin, and nothing but the next k-step's products, 64
+// instructions later, reads an asm one.
+template <bool LAST>
+__device__ __forceinline__ void mfma(f32x4_v &c, const bf16x8_v &b, const bf16x8_v &a) {
+  if constexpr (LAST) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
+  else asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
+}
+
+__shared__ __attribute__((aligned(1024))) char lds[2 * 2 * OPB];
+
+template <bool AX, bool BX>
+__global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int tiles) {
+  typedef Operand<true, BT, AX> OA;
+  typedef Operand<true, BT, BX> OB;
+  typedef typename OA::T T;
+  constexpr int KS = OA::KS;
+  // workgroup i runs on XCD i % 8: chunks of 256 tiles, 32 consecutive ones an XCD
+  const int slot = (int)blockIdx.x >> 3, t = (slot >> 5) * 256 + ((int)blockIdx.x & 7) * 32 + (slot & 31);
+  LinTile x;
+  if (t >= tiles || !find_tile<BT>(a, t, KS, x)) return;
+  const OA oa{static_cast<const T *>(a.a) + (AX ? x.row0 : x.row0 * a.lda), a.lda, x.rows, x.k1};
+  const OB ob{static_cast<const T *>(a.b) + x.group * a.bstride + (BX ? x.col0 : x.col0 * a.ldb), a.ldb,
+              (int)lesser(BT, a.N - x.col0), x.k1};
+  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  f32x4_v acc[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+  const int nk = (int)((x.k1 - x.k0 + KS - 1) / KS);
+  if (nk > 0) {
+    uint32_t offa[8], offb[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      offa[j] = oa.offset(j);
+      offb[j] = ob.offset(j);
+    }
+    bf16x8_v fa[2][8], fb[2][8];
+    // fragment q of a k-step, in the order its products need them: A0, B0..B7, A1..A7
+    auto read1 = [&](int set, int st, int ks, int q) {
+      const char *la = lds + st * 2 * OPB, *lb = la + OPB;
+      if (q == 0 || q > 8) {
+        const int i = q == 0 ? 0 : q - 8;
+        fa[set][i] = read_fragment<BT, AX>(la, wm * 128 + i * 16, ks);
+      } else {
+        fb[set][q - 1] = read_fragment<BT, BX>(lb, wn * 128 + (q - 1) * 16, ks);
+      }
+    };
+    struct Stage {
+      __amdgpu_buffer_rsrc_t a, b;
+      int64_t k;
+    };
+    auto stage_of = [&](int kt) {
+      const int64_t k = x.k0 + (int64_t)kt * KS;
+      return Stage{oa.rsrc(k), ob.rsrc(k), k};
+    };
+    auto dma1 = [&](const Stage &s, int st, int q) {
+      char *la = lds + st * 2 * OPB;
+      if (q < 8) oa.dma(s.a, s.k, offa[q], la, q);
+      else ob.dma(s.b, s.k, offb[q - 8], la + OPB, q - 8);
+    };
+    {
+      const Stage s0 = stage_of(0);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) dma1(s0, 0, q);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (nk > 1) {
+      const Stage s1 = stage_of(1);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) dma1(s1, 1, q);
+    }
+#pragma unroll
+    for (int q = 0; q < 16; ++q) read1(0, 0, 0, q);
+    constexpr int kBar1 = 9;           // group of k-step 0 that ends with the first barrier
+    constexpr int kDma0 = 15 - kBar1;  // loads in k-step 0
+    constexpr int kDma1 = 16 - kDma0;  // in k-step 1
+    static_assert(kDma0 == 6, "the vmcnt immediate of the second barrier");
+    auto body = [&](int kt, auto load, auto last) {
+      constexpr bool LOAD = decltype(load)::value;
+      constexpr bool LAST = decltype(last)::value;
+      const int st = kt & 1;
+      const Stage nn = stage_of(LOAD ? kt + 2 : kt);
+#pragma unroll
+      for (int n = 0; n < 16; ++n) {
+        const int i = n >> 1, j = (n & 1) * 4;
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) mfma<false>(acc[i][j + jj], fb[0][j + jj], fa[0][i]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (n < 8) {
+          read1(1, st, 1, 2 * n);
+          read1(1, st, 1, 2 * n + 1);
+        }
+        if (n == kBar1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if constexpr (LOAD) {
+          if (n > kBar1) dma1(nn, st, n - kBar1 - 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (LOAD) asm volatile("s_waitcnt vmcnt(6)\n\ts_barrier" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+      for (int n = 0; n < 16; ++n) {
+        const int i = n >> 1, j = (n & 1) * 4;
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) mfma<LAST>(acc[i][j + jj], fb[1][j + jj], fa[1][i]);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!LAST) {
+          if (n < 4) {
+            read1(0, st ^ 1, 0, 2 * n);
+            read1(0, st ^ 1, 0, 2 * n + 1);
+          } else if (n < 12) {
+            read1(0, st ^ 1, 0, n + 4);
+          }
+        }
+        if constexpr (LOAD) {
+          // the q-th of the last kDma1 loads in the group where n kDma1 / 16 steps up
+          if (((n + 1) * kDma1) / 16 > (n * kDma1) / 16) dma1(nn, st, kDma0 + (n * kDma1) / 16);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    int kt = 0;
+    for (; kt < nk - 2; ++kt) body(kt, yes, no);
+    if (kt == nk - 2) {
+      body(kt, no, no);
+      ++kt;
+    }
+    body(kt, no, yes);
+  }
+  finish_tile<true, 8>(a, x, acc, lds);
+}
+
+}  // namespace
+
+hipError_t launch_linear256(const LinearArgs &a, int tiles, bool ax, bool bx, hipStream_t s) {
+  const dim3 grid((unsigned)((tiles + 255) / 256 * 256));
+  if (ax) hipLaunchKernelGGL((kl_linear256<true, true>), grid, dim3(LIN_THREADS), 0, s, a, tiles);
+  else if (bx) hipLaunchKernelGGL((kl_linear256<false, true>), grid, dim3(LIN_THREADS), 0, s, a, tiles);
+  else hipLaunchKernelGGL((kl_linear256<false, false>), grid, dim3(LIN_THREADS), 0, s, a, tiles);
+  return hipGetLastError();
+}
+
+}  // namespace muon

@@ -252,7 +252,7 @@ __global__ __launch_bounds__(CT) void kc_combine(CombineArgs a, int64_t vecs) {
   const int64_t t = id / vecs;
   if (t >= a.tokens) return;
   const int64_t c = (id - t * vecs) * N;
-  const int n = (int)min((int64_t)N, a.dim - c);
+  const int n = (int)lesser(N, a.dim - c);
   const T *y = static_cast<const T *>(a.y) + c;
   float sum[N];
 #pragma unroll
@@ -325,7 +325,7 @@ __global__ __launch_bounds__(CT) void kc_backward(CombineBwdArgs a) {
       dot[j] = 0.f;
     }
     for (int64_t c = lane * N; c < a.dim; c += 64 * N) {
-      const int n = (int)min((int64_t)N, a.dim - c);
+      const int n = (int)lesser(N, a.dim - c);
       float d[N];
       if (n == N) {
         E::unpack(load16(g + c), d);

@@ -123,14 +123,14 @@ __device__ __forceinline__ bool find_tile(const LinearArgs &a, int t, int stage_
   x.k1 = a.K;
   if (a.mode == LIN_WEIGHT) {
     x.row0 = (int64_t)tm * BT;
-    x.rows = (int)min<int64_t>(BT, a.M - x.row0);
+    x.rows = (int)lesser(BT, a.M - x.row0);
     if (a.offsets.p) {
       x.k0 = uniform(group_start(a.offsets, x.group, a.K));
-      x.k1 = max(x.k0, uniform(group_start(a.offsets, x.group + 1, a.K)));
+      x.k1 = greater(x.k0, uniform(group_start(a.offsets, x.group + 1, a.K)));
     }
   } else if (!a.offsets.p) {
     x.row0 = (int64_t)tm * BT;
-    x.rows = (int)min<int64_t>(BT, a.M - x.row0);
+    x.rows = (int)lesser(BT, a.M - x.row0);
   } else {
     int before = 0;
     bool found = false;
@@ -156,7 +156,7 @@ __device__ __forceinline__ bool find_tile(const LinearArgs &a, int t, int stage_
         const int first = uni32(__shfl(mine, who));
         const int64_t l = uniform((int64_t)__shfl((long long)lo, who)), h = uniform((int64_t)__shfl((long long)hi, who));
         x.row0 = l + (int64_t)(tm - first) * BT;
-        x.rows = (int)min<int64_t>(BT, h - x.row0);
+        x.rows = (int)lesser(BT, h - x.row0);
         found = true;
       }
       before += uni32(__shfl(sum, 63));
@@ -165,8 +165,8 @@ __device__ __forceinline__ bool find_tile(const LinearArgs &a, int t, int stage_
   }
   if (a.splits > 1) {
     const int64_t stages = (x.k1 - x.k0 + stage_k - 1) / stage_k, start = x.k0, end = x.k1;
-    x.k0 = min(end, start + stages * x.split / a.splits * stage_k);
-    x.k1 = min(end, start + stages * (x.split + 1) / a.splits * stage_k);
+    x.k0 = lesser(end, start + stages * x.split / a.splits * stage_k);
+    x.k1 = lesser(end, start + stages * (x.split + 1) / a.splits * stage_k);
   }
   return true;
 }
@@ -219,7 +219,7 @@ struct Operand {
     const int64_t bytes = ACROSS ? ((k1 - k - 1) * ld + extent) * E : ((int64_t)(extent - 1) * ld + (k1 - k)) * E;
     const uint64_t v = reinterpret_cast<uint64_t>(base);
     const uint64_t b = (uint64_t)uni32((int)(v >> 32)) << 32 | (uint32_t)uni32((int)v);
-    const int limit = uni32((int)min<int64_t>(bytes, 0x7fffffff));
+    const int limit = uni32((int)lesser(bytes, 0x7fffffff));
     return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(b), (short)0, limit, 0x00020000);
   }
   // Load j of the stage that starts at k, into LDS.
@@ -247,6 +247,13 @@ struct Operand {
   }
 };
 
+// The compiler waits for all loads into LDS before a transposing read, unless
+// the read carries alias information, as ordinary ones do: `restrict` gives
+// it some.  The kernels wait for the loads themselves.
+__device__ __forceinline__ i16x4_v read_across(const char *__restrict p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)p);
+}
+
 // bf16 fragment of 16 tile elements from `at` on and 32 k from 32 ks on: lane l
 // holds element l % 16, k 8 (l / 16) to + 7.
 template <int BT, bool ACROSS>
@@ -261,8 +268,8 @@ __device__ __forceinline__ bf16x8_v read_fragment(const char *lds, int at, int k
       i16x4_v h[2];
       bf16x8_v v;
     } u;
-    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(q));
-    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(q + 4 * (BT * 2)));
+    u.h[0] = read_across(q);
+    u.h[1] = read_across(q + 4 * (BT * 2));
     return u.v;
   }
 }
@@ -367,7 +374,7 @@ __device__ __forceinline__ void finish_tile(const LinearArgs &a, const LinTile &
   float *stg = reinterpret_cast<float *>(lds);
   const int tid = threadIdx.x, wave = tid >> 6, lr = tid & 15, lg = tid >> 4 & 3, wm = wave >> 1, wn = wave & 1;
   const int64_t col = x.col0 + (tid % CH) * 8;
-  const int n = (int)min<int64_t>(8, a.N - col);
+  const int n = (int)lesser(8, a.N - col);
   const int64_t rows_all = a.mode == LIN_WEIGHT ? a.M * a.groups : a.M;
   float *part = nullptr;
   if (a.splits > 1) part = a.partial + ((int64_t)x.split * rows_all + (a.mode == LIN_WEIGHT ? x.group * a.M : 0)) * a.N;

@@ -250,3 +250,19 @@ def test_linear_gradients_against_differences(torch):
         u = rng.standard_normal(tuple(g.shape))
         diff = (loss(**{name: 1e-5 * u}) - loss(**{name: -1e-5 * u})) / 2e-5
         assert scale * float((f64(g) * u).sum()) == pytest.approx(diff, rel=1e-4, abs=1e-3)
+
+
+@pytest.mark.parametrize("layout", ["in_out", "out_in"])
+@pytest.mark.parametrize("rows,a,b,groups,ld", [
+    (3501, 8, 3600, None, 0), (3499, 64, 3592, None, 8), (3585, 136, 3600, None, 0), (3501, 200, 3584, None, 0),   # forwards
+    (3500, 3600, 8, None, 8), (3501, 3592, 72, None, 0), (3500, 3584, 192, None, 0),                              # by the input
+    (1, 3600, 3504, None, 0), (65, 3592, 3600, None, 8), (129, 3584, 3584, None, 0), (190, 3600, 3600, None, 0),    # by the weights
+    (5003, 72, 2568, 5, 0), (5003, 2568, 72, 5, 8), (700, 1032, 1024, 12, 8)])
+def test_linear_of_large_tiles(torch, rows, a, b, groups, ld, layout):
+    check_linear(torch, rows, a, b, "bf16", layout, groups, ld=ld, shift=ld, act="relu" if ld else "none", pre=True, first=ld == 0)
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_linear_of_large_tiles_with_activations(torch, act):
+    check_linear(torch, 3501, 200, 3600, "bf16", "in_out", act=act, pre=True, whole=False)
+    check_linear(torch, 3501, 3600, 136, "bf16", "out_in", act=act, pre=True, whole=False)

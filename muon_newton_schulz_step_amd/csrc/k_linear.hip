@@ -65,8 +65,8 @@ __global__ __launch_bounds__(LIN_THREADS, 2) void kl_linear128(LinearArgs a) {
       const auto brs = ob.rsrc(k);
 #pragma unroll
       for (int j = 0; j < L; ++j) {
-        oa.dma(ars, k, offa[j], la, j);
-        ob.dma(brs, k, offb[j], lb, j);
+        OA::dma(ars, oa.left(k), offa[j], la, j);
+        OB::dma(brs, ob.left(k), offb[j], lb, j);
       }
     } else {
 #pragma unroll
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(LIN_THREADS, 2) void kl_linear128(LinearArgs a) {
     }
     if (kt + 1 < nk) land(st ^ 1);
   }
-  finish_tile<BF16, 4>(a, x, acc, lds);
+  finish_tile<BF16, 4, AX, true>(a, x, acc, lds);
 }
 
 // Group of a row, by bisection; -1 for a row of none.

@@ -38,139 +38,163 @@ __device__ __forceinline__ void mfma(f32x4_v &c, const bf16x8_v &b, const bf16x8
 
 __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * OPB];
 
+// A workgroup takes tiles `stride` apart.  With several, the first stage of the
+// next tile is loaded while the last ones of this tile are multiplied, and
+// waits in one stage buffer while the sums leave through the other.
 template <bool AX, bool BX>
-__global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int tiles) {
+__global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int tiles, int stride) {
   typedef Operand<true, BT, AX> OA;
   typedef Operand<true, BT, BX> OB;
   typedef typename OA::T T;
   constexpr int KS = OA::KS;
   // workgroup i runs on XCD i % 8: chunks of 256 tiles, 32 consecutive ones an XCD
-  const int slot = (int)blockIdx.x >> 3, t = (slot >> 5) * 256 + ((int)blockIdx.x & 7) * 32 + (slot & 31);
+  const int slot = (int)blockIdx.x >> 3;
+  int t = (slot >> 5) * 256 + ((int)blockIdx.x & 7) * 32 + (slot & 31);
   LinTile x;
-  if (t >= tiles || !find_tile<BT>(a, t, KS, x)) return;
-  const OA oa{static_cast<const T *>(a.a) + (AX ? x.row0 : x.row0 * a.lda), a.lda, x.rows, x.k1};
-  const OB ob{static_cast<const T *>(a.b) + x.group * a.bstride + (BX ? x.col0 : x.col0 * a.ldb), a.ldb,
-              (int)lesser(BT, a.N - x.col0), x.k1};
+  while (t < tiles && !find_tile<BT>(a, t, KS, x)) t += stride;
+  if (t >= tiles) return;
   const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
-  f32x4_v acc[8][8];
+  uint32_t offa[8], offb[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = f32x4_v{0.f, 0.f, 0.f, 0.f};
-  const int nk = (int)((x.k1 - x.k0 + KS - 1) / KS);
-  if (nk > 0) {
-    uint32_t offa[8], offb[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      offa[j] = oa.offset(j);
-      offb[j] = ob.offset(j);
-    }
-    bf16x8_v fa[2][8], fb[2][8];
-    // fragment q of a k-step, in the order its products need them: A0, B0..B7, A1..A7
-    auto read1 = [&](int set, int st, int ks, int q) {
-      const char *la = lds + st * 2 * OPB, *lb = la + OPB;
-      if (q == 0 || q > 8) {
-        const int i = q == 0 ? 0 : q - 8;
-        fa[set][i] = read_fragment<BT, AX>(la, wm * 128 + i * 16, ks);
-      } else {
-        fb[set][q - 1] = read_fragment<BT, BX>(lb, wn * 128 + (q - 1) * 16, ks);
-      }
-    };
-    struct Stage {
-      __amdgpu_buffer_rsrc_t a, b;
-      int64_t k;
-    };
-    auto stage_of = [&](int kt) {
-      const int64_t k = x.k0 + (int64_t)kt * KS;
-      return Stage{oa.rsrc(k), ob.rsrc(k), k};
-    };
-    auto dma1 = [&](const Stage &s, int st, int q) {
-      char *la = lds + st * 2 * OPB;
-      if (q < 8) oa.dma(s.a, s.k, offa[q], la, q);
-      else ob.dma(s.b, s.k, offb[q - 8], la + OPB, q - 8);
-    };
-    {
-      const Stage s0 = stage_of(0);
-#pragma unroll
-      for (int q = 0; q < 16; ++q) dma1(s0, 0, q);
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (nk > 1) {
-      const Stage s1 = stage_of(1);
-#pragma unroll
-      for (int q = 0; q < 16; ++q) dma1(s1, 1, q);
-    }
-#pragma unroll
-    for (int q = 0; q < 16; ++q) read1(0, 0, 0, q);
-    constexpr int kBar1 = 9;           // group of k-step 0 that ends with the first barrier
-    constexpr int kDma0 = 15 - kBar1;  // loads in k-step 0
-    constexpr int kDma1 = 16 - kDma0;  // in k-step 1
-    static_assert(kDma0 == 6, "the vmcnt immediate of the second barrier");
-    auto body = [&](int kt, auto load, auto last) {
-      constexpr bool LOAD = decltype(load)::value;
-      constexpr bool LAST = decltype(last)::value;
-      const int st = kt & 1;
-      const Stage nn = stage_of(LOAD ? kt + 2 : kt);
-#pragma unroll
-      for (int n = 0; n < 16; ++n) {
-        const int i = n >> 1, j = (n & 1) * 4;
-#pragma unroll
-        for (int jj = 0; jj < 4; ++jj) mfma<false>(acc[i][j + jj], fb[0][j + jj], fa[0][i]);
-        __builtin_amdgcn_sched_barrier(0);
-        if (n < 8) {
-          read1(1, st, 1, 2 * n);
-          read1(1, st, 1, 2 * n + 1);
-        }
-        if (n == kBar1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if constexpr (LOAD) {
-          if (n > kBar1) dma1(nn, st, n - kBar1 - 1);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if constexpr (LOAD) asm volatile("s_waitcnt vmcnt(6)\n\ts_barrier" ::: "memory");
-      else asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-#pragma unroll
-      for (int n = 0; n < 16; ++n) {
-        const int i = n >> 1, j = (n & 1) * 4;
-#pragma unroll
-        for (int jj = 0; jj < 4; ++jj) mfma<LAST>(acc[i][j + jj], fb[1][j + jj], fa[1][i]);
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (!LAST) {
-          if (n < 4) {
-            read1(0, st ^ 1, 0, 2 * n);
-            read1(0, st ^ 1, 0, 2 * n + 1);
-          } else if (n < 12) {
-            read1(0, st ^ 1, 0, n + 4);
-          }
-        }
-        if constexpr (LOAD) {
-          // the q-th of the last kDma1 loads in the group where n kDma1 / 16 steps up
-          if (((n + 1) * kDma1) / 16 > (n * kDma1) / 16) dma1(nn, st, kDma0 + (n * kDma1) / 16);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    };
-    constexpr std::true_type yes{};
-    constexpr std::false_type no{};
-    int kt = 0;
-    for (; kt < nk - 2; ++kt) body(kt, yes, no);
-    if (kt == nk - 2) {
-      body(kt, no, no);
-      ++kt;
-    }
-    body(kt, no, yes);
+  for (int j = 0; j < 8; ++j) {
+    offa[j] = OA{nullptr, a.lda, 0, 0}.offset(j);
+    offb[j] = OB{nullptr, a.ldb, 0, 0}.offset(j);
   }
-  finish_tile<true, 8>(a, x, acc, lds);
+  struct Stage {
+    __amdgpu_buffer_rsrc_t a, b;
+    int left;
+  };
+  auto stage_of = [&](const LinTile &y, int kt) {
+    const int64_t k = y.k0 + (int64_t)kt * KS;
+    const OA oa{static_cast<const T *>(a.a) + (AX ? y.row0 : y.row0 * a.lda), a.lda, y.rows, y.k1};
+    const OB ob{static_cast<const T *>(a.b) + y.group * a.bstride + (BX ? y.col0 : y.col0 * a.ldb), a.ldb,
+                (int)lesser(BT, a.N - y.col0), y.k1};
+    return Stage{oa.rsrc(k), ob.rsrc(k), oa.left(k)};
+  };
+  auto dma1 = [&](const Stage &s, int st, int q) {
+    char *la = lds + st * 2 * OPB;
+    if (q < 8) OA::dma(s.a, s.left, offa[q], la, q);
+    else OB::dma(s.b, s.left, offb[q - 8], la + OPB, q - 8);
+  };
+  auto dma_all = [&](const Stage &s, int st) {
+#pragma unroll
+    for (int q = 0; q < 16; ++q) dma1(s, st, q);
+  };
+  int base = 0;        // buffer of the tile's first stage
+  bool ready = false;  // whose loads are under way
+  bool full = false;   // the tile before was whole, so that every thread's last eight accesses are its stores
+  for (;;) {
+    int tn = t + stride;
+    LinTile y;
+    while (tn < tiles && !find_tile<BT>(a, tn, KS, y)) tn += stride;
+    const bool next = tn < tiles && y.k1 > y.k0;
+    f32x4_v acc[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[i][j] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+    const int nk = (int)((x.k1 - x.k0 + KS - 1) / KS);
+    if (nk > 0) {
+      bf16x8_v fa[2][8], fb[2][8];
+      // fragment q of a k-step, in the order its products need them: A0, B0..B7, A1..A7
+      auto read1 = [&](int set, int st, int ks, int q) {
+        const char *la = lds + st * 2 * OPB, *lb = la + OPB;
+        if (q == 0 || q > 8) {
+          const int i = q == 0 ? 0 : q - 8;
+          fa[set][i] = read_fragment<BT, AX>(la, wm * 128 + i * 16, ks);
+        } else {
+          fb[set][q - 1] = read_fragment<BT, BX>(lb, wn * 128 + (q - 1) * 16, ks);
+        }
+      };
+      if (!ready) dma_all(stage_of(x, 0), base);
+      if (ready && full) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      // the second stage, or of a tile of one stage the next tile's first
+      if (nk > 1) dma_all(stage_of(x, 1), base ^ 1);
+      else if (next) dma_all(stage_of(y, 0), base ^ 1);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) read1(0, base, 0, q);
+      constexpr int kBar1 = 9;           // group of k-step 0 that ends with the first barrier
+      constexpr int kDma0 = 15 - kBar1;  // loads in k-step 0
+      constexpr int kDma1 = 16 - kDma0;  // in k-step 1
+      static_assert(kDma0 == 6, "the vmcnt immediate of the second barrier");
+      auto body = [&](int kt, auto load, auto last) {
+        constexpr bool LOAD = decltype(load)::value;
+        constexpr bool LAST = decltype(last)::value;
+        const int st = (kt ^ base) & 1;
+        Stage nn;
+        if constexpr (LOAD) nn = kt + 2 < nk ? stage_of(x, kt + 2) : stage_of(y, 0);
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          const int i = n >> 1, j = (n & 1) * 4;
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) mfma<false>(acc[i][j + jj], fb[0][j + jj], fa[0][i]);
+          __builtin_amdgcn_sched_barrier(0);
+          if (n < 8) {
+            read1(1, st, 1, 2 * n);
+            read1(1, st, 1, 2 * n + 1);
+          }
+          if (!LAST && n == kBar1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          if constexpr (LOAD) {
+            if (n > kBar1) dma1(nn, st, n - kBar1 - 1);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (LOAD) asm volatile("s_waitcnt vmcnt(6)\n\ts_barrier" ::: "memory");
+        else if constexpr (!LAST) asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          const int i = n >> 1, j = (n & 1) * 4;
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) mfma<LAST>(acc[i][j + jj], fb[1][j + jj], fa[1][i]);
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (!LAST) {
+            if (n < 4) {
+              read1(0, st ^ 1, 0, 2 * n);
+              read1(0, st ^ 1, 0, 2 * n + 1);
+            } else if (n < 12) {
+              read1(0, st ^ 1, 0, n + 4);
+            }
+          }
+          if constexpr (LOAD) {
+            // the q-th of the last kDma1 loads in the group where n kDma1 / 16 steps up
+            if (((n + 1) * kDma1) / 16 > (n * kDma1) / 16) dma1(nn, st, kDma0 + (n * kDma1) / 16);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      constexpr std::true_type yes{};
+      constexpr std::false_type no{};
+      int kt = 0;
+      for (const int end = next ? nk - 1 : nk - 2; kt < end; ++kt) body(kt, yes, no);
+      if (kt == nk - 2) {
+        body(kt, no, no);
+        ++kt;
+      }
+      body(kt, no, yes);
+    }
+    finish_tile<true, 8, AX, false>(a, x, acc, lds + ((nk - 1 + base) & 1) * 2 * OPB);
+    if (tn >= tiles) return;
+    ready = next && nk > 0;
+    full = x.rows == BT && a.N - x.col0 >= BT;
+    base = (nk + base) & 1;
+    x = y;
+    t = tn;
+  }
 }
 
 }  // namespace
 
 hipError_t launch_linear256(const LinearArgs &a, int tiles, bool ax, bool bx, hipStream_t s) {
-  const dim3 grid((unsigned)((tiles + 255) / 256 * 256));
-  if (ax) hipLaunchKernelGGL((kl_linear256<true, true>), grid, dim3(LIN_THREADS), 0, s, a, tiles);
-  else if (bx) hipLaunchKernelGGL((kl_linear256<false, true>), grid, dim3(LIN_THREADS), 0, s, a, tiles);
-  else hipLaunchKernelGGL((kl_linear256<false, false>), grid, dim3(LIN_THREADS), 0, s, a, tiles);
+  // Tiles of equal K go round 256 workgroups, one a CU; a grouped weight
+  // gradient's are of very different K, and taken by whichever CU is free.
+  const bool even = a.mode != LIN_WEIGHT || !a.offsets.p;
+  const int all = (tiles + 255) / 256 * 256, stride = even ? 256 : all;
+  const dim3 grid((unsigned)stride);
+  if (ax) hipLaunchKernelGGL((kl_linear256<true, true>), grid, dim3(LIN_THREADS), 0, s, a, tiles, stride);
+  else if (bx) hipLaunchKernelGGL((kl_linear256<false, true>), grid, dim3(LIN_THREADS), 0, s, a, tiles, stride);
+  else hipLaunchKernelGGL((kl_linear256<false, false>), grid, dim3(LIN_THREADS), 0, s, a, tiles, stride);
   return hipGetLastError();
 }
 

@@ -5,6 +5,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "devops.hpp"
 #include "linear.hpp"
 
@@ -222,13 +224,14 @@ struct Operand {
     const int limit = uni32((int)lesser(bytes, 0x7fffffff));
     return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(b), (short)0, limit, 0x00020000);
   }
-  // Load j of the stage that starts at k, into LDS.
-  __device__ __forceinline__ void dma(__amdgpu_buffer_rsrc_t rs, int64_t k, uint32_t off, char *lds, int j) const {
-    // the last stage of adjacent K: chunks behind k1 are no rows' ends but the last one's
-    if (!ACROSS && (int64_t)chunk(j) * N >= k1 - k) off = 0x80000000u;
+  // Load j of a stage, into LDS; left: k from its first one on that exist, or more than a stage has.
+  static __device__ __forceinline__ void dma(__amdgpu_buffer_rsrc_t rs, int left, uint32_t off, char *lds, int j) {
+    // the last stage of adjacent K: chunks behind it are no rows' ends but the last one's
+    if (!ACROSS && chunk(j) * N >= left) off = 0x80000000u;
     const int w = uni32((int)(threadIdx.x >> 6));
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_any *)(lds + (w * LOADS + j) * 1024), 16, off, 0, 0, 0);
   }
+  __device__ __forceinline__ int left(int64_t k) const { return (int)lesser(k1 - k, KS); }
   // The same through registers, at any alignment and with any end.
   __device__ __forceinline__ uint4 load(int64_t k, int j) const {
     const int r = row(j), c = chunk(j) * N;
@@ -363,23 +366,61 @@ __device__ __forceinline__ void finish8(const LinearArgs &a, int group, int64_t 
   store8<BF16>(a.out, row * a.out_ld + col, n, v);
 }
 
-// The accumulators of a workgroup of 2 x 2 waves, each W x W blocks of 16 x 16
-// (lane l of block (i, j) holds row l % 16, columns 4 (l / 16) to + 3), leave
-// through LDS in passes of 64 rows, so that a thread gets eight neighbours of
-// a row.  Rows in LDS are BT + 4 floats apart: the 16 rows of a write fall on
-// different banks.
-template <bool BF16, int W>
-__device__ __forceinline__ void finish_tile(const LinearArgs &a, const LinTile &x, const f32x4_v (&acc)[W][W], char *lds) {
-  constexpr int BT = 32 * W, SLD = BT + 4, CH = BT / 8, STEP = LIN_THREADS / CH;
+// Eight neighbours of a row as they come from memory.
+template <bool BF16>
+struct Raw8 {
+  uint4 v[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void *base, int64_t at) {
+    typedef typename Elem<BF16>::type T;
+    const T *p = static_cast<const T *>(base) + at;
+    v[0] = load16(p);
+    if constexpr (!BF16) v[1] = load16(p + 4);
+  }
+  __device__ __forceinline__ void get(float *f) const {
+    Elem<BF16>::unpack(v[0], f);
+    if constexpr (!BF16) Elem<BF16>::unpack(v[1], f + 4);
+  }
+};
+
+// A tile's accumulators, as `at(p, h, j)` gives them, leave through LDS in
+// passes of 64 rows, so that a thread gets eight neighbours of a row: wave
+// (wm, wn) of 2 x 2 puts blocks (2 p + h, j), of 16 x 16 (lane l holds row
+// l % 16, columns 4 (l / 16) to + 3).  16-byte pieces of a row are XORed with
+// the row, so that the 16 rows of a write fall on different banks.
+//
+// `work(rows)` is called once a pass; rows(f) calls f(v, x, y, row, n) for each
+// of the thread's rows: eight sums, and the numbers beside them in `beside` and
+// `residual` (neither is read if NULL).  All of a pass's loads are issued
+// before its sums are put, so that a row does not wait for its own (a load a
+// row cost 20 us a tile of 256 x 256).
+template <bool BF16, int W, class Work>
+__device__ __forceinline__ void rows_out(const LinearArgs &a, const LinTile &x, const f32x4_v (&acc)[W][W], char *lds,
+                                         const void *beside, int64_t beside_at, int64_t beside_ld, const void *residual,
+                                         int64_t residual_at, int64_t residual_ld, Work work) {
+  constexpr int BT = 32 * W, CH = BT / 8, STEP = LIN_THREADS / CH, ROWS = 64 / STEP;
   float *stg = reinterpret_cast<float *>(lds);
   const int tid = threadIdx.x, wave = tid >> 6, lr = tid & 15, lg = tid >> 4 & 3, wm = wave >> 1, wn = wave & 1;
-  const int64_t col = x.col0 + (tid % CH) * 8;
+  const int c = tid % CH;
+  const int64_t col = x.col0 + c * 8;
   const int n = (int)lesser(8, a.N - col);
-  const int64_t rows_all = a.mode == LIN_WEIGHT ? a.M * a.groups : a.M;
-  float *part = nullptr;
-  if (a.splits > 1) part = a.partial + ((int64_t)x.split * rows_all + (a.mode == LIN_WEIGHT ? x.group * a.M : 0)) * a.N;
 #pragma unroll 1
   for (int p = 0; p < W / 2; ++p) {
+    Raw8<BF16> br[ROWS], rr[ROWS];
+    const int t0 = p * 32 + tid / CH;  // row q is t0 + STEP q, or from 32 on in the tile's other half
+    auto tile_row = [&](int q) {
+      const int r = STEP * q;
+      return t0 + (r >> 5) * (BT / 2) + (r & 31);
+    };
+    if (n == 8) {
+#pragma unroll
+      for (int q = 0; q < ROWS; ++q) {
+        const int64_t row = tile_row(q);
+        if (row < x.rows) {
+          if (beside) br[q].load(beside, beside_at + row * beside_ld);
+          if (residual) rr[q].load(residual, residual_at + row * residual_ld);
+        }
+      }
+    }
     __syncthreads();
 #pragma unroll
     for (int pp = 0; pp < W / 2; ++pp)
@@ -387,21 +428,112 @@ __device__ __forceinline__ void finish_tile(const LinearArgs &a, const LinTile &
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int j = 0; j < W; ++j)
-            *reinterpret_cast<f32x4_v *>(stg + (wm * 32 + h * 16 + lr) * SLD + wn * (BT / 2) + j * 16 + lg * 4) = acc[2 * pp + h][j];
+          for (int j = 0; j < W; ++j) {
+            const int r = wm * 32 + h * 16 + lr;
+            *reinterpret_cast<f32x4_v *>(stg + r * BT + (((wn * (BT / 2) + j * 16) / 4 + lg) ^ (lr & 15)) * 4) = acc[2 * pp + h][j];
+          }
       }
     __syncthreads();
-#pragma unroll 2
-    for (int r = tid / CH; r < 64; r += STEP) {
-      const int tr = (r >> 5) * (BT / 2) + p * 32 + (r & 31);
-      if (tr >= x.rows || n <= 0) continue;
-      const float *src = stg + r * SLD + (tid % CH) * 8;
-      const f32x4_v lo = *reinterpret_cast<const f32x4_v *>(src), hi = *reinterpret_cast<const f32x4_v *>(src + 4);
-      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      if (part) store8<false>(part, (x.row0 + tr) * a.N + col, n, v);
-      else finish8<BF16>(a, x.group, x.row0 + tr, col, n, v);
-    }
+    work([&](auto f_row) __attribute__((always_inline)) {
+#pragma unroll
+      for (int q = 0; q < ROWS; ++q) {
+        const int r = tid / CH + STEP * q, tr = tile_row(q);
+        if (tr >= x.rows || n <= 0) continue;
+        const f32x4_v lo = *reinterpret_cast<const f32x4_v *>(stg + r * BT + ((2 * c) ^ (r & 15)) * 4);
+        const f32x4_v hi = *reinterpret_cast<const f32x4_v *>(stg + r * BT + ((2 * c + 1) ^ (r & 15)) * 4);
+        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}, f[8], g[8];
+        if (n == 8) {
+          if (beside) br[q].get(f);
+          if (residual) rr[q].get(g);
+        } else {
+          if (beside) load8<BF16>(beside, beside_at + tr * beside_ld, n, f);
+          if (residual) load8<BF16>(residual, residual_at + tr * residual_ld, n, g);
+        }
+        f_row(v, f, g, tr, n);
+      }
+    });
   }
+}
+
+// Calls f with the activation as a constant.
+template <class F>
+__device__ __forceinline__ void with_activation(int32_t act, F f) {
+  switch (act) {
+    case ACT_RELU: f(std::integral_constant<int, ACT_RELU>()); break;
+    case ACT_SILU: f(std::integral_constant<int, ACT_SILU>()); break;
+    case ACT_GELU: f(std::integral_constant<int, ACT_GELU>()); break;
+    case ACT_GELU_TANH: f(std::integral_constant<int, ACT_GELU_TANH>()); break;
+    default: f(std::integral_constant<int, ACT_NONE>()); break;
+  }
+}
+
+// The way of a whole tile.  WEIGHT: of LIN_WEIGHT; PARTS: of a launch that may
+// be cut along K.
+template <bool BF16, int W, bool WEIGHT, bool PARTS>
+__device__ __forceinline__ void finish_tile(const LinearArgs &a, const LinTile &x, const f32x4_v (&acc)[W][W], char *lds) {
+  constexpr int BT = 32 * W, CH = BT / 8;
+#define MUON_ROW [&](float *v, float *f, float *g, int tr, int n) __attribute__((always_inline))
+#define MUON_ALL [&](auto rows) __attribute__((always_inline))
+  const int64_t col = x.col0 + (threadIdx.x % CH) * 8;
+  if (PARTS && a.splits > 1) {
+    const int64_t all = WEIGHT ? a.M * a.groups : a.M;
+    float *part = a.partial + ((int64_t)x.split * all + (WEIGHT ? x.group * a.M : 0) + x.row0) * a.N + col;
+    rows_out<false, W>(a, x, acc, lds, nullptr, 0, 0, nullptr, 0, 0, MUON_ALL {
+      rows(MUON_ROW { store8<false>(part, tr * a.N, n, v); });
+    });
+  } else if constexpr (WEIGHT) {
+    const int64_t at = x.group * a.out_stride + x.row0 * a.out_ld + col;
+    rows_out<false, W>(a, x, acc, lds, nullptr, 0, 0, a.first ? nullptr : a.out, at, a.out_ld, MUON_ALL {
+      rows(MUON_ROW {
+        if (!a.first) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += g[i];
+        }
+        store8<false>(a.out, at + tr * a.out_ld, n, v);
+      });
+    });
+  } else {
+    const bool forward = a.mode == LIN_FORWARD;
+    const int64_t out_at = x.row0 * a.out_ld + col, pre_at = x.row0 * a.pre_ld + col, res_at = x.row0 * a.res_ld + col;
+    const int n = (int)lesser(8, a.N - col);
+    float bias[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) bias[i] = 0.f;
+    if (forward && a.bias && n > 0) load8<BF16>(a.bias, x.group * a.N + col, n, bias);
+    const void *pre = forward || a.act == ACT_NONE ? nullptr : a.pre;
+    rows_out<BF16, W>(a, x, acc, lds, pre, pre_at, a.pre_ld, a.residual, res_at, a.res_ld, MUON_ALL {
+      with_activation(a.act, [&](auto act) __attribute__((always_inline)) {
+        constexpr int ACT = decltype(act)::value;
+        auto last = MUON_ROW {
+          if (a.residual) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += g[i];
+          }
+          store8<BF16>(a.out, out_at + tr * a.out_ld, n, v);
+        };
+        if (forward) {
+          rows(MUON_ROW {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += bias[i];
+            if (a.pre) store8<BF16>(a.pre, pre_at + tr * a.pre_ld, n, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = activate<BF16>(ACT, v[i]);
+            last(v, f, g, tr, n);
+          });
+        } else {
+          rows(MUON_ROW {
+            if constexpr (ACT != ACT_NONE) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] *= slope<BF16>(ACT, f[i]);
+            }
+            last(v, f, g, tr, n);
+          });
+        }
+      });
+    });
+  }
+#undef MUON_ROW
+#undef MUON_ALL
 }
 
 }  // namespace dev

@@ -61,8 +61,8 @@ __global__ __launch_bounds__(LIN_THREADS, 2) void kl_linear128(LinearArgs a) {
     const int64_t k = x.k0 + (int64_t)kt * KS;
     char *la = lds + st * 2 * OPB, *lb = la + OPB;
     if constexpr (DMA) {
-      const auto ars = oa.rsrc(k);
-      const auto brs = ob.rsrc(k);
+      const auto ars = OA::rsrc(oa.first(k), oa.bytes(k));
+      const auto brs = OB::rsrc(ob.first(k), ob.bytes(k));
 #pragma unroll
       for (int j = 0; j < L; ++j) {
         OA::dma(ars, oa.left(k), offa[j], la, j);
@@ -125,7 +125,8 @@ __global__ __launch_bounds__(LIN_THREADS, 2) void kl_linear128(LinearArgs a) {
     }
     if (kt + 1 < nk) land(st ^ 1);
   }
-  finish_tile<BF16, 4, AX, true>(a, x, acc, lds);
+  if constexpr (DMA) finish_aligned<BF16, 4, AX, true>(a, x, acc, (int)threadIdx.x);
+  else finish_any<BF16, 4, AX>(a, x, acc, (int)threadIdx.x);
 }
 
 // Group of a row, by bisection; -1 for a row of none.
@@ -285,7 +286,10 @@ size_t linear_partial_bytes(int64_t M, int64_t N, int64_t K, int32_t groups, boo
 hipError_t launch_linear(LinearArgs a, bool bf16, int la, int lb, hipStream_t s) {
   const int e = bf16 ? 2 : 4;
   const bool ax = la == LIN_K_ACROSS, bx = lb == LIN_K_ACROSS, weight = a.mode == LIN_WEIGHT;
-  const bool dma = aligned(a.a, a.lda, ax ? a.M : a.K, 0, e) && aligned(a.b, a.ldb, bx ? a.N : a.K, a.groups > 1 ? a.bstride : 0, e);
+  const int eo = weight ? 4 : e;
+  const bool dma = aligned(a.a, a.lda, ax ? a.M : a.K, 0, e) && aligned(a.b, a.ldb, bx ? a.N : a.K, a.groups > 1 ? a.bstride : 0, e) &&
+                   a.N % 8 == 0 && aligned(a.out, a.out_ld, 0, a.groups > 1 ? a.out_stride : 0, eo) &&
+                   (!a.pre || aligned(a.pre, a.pre_ld, 0, 0, e)) && (!a.residual || aligned(a.residual, a.res_ld, 0, 0, e));
   if (bf16 && dma && large_tiles(a, weight)) {
     a.splits = 1;
     a.tiles_m = (int32_t)tiles_along(a.M, a.groups, !weight && a.offsets.p, 256);

@@ -25,22 +25,25 @@ namespace {
 constexpr int BT = 256;
 constexpr int OPB = BT * STAGE_BYTES;  // 32 KB an operand and stage
 
-// c += b' a with the sums tied in place: left to itself the compiler rotates
-// the 64 blocks through copies.  It does not see the latency of an asm
-// product, so the last one of every block (the tile's final k-step, LAST) goes
-// through the builtin, and nothing but the next k-step's products, 64
-// instructions later, reads an asm one.
-template <bool LAST>
+enum Kind { FIRST, MIDDLE, LAST };
+
+// c (+)= b' a with the sums tied in place: left to itself the compiler rotates
+// the 64 blocks through copies.  The first product of a block takes no sums.
+// The compiler does not see the latency of an asm product, so the last one of
+// every block goes through the builtin, and nothing but the next k-step's
+// products, 64 instructions later, reads an asm one.
+template <Kind KIND>
 __device__ __forceinline__ void mfma(f32x4_v &c, const bf16x8_v &b, const bf16x8_v &a) {
-  if constexpr (LAST) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
+  if constexpr (KIND == FIRST) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, 0" : "=a"(c) : "v"(b), "v"(a));
+  else if constexpr (KIND == LAST) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
   else asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
 }
 
 __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * OPB];
 
-// A workgroup takes tiles `stride` apart.  With several, the first stage of the
-// next tile is loaded while the last ones of this tile are multiplied, and
-// waits in one stage buffer while the sums leave through the other.
+// A workgroup takes tiles `stride` apart, whose stages form one sequence: the
+// next tile's first two are loaded while this tile's last two are multiplied
+// and wait in LDS while its sums leave.
 template <bool AX, bool BX>
 __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int tiles, int stride) {
   typedef Operand<true, BT, AX> OA;
@@ -60,41 +63,51 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
     offa[j] = OA{nullptr, a.lda, 0, 0}.offset(j);
     offb[j] = OB{nullptr, a.ldb, 0, 0}.offset(j);
   }
+  // The stage to be loaded next.
+  struct Cursor {
+    const char *a, *b;
+    int64_t a_bytes, b_bytes, left;
+  };
+  auto start = [&](const LinTile &y) {
+    const OA oa{static_cast<const T *>(a.a) + (AX ? y.row0 : y.row0 * a.lda), a.lda, y.rows, y.k1};
+    const OB ob{static_cast<const T *>(a.b) + y.group * a.bstride + (BX ? y.col0 : y.col0 * a.ldb), a.ldb,
+                (int)lesser(BT, a.N - y.col0), y.k1};
+    return Cursor{oa.first(y.k0), ob.first(y.k0), oa.bytes(y.k0), ob.bytes(y.k0), y.k1 - y.k0};
+  };
   struct Stage {
     __amdgpu_buffer_rsrc_t a, b;
     int left;
   };
-  auto stage_of = [&](const LinTile &y, int kt) {
-    const int64_t k = y.k0 + (int64_t)kt * KS;
-    const OA oa{static_cast<const T *>(a.a) + (AX ? y.row0 : y.row0 * a.lda), a.lda, y.rows, y.k1};
-    const OB ob{static_cast<const T *>(a.b) + y.group * a.bstride + (BX ? y.col0 : y.col0 * a.ldb), a.ldb,
-                (int)lesser(BT, a.N - y.col0), y.k1};
-    return Stage{oa.rsrc(k), ob.rsrc(k), oa.left(k)};
+  // The cursor's stage; behind a tile's last one a range of nothing, whose loads are zeros.
+  auto take = [&](Cursor &c) {
+    const bool any = c.left > 0;
+    const Stage s{OA::rsrc(c.a, any ? c.a_bytes : 0), OB::rsrc(c.b, any ? c.b_bytes : 0), (int)lesser(c.left, KS)};
+    c.a += OA::step(a.lda);
+    c.b += OB::step(a.ldb);
+    c.a_bytes -= OA::step(a.lda);
+    c.b_bytes -= OB::step(a.ldb);
+    c.left -= KS;
+    return s;
   };
   auto dma1 = [&](const Stage &s, int st, int q) {
     char *la = lds + st * 2 * OPB;
     if (q < 8) OA::dma(s.a, s.left, offa[q], la, q);
     else OB::dma(s.b, s.left, offb[q - 8], la + OPB, q - 8);
   };
-  auto dma_all = [&](const Stage &s, int st) {
-#pragma unroll
-    for (int q = 0; q < 16; ++q) dma1(s, st, q);
-  };
+  Cursor at = start(x);
   int base = 0;        // buffer of the tile's first stage
-  bool ready = false;  // whose loads are under way
-  bool full = false;   // the tile before was whole, so that every thread's last eight accesses are its stores
+  bool ready = false;  // whose loads, and the second one's, are under way
+  bool full = false;   // the tile before was whole: every thread has stored 32 times since
   for (;;) {
     int tn = t + stride;
     LinTile y;
     while (tn < tiles && !find_tile<BT>(a, tn, KS, y)) tn += stride;
-    const bool next = tn < tiles && y.k1 > y.k0;
+    Cursor then = tn < tiles ? start(y) : at;
+    // at least two stages: what is behind the last one is zeros
+    const int nk = (int)greater(2, (x.k1 - x.k0 + KS - 1) / KS);
+    const bool chain = tn < tiles;
     f32x4_v acc[8][8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[i][j] = f32x4_v{0.f, 0.f, 0.f, 0.f};
-    const int nk = (int)((x.k1 - x.k0 + KS - 1) / KS);
-    if (nk > 0) {
+    {
       bf16x8_v fa[2][8], fb[2][8];
       // fragment q of a k-step, in the order its products need them: A0, B0..B7, A1..A7
       auto read1 = [&](int set, int st, int ks, int q) {
@@ -106,50 +119,54 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
           fb[set][q - 1] = read_fragment<BT, BX>(lb, wn * 128 + (q - 1) * 16, ks);
         }
       };
-      if (!ready) dma_all(stage_of(x, 0), base);
-      if (ready && full) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
-      else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      // the second stage, or of a tile of one stage the next tile's first
-      if (nk > 1) dma_all(stage_of(x, 1), base ^ 1);
-      else if (next) dma_all(stage_of(y, 0), base ^ 1);
+      if (!ready) {
+        const Stage s0 = take(at);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) dma1(s0, base, q);
+        const Stage s1 = take(at);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) dma1(s1, base ^ 1, q);
+      }
+      // all but the second stage's 16 loads, and 32 stores
+      if (ready && full) asm volatile("s_waitcnt vmcnt(48)\n\ts_barrier" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(16)\n\ts_barrier" ::: "memory");
 #pragma unroll
       for (int q = 0; q < 16; ++q) read1(0, base, 0, q);
       constexpr int kBar1 = 9;           // group of k-step 0 that ends with the first barrier
       constexpr int kDma0 = 15 - kBar1;  // loads in k-step 0
       constexpr int kDma1 = 16 - kDma0;  // in k-step 1
-      static_assert(kDma0 == 6, "the vmcnt immediate of the second barrier");
-      auto body = [&](int kt, auto load, auto last) {
-        constexpr bool LOAD = decltype(load)::value;
-        constexpr bool LAST = decltype(last)::value;
+      static_assert(kDma0 == 6, "the vmcnt immediates of the second barrier");
+      auto body = [&](int kt, auto kind) {
+        constexpr Kind KIND = decltype(kind)::value;
         const int st = (kt ^ base) & 1;
-        Stage nn;
-        if constexpr (LOAD) nn = kt + 2 < nk ? stage_of(x, kt + 2) : stage_of(y, 0);
+        if (chain && kt == nk - 2) at = then;
+        const Stage nn = take(at);
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
           const int i = n >> 1, j = (n & 1) * 4;
 #pragma unroll
-          for (int jj = 0; jj < 4; ++jj) mfma<false>(acc[i][j + jj], fb[0][j + jj], fa[0][i]);
+          for (int jj = 0; jj < 4; ++jj) mfma<KIND == FIRST ? FIRST : MIDDLE>(acc[i][j + jj], fb[0][j + jj], fa[0][i]);
           __builtin_amdgcn_sched_barrier(0);
           if (n < 8) {
             read1(1, st, 1, 2 * n);
             read1(1, st, 1, 2 * n + 1);
           }
-          if (!LAST && n == kBar1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-          if constexpr (LOAD) {
-            if (n > kBar1) dma1(nn, st, n - kBar1 - 1);
-          }
+          if (n == kBar1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          if (n > kBar1) dma1(nn, st, n - kBar1 - 1);
           __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (LOAD) asm volatile("s_waitcnt vmcnt(6)\n\ts_barrier" ::: "memory");
-        else if constexpr (!LAST) asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+        if constexpr (KIND != LAST) {
+          // the next stage's loads: all but the six since, and after a whole tile its 32 stores
+          if (KIND == FIRST && ready && full) asm volatile("s_waitcnt vmcnt(38)\n\ts_barrier" ::: "memory");
+          else asm volatile("s_waitcnt vmcnt(6)\n\ts_barrier" ::: "memory");
+        }
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
           const int i = n >> 1, j = (n & 1) * 4;
 #pragma unroll
-          for (int jj = 0; jj < 4; ++jj) mfma<LAST>(acc[i][j + jj], fb[1][j + jj], fa[1][i]);
+          for (int jj = 0; jj < 4; ++jj) mfma<KIND == LAST ? LAST : MIDDLE>(acc[i][j + jj], fb[1][j + jj], fa[1][i]);
           __builtin_amdgcn_sched_barrier(0);
-          if constexpr (!LAST) {
+          if constexpr (KIND != LAST) {
             if (n < 4) {
               read1(0, st ^ 1, 0, 2 * n);
               read1(0, st ^ 1, 0, 2 * n + 1);
@@ -157,26 +174,28 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
               read1(0, st ^ 1, 0, n + 4);
             }
           }
-          if constexpr (LOAD) {
-            // the q-th of the last kDma1 loads in the group where n kDma1 / 16 steps up
-            if (((n + 1) * kDma1) / 16 > (n * kDma1) / 16) dma1(nn, st, kDma0 + (n * kDma1) / 16);
-          }
+          // the q-th of the last kDma1 loads in the group where n kDma1 / 16 steps up
+          if (((n + 1) * kDma1) / 16 > (n * kDma1) / 16) dma1(nn, st, kDma0 + (n * kDma1) / 16);
           __builtin_amdgcn_sched_barrier(0);
         }
       };
-      constexpr std::true_type yes{};
-      constexpr std::false_type no{};
-      int kt = 0;
-      for (const int end = next ? nk - 1 : nk - 2; kt < end; ++kt) body(kt, yes, no);
-      if (kt == nk - 2) {
-        body(kt, no, no);
-        ++kt;
-      }
-      body(kt, no, yes);
+      body(0, std::integral_constant<Kind, FIRST>());
+      for (int kt = 1; kt < nk - 1; ++kt) body(kt, std::integral_constant<Kind, MIDDLE>());
+      body(nk - 1, std::integral_constant<Kind, LAST>());
+      // the loads of zeros behind the last tile must not outlive the workgroup
+      if (!chain) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
-    finish_tile<true, 8, AX, false>(a, x, acc, lds + ((nk - 1 + base) & 1) * 2 * OPB);
+    // What the sums' way needs is read and computed here, tile by tile: kept
+    // over the products it does not fit the registers.
+    typedef __attribute__((address_space(4))) const LinearArgs KernelArgs;
+    KernelArgs *args = (KernelArgs *)__builtin_amdgcn_kernarg_segment_ptr();  // the first argument
+    int tid = (int)threadIdx.x;
+    asm volatile("" : "+s"(args), "+v"(tid));
+    LinearArgs b;
+    __builtin_memcpy(&b, (const void *)args, sizeof b);
+    finish_aligned<true, 8, AX, false>(b, x, acc, tid);
     if (tn >= tiles) return;
-    ready = next && nk > 0;
+    ready = chain;
     full = x.rows == BT && a.N - x.col0 >= BT;
     base = (nk + base) & 1;
     x = y;

@@ -214,14 +214,19 @@ struct Operand {
   // 32-bit byte offset of load j from the stage's first element
   __device__ __forceinline__ uint32_t offset(int j) const { return (uint32_t)(row(j) * ld * E) + chunk(j) * 16; }
 
-  // A descriptor whose range ends with the operand's last element: what lies
-  // behind it (rows of the tile or k that do not exist) loads as 0.
-  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(int64_t k) const {
-    const T *base = p + (ACROSS ? k * ld : k);
-    const int64_t bytes = ACROSS ? ((k1 - k - 1) * ld + extent) * E : ((int64_t)(extent - 1) * ld + (k1 - k)) * E;
+  // The operand's first element of k, and the bytes from there to its last one.
+  __device__ __forceinline__ const char *first(int64_t k) const { return reinterpret_cast<const char *>(p + (ACROSS ? k * ld : k)); }
+  __device__ __forceinline__ int64_t bytes(int64_t k) const {
+    return k >= k1 ? 0 : ACROSS ? ((k1 - k - 1) * ld + extent) * E : ((int64_t)(extent - 1) * ld + (k1 - k)) * E;
+  }
+  // From a stage's first element to the next one's.
+  static __device__ __forceinline__ int64_t step(int64_t ld) { return ACROSS ? KS * ld * E : STAGE_BYTES; }
+  // A descriptor of a stage, whose range ends with the operand's last element:
+  // what lies behind it (rows of the tile or k that do not exist) loads as 0.
+  static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const char *base, int64_t bytes) {
     const uint64_t v = reinterpret_cast<uint64_t>(base);
     const uint64_t b = (uint64_t)uni32((int)(v >> 32)) << 32 | (uint32_t)uni32((int)v);
-    const int limit = uni32((int)lesser(bytes, 0x7fffffff));
+    const int limit = uni32((int)(bytes < 0 ? 0 : lesser(bytes, 0x7fffffff)));
     return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(b), (short)0, limit, 0x00020000);
   }
   // Load j of a stage, into LDS; left: k from its first one on that exist, or more than a stage has.
@@ -382,77 +387,42 @@ struct Raw8 {
   }
 };
 
-// A tile's accumulators, as `at(p, h, j)` gives them, leave through LDS in
-// passes of 64 rows, so that a thread gets eight neighbours of a row: wave
-// (wm, wn) of 2 x 2 puts blocks (2 p + h, j), of 16 x 16 (lane l holds row
-// l % 16, columns 4 (l / 16) to + 3).  16-byte pieces of a row are XORed with
-// the row, so that the 16 rows of a write fall on different banks.
-//
-// `work(rows)` is called once a pass; rows(f) calls f(v, x, y, row, n) for each
-// of the thread's rows: eight sums, and the numbers beside them in `beside` and
-// `residual` (neither is read if NULL).  All of a pass's loads are issued
-// before its sums are put, so that a row does not wait for its own (a load a
-// row cost 20 us a tile of 256 x 256).
-template <bool BF16, int W, class Work>
-__device__ __forceinline__ void rows_out(const LinearArgs &a, const LinTile &x, const f32x4_v (&acc)[W][W], char *lds,
-                                         const void *beside, int64_t beside_at, int64_t beside_ld, const void *residual,
-                                         int64_t residual_at, int64_t residual_ld, Work work) {
-  constexpr int BT = 32 * W, CH = BT / 8, STEP = LIN_THREADS / CH, ROWS = 64 / STEP;
-  float *stg = reinterpret_cast<float *>(lds);
-  const int tid = threadIdx.x, wave = tid >> 6, lr = tid & 15, lg = tid >> 4 & 3, wm = wave >> 1, wn = wave & 1;
-  const int c = tid % CH;
-  const int64_t col = x.col0 + c * 8;
-  const int n = (int)lesser(8, a.N - col);
-#pragma unroll 1
-  for (int p = 0; p < W / 2; ++p) {
-    Raw8<BF16> br[ROWS], rr[ROWS];
-    const int t0 = p * 32 + tid / CH;  // row q is t0 + STEP q, or from 32 on in the tile's other half
-    auto tile_row = [&](int q) {
-      const int r = STEP * q;
-      return t0 + (r >> 5) * (BT / 2) + (r & 31);
-    };
-    if (n == 8) {
+// A tile's sums on their way to memory.  Wave (wm, wn) of 2 x 2 holds W x W
+// blocks of 16 x 16, lane l of a block row l % 16, columns 4 (l / 16) to + 3.
+// Two neighbouring blocks exchange quads between lanes 16 apart
+// (v_permlane16_swap), after which a lane has eight neighbours of its row: of
+// the first block where l / 16 is even, of the second one where it is odd.
+
+// Column of the tile that a lane's eight of the first pair of blocks begin at;
+// the next pairs' are 32 apart.
+template <int W>
+__device__ __forceinline__ int pair_column(int tid) {
+  const int lg = tid >> 4 & 3, wn = tid >> 6 & 1;
+  return wn * (16 * W) + (lg & 1) * 16 + (lg >> 1) * 8;
+}
+
+// Row i of blocks, as a lane's eights.
+template <int W>
+__device__ __forceinline__ void take_row(const f32x4_v (&acc)[W][W], int i, float (&v)[W / 2][8]) {
+  f32x4_v q[W];
 #pragma unroll
-      for (int q = 0; q < ROWS; ++q) {
-        const int64_t row = tile_row(q);
-        if (row < x.rows) {
-          if (beside) br[q].load(beside, beside_at + row * beside_ld);
-          if (residual) rr[q].load(residual, residual_at + row * residual_ld);
-        }
+  for (int ii = 0; ii < W; ++ii)
+    if (i == ii) {
+      // (the asm keeps the branches apart: merged, they would index the sums in memory)
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        q[j] = acc[ii][j];
+        asm volatile("" : "+v"(q[j]));
       }
     }
-    __syncthreads();
 #pragma unroll
-    for (int pp = 0; pp < W / 2; ++pp)
-      if (p == pp) {
+  for (int jj = 0; jj < W / 2; ++jj)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < W; ++j) {
-            const int r = wm * 32 + h * 16 + lr;
-            *reinterpret_cast<f32x4_v *>(stg + r * BT + (((wn * (BT / 2) + j * 16) / 4 + lg) ^ (lr & 15)) * 4) = acc[2 * pp + h][j];
-          }
-      }
-    __syncthreads();
-    work([&](auto f_row) __attribute__((always_inline)) {
-#pragma unroll
-      for (int q = 0; q < ROWS; ++q) {
-        const int r = tid / CH + STEP * q, tr = tile_row(q);
-        if (tr >= x.rows || n <= 0) continue;
-        const f32x4_v lo = *reinterpret_cast<const f32x4_v *>(stg + r * BT + ((2 * c) ^ (r & 15)) * 4);
-        const f32x4_v hi = *reinterpret_cast<const f32x4_v *>(stg + r * BT + ((2 * c + 1) ^ (r & 15)) * 4);
-        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}, f[8], g[8];
-        if (n == 8) {
-          if (beside) br[q].get(f);
-          if (residual) rr[q].get(g);
-        } else {
-          if (beside) load8<BF16>(beside, beside_at + tr * beside_ld, n, f);
-          if (residual) load8<BF16>(residual, residual_at + tr * residual_ld, n, g);
-        }
-        f_row(v, f, g, tr, n);
-      }
-    });
-  }
+    for (int e = 0; e < 4; ++e) {
+      const auto two = __builtin_amdgcn_permlane16_swap(__float_as_uint(q[2 * jj][e]), __float_as_uint(q[2 * jj + 1][e]), false, false);
+      v[jj][e] = __uint_as_float(two[0]);
+      v[jj][4 + e] = __uint_as_float(two[1]);
+    }
 }
 
 // Calls f with the activation as a constant.
@@ -467,73 +437,185 @@ __device__ __forceinline__ void with_activation(int32_t act, F f) {
   }
 }
 
-// The way of a whole tile.  WEIGHT: of LIN_WEIGHT; PARTS: of a launch that may
-// be cut along K.
+// A matrix beside the sums, rows of blocks at a time, as buffer accesses: a
+// range that ends with the tile's last element leaves out the rows that do not
+// exist, and columns that do not are given an offset outside it, so that no
+// lane branches.  One wave's half of the tile.
+template <bool BF16, int W>
+struct TileRows {
+  static constexpr int E = BF16 ? 2 : 4, P = W / 2;
+  const char *base;
+  int64_t step;  // bytes of 16 rows
+  int64_t range;
+  uint32_t off[P];
+
+  __device__ __forceinline__ void init(const void *p, int64_t at, int64_t ld, const LinTile &x, int64_t cols, int tid) {
+    const int half = uni32(tid >> 7) * (16 * W), column = pair_column<W>(tid);
+    base = static_cast<const char *>(p) + (at + (x.row0 + half) * ld + x.col0) * E;
+    step = 16 * ld * E;
+    range = ((int64_t)(x.rows - half - 1) * ld + (cols - x.col0)) * E;
+    if (x.rows <= half) range = 0;
+#pragma unroll
+    for (int jj = 0; jj < P; ++jj)
+      off[jj] = x.col0 + column + 32 * jj < cols ? (uint32_t)(((tid & 15) * ld + column + 32 * jj) * E) : 0x80000000u;
+  }
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc() const { return Operand<BF16, 32 * W, false>::rsrc(base, range); }
+  __device__ __forceinline__ void next() {
+    base += step;
+    range -= step;
+  }
+  __device__ __forceinline__ void load(Raw8<BF16> (&r)[P]) const {
+    const auto rs = rsrc();
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int jj = 0; jj < P; ++jj)
+#pragma unroll
+      for (int h = 0; h < E / 2; ++h) {
+        const u32x4 w = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off[jj] + 16 * h, 0, 0));
+        r[jj].v[h] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+  }
+  __device__ __forceinline__ void store(const float (&v)[P][8]) const {
+    const auto rs = rsrc();
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int jj = 0; jj < P; ++jj)
+#pragma unroll
+      for (int h = 0; h < E / 2; ++h) {
+        const uint4 w = Elem<BF16>::pack(v[jj] + h * Elem<BF16>::N);
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{w.x, w.y, w.z, w.w}, rs, off[jj] + 16 * h, 0, 0);
+      }
+  }
+};
+
+// The way of a whole tile whose matrices keep 16-byte alignment, with a
+// multiple of 8 columns.  WEIGHT: of LIN_WEIGHT; PARTS: of a launch that may be
+// cut along K.  What is read beside the sums goes out a row of blocks ahead.
 template <bool BF16, int W, bool WEIGHT, bool PARTS>
-__device__ __forceinline__ void finish_tile(const LinearArgs &a, const LinTile &x, const f32x4_v (&acc)[W][W], char *lds) {
-  constexpr int BT = 32 * W, CH = BT / 8;
-#define MUON_ROW [&](float *v, float *f, float *g, int tr, int n) __attribute__((always_inline))
-#define MUON_ALL [&](auto rows) __attribute__((always_inline))
-  const int64_t col = x.col0 + (threadIdx.x % CH) * 8;
+__device__ __forceinline__ void finish_aligned(const LinearArgs &a, const LinTile &x, const f32x4_v (&acc)[W][W], int tid) {
+  constexpr int P = W / 2;
   if (PARTS && a.splits > 1) {
     const int64_t all = WEIGHT ? a.M * a.groups : a.M;
-    float *part = a.partial + ((int64_t)x.split * all + (WEIGHT ? x.group * a.M : 0) + x.row0) * a.N + col;
-    rows_out<false, W>(a, x, acc, lds, nullptr, 0, 0, nullptr, 0, 0, MUON_ALL {
-      rows(MUON_ROW { store8<false>(part, tr * a.N, n, v); });
-    });
+    TileRows<false, W> out;
+    out.init(a.partial, ((int64_t)x.split * all + (WEIGHT ? x.group * a.M : 0)) * a.N, a.N, x, a.N, tid);
+#pragma unroll 1
+    for (int i = 0; i < W; ++i) {
+      float v[P][8];
+      take_row(acc, i, v);
+      out.store(v);
+      out.next();
+    }
   } else if constexpr (WEIGHT) {
-    const int64_t at = x.group * a.out_stride + x.row0 * a.out_ld + col;
-    rows_out<false, W>(a, x, acc, lds, nullptr, 0, 0, a.first ? nullptr : a.out, at, a.out_ld, MUON_ALL {
-      rows(MUON_ROW {
-        if (!a.first) {
+    TileRows<false, W> out, old;
+    Raw8<false> r[P];
+    out.init(a.out, x.group * a.out_stride, a.out_ld, x, a.N, tid);
+    old = out;
+    if (!a.first) old.load(r);
+#pragma unroll 1
+    for (int i = 0; i < W; ++i) {
+      float v[P][8];
+      take_row(acc, i, v);
+      if (!a.first) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += g[i];
+        for (int jj = 0; jj < P; ++jj) {
+          float f[8];
+          r[jj].get(f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[jj][e] += f[e];
         }
-        store8<false>(a.out, at + tr * a.out_ld, n, v);
-      });
-    });
+        old.next();
+        old.load(r);  // behind the last row: nothing
+      }
+      out.store(v);
+      out.next();
+    }
   } else {
-    const bool forward = a.mode == LIN_FORWARD;
-    const int64_t out_at = x.row0 * a.out_ld + col, pre_at = x.row0 * a.pre_ld + col, res_at = x.row0 * a.res_ld + col;
-    const int n = (int)lesser(8, a.N - col);
-    float bias[8];
+    const bool forward = a.mode == LIN_FORWARD, biased = forward && a.bias, kept = forward && a.pre;
+    const bool sloped = !forward && a.act != ACT_NONE;
+    TileRows<BF16, W> out, pre, res;
+    Raw8<BF16> bias[P], br[P], rr[P];
+    out.init(a.out, 0, a.out_ld, x, a.N, tid);
+    if (kept || sloped) pre.init(a.pre, 0, a.pre_ld, x, a.N, tid);
+    if (a.residual) res.init(a.residual, 0, a.res_ld, x, a.N, tid);
+    if (biased) {
+      const int64_t col = x.col0 + pair_column<W>(tid);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) bias[i] = 0.f;
-    if (forward && a.bias && n > 0) load8<BF16>(a.bias, x.group * a.N + col, n, bias);
-    const void *pre = forward || a.act == ACT_NONE ? nullptr : a.pre;
-    rows_out<BF16, W>(a, x, acc, lds, pre, pre_at, a.pre_ld, a.residual, res_at, a.res_ld, MUON_ALL {
-      with_activation(a.act, [&](auto act) __attribute__((always_inline)) {
-        constexpr int ACT = decltype(act)::value;
-        auto last = MUON_ROW {
-          if (a.residual) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += g[i];
-          }
-          store8<BF16>(a.out, out_at + tr * a.out_ld, n, v);
-        };
+      for (int jj = 0; jj < P; ++jj) bias[jj].load(a.bias, x.group * a.N + lesser(col + 32 * jj, a.N - 8));
+    }
+    if (sloped) pre.load(br);
+    if (a.residual) res.load(rr);
+    with_activation(a.act, [&](auto act) __attribute__((always_inline)) {
+      constexpr int ACT = decltype(act)::value;
+#pragma unroll 1
+      for (int i = 0; i < W; ++i) {
+        float v[P][8], f[8];
+        take_row(acc, i, v);
         if (forward) {
-          rows(MUON_ROW {
+          if (biased) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += bias[i];
-            if (a.pre) store8<BF16>(a.pre, pre_at + tr * a.pre_ld, n, v);
+            for (int jj = 0; jj < P; ++jj) {
+              bias[jj].get(f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = activate<BF16>(ACT, v[i]);
-            last(v, f, g, tr, n);
-          });
-        } else {
-          rows(MUON_ROW {
-            if constexpr (ACT != ACT_NONE) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] *= slope<BF16>(ACT, f[i]);
+              for (int e = 0; e < 8; ++e) v[jj][e] += f[e];
             }
-            last(v, f, g, tr, n);
-          });
+          }
+          if (kept) {
+            pre.store(v);
+            pre.next();
+          }
+#pragma unroll
+          for (int jj = 0; jj < P; ++jj)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[jj][e] = activate<BF16>(ACT, v[jj][e]);
+        } else if constexpr (ACT != ACT_NONE) {
+#pragma unroll
+          for (int jj = 0; jj < P; ++jj) {
+            br[jj].get(f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[jj][e] *= slope<BF16>(ACT, f[e]);
+          }
+          pre.next();
+          pre.load(br);  // behind the last row: nothing
         }
-      });
+        if (a.residual) {
+#pragma unroll
+          for (int jj = 0; jj < P; ++jj) {
+            rr[jj].get(f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[jj][e] += f[e];
+          }
+          res.next();
+          res.load(rr);
+        }
+        out.store(v);
+        out.next();
+      }
     });
   }
-#undef MUON_ROW
-#undef MUON_ALL
+}
+
+// The same without assumptions.
+template <bool BF16, int W, bool WEIGHT>
+__device__ __forceinline__ void finish_any(const LinearArgs &a, const LinTile &x, const f32x4_v (&acc)[W][W], int tid) {
+  const int64_t col = x.col0 + pair_column<W>(tid);
+  float *part = nullptr;
+  if (a.splits > 1) part = a.partial + ((int64_t)x.split * (WEIGHT ? a.M * a.groups : a.M) + (WEIGHT ? x.group * a.M : 0)) * a.N;
+#pragma unroll 1
+  for (int i = 0; i < W; ++i) {
+    const int r = (tid >> 7) * (16 * W) + i * 16 + (tid & 15);
+    const int64_t row = x.row0 + r;
+    float v[W / 2][8];
+    take_row(acc, i, v);
+    if (r >= x.rows) continue;
+#pragma unroll
+    for (int jj = 0; jj < W / 2; ++jj) {
+      const int64_t c = col + 32 * jj;
+      if (c >= a.N) continue;
+      const int n = (int)lesser(8, a.N - c);
+      if (part) store8<false>(part, row * a.N + c, n, v[jj]);
+      else finish8<BF16>(a, x.group, row, c, n, v[jj]);
+    }
+  }
 }
 
 }  // namespace dev

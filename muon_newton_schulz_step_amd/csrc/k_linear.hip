@@ -1,11 +1,11 @@
 // The product with a weight matrix, or with one a group of rows, and its
-// gradients, on gfx950: 128 x 128 tiles, any size, type and alignment.
+// gradients, on gfx950: any size, type and alignment.
 //
 //   forwards       out = act(x w + bias) + residual
 //   input          dx = (dy w') act'(pre) + residual
 //   weights        dw (+)= x' dy,  dbias (+)= the sums of dy's columns
 //
-// A workgroup of 4 waves (2 x 2, each 64 x 64) walks K in stages of 128 bytes
+// A workgroup of 4 waves (2 x 2) takes a tile and walks K in stages of 128 bytes
 // a row, double buffered in LDS: with loads straight into LDS where rows keep
 // 16-byte alignment, through registers otherwise.  bf16 on
 // v_mfma_f32_16x16x32_bf16, fp32 on v_mfma_f32_16x16x4_f32, sums in fp32.
@@ -26,11 +26,11 @@ hipError_t launch_linear256(const LinearArgs &a, int tiles, bool ax, bool bx, hi
 
 namespace {
 
-constexpr int BT = 128;
-constexpr int OPB = BT * STAGE_BYTES;  // an operand's stage in LDS
-
-template <bool BF16, bool AX, bool BX, bool DMA>
-__global__ __launch_bounds__(LIN_THREADS, 2) void kl_linear128(LinearArgs a) {
+// W x W blocks of 16 x 16 a wave: tiles of 128 x 128, or of 64 x 64 where
+// larger ones would leave most of the chip idle.
+template <bool BF16, bool AX, bool BX, bool DMA, int W>
+__global__ __launch_bounds__(LIN_THREADS, 8 / W) void kl_linear(LinearArgs a) {
+  constexpr int BT = 32 * W, OPB = BT * STAGE_BYTES;  // an operand's stage in LDS
   typedef Operand<BF16, BT, AX> OA;
   typedef Operand<BF16, BT, BX> OB;
   typedef typename OA::T T;
@@ -42,11 +42,11 @@ __global__ __launch_bounds__(LIN_THREADS, 2) void kl_linear128(LinearArgs a) {
   const OB ob{static_cast<const T *>(a.b) + x.group * a.bstride + (BX ? x.col0 : x.col0 * a.ldb), a.ldb,
               (int)lesser(BT, a.N - x.col0), x.k1};
   const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
-  f32x4_v acc[4][4];
+  f32x4_v acc[W][W];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < W; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_v{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < W; ++j) acc[i][j] = f32x4_v{0.f, 0.f, 0.f, 0.f};
   const int nk = (int)((x.k1 - x.k0 + KS - 1) / KS);
   uint32_t offa[L], offb[L];
   uint4 ra[L], rb[L];
@@ -98,35 +98,35 @@ __global__ __launch_bounds__(LIN_THREADS, 2) void kl_linear128(LinearArgs a) {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       if constexpr (BF16) {
-        bf16x8_v fa[4], fb[4];
+        bf16x8_v fa[W], fb[W];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          fa[i] = read_fragment<BT, AX>(la, wm * 64 + i * 16, ks);
-          fb[i] = read_fragment<BT, BX>(lb, wn * 64 + i * 16, ks);
+        for (int i = 0; i < W; ++i) {
+          fa[i] = read_fragment<BT, AX>(la, wm * (BT / 2) + i * 16, ks);
+          fb[i] = read_fragment<BT, BX>(lb, wn * (BT / 2) + i * 16, ks);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < W; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+          for (int j = 0; j < W; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
       } else {
-        f32x4_v fa[4], fb[4];
+        f32x4_v fa[W], fb[W];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          fa[i] = read_fragment_f32<BT, AX>(la, wm * 64 + i * 16, ks);
-          fb[i] = read_fragment_f32<BT, BX>(lb, wn * 64 + i * 16, ks);
+        for (int i = 0; i < W; ++i) {
+          fa[i] = read_fragment_f32<BT, AX>(la, wm * (BT / 2) + i * 16, ks);
+          fb[i] = read_fragment_f32<BT, BX>(lb, wn * (BT / 2) + i * 16, ks);
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < W; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fb[j][c], fa[i][c], acc[i][j], 0, 0, 0);
+            for (int j = 0; j < W; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fb[j][c], fa[i][c], acc[i][j], 0, 0, 0);
       }
     }
     if (kt + 1 < nk) land(st ^ 1);
   }
-  if constexpr (DMA) finish_aligned<BF16, 4, AX, true>(a, x, acc, (int)threadIdx.x);
-  else finish_any<BF16, 4, AX>(a, x, acc, (int)threadIdx.x);
+  if constexpr (DMA) finish_aligned<BF16, W, AX, true>(a, x, acc, (int)threadIdx.x);
+  else finish_any<BF16, W, AX>(a, x, acc, (int)threadIdx.x);
 }
 
 // Group of a row, by bisection; -1 for a row of none.
@@ -249,25 +249,36 @@ bool aligned(const void *p, int64_t ld, int64_t extent, int64_t stride, int e) {
   return (uintptr_t)p % 16 == 0 && ld * e % 16 == 0 && extent * e % 16 == 0 && stride * e % 16 == 0 && ld < ((int64_t)1 << 20);
 }
 
-template <bool BF16, bool AX, bool BX>
-void go128(const LinearArgs &a, bool dma, unsigned grid, hipStream_t s) {
-  if (dma) hipLaunchKernelGGL((kl_linear128<BF16, AX, BX, true>), dim3(grid), dim3(LIN_THREADS), 0, s, a);
-  else hipLaunchKernelGGL((kl_linear128<BF16, AX, BX, false>), dim3(grid), dim3(LIN_THREADS), 0, s, a);
-}
-
 int64_t tiles_along(int64_t M, int32_t groups, bool grouped, int bt) {
   return (M + bt - 1) / bt + (grouped ? groups - 1 : 0);
 }
 
-// Parts of K: enough for two workgroups a CU, of four stages each and more,
-// as far as their sums take no more than 64 MB.
-int32_t parts_of(int64_t M, int64_t N, int64_t K, int32_t groups, bool weight) {
-  const int64_t tn = (N + BT - 1) / BT, per = weight ? groups : 1;
-  const int64_t tiles = (weight ? (M + BT - 1) / BT : std::max<int64_t>(1, (M + BT - 1) / BT)) * tn * per;
+// Tiles of 128 x 128 if they fill the chip, of 64 x 64 otherwise, and then K in
+// parts: enough for four workgroups a CU, of four stages each and more, as far
+// as their sums take no more than 64 MB.
+struct LinearPlan {
+  int w;
+  int32_t splits;
+};
+LinearPlan plan_of(int64_t M, int64_t N, int64_t K, int32_t groups, bool weight) {
+  const int64_t per = weight ? groups : 1;
+  if ((M + 127) / 128 * ((N + 127) / 128) * per >= 256) return {4, 1};
+  const int64_t tiles = (M + 63) / 64 * ((N + 63) / 64) * per;
   const int64_t stages = (K / (weight ? groups : 1) + 63) / 64;
   const int64_t bytes = std::max<int64_t>(1, M * per * N * 4);
-  int64_t parts = std::min<int64_t>({512 / std::max<int64_t>(1, tiles), stages / 4, ((int64_t)64 << 20) / bytes, 32});
-  return (int32_t)std::max<int64_t>(1, parts);
+  const int64_t parts = std::min<int64_t>({1024 / std::max<int64_t>(1, tiles), stages / 4, ((int64_t)64 << 20) / bytes, 32});
+  return {2, (int32_t)std::max<int64_t>(1, parts)};
+}
+
+template <bool BF16, bool AX, bool BX>
+void go(const LinearArgs &a, bool dma, int w, unsigned grid, hipStream_t s) {
+  if (w == 4) {
+    if (dma) hipLaunchKernelGGL((kl_linear<BF16, AX, BX, true, 4>), dim3(grid), dim3(LIN_THREADS), 0, s, a);
+    else hipLaunchKernelGGL((kl_linear<BF16, AX, BX, false, 4>), dim3(grid), dim3(LIN_THREADS), 0, s, a);
+  } else {
+    if (dma) hipLaunchKernelGGL((kl_linear<BF16, AX, BX, true, 2>), dim3(grid), dim3(LIN_THREADS), 0, s, a);
+    else hipLaunchKernelGGL((kl_linear<BF16, AX, BX, false, 2>), dim3(grid), dim3(LIN_THREADS), 0, s, a);
+  }
 }
 
 // Whether 256 x 256 tiles are many enough to fill the chip.
@@ -279,7 +290,7 @@ bool large_tiles(const LinearArgs &a, bool weight) {
 }  // namespace
 
 size_t linear_partial_bytes(int64_t M, int64_t N, int64_t K, int32_t groups, bool weight) {
-  const int32_t parts = parts_of(M, N, K, groups, weight);
+  const int32_t parts = plan_of(M, N, K, groups, weight).splits;
   return parts > 1 ? (size_t)parts * (size_t)(M * (weight ? groups : 1)) * (size_t)N * 4 : 0;
 }
 
@@ -296,19 +307,21 @@ hipError_t launch_linear(LinearArgs a, bool bf16, int la, int lb, hipStream_t s)
     a.tiles_n = (int32_t)((a.N + 255) / 256);
     return launch_linear256(a, a.tiles_m * a.tiles_n * (weight ? a.groups : 1), ax, bx, s);
   }
-  a.splits = parts_of(a.M, a.N, a.K, a.groups, weight);
-  a.tiles_m = (int32_t)tiles_along(a.M, a.groups, !weight && a.offsets.p, BT);
-  a.tiles_n = (int32_t)((a.N + BT - 1) / BT);
+  const LinearPlan p = plan_of(a.M, a.N, a.K, a.groups, weight);
+  const int bt = 32 * p.w;
+  a.splits = p.splits;
+  a.tiles_m = (int32_t)tiles_along(a.M, a.groups, !weight && a.offsets.p, bt);
+  a.tiles_n = (int32_t)((a.N + bt - 1) / bt);
   const int64_t grid = (int64_t)a.tiles_m * a.tiles_n * (weight ? a.groups : 1) * a.splits;
   const unsigned g = (unsigned)grid;
   if (bf16) {
-    if (ax) go128<true, true, true>(a, dma, g, s);
-    else if (bx) go128<true, false, true>(a, dma, g, s);
-    else go128<true, false, false>(a, dma, g, s);
+    if (ax) go<true, true, true>(a, dma, p.w, g, s);
+    else if (bx) go<true, false, true>(a, dma, p.w, g, s);
+    else go<true, false, false>(a, dma, p.w, g, s);
   } else {
-    if (ax) go128<false, true, true>(a, dma, g, s);
-    else if (bx) go128<false, false, true>(a, dma, g, s);
-    else go128<false, false, false>(a, dma, g, s);
+    if (ax) go<false, true, true>(a, dma, p.w, g, s);
+    else if (bx) go<false, false, true>(a, dma, p.w, g, s);
+    else go<false, false, false>(a, dma, p.w, g, s);
   }
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || a.splits == 1) return err;

@@ -187,9 +187,11 @@ __device__ __forceinline__ bool find_tile(const LinearArgs &a, int t, int stage_
 // with k / 4 % 4.
 
 __device__ __forceinline__ int adjacent_chunk(int r, int c) { return c ^ (r >> 1 & 7); }
-template <bool BF16>
+template <bool BF16, int BT>
 __device__ __forceinline__ int across_chunk(int k, int c) {
-  return BF16 ? c ^ ((k & 3) << 1 | (k >> 3 & 1) << 3) : c ^ (k >> 2 & 3) << 2;
+  if (!BF16) return c ^ (k >> 2 & 3) << 2;
+  // rows of 128 bytes lie two to the banks' 256
+  return BT == 64 ? c ^ ((k >> 1 & 1) << 1 | (k >> 3 & 1) << 2) : c ^ ((k & 3) << 1 | (k >> 3 & 1) << 3);
 }
 
 // One operand of a BT-wide tile as a stage's loads see it: BT / 32 loads of 16
@@ -209,7 +211,7 @@ struct Operand {
   static __device__ __forceinline__ int row(int j) { return ((threadIdx.x >> 6) * LOADS + j) * RPL + (threadIdx.x & 63) / CPR; }
   static __device__ __forceinline__ int chunk(int j) {
     const int r = row(j), c = (threadIdx.x & 63) % CPR;
-    return ACROSS ? across_chunk<BF16>(r, c) : adjacent_chunk(r, c);
+    return ACROSS ? across_chunk<BF16, BT>(r, c) : adjacent_chunk(r, c);
   }
   // 32-bit byte offset of load j from the stage's first element
   __device__ __forceinline__ uint32_t offset(int j) const { return (uint32_t)(row(j) * ld * E) + chunk(j) * 16; }
@@ -271,7 +273,7 @@ __device__ __forceinline__ bf16x8_v read_fragment(const char *lds, int at, int k
     return *reinterpret_cast<const bf16x8_v *>(lds + (at + lr) * STAGE_BYTES + adjacent_chunk(lr, 4 * ks + lg) * 16);
   } else {
     const int k = 32 * ks + 8 * lg + (lr >> 2);
-    const char *q = lds + k * (BT * 2) + across_chunk<true>(k, at >> 3) * 16 + (lr & 3) * 8;
+    const char *q = lds + k * (BT * 2) + across_chunk<true, BT>(k, at >> 3) * 16 + (lr & 3) * 8;
     union {
       i16x4_v h[2];
       bf16x8_v v;
@@ -294,7 +296,7 @@ __device__ __forceinline__ f32x4_v read_fragment_f32(const char *lds, int at, in
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int k = 16 * ks + 4 * lg + c;
-      v[c] = *reinterpret_cast<const float *>(lds + k * (BT * 4) + across_chunk<false>(k, (at + lr) >> 2) * 16 + (lr & 3) * 4);
+      v[c] = *reinterpret_cast<const float *>(lds + k * (BT * 4) + across_chunk<false, BT>(k, (at + lr) >> 2) * 16 + (lr & 3) * 4);
     }
     return v;
   }

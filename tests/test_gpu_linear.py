@@ -262,6 +262,15 @@ def test_linear_of_large_tiles(torch, rows, a, b, groups, ld, layout):
     check_linear(torch, rows, a, b, "bf16", layout, groups, ld=ld, shift=ld, act="relu" if ld else "none", pre=True, first=ld == 0)
 
 
+@pytest.mark.parametrize("layout", ["in_out", "out_in"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,a,b,groups,ld", [(2050, 40, 2064, None, 0), (2050, 137, 2063, None, 1), (2049, 2064, 72, None, 8), (2051, 2062, 33, None, 0),
+                                                (130, 2064, 2048, None, 0), (33, 2065, 2050, None, 1), (900, 504, 520, 20, 8), (900, 501, 515, 20, 0),
+                                                (2100, 72, 2064, 7, 0), (2100, 2065, 40, 7, 3)])
+def test_linear_of_middle_tiles(torch, rows, a, b, groups, ld, dtype, layout):
+    check_linear(torch, rows, a, b, dtype, layout, groups, ld=ld, shift=ld, act="relu" if ld else "none", pre=True, first=ld == 0)
+
+
 @pytest.mark.parametrize("act", ["gelu", "silu"])
 def test_linear_of_large_tiles_with_activations(torch, act):
     check_linear(torch, 3501, 200, 3600, "bf16", "in_out", act=act, pre=True, whole=False)

@@ -39,23 +39,43 @@ __device__ __forceinline__ void mfma(f32x4_v &c, const bf16x8_v &b, const bf16x8
   else asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
 }
 
-__shared__ __attribute__((aligned(1024))) char lds[2 * 2 * OPB];
+// the stages, and the next place in the queue
+__shared__ __attribute__((aligned(1024))) char lds[2 * 2 * OPB + 64];
 
-// A workgroup takes tiles `stride` apart, whose stages form one sequence: the
-// next tile's first two are loaded while this tile's last two are multiplied
-// and wait in LDS while its sums leave.
-template <bool AX, bool BX>
+// A workgroup takes several tiles, whose stages form one sequence: the next
+// tile's first two are loaded while this tile's last two are multiplied and
+// wait in LDS while its sums leave.  Tiles of equal K are taken `stride` apart;
+// those of a grouped weight gradient (QUEUE) are of very different K, and each
+// XCD's workgroups take theirs from a queue that begins with the longest
+// group's.
+template <bool AX, bool BX, bool QUEUE>
 __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int tiles, int stride) {
   typedef Operand<true, BT, AX> OA;
   typedef Operand<true, BT, BX> OB;
   typedef typename OA::T T;
   constexpr int KS = OA::KS;
   // workgroup i runs on XCD i % 8: chunks of 256 tiles, 32 consecutive ones an XCD
-  const int slot = (int)blockIdx.x >> 3;
-  int t = (slot >> 5) * 256 + ((int)blockIdx.x & 7) * 32 + (slot & 31);
+  const int xcd = (int)blockIdx.x & 7, slot = (int)blockIdx.x >> 3;
+  int t = (slot >> 5) * 256 + xcd * 32 + (slot & 31);
   LinTile x;
-  while (t < tiles && !find_tile<BT>(a, t, KS, x)) t += stride;
-  if (t >= tiles) return;
+  // of each group's tiles, an XCD's: [q0, q0 + qn)
+  const int each = a.tiles_m * a.tiles_n, q0 = xcd * ((each + 7) / 8), qn = min((each + 7) / 8, each - q0);
+  LinearQueue *queue = reinterpret_cast<LinearQueue *>(a.queue);
+  int *next_slot = reinterpret_cast<int *>(lds + 2 * 2 * OPB);
+  auto queued = [&](int place, LinTile &y) {
+    if (place >= qn * a.groups) return false;
+    const int g = place / qn;
+    weight_tile<BT>(a, uni32(queue->group[g]), q0 + place - g * qn, y);
+    y.split = 0;
+    return true;
+  };
+  if constexpr (QUEUE) {
+    if (qn <= 0 || !queued(slot, x)) return;
+    if (threadIdx.x == 0) *next_slot = atomicAdd(&queue->taken[xcd][0], 1);
+  } else {
+    while (t < tiles && !find_tile<BT>(a, t, KS, x)) t += stride;
+    if (t >= tiles) return;
+  }
   const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
   uint32_t offa[8], offb[8];
 #pragma unroll
@@ -99,13 +119,11 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
   bool ready = false;  // whose loads, and the second one's, are under way
   bool full = false;   // the tile before was whole: every thread has stored 32 times since
   for (;;) {
-    int tn = t + stride;
-    LinTile y;
-    while (tn < tiles && !find_tile<BT>(a, tn, KS, y)) tn += stride;
-    Cursor then = tn < tiles ? start(y) : at;
     // at least two stages: what is behind the last one is zeros
     const int nk = (int)greater(2, (x.k1 - x.k0 + KS - 1) / KS);
-    const bool chain = tn < tiles;
+    bool chain;
+    LinTile y;
+    int tn = 0, taken = 0;
     f32x4_v acc[8][8];
     {
       bf16x8_v fa[2][8], fb[2][8];
@@ -128,8 +146,17 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
         for (int q = 0; q < 16; ++q) dma1(s1, base ^ 1, q);
       }
       // all but the second stage's 16 loads, and 32 stores
-      if (ready && full) asm volatile("s_waitcnt vmcnt(48)\n\ts_barrier" ::: "memory");
-      else asm volatile("s_waitcnt vmcnt(16)\n\ts_barrier" ::: "memory");
+      if (ready && full) asm volatile("s_waitcnt vmcnt(48) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if constexpr (QUEUE) {
+        chain = queued(uni32(*next_slot), y);
+        if (threadIdx.x == 0 && chain) taken = atomicAdd(&queue->taken[xcd][0], 1);
+      } else {
+        tn = t + stride;
+        while (tn < tiles && !find_tile<BT>(a, tn, KS, y)) tn += stride;
+        chain = tn < tiles;
+      }
+      const Cursor then = chain ? start(y) : at;
 #pragma unroll
       for (int q = 0; q < 16; ++q) read1(0, base, 0, q);
       constexpr int kBar1 = 9;           // group of k-step 0 that ends with the first barrier
@@ -194,8 +221,11 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
     LinearArgs b;
     __builtin_memcpy(&b, (const void *)args, sizeof b);
     finish_aligned<true, 8, AX, false>(b, x, acc, tid);
-    if (tn >= tiles) return;
-    ready = chain;
+    if (!chain) return;
+    if constexpr (QUEUE) {
+      if (threadIdx.x == 0) *next_slot = taken;
+    }
+    ready = true;
     full = x.rows == BT && a.N - x.col0 >= BT;
     base = (nk + base) & 1;
     x = y;
@@ -205,15 +235,37 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
 
 }  // namespace
 
+// Sorts the groups by their rows, and clears the queues: each XCD's first 32
+// places are its workgroups' own.
+__global__ __launch_bounds__(1024) void kl_queue(LinearArgs a) {
+  __shared__ int64_t size[1024];
+  LinearQueue *queue = reinterpret_cast<LinearQueue *>(a.queue);
+  const int g = threadIdx.x;
+  int64_t mine = 0;
+  if (g < a.groups) mine = group_start(a.offsets, g + 1, a.K) - group_start(a.offsets, g, a.K);
+  size[g] = mine;
+  if (g < 8) queue->taken[g][0] = 32;
+  __syncthreads();
+  if (g >= a.groups) return;
+  int before = 0;
+  for (int h = 0; h < a.groups; ++h) before += size[h] > mine || (size[h] == mine && h < g);
+  queue->group[before] = g;
+}
+
 hipError_t launch_linear256(const LinearArgs &a, int tiles, bool ax, bool bx, hipStream_t s) {
-  // Tiles of equal K go round 256 workgroups, one a CU; a grouped weight
-  // gradient's are of very different K, and taken by whichever CU is free.
-  const bool even = a.mode != LIN_WEIGHT || !a.offsets.p;
-  const int all = (tiles + 255) / 256 * 256, stride = even ? 256 : all;
-  const dim3 grid((unsigned)stride);
-  if (ax) hipLaunchKernelGGL((kl_linear256<true, true>), grid, dim3(LIN_THREADS), 0, s, a, tiles, stride);
-  else if (bx) hipLaunchKernelGGL((kl_linear256<false, true>), grid, dim3(LIN_THREADS), 0, s, a, tiles, stride);
-  else hipLaunchKernelGGL((kl_linear256<false, false>), grid, dim3(LIN_THREADS), 0, s, a, tiles, stride);
+  if (ax && a.offsets.p) {
+    static_assert(sizeof(LinearQueue::group) / 4 == 1024, "a group a thread");
+    hipLaunchKernelGGL(kl_queue, dim3(1), dim3(1024), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((kl_linear256<true, true, true>), dim3(256), dim3(LIN_THREADS), 0, s, a, tiles, 256);
+  } else if (ax) {
+    hipLaunchKernelGGL((kl_linear256<true, true, false>), dim3(256), dim3(LIN_THREADS), 0, s, a, tiles, 256);
+  } else if (bx) {
+    hipLaunchKernelGGL((kl_linear256<false, true, false>), dim3(256), dim3(LIN_THREADS), 0, s, a, tiles, 256);
+  } else {
+    hipLaunchKernelGGL((kl_linear256<false, false, false>), dim3(256), dim3(LIN_THREADS), 0, s, a, tiles, 256);
+  }
   return hipGetLastError();
 }
 

@@ -118,14 +118,15 @@ size_t rounded(size_t n) { return (n + 255) / 256 * 256; }
 
 // Workspace of the weights' gradient.
 struct WeightGradLayout {
-  size_t columns, total;
+  size_t partial, columns, total;
 };
 WeightGradLayout weight_grad_layout(int64_t rows, int64_t in, int64_t out, int64_t groups) {
   WeightGradLayout l{};
   // either layout of dw
-  l.columns = rounded(std::max(linear_partial_bytes(in, out, rows, (int32_t)groups, true),
+  l.partial = rounded(sizeof(LinearQueue));
+  l.columns = l.partial + rounded(std::max(linear_partial_bytes(in, out, rows, (int32_t)groups, true),
                                linear_partial_bytes(out, in, rows, (int32_t)groups, true)));
-  l.total = 256 + l.columns + rounded((size_t)groups * (size_t)column_sum_splits(rows, out, (int32_t)groups) * (size_t)out * 4);
+  l.total = l.columns + rounded((size_t)groups * (size_t)column_sum_splits(rows, out, (int32_t)groups) * (size_t)out * 4);
   return l;
 }
 
@@ -489,7 +490,8 @@ muon_status muon_linear_weight_grad(const void *x, int64_t rows, int64_t in, int
     a.out_ld = dw_ld;
     a.out_stride = dw_stride;
     a.first = first != 0;
-    a.partial = static_cast<float *>(ws);
+    a.queue = static_cast<int32_t *>(ws);
+    a.partial = reinterpret_cast<float *>(static_cast<char *>(ws) + l.partial);
     hipError_t err = launch_linear(a, dtype == MUON_DT_BF16, LIN_K_ACROSS, LIN_K_ACROSS, s);
     if (err == hipSuccess && dbias) {
       const ColumnSumArgs c{dy, rows, out, dy_ld, a.offsets, (int32_t)groups, a.first, dbias,

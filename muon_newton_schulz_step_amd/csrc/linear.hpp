@@ -39,6 +39,15 @@ struct LinearArgs {
   int32_t splits;             // parts of K, whose sums meet in `partial`
   int32_t tiles_m, tiles_n;   // output tiles (over all groups, at most)
   float *partial;             // splits x (rows of all groups' C) x N
+  int32_t *queue;             // LIN_WEIGHT of groups: LinearQueue
+};
+
+// The order in which a grouped weight gradient's tiles are taken: groups from
+// the longest to the shortest, and what each XCD's workgroups have taken, a
+// line of 128 bytes an XCD.
+struct LinearQueue {
+  int32_t taken[8][32];
+  int32_t group[1024];
 };
 
 // How operands lie: K adjacent (rows of A, columns of B), or the other way.

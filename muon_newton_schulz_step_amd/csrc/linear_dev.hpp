@@ -100,11 +100,44 @@ struct LinTile {
   int group, split;
 };
 
-// Tile t of a launch of BT x BT tiles; false if there is none.  Tiles are
-// counted in panels of 8 tile rows, column by column, so that 32 consecutive
-// ones, which the 32 CUs of an XCD take, share 8 + 4 panels of operands.  A
-// product's tile rows are those of its groups one after the other, found by a
-// scan over the groups' tile counts.
+// Tiles are counted in panels of 8 tile rows, column by column, so that 32
+// consecutive ones, which the 32 CUs of an XCD take, share 8 + 4 panels of
+// operands.
+__device__ __forceinline__ void tile_at(const LinearArgs &a, int t, int &tm, int &tn) {
+  const int panel = t / (8 * a.tiles_n), in = t - panel * 8 * a.tiles_n;
+  const int high = min(8, a.tiles_m - panel * 8);
+  tn = in / high;
+  tm = panel * 8 + in - tn * high;
+}
+
+// Tile t of a group's weight gradient.
+template <int BT>
+__device__ __forceinline__ void weight_tile(const LinearArgs &a, int group, int t, LinTile &x) {
+  int tm, tn;
+  tile_at(a, t, tm, tn);
+  x.group = group;
+  x.col0 = (int64_t)tn * BT;
+  x.row0 = (int64_t)tm * BT;
+  x.rows = (int)lesser(BT, a.M - x.row0);
+  x.k0 = 0;
+  x.k1 = a.K;
+  if (a.offsets.p) {
+    x.k0 = uniform(group_start(a.offsets, group, a.K));
+    x.k1 = greater(x.k0, uniform(group_start(a.offsets, group + 1, a.K)));
+  }
+}
+
+// The tile's part of K.
+__device__ __forceinline__ void cut_tile(const LinearArgs &a, int stage_k, LinTile &x) {
+  if (a.splits <= 1) return;
+  const int64_t stages = (x.k1 - x.k0 + stage_k - 1) / stage_k, start = x.k0, end = x.k1;
+  x.k0 = lesser(end, start + stages * x.split / a.splits * stage_k);
+  x.k1 = lesser(end, start + stages * (x.split + 1) / a.splits * stage_k);
+}
+
+// Tile t of a launch of BT x BT tiles; false if there is none.  A product's
+// tile rows are those of its groups one after the other, found by a scan over
+// the groups' tile counts.
 template <int BT>
 __device__ __forceinline__ bool find_tile(const LinearArgs &a, int t, int stage_k, LinTile &x) {
   const int lane = threadIdx.x & 63;
@@ -112,25 +145,19 @@ __device__ __forceinline__ bool find_tile(const LinearArgs &a, int t, int stage_
   x.split = t / per_split;
   t -= x.split * per_split;
   if (x.split >= a.splits) return false;
-  x.group = 0;
   if (a.mode == LIN_WEIGHT) {
-    x.group = t / (a.tiles_m * a.tiles_n);
-    t -= x.group * a.tiles_m * a.tiles_n;
+    const int group = t / (a.tiles_m * a.tiles_n);
+    weight_tile<BT>(a, group, t - group * a.tiles_m * a.tiles_n, x);
+    cut_tile(a, stage_k, x);
+    return true;
   }
-  const int panel = t / (8 * a.tiles_n), in = t - panel * 8 * a.tiles_n;
-  const int high = min(8, a.tiles_m - panel * 8);
-  const int tn = in / high, tm = panel * 8 + in - tn * high;
+  int tm, tn;
+  tile_at(a, t, tm, tn);
+  x.group = 0;
   x.col0 = (int64_t)tn * BT;
   x.k0 = 0;
   x.k1 = a.K;
-  if (a.mode == LIN_WEIGHT) {
-    x.row0 = (int64_t)tm * BT;
-    x.rows = (int)lesser(BT, a.M - x.row0);
-    if (a.offsets.p) {
-      x.k0 = uniform(group_start(a.offsets, x.group, a.K));
-      x.k1 = greater(x.k0, uniform(group_start(a.offsets, x.group + 1, a.K)));
-    }
-  } else if (!a.offsets.p) {
+  if (!a.offsets.p) {
     x.row0 = (int64_t)tm * BT;
     x.rows = (int)lesser(BT, a.M - x.row0);
   } else {
@@ -165,11 +192,7 @@ __device__ __forceinline__ bool find_tile(const LinearArgs &a, int t, int stage_
     }
     if (!found) return false;
   }
-  if (a.splits > 1) {
-    const int64_t stages = (x.k1 - x.k0 + stage_k - 1) / stage_k, start = x.k0, end = x.k1;
-    x.k0 = lesser(end, start + stages * x.split / a.splits * stage_k);
-    x.k1 = lesser(end, start + stages * (x.split + 1) / a.splits * stage_k);
-  }
+  cut_tile(a, stage_k, x);
   return true;
 }
 

@@ -77,6 +77,49 @@ struct Sum {
 // of a row's sum; a row of -inf has none
 __device__ __forceinline__ float inverse(float s) { return s == 0.f ? 0.f : 1.f / s; }
 __device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + exp_term(0.f, x)); }  // exp(0 - x)
+// for ranks: two steps of fp32 off at most
+__device__ __forceinline__ float sigmoid_fast(float x) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-x * kLog2e)); }
+
+// Ranks as whole numbers of the same order, and back.
+__device__ __forceinline__ uint32_t sortable(float r) {
+  const uint32_t b = __float_as_uint(r);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unsorted(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t reduce_max_u(uint32_t v) {
+  v = max(v, (uint32_t)dpp_i<QUAD_XOR1>((int)v));
+  v = max(v, (uint32_t)dpp_i<QUAD_XOR2>((int)v));
+  if constexpr (LANES >= 16) {
+    v = max(v, (uint32_t)dpp_i<ROW_ROR8>((int)v));
+    v = max(v, (uint32_t)dpp_i<ROW_ROR4>((int)v));
+  }
+  if constexpr (LANES == 64) {
+    v = max(v, (uint32_t)__shfl_xor((int)v, 16));
+    v = max(v, (uint32_t)__shfl_xor((int)v, 32));
+  }
+  return v;
+}
+
+// Descending order, by Batcher's merges of odd and even places.
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t a = v[i + j], b = v[i + j + k];
+            v[i + j] = max(a, b);
+            v[i + j + k] = min(a, b);
+          }
+}
 
 template <bool BF16>
 __device__ __forceinline__ float logit(const RouteArgs &a, int64_t t, int e) {
@@ -84,8 +127,11 @@ __device__ __forceinline__ float logit(const RouteArgs &a, int64_t t, int e) {
   return Elem<BF16>::get(static_cast<const T *>(a.logits)[t * a.ld + e]);
 }
 
-// rank as it is compared: -inf is never chosen, a NaN comes last
-__device__ __forceinline__ float orderly(float r) { return r != r ? kLowest : r; }
+// rank as it is compared: -inf is never chosen, a NaN comes last, and a zero has no sign
+__device__ __forceinline__ float orderly(float r) { return r != r ? kLowest : r + 0.f; }
+
+// Whether the logits order the experts: without a bias, as far as no ranks are added up.
+__device__ __forceinline__ bool ranked_by_logit(const RouteArgs &a) { return !a.bias && (a.groups == 1 || a.top == 1); }
 
 // A token's choice in fp64, by a whole wave: expert e belongs to lane e % 64,
 // its rank to rank[e] in LDS.  Writes k experts (-1 where there are no more)
@@ -105,8 +151,13 @@ __device__ __forceinline__ void route_exact(const RouteArgs &a, int64_t t, doubl
     top = fmax(top, rank[e]);
   }
   top = wave_max(top);
+  const bool by_logit = ranked_by_logit(a);
   // exp(x - max) for the softmax, exp(-x) for the sigmoid
   for (int e = lane; e < a.experts; e += 64) {
+    if (by_logit) {
+      if (rank[e] != rank[e]) rank[e] = kLowest;
+      continue;
+    }
     const double x = rank[e];
     if (x == ninf) continue;
     const double y = exp(a.softmax ? x - top : -x);
@@ -120,7 +171,7 @@ __device__ __forceinline__ void route_exact(const RouteArgs &a, int64_t t, doubl
     total = 1.0;
   }
   for (int e = lane; e < a.experts; e += 64) {
-    if (rank[e] == ninf) continue;
+    if (rank[e] == ninf || by_logit) continue;
     const double r = rank[e] / total + (a.bias ? (double)a.bias[e] : 0.0);
     rank[e] = r != r ? (double)kLowest : r;
   }
@@ -178,7 +229,7 @@ __global__ __launch_bounds__(RT) void kr_route(RouteArgs a) {
   const bool in = t < a.tokens;
   const bool ok = in && (!a.valid || a.valid[t]);
   const int e0 = l * V;
-  const bool by_logit = !a.bias && (a.groups == 1 || a.top == 1);
+  const bool by_logit = ranked_by_logit(a);
   float r[V];
   {
     const T *x = static_cast<const T *>(a.logits) + (ok ? t : 0) * a.ld + e0;
@@ -204,105 +255,196 @@ __global__ __launch_bounds__(RT) void kr_route(RouteArgs a) {
     inv = inverse(reduce_f<LANES>(s, Sum()));
   }
   if (!by_logit) {
+    float b[V];
+    if (a.bias && e0 + V <= a.experts) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) Elem<false>::unpack(load16(a.bias + e0 + i), b + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) b[i] = a.bias && e0 + i < a.experts ? a.bias[e0 + i] : 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float s = a.softmax ? exp_term(r[i], m) * inv : sigmoid(r[i]);
-      const float b = a.bias ? a.bias[min(e0 + i, a.experts - 1)] : 0.f;
-      r[i] = r[i] == -INFINITY ? r[i] : s + b;
+      const float s = a.softmax ? exp_term(r[i], m) * inv : sigmoid_fast(r[i]);
+      r[i] = r[i] == -INFINITY ? r[i] : s + b[i];
     }
   }
-  float size_max = 0.f;  // the largest finite rank's magnitude, for the bound on its rounding
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    r[i] = orderly(r[i]);
-    if (fabsf(r[i]) < 3e38f) size_max = fmaxf(size_max, fabsf(r[i]));
-  }
+  for (int i = 0; i < V; ++i) r[i] = orderly(r[i]);
   bool close = false;
-  float tol = 0.f;
-  if (!by_logit) {
-    // What a score may be off by, in units of 2^-24: an exponential of d carries |d| + 2 of itself, which moves a
-    // sigmoid by at most 3 in all; a softmax's sum carries sum p (|d| + 2) <= 7 + 2 for 1024 experts, at most 22 for
-    // its additions and 4 for the quotient and the product, its term s (|d| + 2) < 3.  The bias adds a rounding of
-    // the rank.  Twice that for the difference of two ranks, twice again for values that are sums of two.
-    size_max = reduce_f<LANES>(size_max, Max());
-    tol = (40.f + size_max) * (4.f * 5.9604645e-8f);
-  }
+  // What a score may be off by, in units of 2^-24: an exponential of d carries |d| + 4 of itself, which moves a
+  // sigmoid by at most 5 in all; a softmax's sum carries sum p (|d| + 2) <= 7 + 2 for 1024 experts, at most 22 for
+  // its additions and 4 for the quotient and the product, its term s (|d| + 2) < 3.  The bias adds a rounding of
+  // the rank.  Twice that for the difference of two ranks, twice again for values that are sums of two.
+  auto tol = [&](float rank) { return by_logit ? 0.f : (40.f + fabsf(rank)) * (4.f * 5.9604645e-8f); };
   if (a.groups > 1) {
-    // every lane goes through the groups' values, group by group
-    const int size = a.experts / a.groups;
-    uint32_t open = 0;
-    float value[ROUTE_MAX_GROUPS / 4];  // of group l + LANES i, i < groups / LANES
-#pragma unroll
-    for (int i = 0; i < ROUTE_MAX_GROUPS / 4; ++i) value[i] = -INFINITY;
-    for (int g = 0; g < a.groups; ++g) {
-      const int lo = g * size - e0, hi = lo + size;
+    const int size = a.experts / a.groups, span = size / V;  // lanes of a group
+    if (LANES >= 16 && size % V == 0 && (span & (span - 1)) == 0) {
+      // a lane's experts are of one group: its two best, joined over the group's lanes
       float v1 = -INFINITY, v2 = -INFINITY;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float x = i >= lo && i < hi ? r[i] : -INFINITY;
-        v2 = fmaxf(v2, fminf(v1, x));
-        v1 = fmaxf(v1, x);
+        v2 = fmaxf(v2, fminf(v1, r[i]));
+        v1 = fmaxf(v1, r[i]);
       }
-      const float best = reduce_f<LANES>(v1, Max());
-      if (a.top > 1) {
-        // the second: of the lane that holds the best, its second; of the others, their first
-        const int who = reduce_min<LANES>(v1 == best ? l : LANES);
-        const float second = reduce_f<LANES>(l == who ? v2 : v1, Max());
-        v1 = second == -INFINITY ? best : fmaxf(best + second, kLowest);
-      } else {
-        v1 = best;
+      for (int d = 1; d < span; d <<= 1) {
+        const float o1 = __shfl_xor(v1, d), o2 = __shfl_xor(v2, d);
+        v2 = fmaxf(fmaxf(v2, o2), fminf(v1, o1));
+        v1 = fmaxf(v1, o1);
+      }
+      const float value = a.top > 1 && v2 != -INFINITY ? fmaxf(v1 + v2, kLowest) : v1;
+      // groups before this lane's
+      const int g = l / span, first = (int)(threadIdx.x & 63) - l;
+      int before = 0;
+      for (int q = 1; q < a.groups; ++q) {
+        const int h = g + q < a.groups ? g + q : g + q - a.groups;
+        const float o = __shfl(value, first + (h & (LANES - 1)) * span);
+        before += o > value || (o == value && h < g);
+      }
+      const bool kept = g < a.groups && before < a.keep;
+      if (!by_logit) {
+        const float in_ = -reduce_f<LANES>(kept && value != -INFINITY ? -value : -INFINITY, Max());
+        const float out = reduce_f<LANES>(g < a.groups && !kept ? value : -INFINITY, Max());
+        if (out != -INFINITY && in_ - out <= tol(in_)) close = true;
       }
 #pragma unroll
-      for (int i = 0; i < ROUTE_MAX_GROUPS / 4; ++i)
-        if (g == l + LANES * i) value[i] = v1;
+      for (int i = 0; i < V; ++i) r[i] = kept ? r[i] : -INFINITY;
+    } else {
+      // every lane goes through the groups' values, group by group
+      uint32_t open = 0;
+      float value[ROUTE_MAX_GROUPS / 4];  // of group l + LANES i, i < groups / LANES
+#pragma unroll
+      for (int i = 0; i < ROUTE_MAX_GROUPS / 4; ++i) value[i] = -INFINITY;
+      for (int g = 0; g < a.groups; ++g) {
+        const int lo = g * size - e0, hi = lo + size;
+        float v1 = -INFINITY, v2 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float x = i >= lo && i < hi ? r[i] : -INFINITY;
+          v2 = fmaxf(v2, fminf(v1, x));
+          v1 = fmaxf(v1, x);
+        }
+        const float best = reduce_f<LANES>(v1, Max());
+        if (a.top > 1) {
+          // the second: of the lane that holds the best, its second; of the others, their first
+          const int who = reduce_min<LANES>(v1 == best ? l : LANES);
+          const float second = reduce_f<LANES>(l == who ? v2 : v1, Max());
+          v1 = second == -INFINITY ? best : fmaxf(best + second, kLowest);
+        } else {
+          v1 = best;
+        }
+#pragma unroll
+        for (int i = 0; i < ROUTE_MAX_GROUPS / 4; ++i)
+          if (g == l + LANES * i) value[i] = v1;
+      }
+      // the `keep` best, one at a time; the first that stays outside tells how close it was
+      float last = INFINITY;
+      for (int q = 0; q <= a.keep && q < a.groups; ++q) {
+        float v = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < ROUTE_MAX_GROUPS / 4; ++i) v = fmaxf(v, value[i]);
+        const float best = reduce_f<LANES>(v, Max());
+        if (q == a.keep) {
+          close |= !by_logit && last - best <= tol(last);
+          break;
+        }
+        last = best;
+        int at = INT32_MAX;
+#pragma unroll
+        for (int i = ROUTE_MAX_GROUPS / 4 - 1; i >= 0; --i)
+          if (value[i] == best && best != -INFINITY) at = l + LANES * i;
+        at = reduce_min<LANES>(at);
+        if (at == INT32_MAX) break;
+        open |= 1u << at;
+#pragma unroll
+        for (int i = 0; i < ROUTE_MAX_GROUPS / 4; ++i)
+          if (l + LANES * i == at) value[i] = -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (!(open >> min((e0 + i) / size, 31) & 1)) r[i] = -INFINITY;
     }
-    // the `keep` best, one at a time; the first that stays outside tells how close it was
-    float last = INFINITY;
-    for (int q = 0; q <= a.keep && q < a.groups; ++q) {
-      float v = -INFINITY;
+  }
+  bool done = false;
+  if constexpr (LANES >= 16) {
+    if (a.k + 2 <= LANES) {
+      // The k + 2 best by keys whose low bits are replaced by the expert: each
+      // lane sorts its own, then the best of the lanes' first ones is taken,
+      // time and again.  What the bits left out decide is settled among the
+      // chosen by their full ranks.
+      constexpr uint32_t LOW = LANES * V - 1;
+      static_assert((LANES * V & LOW) == 0, "a power of two");
+      uint32_t key[V];
 #pragma unroll
-      for (int i = 0; i < ROUTE_MAX_GROUPS / 4; ++i) v = fmaxf(v, value[i]);
-      const float best = reduce_f<LANES>(v, Max());
-      if (q == a.keep) {
-        close |= !by_logit && last - best <= tol;
-        break;
+      for (int i = 0; i < V; ++i) {
+        const uint32_t there = r[i] == -INFINITY ? 0u : ~0u;
+        key[i] = ((sortable(r[i]) & ~LOW) | (LOW - (uint32_t)(e0 + i))) & there;
       }
+      sort_down(key);
+      uint32_t mine = 0, least = 0;  // the lane's one of them, and the last
+      for (int j = 0; j < a.k + 2; ++j) {
+        const uint32_t best = reduce_max_u<LANES>(key[0]);
+        if (l == j) mine = best;
+        least = best;
+        // (a choice between neighbours would become an index, and that a chain of comparisons)
+        const uint32_t won = key[0] == best ? ~0u : 0u;
+#pragma unroll
+        for (int i = 0; i + 1 < V; ++i) key[i] = (key[i + 1] & won) | (key[i] & ~won);
+        key[V - 1] &= ~won;
+      }
+      const int e = mine ? (int)(LOW - (mine & LOW)) : -1;
+      float x = -INFINITY, bias = 0.f, rank = -INFINITY;
+      if (e >= 0) {
+        x = logit<BF16>(a, t, e);
+        if (a.bias) bias = a.bias[e];
+        rank = orderly(by_logit ? x : (a.softmax ? exp_term(x, m) * inv : sigmoid_fast(x)) + bias);
+      }
+      int place = 0;
+      bool near = false;
+      const int first = (int)(threadIdx.x & 63) - l;
+      for (int j = 0; j < a.k + 2; ++j) {
+        const float o = __shfl(rank, first + j);
+        const int f = __shfl(e, first + j);
+        const bool other = f >= 0 && f != e;
+        place += other && (o > rank || (o == rank && f < e));
+        if (!by_logit) {
+          const bool same = __shfl(x, first + j) == x && __shfl(bias, first + j) == bias;  // equal by their inputs
+          near |= other && !same && fabsf(o - rank) <= tol(rank);
+        }
+      }
+      if (l < a.k) chosen[slot][l] = -1;
+      __builtin_amdgcn_wave_barrier();
+      if (e >= 0 && place < a.k) chosen[slot][place] = e;
+      // close: a rank near that of another of them, or near what may lie outside
+      const float kth = -reduce_f<LANES>(e >= 0 && place < a.k ? -rank : -INFINITY, Max());
+      const bool exact_keys = by_logit && BF16;
+      if (least != 0 && !exact_keys && !(kth - unsorted(least | LOW) > tol(kth))) close = true;
+      if (reduce_f<LANES>(e >= 0 && near && place < a.k ? 1.f : 0.f, Max()) != 0.f) close = true;
+      done = true;
+    }
+  }
+  if (!done) {
+    // the k best, one at a time, and the first that stays outside
+    float last = INFINITY;
+    for (int j = 0; j <= a.k; ++j) {
+      if (j == a.k && by_logit) break;
+      float v = r[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) v = fmaxf(v, r[i]);
+      const float best = reduce_f<LANES>(v, Max());
+      if (!by_logit && best != -INFINITY && last - best <= tol(best)) close = true;
       last = best;
+      if (j == a.k) break;
       int at = INT32_MAX;
 #pragma unroll
-      for (int i = ROUTE_MAX_GROUPS / 4 - 1; i >= 0; --i)
-        if (value[i] == best && best != -INFINITY) at = l + LANES * i;
+      for (int i = V - 1; i >= 0; --i)
+        if (r[i] == best && best != -INFINITY) at = e0 + i;
       at = reduce_min<LANES>(at);
-      if (at == INT32_MAX) break;
-      open |= 1u << at;
+      if (l == 0) chosen[slot][j] = at == INT32_MAX ? -1 : at;
 #pragma unroll
-      for (int i = 0; i < ROUTE_MAX_GROUPS / 4; ++i)
-        if (l + LANES * i == at) value[i] = -INFINITY;
+      for (int i = 0; i < V; ++i)
+        if (e0 + i == at) r[i] = -INFINITY;
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (!(open >> min((e0 + i) / size, 31) & 1)) r[i] = -INFINITY;
-  }
-  // the k best, one at a time, and the first that stays outside
-  float last = INFINITY;
-  for (int j = 0; j <= a.k; ++j) {
-    if (j == a.k && by_logit) break;
-    float v = r[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) v = fmaxf(v, r[i]);
-    const float best = reduce_f<LANES>(v, Max());
-    if (!by_logit && best != -INFINITY && last - best <= tol) close = true;
-    last = best;
-    if (j == a.k) break;
-    int at = INT32_MAX;
-#pragma unroll
-    for (int i = V - 1; i >= 0; --i)
-      if (r[i] == best && best != -INFINITY) at = e0 + i;
-    at = reduce_min<LANES>(at);
-    if (l == 0) chosen[slot][j] = at == INT32_MAX ? -1 : at;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (e0 + i == at) r[i] = -INFINITY;
   }
   uint64_t redo = __ballot(close && ok && l == 0);
   while (redo) {

@@ -223,6 +223,47 @@ def test_route_of_nearly_equal_ranks(torch, dtype):
     check_route(torch, x, 8, dtype, "int64", np.zeros(n, dtype=np.float32), scoring="sigmoid")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,groups,keep,top", [(256, 1, 1, 1), (64, 8, 4, 1), (256, 8, 4, 2), (1024, 1, 1, 1), (100, 1, 1, 1)])
+def test_route_of_many_equal_ranks(torch, dtype, n, groups, keep, top):
+    # logits of a few values, zeros of both signs among them: most choices are decided by the index
+    rng = np.random.default_rng(n)
+    x = rng.integers(-2, 3, (200, n)) * 0.25
+    x[:, ::3] *= -1.0
+    x[:50] = np.where(x[:50] < 0.5, x[:50], np.where(rng.random((50, n)) < 0.01, 0.5, -0.0))
+    x[50:60] = np.where(rng.random((10, n)) < 0.5, 0.0, -0.0)
+    x[60:70] = 1.0 + rng.integers(0, 3, (10, n)) * 2.0 ** (-23 if dtype == "fp32" else -7)
+    for bias in (None, np.zeros(n, dtype=np.float32), (rng.integers(-1, 2, n) * 0.125).astype(np.float32)):
+        check_route(torch, x, 8, dtype, "int32", bias, scoring="sigmoid", groups=groups, keep_groups=keep, group_top=top)
+        check_route(torch, x, 3, dtype, "int32", bias, scoring="softmax", groups=groups, keep_groups=keep, group_top=top)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_route_of_many_tokens(torch, dtype):
+    # against the definition in torch, in 64 bits: with so many tokens some have ranks that fp32 does not tell apart
+    g = torch.Generator(DEV).manual_seed(3)
+    t, n, k = 20000, 256, 8
+    x = torch.randn(t, n, device=DEV, generator=g).to(dt(torch, dtype))
+    bias = 0.1 * torch.randn(n, device=DEV, generator=g)
+    for scoring in ("sigmoid", "softmax"):
+        s = torch.sigmoid(x.double()) if scoring == "sigmoid" else torch.softmax(x.double(), 1)
+        for b, groups in ((None, 1), (bias, 1), (bias, 8), (None, 8)):
+            rank = s if b is not None or groups > 1 else x.double()
+            rank = rank if b is None else rank + b.double()
+            if groups > 1:
+                value = rank.view(t, groups, -1).topk(2, 2).values.sum(2)
+                keep = value.sort(dim=1, descending=True, stable=True).indices[:, :4]
+                open_ = torch.zeros(t, groups, dtype=torch.bool, device=DEV).scatter_(1, keep, True)
+                rank = torch.where(open_[:, :, None], rank.view(t, groups, -1), -torch.inf).view(t, n)
+            want = rank.sort(dim=1, descending=True, stable=True).indices[:, :k]
+            c, w = torch.empty(t, k, dtype=torch.int64, device=DEV), torch.empty(t, k, device=DEV)
+            M.route_experts(x, c, w, scoring=scoring, bias=b, groups=groups, keep_groups=4 if groups > 1 else 1,
+                            group_top=2 if groups > 1 else 1)
+            assert torch.equal(c, want), (scoring, b is None, groups)
+            sw = s.gather(1, want)
+            assert float((w.double() - sw / sw.sum(1, keepdim=True)).abs().max()) < 2e-6
+
+
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 def test_route_of_masks_and_extremes(torch, scoring):
     rng = np.random.default_rng(2)

@@ -22,7 +22,7 @@ namespace muon {
 
 using namespace dev;
 
-hipError_t launch_linear256(const LinearArgs &a, int tiles, bool ax, bool bx, hipStream_t s);
+hipError_t launch_linear256(const LinearArgs &a, bool ax, bool bx, hipStream_t s);
 
 namespace {
 
@@ -37,7 +37,7 @@ __global__ __launch_bounds__(LIN_THREADS, 8 / W) void kl_linear(LinearArgs a) {
   constexpr int KS = OA::KS, L = OA::LOADS;
   __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * OPB];
   LinTile x;
-  if (!find_tile<BT>(a, (int)blockIdx.x, KS, x)) return;
+  if (!find_tile<BT>(a, tile_groups<BT>(a), (int)blockIdx.x, KS, x)) return;
   const OA oa{static_cast<const T *>(a.a) + (AX ? x.row0 : x.row0 * a.lda), a.lda, x.rows, x.k1};
   const OB ob{static_cast<const T *>(a.b) + x.group * a.bstride + (BX ? x.col0 : x.col0 * a.ldb), a.ldb,
               (int)lesser(BT, a.N - x.col0), x.k1};
@@ -305,7 +305,7 @@ hipError_t launch_linear(LinearArgs a, bool bf16, int la, int lb, hipStream_t s)
     a.splits = 1;
     a.tiles_m = (int32_t)tiles_along(a.M, a.groups, !weight && a.offsets.p, 256);
     a.tiles_n = (int32_t)((a.N + 255) / 256);
-    return launch_linear256(a, a.tiles_m * a.tiles_n * (weight ? a.groups : 1), ax, bx, s);
+    return launch_linear256(a, ax, bx, s);
   }
   const LinearPlan p = plan_of(a.M, a.N, a.K, a.groups, weight);
   const int bt = 32 * p.w;

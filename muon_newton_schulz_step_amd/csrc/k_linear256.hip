@@ -49,7 +49,7 @@ __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * OPB + 64];
 // XCD's workgroups take theirs from a queue that begins with the longest
 // group's.
 template <bool AX, bool BX, bool QUEUE>
-__global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int tiles, int stride) {
+__global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int stride) {
   typedef Operand<true, BT, AX> OA;
   typedef Operand<true, BT, BX> OB;
   typedef typename OA::T T;
@@ -72,10 +72,9 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
   if constexpr (QUEUE) {
     if (qn <= 0 || !queued(slot, x)) return;
     if (threadIdx.x == 0) *next_slot = atomicAdd(&queue->taken[xcd][0], 1);
-  } else {
-    while (t < tiles && !find_tile<BT>(a, t, KS, x)) t += stride;
-    if (t >= tiles) return;
   }
+  const TileGroups groups = tile_groups<BT>(a);
+  if (!QUEUE && !find_tile<BT>(a, groups, t, KS, x)) return;
   const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
   uint32_t offa[8], offb[8];
 #pragma unroll
@@ -123,7 +122,7 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
     const int nk = (int)greater(2, (x.k1 - x.k0 + KS - 1) / KS);
     bool chain;
     LinTile y;
-    int tn = 0, taken = 0;
+    int taken = 0;
     f32x4_v acc[8][8];
     {
       bf16x8_v fa[2][8], fb[2][8];
@@ -152,9 +151,8 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
         chain = queued(uni32(*next_slot), y);
         if (threadIdx.x == 0 && chain) taken = atomicAdd(&queue->taken[xcd][0], 1);
       } else {
-        tn = t + stride;
-        while (tn < tiles && !find_tile<BT>(a, tn, KS, y)) tn += stride;
-        chain = tn < tiles;
+        t += stride;
+        chain = find_tile<BT>(a, groups, t, KS, y);
       }
       const Cursor then = chain ? start(y) : at;
 #pragma unroll
@@ -229,7 +227,6 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
     full = x.rows == BT && a.N - x.col0 >= BT;
     base = (nk + base) & 1;
     x = y;
-    t = tn;
   }
 }
 
@@ -252,19 +249,19 @@ __global__ __launch_bounds__(1024) void kl_queue(LinearArgs a) {
   queue->group[before] = g;
 }
 
-hipError_t launch_linear256(const LinearArgs &a, int tiles, bool ax, bool bx, hipStream_t s) {
+hipError_t launch_linear256(const LinearArgs &a, bool ax, bool bx, hipStream_t s) {
   if (ax && a.offsets.p) {
     static_assert(sizeof(LinearQueue::group) / 4 == 1024, "a group a thread");
     hipLaunchKernelGGL(kl_queue, dim3(1), dim3(1024), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((kl_linear256<true, true, true>), dim3(256), dim3(LIN_THREADS), 0, s, a, tiles, 256);
+    hipLaunchKernelGGL((kl_linear256<true, true, true>), dim3(256), dim3(LIN_THREADS), 0, s, a, 256);
   } else if (ax) {
-    hipLaunchKernelGGL((kl_linear256<true, true, false>), dim3(256), dim3(LIN_THREADS), 0, s, a, tiles, 256);
+    hipLaunchKernelGGL((kl_linear256<true, true, false>), dim3(256), dim3(LIN_THREADS), 0, s, a, 256);
   } else if (bx) {
-    hipLaunchKernelGGL((kl_linear256<false, true, false>), dim3(256), dim3(LIN_THREADS), 0, s, a, tiles, 256);
+    hipLaunchKernelGGL((kl_linear256<false, true, false>), dim3(256), dim3(LIN_THREADS), 0, s, a, 256);
   } else {
-    hipLaunchKernelGGL((kl_linear256<false, false, false>), dim3(256), dim3(LIN_THREADS), 0, s, a, tiles, 256);
+    hipLaunchKernelGGL((kl_linear256<false, false, false>), dim3(256), dim3(LIN_THREADS), 0, s, a, 256);
   }
   return hipGetLastError();
 }

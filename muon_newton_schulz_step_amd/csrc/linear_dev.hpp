@@ -103,9 +103,9 @@ struct LinTile {
 // Tiles are counted in panels of 8 tile rows, column by column, so that 32
 // consecutive ones, which the 32 CUs of an XCD take, share 8 + 4 panels of
 // operands.
-__device__ __forceinline__ void tile_at(const LinearArgs &a, int t, int &tm, int &tn) {
-  const int panel = t / (8 * a.tiles_n), in = t - panel * 8 * a.tiles_n;
-  const int high = min(8, a.tiles_m - panel * 8);
+__device__ __forceinline__ void tile_at(int tiles_m, int tiles_n, int t, int &tm, int &tn) {
+  const int panel = t / (8 * tiles_n), in = t - panel * 8 * tiles_n;
+  const int high = min(8, tiles_m - panel * 8);
   tn = in / high;
   tm = panel * 8 + in - tn * high;
 }
@@ -114,7 +114,7 @@ __device__ __forceinline__ void tile_at(const LinearArgs &a, int t, int &tm, int
 template <int BT>
 __device__ __forceinline__ void weight_tile(const LinearArgs &a, int group, int t, LinTile &x) {
   int tm, tn;
-  tile_at(a, t, tm, tn);
+  tile_at(a.tiles_m, a.tiles_n, t, tm, tn);
   x.group = group;
   x.col0 = (int64_t)tn * BT;
   x.row0 = (int64_t)tm * BT;
@@ -135,16 +135,51 @@ __device__ __forceinline__ void cut_tile(const LinearArgs &a, int stage_k, LinTi
   x.k1 = lesser(end, start + stages * (x.split + 1) / a.splits * stage_k);
 }
 
-// Tile t of a launch of BT x BT tiles; false if there is none.  A product's
-// tile rows are those of its groups one after the other, found by a scan over
-// the groups' tile counts.
+// A product's tile rows are those of its groups one after the other: where
+// they begin, for the first 64 groups a lane each, and how many there are.
+struct TileGroups {
+  int64_t lo, hi;  // the group's rows
+  int first, tiles;
+  int total;       // of all groups
+};
+
+// The tile rows of groups [g0, g0 + 64), behind `before` ones.
 template <int BT>
-__device__ __forceinline__ bool find_tile(const LinearArgs &a, int t, int stage_k, LinTile &x) {
-  const int lane = threadIdx.x & 63;
-  const int per_split = a.tiles_m * a.tiles_n * (a.mode == LIN_WEIGHT ? a.groups : 1);
+__device__ __forceinline__ void scan_groups(const LinearArgs &a, int g0, int before, TileGroups &r) {
+  const int lane = threadIdx.x & 63, g = g0 + lane;
+  r.lo = r.hi = 0;
+  if (g < a.groups) {
+    r.lo = group_start(a.offsets, g, a.M);
+    r.hi = group_start(a.offsets, g + 1, a.M);
+  }
+  r.tiles = r.hi > r.lo ? (int)((r.hi - r.lo + BT - 1) / BT) : 0;
+  int sum = r.tiles;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(sum, d);
+    if (lane >= d) sum += y;
+  }
+  r.first = before + sum - r.tiles;
+  r.total = before + uni32(__shfl(sum, 63));
+}
+template <int BT>
+__device__ __forceinline__ TileGroups tile_groups(const LinearArgs &a) {
+  TileGroups r{0, 0, 0, 0, a.tiles_m};
+  if (a.mode == LIN_WEIGHT || !a.offsets.p) return r;
+  scan_groups<BT>(a, 0, 0, r);
+  TileGroups more = r;
+  for (int g0 = 64; g0 < a.groups; g0 += 64) scan_groups<BT>(a, g0, more.total, more);
+  r.total = more.total;
+  return r;
+}
+
+// Tile t of a launch of BT x BT tiles; false if there is none.
+template <int BT>
+__device__ __forceinline__ bool find_tile(const LinearArgs &a, const TileGroups &groups, int t, int stage_k, LinTile &x) {
+  const int per_split = groups.total * a.tiles_n * (a.mode == LIN_WEIGHT ? a.groups : 1);
+  if (t >= per_split * a.splits) return false;
   x.split = t / per_split;
   t -= x.split * per_split;
-  if (x.split >= a.splits) return false;
   if (a.mode == LIN_WEIGHT) {
     const int group = t / (a.tiles_m * a.tiles_n);
     weight_tile<BT>(a, group, t - group * a.tiles_m * a.tiles_n, x);
@@ -152,7 +187,7 @@ __device__ __forceinline__ bool find_tile(const LinearArgs &a, int t, int stage_
     return true;
   }
   int tm, tn;
-  tile_at(a, t, tm, tn);
+  tile_at(groups.total, a.tiles_n, t, tm, tn);
   x.group = 0;
   x.col0 = (int64_t)tn * BT;
   x.k0 = 0;
@@ -161,36 +196,25 @@ __device__ __forceinline__ bool find_tile(const LinearArgs &a, int t, int stage_
     x.row0 = (int64_t)tm * BT;
     x.rows = (int)lesser(BT, a.M - x.row0);
   } else {
-    int before = 0;
-    bool found = false;
-    for (int g0 = 0; g0 < a.groups && !found; g0 += 64) {
-      const int g = g0 + lane;
-      int64_t lo = 0, hi = 0;
-      if (g < a.groups) {
-        lo = group_start(a.offsets, g, a.M);
-        hi = group_start(a.offsets, g + 1, a.M);
+    TileGroups r = groups;
+    uint64_t has = __ballot(tm >= r.first && tm < r.first + r.tiles);
+    int g0 = 0;
+    if (!has) {
+      // a group behind the 64th: the scan again
+      int before = uni32(__shfl(r.first + r.tiles, 63));
+      for (g0 = 64; !has && g0 < a.groups; g0 += 64) {
+        scan_groups<BT>(a, g0, before, r);
+        before = r.total;
+        has = __ballot(tm >= r.first && tm < r.first + r.tiles);
       }
-      const int tiles = hi > lo ? (int)((hi - lo + BT - 1) / BT) : 0;
-      int sum = tiles;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int y = __shfl_up(sum, d);
-        if (lane >= d) sum += y;
-      }
-      const int mine = before + sum - tiles;  // this group's first tile row
-      const uint64_t has = __ballot(tm >= mine && tm < mine + tiles);
-      if (has) {
-        const int who = __ffsll((unsigned long long)has) - 1;
-        x.group = g0 + who;
-        const int first = uni32(__shfl(mine, who));
-        const int64_t l = uniform((int64_t)__shfl((long long)lo, who)), h = uniform((int64_t)__shfl((long long)hi, who));
-        x.row0 = l + (int64_t)(tm - first) * BT;
-        x.rows = (int)lesser(BT, h - x.row0);
-        found = true;
-      }
-      before += uni32(__shfl(sum, 63));
+      g0 -= 64;
     }
-    if (!found) return false;
+    const int who = __ffsll((unsigned long long)has) - 1;
+    x.group = g0 + who;
+    const int first = uni32(__shfl(r.first, who));
+    const int64_t lo = uniform((int64_t)__shfl((long long)r.lo, who)), hi = uniform((int64_t)__shfl((long long)r.hi, who));
+    x.row0 = lo + (int64_t)(tm - first) * BT;
+    x.rows = (int)lesser(BT, hi - x.row0);
   }
   cut_tile(a, stage_k, x);
   return true;

@@ -22,7 +22,7 @@ namespace muon {
 
 using namespace dev;
 
-hipError_t launch_linear256(const LinearArgs &a, bool ax, bool bx, hipStream_t s);
+hipError_t launch_linear256(const LinearArgs &a, bool bx, hipStream_t s);
 
 namespace {
 
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(LIN_THREADS, 8 / W) void kl_linear(LinearArgs a) {
     }
     if (kt + 1 < nk) land(st ^ 1);
   }
-  if constexpr (DMA) finish_aligned<BF16, W, AX, true>(a, x, acc, (int)threadIdx.x);
+  if constexpr (DMA) finish_aligned<BF16, W, AX ? (int)LIN_WEIGHT : -1, true>(a, x, acc, (int)threadIdx.x);
   else finish_any<BF16, W, AX>(a, x, acc, (int)threadIdx.x);
 }
 
@@ -305,7 +305,7 @@ hipError_t launch_linear(LinearArgs a, bool bf16, int la, int lb, hipStream_t s)
     a.splits = 1;
     a.tiles_m = (int32_t)tiles_along(a.M, a.groups, !weight && a.offsets.p, 256);
     a.tiles_n = (int32_t)((a.N + 255) / 256);
-    return launch_linear256(a, ax, bx, s);
+    return launch_linear256(a, bx, s);
   }
   const LinearPlan p = plan_of(a.M, a.N, a.K, a.groups, weight);
   const int bt = 32 * p.w;

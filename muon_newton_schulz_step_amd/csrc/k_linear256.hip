@@ -48,8 +48,9 @@ __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * OPB + 64];
 // those of a grouped weight gradient (QUEUE) are of very different K, and each
 // XCD's workgroups take theirs from a queue that begins with the longest
 // group's.
-template <bool AX, bool BX, bool QUEUE>
+template <int MODE, bool BX, bool QUEUE>
 __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int stride) {
+  constexpr bool AX = MODE == LIN_WEIGHT;
   typedef Operand<true, BT, AX> OA;
   typedef Operand<true, BT, BX> OB;
   typedef typename OA::T T;
@@ -218,7 +219,7 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
     asm volatile("" : "+s"(args), "+v"(tid));
     LinearArgs b;
     __builtin_memcpy(&b, (const void *)args, sizeof b);
-    finish_aligned<true, 8, AX, false>(b, x, acc, tid);
+    finish_aligned<true, 8, MODE, false>(b, x, acc, tid);
     if (!chain) return;
     if constexpr (QUEUE) {
       if (threadIdx.x == 0) *next_slot = taken;
@@ -249,19 +250,24 @@ __global__ __launch_bounds__(1024) void kl_queue(LinearArgs a) {
   queue->group[before] = g;
 }
 
-hipError_t launch_linear256(const LinearArgs &a, bool ax, bool bx, hipStream_t s) {
-  if (ax && a.offsets.p) {
+template <int MODE, bool BX, bool QUEUE>
+void go(const LinearArgs &a, hipStream_t s) {
+  hipLaunchKernelGGL((kl_linear256<MODE, BX, QUEUE>), dim3(256), dim3(LIN_THREADS), 0, s, a, 256);
+}
+
+hipError_t launch_linear256(const LinearArgs &a, bool bx, hipStream_t s) {
+  if (a.mode == LIN_WEIGHT && a.offsets.p) {
     static_assert(sizeof(LinearQueue::group) / 4 == 1024, "a group a thread");
     hipLaunchKernelGGL(kl_queue, dim3(1), dim3(1024), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((kl_linear256<true, true, true>), dim3(256), dim3(LIN_THREADS), 0, s, a, 256);
-  } else if (ax) {
-    hipLaunchKernelGGL((kl_linear256<true, true, false>), dim3(256), dim3(LIN_THREADS), 0, s, a, 256);
-  } else if (bx) {
-    hipLaunchKernelGGL((kl_linear256<false, true, false>), dim3(256), dim3(LIN_THREADS), 0, s, a, 256);
+    go<LIN_WEIGHT, true, true>(a, s);
+  } else if (a.mode == LIN_WEIGHT) {
+    go<LIN_WEIGHT, true, false>(a, s);
+  } else if (a.mode == LIN_FORWARD) {
+    bx ? go<LIN_FORWARD, true, false>(a, s) : go<LIN_FORWARD, false, false>(a, s);
   } else {
-    hipLaunchKernelGGL((kl_linear256<false, false, false>), dim3(256), dim3(LIN_THREADS), 0, s, a, 256);
+    bx ? go<LIN_INPUT, true, false>(a, s) : go<LIN_INPUT, false, false>(a, s);
   }
   return hipGetLastError();
 }

@@ -450,20 +450,26 @@ __device__ __forceinline__ int pair_column(int tid) {
   return wn * (16 * W) + (lg & 1) * 16 + (lg >> 1) * 8;
 }
 
+// q = row i of blocks, I <= i < W.
+template <int W, int I>
+__device__ __forceinline__ void pick_row(const f32x4_v (&acc)[W][W], int i, f32x4_v (&q)[W]) {
+  if (I == W - 1 || i == I) {
+    // (the asm keeps the rows apart: merged, they would index the sums in memory)
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      q[j] = acc[I][j];
+      asm volatile("" : "+v"(q[j]));
+    }
+  } else if constexpr (I < W - 1) {
+    pick_row<W, I + 1>(acc, i, q);
+  }
+}
+
 // Row i of blocks, as a lane's eights.
 template <int W>
 __device__ __forceinline__ void take_row(const f32x4_v (&acc)[W][W], int i, float (&v)[W / 2][8]) {
   f32x4_v q[W];
-#pragma unroll
-  for (int ii = 0; ii < W; ++ii)
-    if (i == ii) {
-      // (the asm keeps the branches apart: merged, they would index the sums in memory)
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        q[j] = acc[ii][j];
-        asm volatile("" : "+v"(q[j]));
-      }
-    }
+  pick_row<W, 0>(acc, i, q);
 #pragma unroll
   for (int jj = 0; jj < W / 2; ++jj)
 #pragma unroll
@@ -538,11 +544,13 @@ struct TileRows {
 };
 
 // The way of a whole tile whose matrices keep 16-byte alignment, with a
-// multiple of 8 columns.  WEIGHT: of LIN_WEIGHT; PARTS: of a launch that may be
+// multiple of 8 columns.  PARTS: of a launch that may be
 // cut along K.  What is read beside the sums goes out a row of blocks ahead.
-template <bool BF16, int W, bool WEIGHT, bool PARTS>
+// MODE: a LinearMode, or -1 for either of the products.
+template <bool BF16, int W, int MODE, bool PARTS>
 __device__ __forceinline__ void finish_aligned(const LinearArgs &a, const LinTile &x, const f32x4_v (&acc)[W][W], int tid) {
   constexpr int P = W / 2;
+  constexpr bool WEIGHT = MODE == LIN_WEIGHT;
   if (PARTS && a.splits > 1) {
     const int64_t all = WEIGHT ? a.M * a.groups : a.M;
     TileRows<false, W> out;
@@ -579,7 +587,7 @@ __device__ __forceinline__ void finish_aligned(const LinearArgs &a, const LinTil
       out.next();
     }
   } else {
-    const bool forward = a.mode == LIN_FORWARD, biased = forward && a.bias, kept = forward && a.pre;
+    const bool forward = MODE < 0 ? a.mode == LIN_FORWARD : MODE == LIN_FORWARD, biased = forward && a.bias, kept = forward && a.pre;
     const bool sloped = !forward && a.act != ACT_NONE;
     TileRows<BF16, W> out, pre, res;
     Raw8<BF16> bias[P], br[P], rr[P];

@@ -37,7 +37,7 @@ __global__ __launch_bounds__(LIN_THREADS, 8 / W) void kl_linear(LinearArgs a) {
   constexpr int KS = OA::KS, L = OA::LOADS;
   __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * OPB];
   LinTile x;
-  if (!find_tile<BT>(a, tile_groups<BT>(a), (int)blockIdx.x, KS, x)) return;
+  if (!find_tile<BT, true>(a, tile_groups<BT>(a), (int)blockIdx.x, KS, x)) return;
   const OA oa{static_cast<const T *>(a.a) + (AX ? x.row0 : x.row0 * a.lda), a.lda, x.rows, x.k1};
   const OB ob{static_cast<const T *>(a.b) + x.group * a.bstride + (BX ? x.col0 : x.col0 * a.ldb), a.ldb,
               (int)lesser(BT, a.N - x.col0), x.k1};

@@ -74,8 +74,16 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
     if (qn <= 0 || !queued(slot, x)) return;
     if (threadIdx.x == 0) *next_slot = atomicAdd(&queue->taken[xcd][0], 1);
   }
-  const TileGroups groups = tile_groups<BT>(a);
-  if (!QUEUE && !find_tile<BT>(a, groups, t, KS, x)) return;
+  TileGroups groups;
+  if constexpr (MODE != LIN_WEIGHT) groups = tile_groups<BT>(a);
+  auto find = [&](int t, LinTile &y) {
+    if constexpr (MODE != LIN_WEIGHT) return find_tile<BT, false>(a, groups, t, KS, y);
+    if (t >= each) return false;
+    weight_tile<BT>(a, 0, t, y);
+    y.split = 0;
+    return true;
+  };
+  if (!QUEUE && !find(t, x)) return;
   const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
   uint32_t offa[8], offb[8];
 #pragma unroll
@@ -153,7 +161,7 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
         if (threadIdx.x == 0 && chain) taken = atomicAdd(&queue->taken[xcd][0], 1);
       } else {
         t += stride;
-        chain = find_tile<BT>(a, groups, t, KS, y);
+        chain = find(t, y);
       }
       const Cursor then = chain ? start(y) : at;
 #pragma unroll

@@ -173,17 +173,18 @@ __device__ __forceinline__ TileGroups tile_groups(const LinearArgs &a) {
   return r;
 }
 
-// Tile t of a launch of BT x BT tiles; false if there is none.
-template <int BT>
+// Tile t of a launch of BT x BT tiles; false if there is none.  PARTS: of one
+// that may be cut along K.
+template <int BT, bool PARTS>
 __device__ __forceinline__ bool find_tile(const LinearArgs &a, const TileGroups &groups, int t, int stage_k, LinTile &x) {
   const int per_split = groups.total * a.tiles_n * (a.mode == LIN_WEIGHT ? a.groups : 1);
-  if (t >= per_split * a.splits) return false;
-  x.split = t / per_split;
+  if (t >= per_split * (PARTS ? a.splits : 1)) return false;
+  x.split = PARTS ? t / per_split : 0;
   t -= x.split * per_split;
   if (a.mode == LIN_WEIGHT) {
     const int group = t / (a.tiles_m * a.tiles_n);
     weight_tile<BT>(a, group, t - group * a.tiles_m * a.tiles_n, x);
-    cut_tile(a, stage_k, x);
+    if (PARTS) cut_tile(a, stage_k, x);
     return true;
   }
   int tm, tn;
@@ -216,7 +217,7 @@ __device__ __forceinline__ bool find_tile(const LinearArgs &a, const TileGroups 
     x.row0 = lo + (int64_t)(tm - first) * BT;
     x.rows = (int)lesser(BT, hi - x.row0);
   }
-  cut_tile(a, stage_k, x);
+  if (PARTS) cut_tile(a, stage_k, x);
   return true;
 }
 
@@ -519,7 +520,8 @@ struct TileRows {
     base += step;
     range -= step;
   }
-  __device__ __forceinline__ void load(Raw8<BF16> (&r)[P]) const {
+  // A row of blocks, then on to the next one (behind the last row: nothing).
+  __device__ __forceinline__ void take(Raw8<BF16> (&r)[P]) {
     const auto rs = rsrc();
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
@@ -529,6 +531,7 @@ struct TileRows {
         const u32x4 w = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off[jj] + 16 * h, 0, 0));
         r[jj].v[h] = make_uint4(w[0], w[1], w[2], w[3]);
       }
+    next();
   }
   __device__ __forceinline__ void store(const float (&v)[P][8]) const {
     const auto rs = rsrc();
@@ -545,7 +548,7 @@ struct TileRows {
 
 // The way of a whole tile whose matrices keep 16-byte alignment, with a
 // multiple of 8 columns.  PARTS: of a launch that may be
-// cut along K.  What is read beside the sums goes out a row of blocks ahead.
+// cut along K.  What is read beside the sums goes out two rows of blocks ahead.
 // MODE: a LinearMode, or -1 for either of the products.
 template <bool BF16, int W, int MODE, bool PARTS>
 __device__ __forceinline__ void finish_aligned(const LinearArgs &a, const LinTile &x, const f32x4_v (&acc)[W][W], int tid) {
@@ -564,33 +567,38 @@ __device__ __forceinline__ void finish_aligned(const LinearArgs &a, const LinTil
     }
   } else if constexpr (WEIGHT) {
     TileRows<false, W> out, old;
-    Raw8<false> r[P];
+    Raw8<false> r[2][P];
     out.init(a.out, x.group * a.out_stride, a.out_ld, x, a.N, tid);
     old = out;
-    if (!a.first) old.load(r);
+    if (!a.first) {
+      old.take(r[0]);
+      old.take(r[1]);
+    }
 #pragma unroll 1
-    for (int i = 0; i < W; ++i) {
-      float v[P][8];
-      take_row(acc, i, v);
-      if (!a.first) {
+    for (int i = 0; i < W; i += 2) {
 #pragma unroll
-        for (int jj = 0; jj < P; ++jj) {
-          float f[8];
-          r[jj].get(f);
+      for (int u = 0; u < 2; ++u) {
+        float v[P][8];
+        take_row(acc, i + u, v);
+        if (!a.first) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[jj][e] += f[e];
+          for (int jj = 0; jj < P; ++jj) {
+            float f[8];
+            r[u][jj].get(f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[jj][e] += f[e];
+          }
+          old.take(r[u]);
         }
-        old.next();
-        old.load(r);  // behind the last row: nothing
+        out.store(v);
+        out.next();
       }
-      out.store(v);
-      out.next();
     }
   } else {
     const bool forward = MODE < 0 ? a.mode == LIN_FORWARD : MODE == LIN_FORWARD, biased = forward && a.bias, kept = forward && a.pre;
     const bool sloped = !forward && a.act != ACT_NONE;
     TileRows<BF16, W> out, pre, res;
-    Raw8<BF16> bias[P], br[P], rr[P];
+    Raw8<BF16> bias[P], br[2][P], rr[2][P];
     out.init(a.out, 0, a.out_ld, x, a.N, tid);
     if (kept || sloped) pre.init(a.pre, 0, a.pre_ld, x, a.N, tid);
     if (a.residual) res.init(a.residual, 0, a.res_ld, x, a.N, tid);
@@ -599,53 +607,57 @@ __device__ __forceinline__ void finish_aligned(const LinearArgs &a, const LinTil
 #pragma unroll
       for (int jj = 0; jj < P; ++jj) bias[jj].load(a.bias, x.group * a.N + lesser(col + 32 * jj, a.N - 8));
     }
-    if (sloped) pre.load(br);
-    if (a.residual) res.load(rr);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (sloped) pre.take(br[u]);
+      if (a.residual) res.take(rr[u]);
+    }
     with_activation(a.act, [&](auto act) __attribute__((always_inline)) {
       constexpr int ACT = decltype(act)::value;
 #pragma unroll 1
-      for (int i = 0; i < W; ++i) {
-        float v[P][8], f[8];
-        take_row(acc, i, v);
-        if (forward) {
-          if (biased) {
+      for (int i = 0; i < W; i += 2) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float v[P][8], f[8];
+          take_row(acc, i + u, v);
+          if (forward) {
+            if (biased) {
+#pragma unroll
+              for (int jj = 0; jj < P; ++jj) {
+                bias[jj].get(f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[jj][e] += f[e];
+              }
+            }
+            if (kept) {
+              pre.store(v);
+              pre.next();
+            }
+#pragma unroll
+            for (int jj = 0; jj < P; ++jj)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[jj][e] = activate<BF16>(ACT, v[jj][e]);
+          } else if constexpr (ACT != ACT_NONE) {
 #pragma unroll
             for (int jj = 0; jj < P; ++jj) {
-              bias[jj].get(f);
+              br[u][jj].get(f);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[jj][e] *= slope<BF16>(ACT, f[e]);
+            }
+            pre.take(br[u]);
+          }
+          if (a.residual) {
+#pragma unroll
+            for (int jj = 0; jj < P; ++jj) {
+              rr[u][jj].get(f);
 #pragma unroll
               for (int e = 0; e < 8; ++e) v[jj][e] += f[e];
             }
+            res.take(rr[u]);
           }
-          if (kept) {
-            pre.store(v);
-            pre.next();
-          }
-#pragma unroll
-          for (int jj = 0; jj < P; ++jj)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[jj][e] = activate<BF16>(ACT, v[jj][e]);
-        } else if constexpr (ACT != ACT_NONE) {
-#pragma unroll
-          for (int jj = 0; jj < P; ++jj) {
-            br[jj].get(f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[jj][e] *= slope<BF16>(ACT, f[e]);
-          }
-          pre.next();
-          pre.load(br);  // behind the last row: nothing
+          out.store(v);
+          out.next();
         }
-        if (a.residual) {
-#pragma unroll
-          for (int jj = 0; jj < P; ++jj) {
-            rr[jj].get(f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[jj][e] += f[e];
-          }
-          res.next();
-          res.load(rr);
-        }
-        out.store(v);
-        out.next();
       }
     });
   }

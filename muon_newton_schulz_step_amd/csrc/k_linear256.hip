@@ -125,7 +125,6 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
   Cursor at = start(x);
   int base = 0;        // buffer of the tile's first stage
   bool ready = false;  // whose loads, and the second one's, are under way
-  bool full = false;   // the tile before was whole: every thread has stored 32 times since
   for (;;) {
     // at least two stages: what is behind the last one is zeros
     const int nk = (int)greater(2, (x.k1 - x.k0 + KS - 1) / KS);
@@ -153,8 +152,8 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
 #pragma unroll
         for (int q = 0; q < 16; ++q) dma1(s1, base ^ 1, q);
       }
-      // all but the second stage's 16 loads, and 32 stores
-      if (ready && full) asm volatile("s_waitcnt vmcnt(48) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      // all but the second stage's 16 loads, and behind a tile its 32 stores or more
+      if (ready) asm volatile("s_waitcnt vmcnt(48) lgkmcnt(0)\n\ts_barrier" ::: "memory");
       else asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)\n\ts_barrier" ::: "memory");
       if constexpr (QUEUE) {
         chain = queued(uni32(*next_slot), y);
@@ -190,8 +189,8 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
           __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (KIND != LAST) {
-          // the next stage's loads: all but the six since, and after a whole tile its 32 stores
-          if (KIND == FIRST && ready && full) asm volatile("s_waitcnt vmcnt(38)\n\ts_barrier" ::: "memory");
+          // the next stage's loads: all but the six since, and behind a tile its 32 stores or more
+          if (KIND == FIRST && ready) asm volatile("s_waitcnt vmcnt(38)\n\ts_barrier" ::: "memory");
           else asm volatile("s_waitcnt vmcnt(6)\n\ts_barrier" ::: "memory");
         }
 #pragma unroll
@@ -233,7 +232,6 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
       if (threadIdx.x == 0) *next_slot = taken;
     }
     ready = true;
-    full = x.rows == BT && a.N - x.col0 >= BT;
     base = (nk + base) & 1;
     x = y;
   }

@@ -157,11 +157,11 @@ def expert_combine(y, place, out, weights=None, residual=None, stream=None) -> N
 def expert_combine_backward(dout, place, dy=None, weights=None, y=None, dweights=None, stream=None) -> None:
     """dy[place[t, j]] = weights[t, j] * dout[t] (rows of no place are kept) and dweights[t, j] = the sum of dout[t] *
     y[place[t, j]] (0 for a place outside); either may be None.  y is needed for dweights only; dy may be y."""
+    if dy is None and dweights is None:
+        _refuse("expert_combine_backward", "neither dy nor dweights is asked for")
     tokens, dim, dold, dt = _matrix(dout, "dout")
     k = _place(place, tokens)
     rows = yld = dyld = 0
-    if dy is None and dweights is None:
-        _refuse("expert_combine_backward", "neither dy nor dweights is asked for")
     if dweights is not None:
         if y is None:
             _refuse("dweights", "needs y")

@@ -75,6 +75,7 @@ __device__ __forceinline__ float slope(int32_t act, float v) {
     }
     case ACT_GELU: return fmaf(v * 0.39894228f, exp_fast(-0.5f * v * v), normal_cdf<BF16>(v));
     case ACT_GELU_TANH: {
+      v = v < -64.f ? -64.f : v > 64.f ? 64.f : v;  // 0 and 1 from there on, where v^2 is still finite
       const float q = tanh_gate<BF16>(v);
       return fmaf(v * q * (1.f - q), fmaf(0.2140644489f, v * v, 1.5957691216f), q);
     }

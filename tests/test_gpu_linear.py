@@ -275,3 +275,79 @@ def test_linear_of_middle_tiles(torch, rows, a, b, groups, ld, dtype, layout):
 def test_linear_of_large_tiles_with_activations(torch, act):
     check_linear(torch, 3501, 200, 3600, "bf16", "in_out", act=act, pre=True, whole=False)
     check_linear(torch, 3501, 3600, 136, "bf16", "out_in", act=act, pre=True, whole=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,a,b", [(1, 1, 1), (1, 3, 1), (3, 1, 1), (1, 1, 3), (2, 2, 2), (1, 33, 67), (5, 65, 1), (130, 7, 3), (131, 197, 129), (2051, 130, 2062)])
+@pytest.mark.parametrize("layout", ["in_out", "out_in"])
+def test_linear_of_unaligned_rows_between_others(torch, dtype, rows, a, b, layout):
+    # NaN before, between and behind the rows of every operand, at every remainder of 16 bytes, reaches nothing
+    rng = np.random.default_rng(rows + a)
+
+    def inside(values, shift):
+        r, c = values.shape
+        buf = torch.full((shift + (r + 1) * (c + 3) + 16,), float("nan"), dtype=dt(torch, dtype), device=DEV)
+        v = torch.as_strided(buf, (r, c), (c + 3, 1), shift)
+        v.copy_(torch.from_numpy(values).to(DEV))
+        return v
+    x, w, dy = (rng.integers(-2, 3, s).astype(np.float64) for s in ((rows, a), (a, b), (rows, b)))
+    for shift in (1, 2, 3):
+        xd, dyd = inside(x, shift), inside(dy, shift)
+        wd = inside(w, shift) if layout == "in_out" else inside(np.ascontiguousarray(w.T), shift).t()
+        out, dx, dw = (torch.empty(s, dtype=xd.dtype, device=DEV) for s in ((rows, b), (rows, a), (a, b)))
+        dw = dw.float()
+        ws = poisoned(torch, max(M.linear_workspace_bytes(rows, a, b, 1), M.linear_workspace_bytes(rows, b, a, 1),
+                                 M.linear_weight_grad_workspace_bytes(rows, a, b, 1)))
+        M.linear_forward(xd, wd, out, ws)
+        M.linear_input_grad(dyd, wd, dx, ws)
+        M.linear_weight_grad(xd, dyd, dw, True, ws)
+        assert np.array_equal(f64(out), rounded(torch, x @ w, dtype))
+        assert np.array_equal(f64(dx), rounded(torch, dy @ w.T, dtype))
+        assert np.array_equal(f64(dw), x.T @ dy)
+
+
+@pytest.mark.parametrize("act", ACTS[1:])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_activations_of_huge_numbers(torch, act, dtype):
+    # far out every activation is v or 0 and its slope 1 or 0, also where v^2 is no longer a number of the type
+    v = np.array([100.0, 1e4, 3e9, 2e19, 1e30, 3e38])
+    for sign in (1, -1):
+        x = torch.from_numpy(sign * v).to(dt(torch, dtype)).to(DEV)[:, None].contiguous()
+        out, dx, one = torch.empty_like(x), torch.empty_like(x), torch.ones(1, 1, dtype=x.dtype, device=DEV)
+        ws = poisoned(torch, M.linear_workspace_bytes(len(v), 1, 1, 1))
+        M.linear_forward(x, one, out, ws, activation=act)
+        M.activation_grad(torch.ones_like(x), x, dx, act)
+        assert torch.equal(out, x if sign > 0 else torch.zeros_like(x))
+        assert torch.equal(dx, torch.full_like(x, max(sign, 0)))
+        M.linear_input_grad(torch.ones_like(x), one, dx, ws, pre=x, activation=act)
+        assert torch.equal(dx, torch.full_like(x, max(sign, 0)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("layout", ["in_out", "out_in"])
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("a,b,groups", [(8, 8, None), (2056, 72, None), (1032, 4112, None), (136, 264, 5), (3080, 40, 70)])
+def test_linear_of_few_rows(torch, rows, dtype, layout, a, b, groups):
+    check_linear(torch, rows, a, b, dtype, layout, groups, kind="full" if rows % 2 else "any", pre=True, ld=8, shift=8, first=rows % 2 == 0)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("layout", ["in_out", "out_in"])
+def test_linear_of_few_rows_with_activations(torch, act, dtype, layout):
+    check_linear(torch, 3, 2048, 136, dtype, layout, act=act, pre=True, whole=False)
+    check_linear(torch, 8, 96, 2064, dtype, layout, groups=4, act=act, pre=True, whole=False)
+
+
+def test_linear_of_few_rows_beside_nan(torch):
+    # a row, an expert and what lies between the rows hold NaN: other rows do not see them
+    for layout in ("in_out", "out_in"):
+        w, _ = matrices(torch, np.ones((3, 1096, 72)), "bf16", layout, 8, 8, 16)
+        w[1].fill_(float("nan"))
+        x = torch.full((6, 1104), float("nan"), dtype=torch.bfloat16, device=DEV)
+        x[1:4, :1096] = 1.0
+        x[5, :1096] = 1.0
+        off = torch.tensor([1, 4, 4, 6], dtype=torch.int32, device=DEV)
+        out = torch.full((6, 72), 7.0, dtype=torch.bfloat16, device=DEV)
+        M.linear_forward(x[:, :1096], w, out, poisoned(torch, M.linear_workspace_bytes(6, 1096, 72, 3)), offsets=off)
+        assert bool((out[0] == 7).all()) and bool((out[[1, 2, 3, 5]] == 1096).all()) and bool(out[4].isnan().all())

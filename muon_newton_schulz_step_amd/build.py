@@ -24,7 +24,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["plan.cpp", "abi.cpp", "noalloc.hip", "k_elem.hip", "k_gemm.hip", "k_gemm256.hip", "k_head.hip",
            "train_abi.cpp", "k_embed.hip", "k_logits.hip", "k_balance.hip", "layer_abi.cpp", "k_dropout.hip", "k_route.hip",
-           "k_order.hip", "k_linear.hip", "k_linear256.hip"]
+           "k_order.hip", "k_linear.hip", "k_linear256.hip", "k_linear_few.hip"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops: keep the compiler from emitting packed fp32 VALU ops.

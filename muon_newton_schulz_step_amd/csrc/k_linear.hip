@@ -142,6 +142,8 @@ __device__ __forceinline__ int group_of(const LinearArgs &a, int64_t row) {
   return lo;
 }
 
+constexpr int JOINED = 4;
+
 // Adds up the parts of the sums, in their order: a thread eight neighbours.
 template <bool BF16>
 __global__ __launch_bounds__(256) void kl_join(LinearArgs a, int64_t rows) {
@@ -157,12 +159,25 @@ __global__ __launch_bounds__(256) void kl_join(LinearArgs a, int64_t rows) {
     g = group_of(a, row);
     if (g < 0) return;
   }
-  float v[8], w[8];
-  load8<false>(a.partial, row * a.N + col, n, v);
-  for (int s = 1; s < a.splits; ++s) {
-    load8<false>(a.partial, (s * rows + row) * a.N + col, n, w);
+  const float *p = a.partial + row * a.N + col;
+  const int64_t part = rows * a.N;
+  float v[8];
+  load8<false>(p, 0, n, v);
+  for (int s = 1; s < a.splits; s += JOINED) {
+    // loads of several parts under way together: one at a time costs 2.5 us more with 16 parts, 5 with 32
+    float w[JOINED][8];
+    if (n == 8) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += w[i];
+      for (int u = 0; u < JOINED; ++u) load8<false>(p, lesser(s + u, a.splits - 1) * part, 8, w[u]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < JOINED; ++u) load8<false>(p, lesser(s + u, a.splits - 1) * part, n, w[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < JOINED; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (s + u < a.splits) v[i] += w[u][i];
   }
   finish8<BF16>(a, g, a.mode == LIN_WEIGHT ? row - g * a.M : row, col, n, v);
 }
@@ -224,8 +239,18 @@ __global__ __launch_bounds__(CS_THREADS) void kl_column_join(ColumnSumArgs a) {
   const int64_t at = (int64_t)blockIdx.x * CS_THREADS + threadIdx.x;
   if (at >= a.cols) return;
   const int g = (int)blockIdx.y;
+  const float *p = a.partial + (int64_t)g * a.splits * a.cols + at;
   double v = 0.0;
-  for (int s = 0; s < a.splits; ++s) v += (double)a.partial[((int64_t)g * a.splits + s) * a.cols + at];
+  int s = 0;
+  // eight loads under way together: one at a time 32 parts take 11 us
+  for (; s + 8 <= a.splits; s += 8) {
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = p[(s + i) * a.cols];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += (double)w[i];
+  }
+  for (; s < a.splits; ++s) v += (double)p[s * a.cols];
   a.out[g * a.cols + at] = a.first ? (float)v : (float)((double)a.out[g * a.cols + at] + v);
 }
 
@@ -287,6 +312,13 @@ bool large_tiles(const LinearArgs &a, bool weight) {
   return tiles >= 192 && a.N >= 256 && (weight ? a.M >= 256 : a.M / a.groups >= 256);
 }
 
+// Whether a product's rows are few enough for kl_few.  4096 x 11008, kl_few
+// against 64 x 64 tiles: fp32 of 8 rows 38 and 53 us (K adjacent, across)
+// against 70; bf16 of 4 rows 19 and 21 against 24, of 8 rows 26 and 29 against
+// 24.  Where K is adjacent smaller weights still gain with 8 (4096 x 4096: 11
+// against 17), and rows of groups are mostly of different ones.
+bool few_rows(const LinearArgs &a, bool bf16, bool bx) { return a.M <= (bf16 && bx && !a.offsets.p ? 4 : FEW_ROWS); }
+
 }  // namespace
 
 size_t linear_partial_bytes(int64_t M, int64_t N, int64_t K, int32_t groups, bool weight) {
@@ -307,23 +339,28 @@ hipError_t launch_linear(LinearArgs a, bool bf16, int la, int lb, hipStream_t s)
     a.tiles_n = (int32_t)((a.N + 255) / 256);
     return launch_linear256(a, bx, s);
   }
-  const LinearPlan p = plan_of(a.M, a.N, a.K, a.groups, weight);
-  const int bt = 32 * p.w;
-  a.splits = p.splits;
-  a.tiles_m = (int32_t)tiles_along(a.M, a.groups, !weight && a.offsets.p, bt);
-  a.tiles_n = (int32_t)((a.N + bt - 1) / bt);
-  const int64_t grid = (int64_t)a.tiles_m * a.tiles_n * (weight ? a.groups : 1) * a.splits;
-  const unsigned g = (unsigned)grid;
-  if (bf16) {
-    if (ax) go<true, true, true>(a, dma, p.w, g, s);
-    else if (bx) go<true, false, true>(a, dma, p.w, g, s);
-    else go<true, false, false>(a, dma, p.w, g, s);
+  hipError_t err;
+  if (dma && !weight && few_rows(a, bf16, bx)) {
+    err = launch_linear_few(a, bf16, bx, s);
   } else {
-    if (ax) go<false, true, true>(a, dma, p.w, g, s);
-    else if (bx) go<false, false, true>(a, dma, p.w, g, s);
-    else go<false, false, false>(a, dma, p.w, g, s);
+    const LinearPlan p = plan_of(a.M, a.N, a.K, a.groups, weight);
+    const int bt = 32 * p.w;
+    a.splits = p.splits;
+    a.tiles_m = (int32_t)tiles_along(a.M, a.groups, !weight && a.offsets.p, bt);
+    a.tiles_n = (int32_t)((a.N + bt - 1) / bt);
+    const int64_t grid = (int64_t)a.tiles_m * a.tiles_n * (weight ? a.groups : 1) * a.splits;
+    const unsigned g = (unsigned)grid;
+    if (bf16) {
+      if (ax) go<true, true, true>(a, dma, p.w, g, s);
+      else if (bx) go<true, false, true>(a, dma, p.w, g, s);
+      else go<true, false, false>(a, dma, p.w, g, s);
+    } else {
+      if (ax) go<false, true, true>(a, dma, p.w, g, s);
+      else if (bx) go<false, false, true>(a, dma, p.w, g, s);
+      else go<false, false, false>(a, dma, p.w, g, s);
+    }
+    err = hipGetLastError();
   }
-  hipError_t err = hipGetLastError();
   if (err != hipSuccess || a.splits == 1) return err;
   const int64_t rows = a.M * (weight ? a.groups : 1), threads = rows * ((a.N + 7) / 8);
   if (bf16) hipLaunchKernelGGL(kl_join<true>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a, rows);

@@ -279,19 +279,24 @@ int64_t tiles_along(int64_t M, int32_t groups, bool grouped, int bt) {
 }
 
 // Tiles of 128 x 128 if they fill the chip, of 64 x 64 otherwise, and then K in
-// parts: enough for four workgroups a CU, of four stages each and more, as far
-// as their sums take no more than 64 MB.
+// parts: enough for four workgroups a CU, of 8 stages of 64 (bf16) or 4 (fp32,
+// whose stages take twice as long) and more, as far as their sums take no more
+// than 64 MB.  64 x 4096 x 4096 bf16: 15.0 us in parts of 8 stages, 17.8 of 4;
+// 64 x 1024 x 1024 fp32: 13.1 in parts of 4, 19.1 of 8.  Where one tile a CU
+// fills the chip, parts begin to pay at 24 stages (1021 x 1000 bf16, whole and
+// in parts: K = 512 6.8 and 14.5 us, 1024 13.4 and 16.9, 2048 23.6 and 21.3).
 struct LinearPlan {
   int w;
   int32_t splits;
 };
-LinearPlan plan_of(int64_t M, int64_t N, int64_t K, int32_t groups, bool weight) {
+LinearPlan plan_of(int64_t M, int64_t N, int64_t K, int32_t groups, bool weight, bool bf16) {
   const int64_t per = weight ? groups : 1;
   if ((M + 127) / 128 * ((N + 127) / 128) * per >= 256) return {4, 1};
   const int64_t tiles = (M + 63) / 64 * ((N + 63) / 64) * per;
   const int64_t stages = (K / (weight ? groups : 1) + 63) / 64;
+  if (tiles >= 256 && stages < 24) return {2, 1};
   const int64_t bytes = std::max<int64_t>(1, M * per * N * 4);
-  const int64_t parts = std::min<int64_t>({1024 / std::max<int64_t>(1, tiles), stages / 4, ((int64_t)64 << 20) / bytes, 32});
+  const int64_t parts = std::min<int64_t>({1024 / std::max<int64_t>(1, tiles), stages / (bf16 ? 8 : 4), ((int64_t)64 << 20) / bytes, 32});
   return {2, (int32_t)std::max<int64_t>(1, parts)};
 }
 
@@ -322,7 +327,7 @@ bool few_rows(const LinearArgs &a, bool bf16, bool bx) { return a.M <= (bf16 && 
 }  // namespace
 
 size_t linear_partial_bytes(int64_t M, int64_t N, int64_t K, int32_t groups, bool weight) {
-  const int32_t parts = plan_of(M, N, K, groups, weight).splits;
+  const int32_t parts = std::max(plan_of(M, N, K, groups, weight, false).splits, plan_of(M, N, K, groups, weight, true).splits);
   return parts > 1 ? (size_t)parts * (size_t)(M * (weight ? groups : 1)) * (size_t)N * 4 : 0;
 }
 
@@ -343,7 +348,7 @@ hipError_t launch_linear(LinearArgs a, bool bf16, int la, int lb, hipStream_t s)
   if (dma && !weight && few_rows(a, bf16, bx)) {
     err = launch_linear_few(a, bf16, bx, s);
   } else {
-    const LinearPlan p = plan_of(a.M, a.N, a.K, a.groups, weight);
+    const LinearPlan p = plan_of(a.M, a.N, a.K, a.groups, weight, bf16);
     const int bt = 32 * p.w;
     a.splits = p.splits;
     a.tiles_m = (int32_t)tiles_along(a.M, a.groups, !weight && a.offsets.p, bt);

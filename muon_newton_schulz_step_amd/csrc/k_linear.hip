@@ -57,7 +57,16 @@ __global__ __launch_bounds__(LIN_THREADS, 8 / W) void kl_linear(LinearArgs a) {
       offb[j] = ob.offset(j);
     }
   }
-  auto fetch = [&](int kt, int st) {
+  const T *qa[L], *qb[L];  // (not DMA) the next plain stage
+  if constexpr (!DMA) {
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      qa[j] = oa.plain(x.k0, j);
+      qb[j] = ob.plain(x.k0, j);
+    }
+  }
+  // PLAIN: of a stage with another k behind it (see Operand)
+  auto fetch = [&](int kt, int st, auto plain) {
     const int64_t k = x.k0 + (int64_t)kt * KS;
     char *la = lds + st * 2 * OPB, *lb = la + OPB;
     if constexpr (DMA) {
@@ -67,6 +76,14 @@ __global__ __launch_bounds__(LIN_THREADS, 8 / W) void kl_linear(LinearArgs a) {
       for (int j = 0; j < L; ++j) {
         OA::dma(ars, oa.left(k), offa[j], la, j);
         OB::dma(brs, ob.left(k), offb[j], lb, j);
+      }
+    } else if constexpr (decltype(plain)::value) {
+#pragma unroll
+      for (int j = 0; j < L; ++j) {
+        ra[j] = load16(qa[j]);
+        rb[j] = load16(qb[j]);
+        qa[j] += OA::step(a.lda) / (int)sizeof(T);
+        qb[j] += OB::step(a.ldb) / (int)sizeof(T);
       }
     } else {
 #pragma unroll
@@ -87,14 +104,8 @@ __global__ __launch_bounds__(LIN_THREADS, 8 / W) void kl_linear(LinearArgs a) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
   };
-  if (nk > 0) {
-    fetch(0, 0);
-    land(0);
-  }
-  for (int kt = 0; kt < nk; ++kt) {
-    const int st = kt & 1;
+  auto multiply = [&](int st) {
     const char *la = lds + st * 2 * OPB, *lb = la + OPB;
-    if (kt + 1 < nk) fetch(kt + 1, st ^ 1);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       if constexpr (BF16) {
@@ -123,7 +134,30 @@ __global__ __launch_bounds__(LIN_THREADS, 8 / W) void kl_linear(LinearArgs a) {
             for (int j = 0; j < W; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fb[j][c], fa[i][c], acc[i][j], 0, 0, 0);
       }
     }
-    if (kt + 1 < nk) land(st ^ 1);
+  };
+  // Plain stages, in a loop of their own, as loads under questions keep each
+  // other waiting (2047 x 4095 x 4095 bf16: 107 us, 329 with questions in every
+  // stage).
+  int np = 0;
+  if constexpr (!DMA) np = nk > 0 && oa.has_plain() && ob.has_plain() ? nk - 1 : 0;
+  const std::true_type yes;
+  const std::false_type no;
+  if (nk > 0) {
+    if (np > 0) fetch(0, 0, yes);
+    else fetch(0, 0, no);
+    land(0);
+  }
+  int kt = 0;
+  if constexpr (!DMA)
+    for (; kt + 1 < np; ++kt) {
+      fetch(kt + 1, (kt & 1) ^ 1, yes);
+      multiply(kt & 1);
+      land((kt & 1) ^ 1);
+    }
+  for (; kt < nk; ++kt) {
+    if (kt + 1 < nk) fetch(kt + 1, (kt & 1) ^ 1, no);
+    multiply(kt & 1);
+    if (kt + 1 < nk) land((kt & 1) ^ 1);
   }
   if constexpr (DMA) finish_aligned<BF16, W, AX ? (int)LIN_WEIGHT : -1, true>(a, x, acc, (int)threadIdx.x);
   else finish_any<BF16, W, AX>(a, x, acc, (int)threadIdx.x);

@@ -288,17 +288,44 @@ struct Operand {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_any *)(lds + (w * LOADS + j) * 1024), 16, off, 0, 0, 0);
   }
   __device__ __forceinline__ int left(int64_t k) const { return (int)lesser(k1 - k, KS); }
-  // The same through registers, at any alignment and with any end.
+  // The same through registers, at any alignment.  A stage with another k
+  // behind it is loaded by sixteen bytes without a question: a row that does
+  // not exist repeats the last one, and of columns that do not exist the first
+  // ones or what lies behind the row's end; their sums are not stored.  (Rows
+  // across K have to be 16 bytes apart for that to stay inside the operand.)
+  __device__ __forceinline__ const T *plain(int64_t k, int j) const {
+    const int r = row(j), c = chunk(j) * N;
+    return p + (ACROSS ? (k + r) * ld + (c < extent ? c : 0) : lesser(r, extent - 1) * ld + c + k);
+  }
+  __device__ __forceinline__ bool has_plain() const { return !ACROSS || ld >= N; }
+  // Any stage.  Sixteen bytes that do not all exist are loaded as a whole too,
+  // unless they go past the operand's last element, and what does not exist
+  // along K becomes 0.
   __device__ __forceinline__ uint4 load(int64_t k, int j) const {
     const int r = row(j), c = chunk(j) * N;
     const int64_t have = ACROSS ? (k + r < k1 ? (int64_t)extent - c : 0) : (r < extent ? k1 - k - c : 0);
-    const T *q = p + (ACROSS ? (k + r) * ld + c : r * ld + k + c);
-    if (have >= N) return load16(q);
+    const int64_t at = ACROSS ? (k + r) * ld + c : r * ld + k + c;
+    if (have >= N) return load16(p + at);
+    if (have <= 0) return make_uint4(0, 0, 0, 0);
+    if (at + N <= (ACROSS ? (k1 - 1) * ld + extent : (int64_t)(extent - 1) * ld + k1)) {
+      const uint4 v = load16(p + at);
+      return ACROSS ? v : first_of(v, (int)have);
+    }
     T e[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) e[i] = i < have ? q[i] : T(0);
+    for (int i = 0; i < N; ++i) e[i] = i < have ? p[at + i] : T(0);
     uint4 v;
     __builtin_memcpy(&v, e, 16);
+    return v;
+  }
+  // The first n elements (0 < n < N), and zeros.
+  static __device__ __forceinline__ uint4 first_of(uint4 v, int n) {
+    uint64_t q[2];
+    __builtin_memcpy(q, &v, 16);
+    const int bits = n * E * 8;
+    q[0] &= bits >= 64 ? ~0ull : (1ull << bits) - 1;
+    q[1] &= bits <= 64 ? 0ull : (1ull << (bits - 64)) - 1;
+    __builtin_memcpy(&v, q, 16);
     return v;
   }
   static __device__ __forceinline__ void put(char *lds, int j, uint4 v) {

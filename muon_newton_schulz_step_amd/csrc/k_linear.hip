@@ -345,10 +345,12 @@ void go(const LinearArgs &a, bool dma, int w, unsigned grid, hipStream_t s) {
   }
 }
 
-// Whether 256 x 256 tiles are many enough to fill the chip.
+// Whether 256 x 256 tiles are many enough: 128 of them are 512 of 128 x 128,
+// which fill the chip once (4096 x 4096 weights, on large and small tiles: 128
+// large ones 113 and 69 us, 160 108 and 122, 208 108 and 129, 256 110 and 134).
 bool large_tiles(const LinearArgs &a, bool weight) {
   const int64_t tiles = (a.M + 255) / 256 * ((a.N + 255) / 256) * (weight ? a.groups : 1);
-  return tiles >= 192 && a.N >= 256 && (weight ? a.M >= 256 : a.M / a.groups >= 256);
+  return tiles >= 160 && a.N >= 256 && (weight ? a.M >= 256 : a.M / a.groups >= 256);
 }
 
 // Whether a product's rows are few enough for kl_few.  4096 x 11008, kl_few

@@ -8,10 +8,11 @@
 // plus the number of lanes before it with the same expert, found by comparing
 // the experts' bits across the wave (a ballot a bit).  Nothing depends on the
 // order in which workgroups run.  Bound by latency: a few dependent passes over
-// some hundred KB.
+// some hundred KB (131072 choices of 256 experts: 4.8 + 5.3 + 7.6 us).
 //
 // Sum: out[t] = residual[t] + sum_j w[t][j] y[place[t][j]], in fp32, j by j,
-// rounded once.  Bound by HBM: every row of y is read once.
+// rounded once.  Bound by HBM: every row of y is read once (16384 x 8 rows of
+// 4096 bf16: 240 us, 5.0 TB/s; the gradients 449).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -28,7 +29,9 @@ namespace {
 constexpr int OW = 4;            // waves of a workgroup, a part each
 constexpr int OP = 1024;         // parts, at most (a multiple of 64)
 constexpr int SOLO_WAVES = 16;
-constexpr int64_t ORDER_SOLO = 16384;  // up to so many choices one workgroup does the whole call
+// Up to so many choices one workgroup does the whole call: 8192 of 64 experts
+// take 11.7 us, 16384 20.3; three launches 13 of either.
+constexpr int64_t ORDER_SOLO = 8192;
 constexpr int SOLO_EXPERTS = 512;      // and up to so many experts (its counts are 32 KB of LDS)
 
 __device__ __forceinline__ int expert_at(const OrderArgs &a, int64_t i) {

@@ -8,7 +8,8 @@
 //
 //   d s_j = scale (dw_j - sum_i dw_i s_i / S) / S, or scale dw_j
 //   softmax: d x_e = [e chosen] s_e ds_e - s_e sum_j s_j ds_j
-//   sigmoid: d x_e = [e chosen] s_e (1 - s_e) ds_e
+//   sigmoid: d x_e = [e chosen] s_e (1 - s_e) ds_e, with 1 - s(x) = s(-x): from
+//   an s near 1 the difference keeps few digits, and none from x = 17 on
 //
 // Ranks are computed in fp32; a token in which two ranks that decide about the
 // choice or its order are closer than fp32 tells apart is decided again in
@@ -567,7 +568,7 @@ __global__ __launch_bounds__(RT) void kr_backward(RouteArgs a) {
     const float z = E::get(x[e]);
     const float s = a.softmax ? exp_term(z, m) * inv : sigmoid(z);
     const float ds = f * (a.dweights[t * a.k + j] - mean);
-    const float add = a.softmax ? s * ds : s * (1.f - s) * ds;
+    const float add = a.softmax ? s * ds : s * sigmoid(-z) * ds;
     const int at = e - l * N;
 #pragma unroll
     for (int i = 0; i < VECS; ++i)

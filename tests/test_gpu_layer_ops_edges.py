@@ -1,0 +1,100 @@
+"""The operators of a trained layer where digits, experts or limits are easily lost: routers that are sure of an
+expert, NaN beside masks, more tokens than a grid has lanes for, long sums of columns, activations far out.
+
+e = 2^-24 (half a step of fp32), h = half a step of the output's type.  Tolerances stand at each test.
+"""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import muon_newton_schulz_step_amd as M
+import oracle.layer_ops as L
+from test_gpu_train_ops import DEV, E, HALF, TINY, dt, f64, poisoned, torch, vec, within  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- routing
+
+
+def sure_logits(rng, t, n):
+    """Rows whose scores reach from almost 0 to almost 1."""
+    x = rng.standard_normal((t, n)).astype(np.float32)
+    far = np.linspace(0.0, 40.0, t).astype(np.float32)
+    x[:, n // 3] += far
+    x[::3, n // 2] += far[::3]
+    x[1::4] -= far[1::4, None]
+    return x
+
+
+def gradient(x, choices, dw, scoring, renormalize, scale):
+    """(the gradient, the size of what it is a sum of) in fp64, with the differences taken before the sums: of dw_e and
+    dw_j instead of dw_e and the mean, of the scores left over instead of 1 and the chosen ones."""
+    t, n = x.shape
+    x = x.astype(np.float64)
+    d, size = np.zeros((t, n)), np.zeros((t, n))
+    for r in range(t):
+        idx = choices[r]
+        g = dw[r].astype(np.float64)
+        if scoring == "sigmoid":
+            s, comp = 1.0 / (1.0 + np.exp(-x[r, idx])), 1.0 / (1.0 + np.exp(x[r, idx]))
+        else:
+            e = np.exp(x[r] - x[r].max())
+            p = e / e.sum()
+            s, left = p[idx], np.delete(e, idx).sum() / e.sum()
+        total = s.sum() + L.NORM_EPS
+        if renormalize:
+            pair = g[:, None] - g[None, :]                       # dw_j - dw_i
+            ds = scale / total ** 2 * (pair @ s + L.NORM_EPS * g)
+            dsize = scale / total ** 2 * (np.abs(pair) @ s + L.NORM_EPS * np.abs(g))
+            diff = scale / total * pair                          # ds_j - ds_i
+        else:
+            ds, dsize, diff = scale * g, scale * np.abs(g), scale * (g[:, None] - g[None, :])
+        if scoring == "sigmoid":
+            d[r, idx], size[r, idx] = s * comp * ds, s * comp * dsize
+            continue
+        inner = (s * ds).sum()
+        if renormalize:
+            inner = (scale * g * s).sum() * L.NORM_EPS / total ** 2
+            d[r] = -p * inner
+            d[r, idx] = s * (ds - inner)
+            size[r] = p * abs(inner)
+            size[r, idx] += s * dsize
+        else:
+            d[r] = -p * inner
+            size[r] = p * (s * np.abs(ds)).sum()
+            d[r, idx] = s * (left * ds + diff @ s)
+            size[r, idx] = s * (left * np.abs(ds) + np.abs(diff) @ s)
+    return d, size
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid"])
+@pytest.mark.parametrize("renorm", [False])
+@pytest.mark.parametrize("n,k", [(8, 1), (8, 2), (40, 6), (256, 8), (700, 20), (30, 30), (200, 32)])
+def test_gradient_of_a_sure_router(torch, n, k, scoring, renorm):
+    # A score near 1 leaves 1 - s, and a mean of dw that is all but one dw, with few digits: what is left over has to
+    # be had from what it is made of.
+    # Tolerance: scores carry (|d| + 60) e of themselves (sigmoid: (|x| + 8) e, its complement as much), of which an
+    # element has four, and 12 e of operations; 2^-50 of dw s / total for sums in 64 bits.
+    rng = np.random.default_rng(n + k)
+    t, scale = 41, 2.5
+    x = sure_logits(rng, t, n)
+    choices = np.stack([rng.permutation(n)[:k] for _ in range(t)])
+    choices[:, 0] = n // 3
+    for r in range(t):
+        others = [e for e in choices[r, 1:] if e != n // 3]
+        more = [e for e in range(n) if e != n // 3 and e not in others]
+        choices[r, 1:] = (others + more)[:k - 1]
+    dw = rng.standard_normal((t, k)).astype(np.float32)
+    want, size = gradient(x, choices, dw, scoring, renorm, scale)
+    out = torch.full((t, n), 9.0, device=DEV)
+    M.route_backward(vec(torch, x), vec(torch, choices, "int32"), vec(torch, dw), out, True, scoring=scoring,
+                     renormalize=renorm, scale=scale)
+    x = x.astype(np.float64)
+    rel = (np.abs(x).max(axis=1) + 8) if scoring == "sigmoid" else (x.max(axis=1) - x.min(axis=1) + 60)
+    s = L.scores(x, scoring)
+    total = (np.take_along_axis(s, choices, 1).sum(axis=1, keepdims=True) if renorm else 1.0)
+    sums = 2.0 ** -50 * scale * np.abs(dw).max(axis=1, keepdims=True) * s / total
+    within(f64(out), want, size * (4 * rel[:, None] + 12) * E + np.abs(want) * E + sums + TINY, "gradient by the logits")

@@ -18,7 +18,7 @@
 //
 // Few lanes a token, so that what a choice exchanges stays within a row of
 // lanes.  131072 x 256 fp32, 8 of 256 in 4 of 8 groups: the choice 96 us, bound
-// by its comparisons (the bytes take 26), the gradient 50, bound by HBM.
+// by its comparisons (the bytes take 26), the gradient 41.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -70,6 +70,13 @@ __device__ __forceinline__ int reduce_min(int v) {
     v = min(v, __shfl_xor(v, 16));
     v = min(v, __shfl_xor(v, 32));
   }
+  return v;
+}
+// Sum over LANES consecutive lanes; every lane gets it.
+template <int LANES>
+__device__ __forceinline__ double add_up(double v) {
+#pragma unroll
+  for (int d = 1; d < LANES; d <<= 1) v += shfl_xor_f64(v, d);
   return v;
 }
 struct Max {
@@ -487,20 +494,28 @@ __global__ __launch_bounds__(RT) void kr_route(RouteArgs a) {
   }
 }
 
-// LANES lanes take a token, VECS 16-byte vectors a lane.
-template <bool BF16, int LANES, int VECS>
+// LANES lanes take a token, VECS 16-byte vectors a lane, and the choices a lane
+// each, in up to Q rounds.
+//
+// Where one score holds nearly all of a sum, what the gradient is made of
+// cancels: dw_j against the mean of dw, ds_e against sum_j s_j ds_j.  Sums and
+// differences of the chosen are in fp64, on scores whose own error is a factor
+// (softmax: exponentials over their sum in fp64), so that only the factors'
+// errors are left; in fp32 a score of 1 - 1e-6 left 6% of error.
+template <bool BF16, int LANES, int VECS, int Q>
 __global__ __launch_bounds__(RT) void kr_backward(RouteArgs a) {
   typedef Elem<BF16> E;
   typedef typename E::type T;
   constexpr int PER = RT / LANES, N = E::N;
-  const int l = threadIdx.x & (LANES - 1);
+  const int l = threadIdx.x & (LANES - 1), lane0 = (int)(threadIdx.x & 63) - l;
   const int64_t t = (int64_t)blockIdx.x * PER + threadIdx.x / LANES;
   const bool in = t < a.tokens;
   const bool ok = in && (!a.valid || a.valid[t]);
   const int64_t row = ok ? t : 0;
   const T *x = static_cast<const T *>(a.logits) + row * a.ld;
   float v[VECS][N];
-  float m = 0.f, inv = 0.f;
+  float m = 0.f;
+  double inv = 0.0;
   if (a.softmax) {
     m = kLowest;
 #pragma unroll
@@ -516,65 +531,84 @@ __global__ __launch_bounds__(RT) void kr_backward(RouteArgs a) {
       for (int j = 0; j < N; ++j) m = fmaxf(m, v[i][j]);
     }
     m = reduce_f<LANES>(m, Max());
-    float s = 0.f;
+    double s = 0.0;
 #pragma unroll
     for (int i = 0; i < VECS; ++i)
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         v[i][j] = exp_term(v[i][j], m);
-        s += v[i][j];
+        s += (double)v[i][j];
       }
-    inv = inverse(reduce_f<LANES>(s, Sum()));
+    s = add_up<LANES>(s);
+    inv = s == 0.0 ? 0.0 : 1.0 / s;
   }
   // the chosen experts' scores, their sum S and sum_i dw_i s_i
-  float total = 0.f, dot = 0.f;
-  for (int j0 = 0; j0 < a.k; j0 += LANES) {
-    const int j = j0 + l;
-    float s = 0.f, dw = 0.f;
+  int e[Q];
+  float dw[Q];
+  double s[Q], total = 0.0, dot = 0.0;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    const int j = l + LANES * q;
+    e[q] = -1;
+    dw[q] = 0.f;
+    s[q] = 0.0;
     if (ok && j < a.k) {
-      const int64_t e = index_at(a.choices, t * a.k + j);
-      if (e >= 0 && e < a.experts) {
-        const float z = E::get(x[e]);
-        s = a.softmax ? exp_term(z, m) * inv : sigmoid(z);
-        dw = a.dweights[t * a.k + j];
-        dot += dw * s;
+      const int64_t c = index_at(a.choices, t * a.k + j);
+      if (c >= 0 && c < a.experts) {
+        e[q] = (int)c;
+        const float z = E::get(x[e[q]]);
+        s[q] = a.softmax ? (double)exp_term(z, m) * inv : (double)sigmoid(z);
+        dw[q] = a.dweights[t * a.k + j];
+        dot += (double)dw[q] * s[q];
       }
     }
-    total += s;
+    total += s[q];
   }
-  total = reduce_f<LANES>(total, Sum());
-  dot = reduce_f<LANES>(dot, Sum());
-  const float S = a.renormalize ? total + NORM_EPS : 1.f;
-  const float f = a.scale / S;
-  const float mean = a.renormalize ? dot / S : 0.f;
+  total = add_up<LANES>(total);
+  dot = add_up<LANES>(dot);
+  const double over = a.renormalize ? 1.0 / (total + (double)NORM_EPS) : 1.0;  // 1 / S
+  const double f = (double)a.scale * over;
+  const double mean = a.renormalize ? dot * over : 0.0;
   // sum_j s_j ds_j; renormalised it is scale / S dot (1 - total / S), all but 0
-  const float inner = a.renormalize ? f * dot * (NORM_EPS / S) : f * dot;
-  if (a.softmax) {
+  const double inner = !a.softmax ? 0.0 : a.renormalize ? f * dot * ((double)NORM_EPS * over) : f * dot;
+  // what a choice gives its expert: the whole element, or where an earlier
+  // choice is the same expert what it adds to that
+  float whole[Q], more[Q];
 #pragma unroll
-    for (int i = 0; i < VECS; ++i)
-#pragma unroll
-      for (int j = 0; j < N; ++j) v[i][j] = -(v[i][j] * inv) * inner;
-  } else {
-#pragma unroll
-    for (int i = 0; i < VECS; ++i)
-#pragma unroll
-      for (int j = 0; j < N; ++j) v[i][j] = 0.f;
+  for (int q = 0; q < Q; ++q) {
+    const double ds = f * ((double)dw[q] - mean);
+    if (a.softmax) {
+      whole[q] = (float)(s[q] * (ds - inner));
+      more[q] = (float)(s[q] * ds);
+    } else {
+      whole[q] = more[q] = e[q] >= 0 ? (float)(s[q] * (double)sigmoid(-E::get(x[e[q]])) * ds) : 0.f;
+    }
   }
-  for (int j = 0; j < a.k; ++j) {
-    if (!ok) break;
-    const int64_t e64 = index_at(a.choices, t * a.k + j);
-    if (e64 < 0 || e64 >= a.experts) continue;
-    const int e = (int)e64;
-    const float z = E::get(x[e]);
-    const float s = a.softmax ? exp_term(z, m) * inv : sigmoid(z);
-    const float ds = f * (a.dweights[t * a.k + j] - mean);
-    const float add = a.softmax ? s * ds : s * sigmoid(-z) * ds;
-    const int at = e - l * N;
+  const float part = (float)(inv * inner);
 #pragma unroll
-    for (int i = 0; i < VECS; ++i)
+  for (int i = 0; i < VECS; ++i)
 #pragma unroll
-      for (int q = 0; q < N; ++q)
-        if (at == LANES * N * i + q) v[i][q] += add;
+    for (int j = 0; j < N; ++j) v[i][j] = a.softmax ? -v[i][j] * part : 0.f;
+  uint32_t again = 0;  // of this lane's choices, those whose expert has come before
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    for (int u = 0; u < LANES && u + LANES * q < a.k; ++u) {
+      const bool second = again >> q & 1;
+      const int c = __shfl(second ? -2 - e[q] : e[q], lane0 + u);  // -1: none; below: second
+      const float add = __shfl(second ? more[q] : whole[q], lane0 + u);
+      if (c != -1) {
+        const int which = c < 0 ? -2 - c : c;
+#pragma unroll
+        for (int p = 0; p < Q; ++p)
+          if (e[p] == which && (p > q || (p == q && l > u))) again |= 1u << p;
+        const int at = which - l * N;
+#pragma unroll
+        for (int i = 0; i < VECS; ++i)
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (at == LANES * N * i + j) v[i][j] = c < 0 ? v[i][j] + add : add;
+      }
+    }
   }
   if (!in) return;
   T *d = static_cast<T *>(a.dlogits) + t * a.dld;
@@ -631,7 +665,10 @@ hipError_t route_backward(const RouteArgs &a, hipStream_t s) {
   auto go = [&](auto lanes, auto per) {
     constexpr int L = decltype(lanes)::value, V = decltype(per)::value;
     const int64_t grid = (a.tokens + RT / L - 1) / (RT / L);
-    hipLaunchKernelGGL((kr_backward<BF16, L, V>), dim3((unsigned)grid), dim3(RT), 0, s, a);
+    // 131072 x 8 bf16 logits: 10 us with every round there may be, 7.5 with one
+    constexpr int ALL = (ROUTE_MAX_CHOICES + L - 1) / L;
+    if (ALL == 1 || a.k <= L) hipLaunchKernelGGL((kr_backward<BF16, L, V, 1>), dim3((unsigned)grid), dim3(RT), 0, s, a);
+    else hipLaunchKernelGGL((kr_backward<BF16, L, V, ALL>), dim3((unsigned)grid), dim3(RT), 0, s, a);
     return hipGetLastError();
   };
   constexpr int N = Elem<BF16>::N;

@@ -70,8 +70,8 @@ def gradient(x, choices, dw, scoring, renormalize, scale):
     return d, size
 
 
-@pytest.mark.parametrize("scoring", ["sigmoid"])
-@pytest.mark.parametrize("renorm", [False])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("n,k", [(8, 1), (8, 2), (40, 6), (256, 8), (700, 20), (30, 30), (200, 32)])
 def test_gradient_of_a_sure_router(torch, n, k, scoring, renorm):
     # A score near 1 leaves 1 - s, and a mean of dw that is all but one dw, with few digits: what is left over has to
@@ -98,3 +98,20 @@ def test_gradient_of_a_sure_router(torch, n, k, scoring, renorm):
     total = (np.take_along_axis(s, choices, 1).sum(axis=1, keepdims=True) if renorm else 1.0)
     sums = 2.0 ** -50 * scale * np.abs(dw).max(axis=1, keepdims=True) * s / total
     within(f64(out), want, size * (4 * rel[:, None] + 12) * E + np.abs(want) * E + sums + TINY, "gradient by the logits")
+
+
+def test_gradient_of_repeated_choices(torch):
+    # the same expert several times, chosen first and last, beside others
+    rng = np.random.default_rng(5)
+    for scoring in ("softmax", "sigmoid"):
+        for n, k in ((8, 8), (64, 12), (300, 32)):
+            x = rng.standard_normal((50, n)).astype(np.float32)
+            choices = rng.integers(-1, min(n, k // 2) + 1, (50, k))  # some outside where n is small
+            dw = rng.standard_normal((50, k)).astype(np.float32)
+            out = torch.empty(50, n, device=DEV)
+            for renorm in (True, False):
+                M.route_backward(vec(torch, x), vec(torch, choices, "int64"), vec(torch, dw), out, True, scoring=scoring,
+                                 renormalize=renorm)
+                want = L.route_backward(x, choices, dw, scoring, renormalize=renorm)
+                # k products of scores below 1, each within (8 + 60 + 12) 4 e, weights' sums at least 1 / n of a score
+                within(f64(out), want, np.abs(dw).sum(axis=1, keepdims=True) * 400 * E * (n if renorm else 1), scoring)

@@ -13,7 +13,8 @@
 //
 // Ranks are computed in fp32; a token in which two ranks that decide about the
 // choice or its order are closer than fp32 tells apart is decided again in
-// fp64 (route_exact), so that the choice is that of the definition.  Without a
+// fp64 (route_exact), so that the choice is that of the definition; so is one
+// with a NaN, for which fp32 has no place below its lowest number.  Without a
 // bias the logits themselves order the experts, and nothing is ever close.
 //
 // Few lanes a token, so that what a choice exchanges stays within a row of
@@ -139,8 +140,10 @@ __device__ __forceinline__ float logit(const RouteArgs &a, int64_t t, int e) {
   return Elem<BF16>::get(static_cast<const T *>(a.logits)[t * a.ld + e]);
 }
 
-// rank as it is compared: -inf is never chosen, a NaN comes last, and a zero has no sign
+// rank as it is compared: -inf is never chosen, and a zero has no sign (tokens with a NaN are decided in fp64)
 __device__ __forceinline__ float orderly(float r) { return r != r ? kLowest : r + 0.f; }
+// In fp64 there is room below every fp32 rank, and below the sum of two.
+constexpr double kNanRank = -1e39;
 
 // Whether the logits order the experts: without a bias, as far as no ranks are added up.
 __device__ __forceinline__ bool ranked_by_logit(const RouteArgs &a) { return !a.bias && (a.groups == 1 || a.top == 1); }
@@ -167,7 +170,7 @@ __device__ __forceinline__ void route_exact(const RouteArgs &a, int64_t t, doubl
   // exp(x - max) for the softmax, exp(-x) for the sigmoid
   for (int e = lane; e < a.experts; e += 64) {
     if (by_logit) {
-      if (rank[e] != rank[e]) rank[e] = kLowest;
+      if (rank[e] != rank[e]) rank[e] = kNanRank;
       continue;
     }
     const double x = rank[e];
@@ -184,8 +187,8 @@ __device__ __forceinline__ void route_exact(const RouteArgs &a, int64_t t, doubl
   }
   for (int e = lane; e < a.experts; e += 64) {
     if (rank[e] == ninf || by_logit) continue;
-    const double r = rank[e] / total + (a.bias ? (double)a.bias[e] : 0.0);
-    rank[e] = r != r ? (double)kLowest : r;
+    const double b = a.bias ? (double)a.bias[e] : 0.0, r = rank[e] / total + b;
+    rank[e] = b == ninf ? ninf : r != r ? kNanRank : r;
   }
   // the best rank in [lo, hi) but for expert `but`, and the expert (or INT_MAX)
   auto best = [&](int lo, int hi, int but, double &v) {
@@ -281,9 +284,14 @@ __global__ __launch_bounds__(RT) void kr_route(RouteArgs a) {
       r[i] = r[i] == -INFINITY ? r[i] : s + b[i];
     }
   }
+  bool nan = false;
 #pragma unroll
-  for (int i = 0; i < V; ++i) r[i] = orderly(r[i]);
-  bool close = false;
+  for (int i = 0; i < V; ++i) {
+    nan |= r[i] != r[i];
+    r[i] = orderly(r[i]);
+  }
+  // of lane 0: whether the token is decided again in fp64
+  bool close = __ballot(nan) >> (threadIdx.x & 63 & ~(LANES - 1)) & (LANES == 64 ? ~0ull : (1ull << (LANES & 63)) - 1);
   // What a score may be off by, in units of 2^-24: an exponential of d carries |d| + 4 of itself, which moves a
   // sigmoid by at most 5 in all; a softmax's sum carries sum p (|d| + 2) <= 7 + 2 for 1024 experts, at most 22 for
   // its additions and 4 for the quotient and the product, its term s (|d| + 2) < 3.  The bias adds a rounding of

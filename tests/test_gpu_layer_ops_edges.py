@@ -115,3 +115,43 @@ def test_gradient_of_repeated_choices(torch):
                 want = L.route_backward(x, choices, dw, scoring, renormalize=renorm)
                 # k products of scores below 1, each within (8 + 60 + 12) 4 e, weights' sums at least 1 / n of a score
                 within(f64(out), want, np.abs(dw).sum(axis=1, keepdims=True) * 400 * E * (n if renorm else 1), scoring)
+
+
+@pytest.mark.parametrize("n,k", [(6, 6), (8, 2), (32, 8), (64, 6), (256, 8), (300, 32), (1000, 8)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_route_of_nan_beside_masks(torch, n, k, scoring, dtype):
+    # A NaN ranks below every number, the lowest one too; an expert masked by its bias stays out whatever its logit is.
+    rng = np.random.default_rng(n)
+    x = rng.standard_normal((12, n))
+    low = -3.4028235e38 if dtype == "fp32" else -3.3895314e38
+    x[0, :-1] = low                          # a mask of the type's lowest value
+    x[0, 0] = np.nan
+    x[1, 1::2] = low
+    x[1, ::3] = np.nan
+    x[2] = np.nan
+    x[3, 0] = np.nan
+    x[4, n // 2:] = np.nan
+    x[5, 1:] = -np.inf
+    x[5, 0] = np.nan
+    x[6, :] = low
+    x[6, n - 1] = np.nan
+    x[7, 0] = np.inf
+    x = x.astype(np.float32)
+    xd = torch.from_numpy(x).to(DEV).to(dt(torch, dtype))
+    x = f64(xd)
+    lowest, masked = np.zeros(n, dtype=np.float32), np.zeros(n, dtype=np.float32)
+    lowest[::2] = -3.4028235e38
+    masked[0], masked[n // 2] = -np.inf, -np.inf
+    for bias in (None, masked, lowest):
+        for groups in (1, 2):
+            choices, weights = torch.full((12, k), 99, dtype=torch.int32, device=DEV), torch.empty(12, k, device=DEV)
+            how = dict(scoring=scoring, groups=groups, keep_groups=1, group_top=2)
+            if groups > 1 and k > n // 2:
+                continue
+            M.route_experts(xd, choices, weights, bias=None if bias is None else vec(torch, bias), **how)
+            with np.errstate(invalid="ignore"):
+                want, w = L.route(x, k, bias=bias, **how)
+            assert np.array_equal(choices.cpu().numpy(), want), (bias is None, groups)
+            # a row's weights are NaN where a score among them is
+            assert np.array_equal(np.isnan(f64(weights)), np.isnan(w)), (bias is None, groups)

@@ -531,7 +531,8 @@ muon_status muon_dropout(const void *x, int64_t rows, int64_t cols, int64_t ld, 
  * tokens that are not valid get zeros, or keep what they hold.  It takes the
  * scoring, renormalize and scale of the choice, and no notice of the groups.
  * Limits: experts <= MUON_BALANCE_MAX_EXPERTS, k <= MUON_ROUTE_MAX_CHOICES,
- * groups <= MUON_ROUTE_MAX_GROUPS, tokens * k < 2^31. */
+ * groups <= MUON_ROUTE_MAX_GROUPS, tokens * k < 2^31, and tokens < 2^26 of
+ * more than 256 experts. */
 typedef enum { MUON_SCORE_SOFTMAX = 0, MUON_SCORE_SIGMOID = 1 } muon_scoring;
 #define MUON_ROUTE_MAX_CHOICES 32
 #define MUON_ROUTE_MAX_GROUPS 32

@@ -24,6 +24,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "devops.hpp"
 #include "layer_ops.hpp"
@@ -646,13 +647,38 @@ __global__ __launch_bounds__(RT) void kr_backward(RouteArgs a) {
   }
 }
 
+// Calls launch(args, workgroups) for as many tokens at a time as a grid of
+// below 2^32 threads takes, LANES a token.
+template <bool BF16, int LANES, class F>
+hipError_t in_grids(RouteArgs a, F launch) {
+  constexpr int PER = RT / LANES;
+  constexpr int64_t MOST = (((int64_t)1 << 32) / RT - 1) * PER;
+  const int64_t e = sizeof(typename Elem<BF16>::type), ids = (a.choices.is64 ? 8 : 4) * (int64_t)a.k;
+  auto on = [](auto &p, int64_t bytes) {
+    if (p) p = reinterpret_cast<std::remove_reference_t<decltype(p)>>(reinterpret_cast<uintptr_t>(p) + bytes);
+  };
+  for (int64_t left = a.tokens; left > 0; left -= MOST) {
+    a.tokens = std::min(left, MOST);
+    launch(a, (unsigned)((a.tokens + PER - 1) / PER));
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    on(a.logits, MOST * a.ld * e);
+    on(a.valid, MOST);
+    on(a.choices.p, MOST * ids);
+    on(a.weights, MOST * a.k * 4);
+    on(a.dweights, MOST * a.k * 4);
+    on(a.dlogits, MOST * a.dld * e);
+  }
+  return hipSuccess;
+}
+
 template <bool BF16>
 hipError_t route(const RouteArgs &a, hipStream_t s) {
   auto go = [&](auto lanes, auto per) {
     constexpr int L = decltype(lanes)::value, V = decltype(per)::value;
-    const int64_t grid = (a.tokens + RT / L - 1) / (RT / L);
-    hipLaunchKernelGGL((kr_route<BF16, L, V>), dim3((unsigned)grid), dim3(RT), 0, s, a);
-    return hipGetLastError();
+    return in_grids<BF16, L>(a, [&](const RouteArgs &b, unsigned grid) {
+      hipLaunchKernelGGL((kr_route<BF16, L, V>), dim3(grid), dim3(RT), 0, s, b);
+    });
   };
   typedef std::integral_constant<int, 4> c4;
   typedef std::integral_constant<int, 8> c8;
@@ -672,12 +698,12 @@ template <bool BF16>
 hipError_t route_backward(const RouteArgs &a, hipStream_t s) {
   auto go = [&](auto lanes, auto per) {
     constexpr int L = decltype(lanes)::value, V = decltype(per)::value;
-    const int64_t grid = (a.tokens + RT / L - 1) / (RT / L);
     // 131072 x 8 bf16 logits: 10 us with every round there may be, 7.5 with one
     constexpr int ALL = (ROUTE_MAX_CHOICES + L - 1) / L;
-    if (ALL == 1 || a.k <= L) hipLaunchKernelGGL((kr_backward<BF16, L, V, 1>), dim3((unsigned)grid), dim3(RT), 0, s, a);
-    else hipLaunchKernelGGL((kr_backward<BF16, L, V, ALL>), dim3((unsigned)grid), dim3(RT), 0, s, a);
-    return hipGetLastError();
+    return in_grids<BF16, L>(a, [&](const RouteArgs &b, unsigned grid) {
+      if (ALL == 1 || a.k <= L) hipLaunchKernelGGL((kr_backward<BF16, L, V, 1>), dim3(grid), dim3(RT), 0, s, b);
+      else hipLaunchKernelGGL((kr_backward<BF16, L, V, ALL>), dim3(grid), dim3(RT), 0, s, b);
+    });
   };
   constexpr int N = Elem<BF16>::N;
   typedef std::integral_constant<int, 1> c1;

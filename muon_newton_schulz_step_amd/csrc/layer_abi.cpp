@@ -43,8 +43,8 @@ muon_status check_route(const char *me, const void *logits, int64_t tokens, int6
   if (experts > ROUTE_MAX_EXPERTS || k > ROUTE_MAX_CHOICES)
     return fail(MUON_ERR_UNSUPPORTED, me, "at most 1024 experts and 32 choices");
   if (tokens >= kMax || tokens * k >= kMax || !fits(tokens, ld)) return fail(MUON_ERR_UNSUPPORTED, me, "tokens * k must be below 2^31");
-  // 64 lanes a token at the most
-  if (tokens > kThreads / 64 && experts > 256) return fail(MUON_ERR_UNSUPPORTED, me, "too many tokens of more than 256 experts");
+  if (tokens >= (int64_t)1 << 26 && experts > 256)
+    return fail(MUON_ERR_UNSUPPORTED, me, "tokens of more than 256 experts must be below 2^26");
   return MUON_OK;
 }
 

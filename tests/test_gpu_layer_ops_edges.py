@@ -155,3 +155,28 @@ def test_route_of_nan_beside_masks(torch, n, k, scoring, dtype):
             assert np.array_equal(choices.cpu().numpy(), want), (bias is None, groups)
             # a row's weights are NaN where a score among them is
             assert np.array_equal(np.isnan(f64(weights)), np.isnan(w)), (bias is None, groups)
+
+
+@pytest.mark.parametrize("tokens,n", [((1 << 30) + 70, 2), ((1 << 28) + 40, 33)])
+def test_route_of_more_tokens_than_a_grid_has_lanes_for(torch, tokens, n):
+    # 4 and 16 lanes a token: more than 2^32 in all.  Against calls on the tokens of both sides of the seams.
+    torch.cuda.empty_cache()
+    x = torch.empty(tokens, n, dtype=torch.bfloat16, device=DEV).normal_(generator=torch.Generator(DEV).manual_seed(1))
+    valid = torch.ones(tokens, dtype=torch.bool, device=DEV)
+    valid[5::1000] = False
+    c, w = torch.full((tokens, 1), 99, dtype=torch.int32, device=DEV), torch.full((tokens, 1), 9.0, device=DEV)
+    M.route_experts(x, c, w, valid=valid, renormalize=False)
+    assert int(c.min()) == -1 and int(c.max()) == n - 1 and float(w.max()) <= 1.0
+    d = torch.full_like(x, 9.0)
+    M.route_backward(x, c, w, d, True, valid=valid, renormalize=False)
+    assert float(d.max()) < 1.0
+    lanes = 4 if n == 2 else 16
+    seam = (1 << 32) // lanes
+    for at in (0, seam // 2, seam - 4096, tokens - 4096):
+        part = slice(at, min(tokens, at + 8192))
+        c2, w2, d2 = torch.empty_like(c[part]), torch.empty_like(w[part]), torch.empty_like(d[part])
+        M.route_experts(x[part], c2, w2, valid=valid[part], renormalize=False)
+        M.route_backward(x[part], c2, w2, d2, True, valid=valid[part], renormalize=False)
+        assert torch.equal(c[part], c2) and torch.equal(w[part], w2) and torch.equal(d[part], d2), at
+    del x, c, w, d, valid
+    torch.cuda.empty_cache()

@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "linear_dev.hpp"
+#include "linear_plan.hpp"
 
 namespace muon {
 
@@ -312,28 +313,6 @@ int64_t tiles_along(int64_t M, int32_t groups, bool grouped, int bt) {
   return (M + bt - 1) / bt + (grouped ? groups - 1 : 0);
 }
 
-// Tiles of 128 x 128 if they fill the chip, of 64 x 64 otherwise, and then K in
-// parts: enough for four workgroups a CU, of 8 stages of 64 (bf16) or 4 (fp32,
-// whose stages take twice as long) and more, as far as their sums take no more
-// than 64 MB.  64 x 4096 x 4096 bf16: 15.0 us in parts of 8 stages, 17.8 of 4;
-// 64 x 1024 x 1024 fp32: 13.1 in parts of 4, 19.1 of 8.  Where one tile a CU
-// fills the chip, parts begin to pay at 24 stages (1021 x 1000 bf16, whole and
-// in parts: K = 512 6.8 and 14.5 us, 1024 13.4 and 16.9, 2048 23.6 and 21.3).
-struct LinearPlan {
-  int w;
-  int32_t splits;
-};
-LinearPlan plan_of(int64_t M, int64_t N, int64_t K, int32_t groups, bool weight, bool bf16) {
-  const int64_t per = weight ? groups : 1;
-  if ((M + 127) / 128 * ((N + 127) / 128) * per >= 256) return {4, 1};
-  const int64_t tiles = (M + 63) / 64 * ((N + 63) / 64) * per;
-  const int64_t stages = (K / (weight ? groups : 1) + 63) / 64;
-  if (tiles >= 256 && stages < 24) return {2, 1};
-  const int64_t bytes = std::max<int64_t>(1, M * per * N * 4);
-  const int64_t parts = std::min<int64_t>({1024 / std::max<int64_t>(1, tiles), stages / (bf16 ? 8 : 4), ((int64_t)64 << 20) / bytes, 32});
-  return {2, (int32_t)std::max<int64_t>(1, parts)};
-}
-
 template <bool BF16, bool AX, bool BX>
 void go(const LinearArgs &a, bool dma, int w, unsigned grid, hipStream_t s) {
   if (w == 4) {
@@ -353,19 +332,7 @@ bool large_tiles(const LinearArgs &a, bool weight) {
   return tiles >= 160 && a.N >= 256 && (weight ? a.M >= 256 : a.M / a.groups >= 256);
 }
 
-// Whether a product's rows are few enough for kl_few.  4096 x 11008, kl_few
-// against 64 x 64 tiles: fp32 of 8 rows 38 and 53 us (K adjacent, across)
-// against 70; bf16 of 4 rows 19 and 21 against 24, of 8 rows 26 and 29 against
-// 24.  Where K is adjacent smaller weights still gain with 8 (4096 x 4096: 11
-// against 17), and rows of groups are mostly of different ones.
-bool few_rows(const LinearArgs &a, bool bf16, bool bx) { return a.M <= (bf16 && bx && !a.offsets.p ? 4 : FEW_ROWS); }
-
 }  // namespace
-
-size_t linear_partial_bytes(int64_t M, int64_t N, int64_t K, int32_t groups, bool weight) {
-  const int32_t parts = std::max(plan_of(M, N, K, groups, weight, false).splits, plan_of(M, N, K, groups, weight, true).splits);
-  return parts > 1 ? (size_t)parts * (size_t)(M * (weight ? groups : 1)) * (size_t)N * 4 : 0;
-}
 
 hipError_t launch_linear(LinearArgs a, bool bf16, int la, int lb, hipStream_t s) {
   const int e = bf16 ? 2 : 4;
@@ -381,10 +348,10 @@ hipError_t launch_linear(LinearArgs a, bool bf16, int la, int lb, hipStream_t s)
     return launch_linear256(a, bx, s);
   }
   hipError_t err;
-  if (dma && !weight && few_rows(a, bf16, bx)) {
+  if (dma && !weight && few_rows(a.M, bf16, bx, a.offsets.p != nullptr)) {
     err = launch_linear_few(a, bf16, bx, s);
   } else {
-    const LinearPlan p = plan_of(a.M, a.N, a.K, a.groups, weight, bf16);
+    const LinearPlan p = linear_plan(a.M, a.N, a.K, a.groups, weight, bf16);
     const int bt = 32 * p.w;
     a.splits = p.splits;
     a.tiles_m = (int32_t)tiles_along(a.M, a.groups, !weight && a.offsets.p, bt);

@@ -17,6 +17,7 @@
 #include <algorithm>
 
 #include "linear_dev.hpp"
+#include "linear_plan.hpp"
 
 namespace muon {
 
@@ -24,8 +25,8 @@ using namespace dev;
 
 namespace {
 
-constexpr int AW = 8, AC = FEW_COLUMNS;  // across: waves, columns
-constexpr int BW = 4, BC = 8;            // adjacent
+constexpr int AW = 8, AC = FEW_ACROSS;    // across: waves, columns
+constexpr int BW = 4, BC = FEW_ADJACENT;  // adjacent
 
 // Adds up v over the lanes that differ in bits D, D / 2 to LOW.  While several
 // values are left, lanes D apart give each other half of theirs: a lane ends
@@ -199,16 +200,11 @@ void go(const LinearArgs &a, unsigned grid, hipStream_t s) {
 
 // Sets the launch's tiles and parts; the parts' sums are joined by the caller.
 hipError_t launch_linear_few(LinearArgs &a, bool bf16, bool bx, hipStream_t s) {
-  // groups that have rows: no more than the rows
-  a.tiles_m = a.offsets.p ? (int32_t)std::min<int64_t>(a.M, a.groups) : 1;
-  a.tiles_n = (int32_t)((a.N + (bx ? AC : BC) - 1) / (bx ? AC : BC));
-  a.splits = 1;
+  const FewPlan p = few_plan(a.M, a.N, a.K, a.groups, bf16, bx);
+  a.tiles_m = p.tiles_m;
+  a.tiles_n = p.tiles_n;
+  a.splits = p.splits;
   const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
-  // K across, in parts while there are CUs for them and K is long enough to pay
-  // for the second launch, 3 us (2048 x 512 bf16: 5.7 us whole, 6.7 in 4 parts;
-  // 2048 x 512 fp32: 8.7 in 2 parts, 7.9 in 4; 1024 x 4096 fp32: 7.5, 8.7 in 2)
-  const int64_t bytes = a.K * (bf16 ? 2 : 4);
-  if (bx && bytes >= 8192) a.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>({256 / tiles, bytes / 2048, 32}));
   const unsigned grid = (unsigned)(tiles * a.splits);
   if (bf16) bx ? go<true, true>(a, grid, s) : go<true, false>(a, grid, s);
   else bx ? go<false, true>(a, grid, s) : go<false, false>(a, grid, s);

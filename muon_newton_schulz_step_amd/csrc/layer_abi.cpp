@@ -10,6 +10,7 @@
 #include "abi_checks.hpp"
 #include "layer_ops.hpp"
 #include "linear.hpp"
+#include "linear_plan.hpp"
 #include "muon.h"
 
 using namespace muon;

@@ -53,12 +53,8 @@ struct LinearQueue {
 // How operands lie: K adjacent (rows of A, columns of B), or the other way.
 enum LinearOperand : int32_t { LIN_K_ADJACENT = 0, LIN_K_ACROSS = 1 };
 
-// Products of up to FEW_ROWS rows take kl_few, whose workgroups take
-// FEW_COLUMNS columns where K is across, in parts of a multiple of FEW_PART.
-constexpr int FEW_ROWS = 8, FEW_COLUMNS = 64, FEW_PART = 512;
 hipError_t launch_linear_few(LinearArgs &a, bool bf16, bool bx, hipStream_t s);
 
-size_t linear_partial_bytes(int64_t M, int64_t N, int64_t K, int32_t groups, bool weight);
 hipError_t launch_linear(LinearArgs a, bool bf16, int la, int lb, hipStream_t s);
 
 // dbias[g] (+)= the sums of dy's columns over the group's rows

@@ -221,14 +221,16 @@ __global__ __launch_bounds__(256) void kl_join(LinearArgs a, int64_t rows) {
 
 constexpr int CS_THREADS = 256;
 
-// A thread takes 16 bytes of columns over part of a group's rows.
+// A thread takes 16 bytes of columns over part of a group's rows.  Sums are
+// fp64, as a thread may add up thousands of rows of one sign (131072 rows of
+// 0.1 in one part are 6e-5 off in fp32); a part's leaves rounded to fp32.
 template <bool BF16>
 __global__ __launch_bounds__(CS_THREADS) void kl_column_sums(ColumnSumArgs a) {
   typedef Elem<BF16> E;
   typedef typename E::type T;
   constexpr int N = E::N;
   // 16 lanes across (256 bytes), 16 rows a round
-  __shared__ float red[16][16 * N + 1];
+  __shared__ double red[16][16 * N + 1];
   const int lx = threadIdx.x & 15, ly = threadIdx.x >> 4;
   const int64_t col = ((int64_t)blockIdx.x * 16 + lx) * N;
   const int g = (int)blockIdx.y / a.splits, part = (int)blockIdx.y % a.splits;
@@ -239,9 +241,9 @@ __global__ __launch_bounds__(CS_THREADS) void kl_column_sums(ColumnSumArgs a) {
   }
   const int64_t r0 = lo + (hi - lo) * part / a.splits, r1 = lo + (hi - lo) * (part + 1) / a.splits;
   const int n = (int)lesser(N, a.cols - col);
-  float sum[N];
+  double sum[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) sum[i] = 0.f;
+  for (int i = 0; i < N; ++i) sum[i] = 0.0;
   const T *p = static_cast<const T *>(a.dy) + col;
   if (n == N) {
 #pragma unroll 4
@@ -249,13 +251,13 @@ __global__ __launch_bounds__(CS_THREADS) void kl_column_sums(ColumnSumArgs a) {
       float v[N];
       E::unpack(load16(p + r * a.ld), v);
 #pragma unroll
-      for (int i = 0; i < N; ++i) sum[i] += v[i];
+      for (int i = 0; i < N; ++i) sum[i] += (double)v[i];
     }
   } else if (n > 0) {
     for (int64_t r = r0 + ly; r < r1; r += 16)
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (i < n) sum[i] += E::get(p[r * a.ld + i]);
+        if (i < n) sum[i] += (double)E::get(p[r * a.ld + i]);
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) red[ly][lx * N + i] = sum[i];
@@ -263,11 +265,11 @@ __global__ __launch_bounds__(CS_THREADS) void kl_column_sums(ColumnSumArgs a) {
   const int c = threadIdx.x;
   const int64_t at = (int64_t)blockIdx.x * 16 * N + c;
   if (c >= 16 * N || at >= a.cols) return;
-  float v = 0.f;
+  double v = 0.0;
 #pragma unroll
   for (int y = 0; y < 16; ++y) v += red[y][c];
-  if (a.splits > 1) a.partial[((int64_t)g * a.splits + part) * a.cols + at] = v;
-  else a.out[g * a.cols + at] = a.first ? v : a.out[g * a.cols + at] + v;
+  if (a.splits > 1) a.partial[((int64_t)g * a.splits + part) * a.cols + at] = (float)v;
+  else a.out[g * a.cols + at] = a.first ? (float)v : (float)((double)a.out[g * a.cols + at] + v);
 }
 
 __global__ __launch_bounds__(CS_THREADS) void kl_column_join(ColumnSumArgs a) {

@@ -180,3 +180,26 @@ def test_route_of_more_tokens_than_a_grid_has_lanes_for(torch, tokens, n):
         assert torch.equal(c[part], c2) and torch.equal(w[part], w2) and torch.equal(d[part], d2), at
     del x, c, w, d, valid
     torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------- product
+
+
+@pytest.mark.parametrize("rows,cols,groups,dtype", [(1 << 17, 128, 1024, "fp32"), (1 << 17, 128, 1024, "bf16"), (40000, 4096, 32, "bf16"),
+                                                    (100003, 130, 1, "fp32"), (5000, 1000, 3, "fp32")])
+def test_bias_gradient_of_long_groups(torch, rows, cols, groups, dtype):
+    # One value throughout: every addition in 32 bits would round the same way.  Sums in 64 bits leave each part's
+    # rounding, that of the parts' sum, and of what was held: 4 e of the sum of magnitudes.
+    value = 0.1
+    dy = torch.full((rows, cols), value, dtype=dt(torch, dtype), device=DEV)
+    x = torch.ones(rows, 4, dtype=dy.dtype, device=DEV)
+    value = float(dy[0, 0].double())
+    offsets = torch.zeros(groups + 1, dtype=torch.int32, device=DEV)
+    offsets[groups // 2 + 1:] = rows                   # one group has every row
+    for first in (True, False):
+        dw, db = torch.full((groups, 4, cols), 3.0, device=DEV), torch.full((groups, cols), 3.0, device=DEV)
+        M.linear_weight_grad(x, dy, dw, first, poisoned(torch, M.linear_weight_grad_workspace_bytes(rows, 4, cols, groups)),
+                             dbias=db, offsets=offsets)
+        want = np.full((groups, cols), 0.0 if first else 3.0)
+        want[groups // 2] += rows * value
+        within(f64(db), want, 4 * E * np.abs(want), "dbias")

@@ -26,7 +26,16 @@ constexpr int STAGE_BYTES = 128;  // of K a stage holds: 64 bf16 or 32 fp32
 
 enum : int32_t { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4 };
 
-__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+// exp(x).  The rounding of x log2(e) moves it by |x| 2^-24 of itself: hidden
+// by a bf16 result's rounding, while for an fp32 result what the product
+// leaves over is multiplied in.
+template <bool BF16>
+__device__ __forceinline__ float exp_of(float x) {
+  const float p = x * kLog2e, e = __builtin_amdgcn_exp2f(p);
+  if (BF16) return e;
+  const float low = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -p));
+  return fabsf(p) < 256.f ? e * fmaf(low, 0.69314718f, 1.f) : e;  // further out 0 or infinity, and low no number
+}
 
 // Phi(v) = (1 + erf(v / sqrt 2)) / 2.  For bf16 results by Abramowitz and
 // Stegun 7.1.26, off by at most 0.8e-7 (a tenth of the instructions of
@@ -38,46 +47,52 @@ __device__ __forceinline__ float normal_cdf(float v) {
     const float x = fabsf(v) * 0.70710678f;
     const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
     const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
-    const float tail = 0.5f * p * exp_fast(-x * x);
+    const float tail = 0.5f * p * exp_of<true>(-x * x);
     return v < 0.f ? tail : 1.f - tail;
   } else {
     return 0.5f * erfcf(-0.70710678f * v);
   }
 }
-// (1 + tanh(c (v + 0.044715 v^3))) / 2 = 1 / (1 + exp(-2 c (...)))
 template <bool BF16>
 __device__ __forceinline__ float quotient(float d) {
   return BF16 ? __builtin_amdgcn_rcpf(d) : 1.f / d;
 }
+// q = 1 / (1 + exp(-u)), and 1 - q: for an fp32 result from the exponential
+// where q is near 1, which leaves 1 - q few digits.
 template <bool BF16>
-__device__ __forceinline__ float tanh_gate(float v) {
-  const float u = v * fmaf(0.0713548163f, v * v, 1.5957691216f);  // 2 sqrt(2 / pi) (v + 0.044715 v^3)
-  return quotient<BF16>(1.f + exp_fast(-u));
+__device__ __forceinline__ float logistic(float u, float &rest) {
+  const float e = exp_of<BF16>(-u), q = quotient<BF16>(1.f + e);
+  rest = !BF16 && u > 0.f ? e * q : 1.f - q;
+  return q;
 }
+// 2 sqrt(2 / pi) (v + 0.044715 v^3): (1 + tanh(half of it)) / 2 is its logistic
+__device__ __forceinline__ float tanh_argument(float v) { return v * fmaf(0.0713548163f, v * v, 1.5957691216f); }
 
 template <bool BF16>
 __device__ __forceinline__ float activate(int32_t act, float v) {
+  float rest;
   switch (act) {
     case ACT_RELU: return v < 0.f ? 0.f : v;
-    case ACT_SILU: return v * quotient<BF16>(1.f + exp_fast(-v));
+    case ACT_SILU: return v * logistic<BF16>(v, rest);
     case ACT_GELU: return v * normal_cdf<BF16>(v);
-    case ACT_GELU_TANH: return v * tanh_gate<BF16>(v);
+    case ACT_GELU_TANH: return v * logistic<BF16>(tanh_argument(v), rest);
     default: return v;
   }
 }
 template <bool BF16>
 __device__ __forceinline__ float slope(int32_t act, float v) {
+  float rest;
   switch (act) {
     case ACT_RELU: return v > 0.f ? 1.f : 0.f;
     case ACT_SILU: {
-      const float q = quotient<BF16>(1.f + exp_fast(-v));
-      return q * fmaf(v, 1.f - q, 1.f);
+      const float q = logistic<BF16>(v, rest);
+      return q * fmaf(v, rest, 1.f);
     }
-    case ACT_GELU: return fmaf(v * 0.39894228f, exp_fast(-0.5f * v * v), normal_cdf<BF16>(v));
+    case ACT_GELU: return fmaf(v * 0.39894228f, exp_of<BF16>(-0.5f * v * v), normal_cdf<BF16>(v));
     case ACT_GELU_TANH: {
       v = v < -64.f ? -64.f : v > 64.f ? 64.f : v;  // 0 and 1 from there on, where v^2 is still finite
-      const float q = tanh_gate<BF16>(v);
-      return fmaf(v * q * (1.f - q), fmaf(0.2140644489f, v * v, 1.5957691216f), q);
+      const float q = logistic<BF16>(tanh_argument(v), rest);
+      return fmaf(v * q * rest, fmaf(0.2140644489f, v * v, 1.5957691216f), q);
     }
     default: return 1.f;
   }

@@ -203,3 +203,45 @@ def test_bias_gradient_of_long_groups(torch, rows, cols, groups, dtype):
         want = np.full((groups, cols), 0.0 if first else 3.0)
         want[groups // 2] += rows * value
         within(f64(db), want, 4 * E * np.abs(want), "dbias")
+
+
+@pytest.mark.parametrize("act,dtype", [("silu", "bf16"), ("silu", "fp32"), ("gelu", "fp32"), ("gelu_tanh", "bf16"), ("gelu_tanh", "fp32")])
+def test_activations_far_out(torch, act, dtype):
+    # Relative to the value itself, down to where results leave the normal numbers.
+    #   silu       exp in two parts 4 e, 1 + exp, the quotient, the product: 10 e (bf16: a quotient of 2^-22: 16 e)
+    #   gelu_tanh  its exponent u = 1.6 v + 0.07 v^3 is rounded: 4 |u| e more
+    #   gelu       fp32: erfc's argument is rounded: (v^2 + 1) 2 e more, erfc itself 16 e;
+    #              bf16: the polynomial's 8e-5, the exponent v^2 / 2 in fp32: 4 v^2 e more
+    v = np.concatenate([np.linspace(-13.0, 13.0, 5001), np.linspace(-85.0, 85.0, 3001)])
+    if act != "silu":
+        v = v[np.abs(v) < (13.0 if act == "gelu" else 9.5)]
+    x = torch.from_numpy(v).to(dt(torch, dtype)).to(DEV)[:, None].contiguous()
+    out = torch.empty_like(x)
+    M.linear_forward(x, torch.ones(1, 1, dtype=x.dtype, device=DEV), out, poisoned(torch, M.linear_workspace_bytes(len(v), 1, 1, 1)),
+                     activation=act)
+    v = f64(x)
+    want, _ = L.activation(act, v)
+    rel = {"silu": 16.0 + 0 * v, "gelu_tanh": 16.0 + 4 * np.abs(1.6 * v + 0.0714 * v ** 3),
+           "gelu": 24.0 + 4 * v * v + (8e-5 / E if dtype == "bf16" else 0.0)}[act] * E
+    within(f64(out), want, np.abs(want) * (rel + HALF[dtype]), act)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_slopes_of_large_numbers(torch, act):
+    # The slope's second part is v (1 - q) q with q near 1: 1 - q from exp(-v) instead of q.
+    #   silu      a product and three sums near 1: 8 e of the sum of the parts' magnitudes (at most 1.3)
+    #   gelu_tanh the same, with its exponent u rounded: 4 |u| e of the second part
+    v = np.linspace(0.5, 30.0, 3001)
+    x = torch.from_numpy(v).float().to(DEV)[:, None].contiguous()
+    d = torch.empty_like(x)
+    M.activation_grad(torch.ones_like(x), x, d, act)
+    v = f64(x)
+    if act == "silu":
+        e = np.exp(-v)
+        q, second, u = 1 / (1 + e), v * e / (1 + e) ** 2, 0.0
+    else:
+        c = np.sqrt(2 / np.pi)
+        u = 2 * c * (v + 0.044715 * v ** 3)
+        e = np.exp(-u)
+        q, second = 1 / (1 + e), v * 2 * c * (1 + 0.134145 * v * v) * e / (1 + e) ** 2
+    within(f64(d), q + second, (q + second) * 8 * E + second * (4 * u + 16) * E, act + "'")

@@ -56,6 +56,11 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
   typedef Operand<true, BT, BX> OB;
   typedef typename OA::T T;
   constexpr int KS = OA::KS;
+  // What a wave has under way when it waits: a stage's loads, and behind a tile
+  // at least kStores stores of its sums (every row of blocks is stored, those
+  // that do not exist outside the range).  Fewer would leave a wait too short.
+  constexpr int kLoads = OA::LOADS + OB::LOADS, kStores = 32;
+  static_assert(TileRows<MODE != LIN_WEIGHT, 8>::STORES >= kStores && kLoads + kStores < 64, "the vmcnt immediates behind a tile");
   // workgroup i runs on XCD i % 8: chunks of 256 tiles, 32 consecutive ones an XCD
   const int xcd = (int)blockIdx.x & 7, slot = (int)blockIdx.x >> 3;
   int t = (slot >> 5) * 256 + xcd * 32 + (slot & 31);
@@ -153,9 +158,9 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
 #pragma unroll
         for (int q = 0; q < 16; ++q) dma1(s1, base ^ 1, q);
       }
-      // all but the second stage's 16 loads, and behind a tile its 32 stores or more
-      if (ready) asm volatile("s_waitcnt vmcnt(48) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      else asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      // all but the second stage's loads, and behind a tile its stores
+      if (ready) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads + kStores) : "memory");
+      else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads) : "memory");
       if constexpr (QUEUE) {
         chain = queued(uni32(*next_slot), y);
         if (threadIdx.x == 0 && chain) taken = atomicAdd(&queue->taken[xcd][0], 1);
@@ -168,8 +173,8 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
       for (int q = 0; q < 16; ++q) read1(0, base, 0, q);
       constexpr int kBar1 = 9;           // group of k-step 0 that ends with the first barrier
       constexpr int kDma0 = 15 - kBar1;  // loads in k-step 0
-      constexpr int kDma1 = 16 - kDma0;  // in k-step 1
-      static_assert(kDma0 == 6, "the vmcnt immediates of the second barrier");
+      constexpr int kDma1 = kLoads - kDma0;  // in k-step 1
+      static_assert(kLoads == 16 && kDma0 > 0, "the loads' places among the products");
       auto body = [&](int kt, auto kind) {
         constexpr Kind KIND = decltype(kind)::value;
         const int st = (kt ^ base) & 1;
@@ -190,9 +195,9 @@ __global__ __launch_bounds__(LIN_THREADS, 1) void kl_linear256(LinearArgs a, int
           __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (KIND != LAST) {
-          // the next stage's loads: all but the six since, and behind a tile its 32 stores or more
-          if (KIND == FIRST && ready) asm volatile("s_waitcnt vmcnt(38)\n\ts_barrier" ::: "memory");
-          else asm volatile("s_waitcnt vmcnt(6)\n\ts_barrier" ::: "memory");
+          // the next stage's loads: all but those of this k-step, and behind a tile its stores
+          if (KIND == FIRST && ready) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kDma0 + kStores) : "memory");
+          else asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kDma0) : "memory");
         }
 #pragma unroll
         for (int n = 0; n < 16; ++n) {

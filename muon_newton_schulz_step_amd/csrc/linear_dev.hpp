@@ -544,6 +544,7 @@ __device__ __forceinline__ void with_activation(int32_t act, F f) {
 template <bool BF16, int W>
 struct TileRows {
   static constexpr int E = BF16 ? 2 : 4, P = W / 2;
+  static constexpr int STORES = W * P * (E / 2);  // of a whole tile, by a wave
   const char *base;
   int64_t step;  // bytes of 16 rows
   int64_t range;

@@ -596,7 +596,10 @@ muon_status muon_expert_combine_backward(const void *dout, int64_t tokens, int64
  * what falls outside [0, rows) is cut off).  Rows of no group are not
  * touched.  offsets may be NULL for one group of all rows.
  * Sums are fp32, of bf16 products or of fp32 ones; what leaves is rounded
- * once. */
+ * once.
+ * Limits, of the gradients too: rows, in, out < 2^31, groups <=
+ * MUON_LINEAR_MAX_GROUPS, and with R = rows / 128 + groups, I = in / 128 + 1,
+ * O = out / 128 + 1 (rounded down) each of R I, R O and I O groups < 2^23. */
 typedef enum {
   MUON_ACT_NONE = 0, MUON_ACT_RELU = 1, MUON_ACT_SILU = 2, MUON_ACT_GELU = 3, MUON_ACT_GELU_TANH = 4
 } muon_activation;

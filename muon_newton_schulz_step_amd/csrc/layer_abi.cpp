@@ -71,7 +71,7 @@ muon_status check_rows(const char *me, int64_t tokens, int64_t k, int64_t rows, 
 }
 
 constexpr int64_t kMaxGroups = 1024;
-constexpr int64_t kMaxTiles = (int64_t)1 << 23;  // of 128 x 128 elements, in a launch
+constexpr int64_t kMaxTiles = (int64_t)1 << 23;  // of 128 x 128 elements: a launch has fewer, and every grid its threads
 
 muon_status check_linear(const char *me, int64_t rows, int64_t in, int64_t out, int64_t groups) {
   static_assert(MUON_LINEAR_MAX_GROUPS == kMaxGroups, "the header's limit");
@@ -80,8 +80,8 @@ muon_status check_linear(const char *me, int64_t rows, int64_t in, int64_t out, 
   if (rows >= kMax || in >= kMax || out >= kMax || groups > kMaxGroups)
     return fail(MUON_ERR_UNSUPPORTED, me, "rows, in and out must be below 2^31, groups at most 1024");
   const int64_t r = rows / 128 + groups, i = in / 128 + 1, o = out / 128 + 1;
-  if (r > kMaxTiles / i || r > kMaxTiles / o || i > kMaxTiles / o / groups)
-    return fail(MUON_ERR_UNSUPPORTED, me, "more than 2^23 tiles of 128 x 128 elements");
+  if (r * i >= kMaxTiles || r * o >= kMaxTiles || i * o * groups >= kMaxTiles)
+    return fail(MUON_ERR_UNSUPPORTED, me, "2^23 tiles of 128 x 128 elements or more");
   return MUON_OK;
 }
 

@@ -3,6 +3,7 @@ place in the workspace (nothing reaches a device)."""
 
 from __future__ import annotations
 
+import ctypes as C
 import os
 import shutil
 import subprocess
@@ -45,3 +46,14 @@ def test_the_library_asks_for_that_workspace():
     # few rows by long weights: 32 parts of fp32 sums; many rows: none
     assert M.linear_workspace_bytes(4, 16384, 512, 1) >= 256 + 32 * 4 * 512 * 4
     assert M.linear_workspace_bytes(8192, 4096, 11008, 1) == 256
+
+
+def test_products_refuse_from_their_limit_of_tiles_on():
+    # of 128 x 128 elements; a grid of 64 columns a workgroup has 2^32 threads from 2^30 - 63 columns on
+    n = C.c_size_t()
+    for f in ("muon_linear_workspace_bytes", "muon_linear_weight_grad_workspace_bytes"):
+        for rows, a, b, groups in ((1, 1, (1 << 30) - 64, 1), (1, (1 << 30) - 64, 1, 1), (1 << 20, 1 << 17, 8, 1), (1 << 20, 8, 1 << 17, 1),
+                                   (8, 1 << 13, 1 << 14, 1024)):
+            _expect(f, "MUON_ERR_UNSUPPORTED", rows, a, b, groups, C.byref(n))
+    for f in (M.linear_workspace_bytes, M.linear_weight_grad_workspace_bytes):
+        assert f(1, 1, (1 << 30) - 129, 1) >= 256 and f((1 << 20) - 256, (1 << 17) - 128, 8, 1) >= 256

@@ -657,11 +657,11 @@ hipError_t in_grids(RouteArgs a, F launch) {
   auto on = [](auto &p, int64_t bytes) {
     if (p) p = reinterpret_cast<std::remove_reference_t<decltype(p)>>(reinterpret_cast<uintptr_t>(p) + bytes);
   };
-  for (int64_t left = a.tokens; left > 0; left -= MOST) {
+  for (int64_t left = a.tokens;; left -= MOST) {
     a.tokens = std::min(left, MOST);
     launch(a, (unsigned)((a.tokens + PER - 1) / PER));
     const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
+    if (err != hipSuccess || left <= MOST) return err;  // (behind the last one a row stride may be any)
     on(a.logits, MOST * a.ld * e);
     on(a.valid, MOST);
     on(a.choices.p, MOST * ids);
@@ -669,7 +669,6 @@ hipError_t in_grids(RouteArgs a, F launch) {
     on(a.dweights, MOST * a.k * 4);
     on(a.dlogits, MOST * a.dld * e);
   }
-  return hipSuccess;
 }
 
 template <bool BF16>

@@ -182,6 +182,18 @@ def test_route_of_more_tokens_than_a_grid_has_lanes_for(torch, tokens, n):
     torch.cuda.empty_cache()
 
 
+def test_route_of_a_row_of_any_stride(torch):
+    x = torch.randn(40, device=DEV)
+    far = torch.as_strided(x, (1, 40), (1 << 54, 1))
+    c, w, d = torch.empty(1, 3, dtype=torch.int32, device=DEV), torch.empty(1, 3, device=DEV), torch.empty(1, 40, device=DEV)
+    M.route_experts(far, c, w)
+    M.route_backward(far, c, w, d, True)
+    c2, w2, d2 = torch.empty_like(c), torch.empty_like(w), torch.empty_like(d)
+    M.route_experts(x[None], c2, w2)
+    M.route_backward(x[None], c2, w2, d2, True)
+    assert torch.equal(c, c2) and torch.equal(w, w2) and torch.equal(d, d2)
+
+
 # ---------------------------------------------------------------- product
 
 

@@ -10,7 +10,7 @@
 // A stage has two barriers: one when every wave has read the stage's last
 // fragments, which frees its buffer for the stage after the next, and one
 // between its two k-steps, which waits for the next stage's loads alone.
-// 8192 x 4096 x 11008: 615 us, 1.20 PFLOP/s, 1.45 us a stage and round.
+// 8192 x 4096 x 11008: 630 us, 1.17 PFLOP/s, 1.45 us a stage and round.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

@@ -15,7 +15,8 @@
 // choice or its order are closer than fp32 tells apart is decided again in
 // fp64 (route_exact), so that the choice is that of the definition; so is one
 // with a NaN, for which fp32 has no place below its lowest number.  Without a
-// bias the logits themselves order the experts, and nothing is ever close.
+// bias the logits themselves order the experts, and only fp32 ones that differ
+// in the last bits at the border, or in none, are decided again.
 //
 // Scores and weights are fp32, a weight off by the errors of its scores (as
 // tol() below counts them): what takes the weights has no more bits.
